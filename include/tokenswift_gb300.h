@@ -464,6 +464,163 @@ int ts_ngram_build_tree(const int32_t* table, int V, int cap, const int32_t* roo
                         const uint32_t* rand_keys, int T_max, int32_t* parents,
                         int32_t* tokens, int32_t* n_nodes, int32_t* status, void* stream);
 
+/* ------------------------------------------------------------------------
+ * (6) The paged cache: several streams' K/V rows in shared memory.
+ *
+ * The source method keeps one contiguous cache a stream and takes rotated
+ * queries and keys as given; these calls hold many streams in one pool of
+ * pages, rotate and write their new tokens, run the prompts' own attention in
+ * chunks, and attend to a few chosen pages of a long cache (§3.3 Dynamic KV
+ * Cache Management selects single rows once a step; here every query chooses
+ * pages).
+ *
+ * Cache    k_pages, v_pages [n_pages, Hkv, page_size, d], page_size 16, 32,
+ *          64 or 128, d 64 or 128, bf16, or fp16 with TS_PAGED_FP16 (then
+ *          every 16-bit tensor of the call is fp16).  16-byte aligned, and
+ *          n_pages * Hkv * page_size < 2^31.
+ * Batch    n token rows hold the new tokens of n_seq sequences: sequence s
+ *          owns tokens [cu_q[s], cu_q[s+1]), cu_q [n_seq + 1] int32
+ *          non-decreasing, and has seq_lens[s] rows, the new ones included
+ *          (seq_lens [n_seq] int32).  A sequence may own no token, and tokens
+ *          behind cu_q[n_seq] belong to none: their outputs are left as they
+ *          were.  New token i of a sequence stands at row
+ *          seq_lens[s] - q_len + i.
+ * Table    page_table [n_seq, max_pages] int32: row p of sequence s is row
+ *          p % page_size of page page_table[s][p / page_size].  Entries
+ *          behind the sequence's last row are not read.
+ * cu_q, seq_lens and page_table are device arrays and may change between
+ * replays of a captured graph.  A value out of its range (a page id, a length
+ * above max_pages * page_size, a decreasing cu_q) is reported as
+ * TS_ERR_INVALID_ARG in `status`; the outputs of that sequence are then
+ * unspecified, and no access leaves the buffers.  n = 0 does nothing and
+ * accepts NULL tensors.
+ * ------------------------------------------------------------------------ */
+#define TS_PAGED_FP16 1
+#define TS_ROPE_INTERLEAVED 2
+
+/* Rotary frequencies (host only): freqs [rot_dim / 2] HOST doubles, radians a
+ * position, and the factor the rotated rows carry.  f_c = base^(-2c/rot_dim),
+ * c = 0 .. rot_dim/2 - 1, then by `scaling` (factor s >= 1):
+ *   TS_ROPE_PLAIN       f_c
+ *   TS_ROPE_LINEAR      f_c / s (positions interpolated)
+ *   TS_ROPE_BASE        base * s^(rot_dim / (rot_dim - 2)) in place of base
+ *                       (rot_dim >= 4)
+ *   TS_ROPE_WAVELENGTH  by the turns r = original_len * f_c / 2 pi a pair
+ *                       makes: f_c where r > high, f_c / s where r < low, and
+ *                       ((1 - w) / s + w) f_c with w = (r - low) / (high - low)
+ *                       between
+ *   TS_ROPE_RAMP        by the pair's index: with x(r) = rot_dim *
+ *                       ln(original_len / (2 pi r)) / (2 ln base), first =
+ *                       max(floor(x(high)), 0), last = min(ceil(x(low)),
+ *                       rot_dim - 1) and w = clamp((c - first) /
+ *                       max(last - first, 0.001), 0, 1):
+ *                       (1 - w) f_c + w f_c / s; *rope_scale = 0.1 ln s + 1
+ * *rope_scale is 1 but for TS_ROPE_RAMP (rope_scale may be NULL).
+ * rot_dim even, 2 .. 1024; base > 1; original_len, low, high are read by the
+ * last two kinds only: original_len > 0, 0 < low < high. */
+#define TS_ROPE_PLAIN 0
+#define TS_ROPE_LINEAR 1
+#define TS_ROPE_BASE 2
+#define TS_ROPE_WAVELENGTH 3
+#define TS_ROPE_RAMP 4
+int ts_rope_frequencies(int rot_dim, double base, int scaling, double factor,
+                        double original_len, double low, double high, double* freqs,
+                        float* rope_scale);
+
+/* Rotate the batch's new queries and keys and write keys and values into the
+ * cache.  The first rot_dim columns of every query and key row turn by
+ * a = p * freqs[c]: (x, y) -> (x cos a - y sin a, y cos a + x sin a) *
+ * rope_scale, pairs (c, c + rot_dim/2), or (2c, 2c + 1) with
+ * TS_ROPE_INTERLEAVED; the columns behind are copied unscaled.
+ *
+ * q        n rows of [Hq, d], q_stride elements apart (likewise k, v of
+ *          [Hkv, d]): a stride of the layer's fused projection is fine.
+ *          16-byte aligned, strides multiples of 8.
+ * positions [n] int32, or NULL: the token's row.  A draft tree's nodes stand
+ *          at seq_len - q_len + depth.  |position| < 2^30.
+ * freqs    [rot_dim / 2] fp64, device (NULL with rot_dim = 0).
+ * rot_dim  0 or a multiple of 16, at most d.
+ * q_out    [n, Hq, d]; may be q itself where q is dense.
+ * key_min, key_max  [n_pages, Hkv, d] in/out, or both NULL: the element-wise
+ *          bounds of each page's key rows, for ts_paged_select_pages.  A page
+ *          whose first row is written now starts over; else its bounds are
+ *          widened.  (A row written again leaves its old value inside the
+ *          bounds: they stay bounds.)
+ * No two sequences of one call may write the same page. */
+int ts_paged_rope_append(const void* q, const void* k, const void* v, int64_t q_stride,
+                         int64_t k_stride, int64_t v_stride, int n, int Hq, int Hkv, int d,
+                         const int32_t* cu_q, const int32_t* seq_lens, int n_seq,
+                         const int32_t* page_table, int max_pages, int page_size,
+                         int64_t n_pages, const int32_t* positions, const double* freqs,
+                         int rot_dim, float rope_scale, void* q_out, void* k_pages,
+                         void* v_pages, void* key_min, void* key_max, int flags,
+                         int32_t* status, void* stream);
+
+/* Causal attention of the batch's new tokens over their caches: prompts and
+ * prompt chunks, single tokens, or both in one call.  The new tokens' own
+ * rows are in the cache already (ts_paged_rope_append).  New token i of
+ * sequence s, at row p = seq_lens[s] - q_len + i, head h, KV head
+ * kv = h / (Hq/Hkv):
+ *   s_j = q[t,h,:] . k_j / sqrt(d) over the sequence's rows j <= p,
+ *   o[t,h,:] = softmax_j(s) . v_j,  lse[t,h] = ln sum_j exp(s_j).
+ * A token with no row to see (seq_lens[s] < q_len - i) gets o = 0, lse = -inf.
+ * Rows [0, seq_lens[s]) must hold finite values; what the pages hold behind
+ * them does not matter.
+ *
+ * q [n, Hq, d]; o [n, Hq, d] of q's type, out; lse [n, Hq] fp32 out, or NULL.
+ * max_q    a bound on the sequences' new tokens, 1 .. n (a longer sequence is
+ *          reported in `status` and its tokens behind max_q are not written).
+ * max_kv   the longest sequence, as far as the host knows: it sizes the split
+ *          of the keys and bounds nothing (<= 0: max_pages * page_size).
+ * workspace >= ts_paged_attention_workspace_bytes of the same arguments. */
+size_t ts_paged_attention_workspace_bytes(int n, int n_seq, int Hq, int Hkv, int d,
+                                          int max_pages, int page_size, int max_q,
+                                          int64_t max_kv);
+int ts_paged_attention(const void* q, const void* k_pages, const void* v_pages, int n, int Hq,
+                       int Hkv, int d, const int32_t* cu_q, const int32_t* seq_lens, int n_seq,
+                       const int32_t* page_table, int max_pages, int page_size,
+                       int64_t n_pages, int max_q, int64_t max_kv, void* o, float* lse,
+                       void* workspace, size_t workspace_bytes, int flags, int32_t* status,
+                       void* stream);
+
+/* Choose the pages each new token attends to.  A page's score for a KV head is
+ * the largest sum of scores its key bounds allow the head's group:
+ *   score = sum over the group's heads h and columns c of
+ *           max(q[t,h,c] * key_min[c], q[t,h,c] * key_max[c]),
+ * rounded to fp32 once.  A token at row p sees pages 0 .. p / page_size; kept
+ * are the first n_sink of them, the last n_recent, and the n_top best of those
+ * between by (score desc, page asc), or all when they are no more than
+ * N = n_sink + n_top + n_recent.  Scores that are not finite rank last.
+ *
+ * q        [n, Hq, d] rotated; key_min, key_max [n_pages, Hkv, d].
+ * n_recent >= 1 (the last page is the token's own); n_sink, n_top >= 0;
+ *          n <= 65535.
+ * pages    [n, Hkv, N] int32 out: positions in the page table's row,
+ *          ascending, -1 behind the last; counts [n, Hkv] int32 out.
+ * workspace >= ts_paged_select_workspace_bytes(n, Hkv, max_pages). */
+size_t ts_paged_select_workspace_bytes(int n, int Hkv, int max_pages);
+int ts_paged_select_pages(const void* q, const void* key_min, const void* key_max, int n, int Hq,
+                          int Hkv, int d, const int32_t* cu_q, const int32_t* seq_lens,
+                          int n_seq, const int32_t* page_table, int max_pages, int page_size,
+                          int64_t n_pages, int n_top, int n_sink, int n_recent, int32_t* pages,
+                          int32_t* counts, void* workspace, size_t workspace_bytes, int flags,
+                          int32_t* status, void* stream);
+
+/* ts_paged_attention over chosen pages: token t's heads of KV head kv see the
+ * rows j <= p of the pages pages[t, kv, 0 : counts[t, kv]] (positions in the
+ * page table's row, each at most once; [n, Hkv, n_sel], as
+ * ts_paged_select_pages writes them).  counts = 0 gives o = 0, lse = -inf.  A
+ * listed page behind the token's own is reported in `status` and left out.
+ * workspace >= ts_paged_selected_workspace_bytes of the same arguments. */
+size_t ts_paged_selected_workspace_bytes(int n, int Hq, int Hkv, int d, int page_size, int n_sel);
+int ts_paged_attention_selected(const void* q, const void* k_pages, const void* v_pages, int n,
+                                int Hq, int Hkv, int d, const int32_t* cu_q,
+                                const int32_t* seq_lens, int n_seq, const int32_t* page_table,
+                                int max_pages, int page_size, int64_t n_pages,
+                                const int32_t* pages, const int32_t* counts, int n_sel, void* o,
+                                float* lse, void* workspace, size_t workspace_bytes, int flags,
+                                int32_t* status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

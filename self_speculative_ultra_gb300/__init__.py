@@ -26,6 +26,10 @@ __all__ = [
     "ts_sample_workspace_bytes", "ts_penalized_sample_accept", "ts_kv_commit",
     "ts_kv_commit_batched", "commit_pointer_table", "ts_kv_append_batched",
     "ts_reject_workspace_bytes", "ts_rejection_sample_accept",
+    "ts_rope_frequencies", "ts_paged_rope_append",
+    "ts_paged_attention_workspace_bytes", "ts_paged_attention",
+    "ts_paged_select_workspace_bytes", "ts_paged_select_pages",
+    "ts_paged_selected_workspace_bytes", "ts_paged_attention_selected",
 ]
 
 TS_OK, TS_ERR_INVALID_ARG, TS_ERR_UNSUPPORTED, TS_ERR_CUDA, TS_ERR_TIMEOUT, TS_ERR_WORKSPACE = range(6)
@@ -33,6 +37,7 @@ TS_VERIFY_V_FP16 = 1     # ts_verify_attention_flags: the V cache holds fp16
 TS_KV_V_FP16 = 1         # ts_kv_append_batched_flags: write V rows into fp16 caches
 
 _c_void_p, _i32, _i64, _sz, _f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
+_f64 = ctypes.c_double
 
 _SIGNATURES = {
     "ts_status_string": (ctypes.c_char_p, [_i32]),
@@ -105,6 +110,28 @@ _SIGNATURES = {
     "ts_ngram_build_tree": (_i32, [_c_void_p, _i32, _i32, _c_void_p, _c_void_p, _i32, _i32, _i32,
                                    _c_void_p, _i32, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
                                    _c_void_p]),
+    "ts_rope_frequencies": (_i32, [_i32, _f64, _i32, _f64, _f64, _f64, _f64,
+                                   ctypes.POINTER(_f64), ctypes.POINTER(_f32)]),
+    "ts_paged_rope_append": (_i32, [_c_void_p, _c_void_p, _c_void_p, _i64, _i64, _i64, _i32, _i32,
+                                    _i32, _i32, _c_void_p, _c_void_p, _i32, _c_void_p, _i32, _i32,
+                                    _i64, _c_void_p, _c_void_p, _i32, _f32, _c_void_p, _c_void_p,
+                                    _c_void_p, _c_void_p, _c_void_p, _i32, _c_void_p, _c_void_p]),
+    "ts_paged_attention_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
+                                                 _i64]),
+    "ts_paged_attention": (_i32, [_c_void_p, _c_void_p, _c_void_p, _i32, _i32, _i32, _i32,
+                                  _c_void_p, _c_void_p, _i32, _c_void_p, _i32, _i32, _i64, _i32,
+                                  _i64, _c_void_p, _c_void_p, _c_void_p, _sz, _i32, _c_void_p,
+                                  _c_void_p]),
+    "ts_paged_select_workspace_bytes": (_sz, [_i32, _i32, _i32]),
+    "ts_paged_select_pages": (_i32, [_c_void_p, _c_void_p, _c_void_p, _i32, _i32, _i32, _i32,
+                                     _c_void_p, _c_void_p, _i32, _c_void_p, _i32, _i32, _i64, _i32,
+                                     _i32, _i32, _c_void_p, _c_void_p, _c_void_p, _sz, _i32,
+                                     _c_void_p, _c_void_p]),
+    "ts_paged_selected_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32]),
+    "ts_paged_attention_selected": (_i32, [_c_void_p, _c_void_p, _c_void_p, _i32, _i32, _i32, _i32,
+                                           _c_void_p, _c_void_p, _i32, _c_void_p, _i32, _i32, _i64,
+                                           _c_void_p, _c_void_p, _i32, _c_void_p, _c_void_p,
+                                           _c_void_p, _sz, _i32, _c_void_p, _c_void_p]),
 }
 
 _LIB = None
@@ -581,3 +608,231 @@ def ts_ngram_build_tree(table, V, cap, root_token, head_topk, k, rand_keys, T_ma
                                      n_heads, head_k, k, _ptr(rand_keys), T_max, _ptr(parents),
                                      _ptr(tokens), _ptr(n_nodes), _ptr(status), _stream(stream)))
     return parents, tokens, n_nodes
+
+
+# ---------------------------------------------------------------------------
+# the paged cache
+# ---------------------------------------------------------------------------
+TS_PAGED_FP16 = 1
+TS_ROPE_INTERLEAVED = 2
+_ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "wavelength": 3, "ramp": 4}
+
+
+def ts_rope_frequencies(rot_dim, base=10000.0, scaling="plain", factor=1.0, original_len=0.0,
+                        low=1.0, high=32.0, device="cuda"):
+    """Rotary frequencies [rot_dim / 2] fp64 (radians a position) on `device`
+    and the factor rotated rows carry, for scaling "plain", "linear", "base",
+    "wavelength" or "ramp" (formulas in the C header).  Make it once a model."""
+    if scaling not in _ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(_ROPE_SCALINGS)}")
+    host = (_f64 * max(rot_dim // 2, 1))()
+    scale = _f32(0.0)
+    _check(lib().ts_rope_frequencies(rot_dim, base, _ROPE_SCALINGS[scaling], factor, original_len,
+                                     low, high, host, ctypes.byref(scale)))
+    return torch.tensor(list(host), dtype=torch.float64).to(device), scale.value
+
+
+class _On:
+    """The device and stream of one paged call: every tensor on one device,
+    which is made current for the launch; memory the call takes from the
+    allocator is tied to the stream it is used on."""
+
+    __slots__ = ("device", "stream", "given", "guard")
+
+    def __init__(self, first, stream, **tensors):
+        self.device = first.device
+        for name, t in tensors.items():
+            if t is not None and t.device != self.device:
+                raise ValueError(f"{name} is on {t.device}, q is on {self.device}")
+        self.given = stream is not None
+        self.stream = torch.cuda.current_stream(self.device) if stream is None else stream
+        self.guard = None if self.device.index == torch.cuda.current_device() \
+            else torch.cuda.device(self.device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+    def empty(self, shape, dtype):
+        t = torch.empty(shape, dtype=dtype, device=self.device)
+        if self.given:
+            t.record_stream(self.stream)
+        return t
+
+    def workspace(self, nbytes, workspace):
+        if workspace is None and nbytes:
+            workspace = self.empty(nbytes, torch.uint8)
+        return _workspace(nbytes, self.device, workspace)
+
+    @property
+    def handle(self):
+        return ctypes.c_void_p(self.stream.cuda_stream)
+
+
+_PAGED_DTYPES = (torch.bfloat16, torch.float16)
+
+
+def _paged_batch(q, cu_q, seq_lens, page_table):
+    _dev(cu_q, torch.int32, "cu_q")
+    n_seq = cu_q.numel() - 1
+    _dev(seq_lens, torch.int32, "seq_lens", (n_seq,))
+    _dev(page_table, torch.int32, "page_table")
+    if page_table.dim() != 2 or page_table.shape[0] != n_seq:
+        raise ValueError(f"page_table has shape {tuple(page_table.shape)}, expected ({n_seq}, pages)")
+    return n_seq, page_table.shape[1]
+
+
+def _paged_out(on, t, shape, dtype, name):
+    return on.empty(shape, dtype) if t is None else _dev(t, dtype, name, shape)
+
+
+def ts_paged_rope_append(q, k, v, cu_q, seq_lens, page_table, k_pages, v_pages, freqs,
+                         positions=None, rope_scale=1.0, interleaved=False, key_min=None,
+                         key_max=None, q_out=None, status=None, stream=None):
+    """Rotate new queries and keys and write keys and values into a paged
+    cache.  q [n, Hq, d], k, v [n, Hkv, d] bf16 or fp16 (any token stride that
+    is a multiple of 8 elements; the heads dense), k_pages, v_pages [n_pages,
+    Hkv, page_size, d], freqs [rot_dim / 2] fp64 (see ts_rope_frequencies).
+    key_min, key_max [n_pages, Hkv, d]: the pages' key bounds, updated.
+    Returns the rotated queries [n, Hq, d]."""
+    n, Hq, d = q.shape
+    n_pages, Hkv, ps = k_pages.shape[:3]
+    dt = q.dtype
+    for t, name, heads in ((q, "q", Hq), (k, "k", Hkv), (v, "v", Hkv)):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if t.dtype not in _PAGED_DTYPES or t.dtype != dt:
+            raise TypeError(f"{name} must be {dt if dt in _PAGED_DTYPES else _PAGED_DTYPES}, "
+                            f"got {t.dtype}")
+        if tuple(t.shape) != (n, heads, d):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(n, heads, d)}")
+        if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
+            raise ValueError(f"{name}: the heads of a token must be dense")
+    n_seq, max_pages = _paged_batch(q, cu_q, seq_lens, page_table)
+    _dev(k_pages, dt, "k_pages", (n_pages, Hkv, ps, d))
+    _dev(v_pages, dt, "v_pages", (n_pages, Hkv, ps, d))
+    _dev(freqs, torch.float64, "freqs")
+    if positions is not None:
+        _dev(positions, torch.int32, "positions", (n,))
+    for t, name in ((key_min, "key_min"), (key_max, "key_max")):
+        if t is not None:
+            _dev(t, dt, name, (n_pages, Hkv, d))
+    # a single token's stride is never walked; a view may report any
+    stride = lambda t, heads: t.stride(0) if n > 1 else heads * d  # noqa: E731
+    flags = (TS_PAGED_FP16 if dt == torch.float16 else 0) | (TS_ROPE_INTERLEAVED if interleaved else 0)
+    with _On(q, stream, k=k, v=v, cu_q=cu_q, seq_lens=seq_lens, page_table=page_table,
+             k_pages=k_pages, v_pages=v_pages, freqs=freqs, positions=positions, key_min=key_min,
+             key_max=key_max, q_out=q_out, status=status) as on:
+        q_out = _paged_out(on, q_out, (n, Hq, d), dt, "q_out")
+        _check(lib().ts_paged_rope_append(
+            _ptr(q), _ptr(k), _ptr(v), stride(q, Hq), stride(k, Hkv), stride(v, Hkv), n, Hq, Hkv,
+            d, _ptr(cu_q), _ptr(seq_lens), n_seq, _ptr(page_table), max_pages, ps, n_pages,
+            _ptr(positions), _ptr(freqs), 2 * freqs.numel(), rope_scale, _ptr(q_out),
+            _ptr(k_pages), _ptr(v_pages), _ptr(key_min), _ptr(key_max), flags, _ptr(status),
+            on.handle))
+    return q_out
+
+
+def ts_paged_attention_workspace_bytes(n, n_seq, Hq, Hkv, d, max_pages, page_size, max_q,
+                                       max_kv=0) -> int:
+    return lib().ts_paged_attention_workspace_bytes(n, n_seq, Hq, Hkv, d, max_pages, page_size,
+                                                    max_q, max_kv)
+
+
+def _paged_qkv(q, k_pages, v_pages):
+    n, Hq, d = q.shape
+    n_pages, Hkv, ps = k_pages.shape[:3]
+    _dev(q, _PAGED_DTYPES, "q")
+    _dev(k_pages, q.dtype, "k_pages", (n_pages, Hkv, ps, d))
+    _dev(v_pages, q.dtype, "v_pages", (n_pages, Hkv, ps, d))
+    return n, Hq, d, n_pages, Hkv, ps, TS_PAGED_FP16 if q.dtype == torch.float16 else 0
+
+
+def ts_paged_attention(q, k_pages, v_pages, cu_q, seq_lens, page_table, max_q, max_kv=0, o=None,
+                       lse=None, want_lse=True, workspace=None, status=None, stream=None):
+    """Causal attention of new tokens (prompts, chunks, single tokens) over a
+    paged cache that holds their rows already.  q [n, Hq, d] bf16 or fp16,
+    k_pages, v_pages [n_pages, Hkv, page_size, d]; max_q bounds the sequences'
+    new tokens, max_kv (0: the page table's width) is the longest sequence as
+    far as the host knows.  Returns (o [n, Hq, d], lse [n, Hq] fp32)."""
+    n, Hq, d, n_pages, Hkv, ps, flags = _paged_qkv(q, k_pages, v_pages)
+    n_seq, max_pages = _paged_batch(q, cu_q, seq_lens, page_table)
+    with _On(q, stream, k_pages=k_pages, v_pages=v_pages, cu_q=cu_q, seq_lens=seq_lens,
+             page_table=page_table, o=o, lse=lse, workspace=workspace, status=status) as on:
+        o = _paged_out(on, o, (n, Hq, d), q.dtype, "o")
+        if lse is not None or want_lse:
+            lse = _paged_out(on, lse, (n, Hq), torch.float32, "lse")
+        ws, nb = on.workspace(lib().ts_paged_attention_workspace_bytes(
+            n, n_seq, Hq, Hkv, d, max_pages, ps, max_q, max_kv), workspace)
+        _check(lib().ts_paged_attention(
+            _ptr(q), _ptr(k_pages), _ptr(v_pages), n, Hq, Hkv, d, _ptr(cu_q), _ptr(seq_lens),
+            n_seq, _ptr(page_table), max_pages, ps, n_pages, max_q, max_kv, _ptr(o), _ptr(lse),
+            _ptr(ws), nb, flags, _ptr(status), on.handle))
+    return o, lse
+
+
+def ts_paged_select_workspace_bytes(n, Hkv, max_pages) -> int:
+    return lib().ts_paged_select_workspace_bytes(n, Hkv, max_pages)
+
+
+def ts_paged_select_pages(q, key_min, key_max, cu_q, seq_lens, page_table, page_size, n_top,
+                          n_sink, n_recent, pages=None, counts=None, workspace=None, status=None,
+                          stream=None):
+    """Choose each new token's pages by the bound their key bounds put on its
+    scores: the first n_sink, the last n_recent and the n_top best between.
+    q [n, Hq, d] rotated, key_min, key_max [n_pages, Hkv, d].  Returns
+    (pages [n, Hkv, n_sink + n_top + n_recent], counts [n, Hkv]) int32:
+    ascending positions in the page table's row, -1 behind the last."""
+    n, Hq, d = q.shape
+    n_pages, Hkv = key_min.shape[:2]
+    _dev(q, _PAGED_DTYPES, "q")
+    _dev(key_min, q.dtype, "key_min", (n_pages, Hkv, d))
+    _dev(key_max, q.dtype, "key_max", (n_pages, Hkv, d))
+    n_seq, max_pages = _paged_batch(q, cu_q, seq_lens, page_table)
+    flags = TS_PAGED_FP16 if q.dtype == torch.float16 else 0
+    with _On(q, stream, key_min=key_min, key_max=key_max, cu_q=cu_q, seq_lens=seq_lens,
+             page_table=page_table, pages=pages, counts=counts, workspace=workspace,
+             status=status) as on:
+        pages = _paged_out(on, pages, (n, Hkv, n_sink + n_top + n_recent), torch.int32, "pages")
+        counts = _paged_out(on, counts, (n, Hkv), torch.int32, "counts")
+        ws, nb = on.workspace(lib().ts_paged_select_workspace_bytes(n, Hkv, max_pages), workspace)
+        _check(lib().ts_paged_select_pages(
+            _ptr(q), _ptr(key_min), _ptr(key_max), n, Hq, Hkv, d, _ptr(cu_q), _ptr(seq_lens),
+            n_seq, _ptr(page_table), max_pages, page_size, n_pages, n_top, n_sink, n_recent,
+            _ptr(pages), _ptr(counts), _ptr(ws), nb, flags, _ptr(status), on.handle))
+    return pages, counts
+
+
+def ts_paged_selected_workspace_bytes(n, Hq, Hkv, d, page_size, n_sel) -> int:
+    return lib().ts_paged_selected_workspace_bytes(n, Hq, Hkv, d, page_size, n_sel)
+
+
+def ts_paged_attention_selected(q, k_pages, v_pages, cu_q, seq_lens, page_table, pages, counts,
+                                o=None, lse=None, want_lse=True, workspace=None, status=None,
+                                stream=None):
+    """ts_paged_attention over each token's chosen pages (pages [n, Hkv,
+    n_sel], counts [n, Hkv] int32, as ts_paged_select_pages returns them).
+    Returns (o [n, Hq, d], lse [n, Hq] fp32)."""
+    n, Hq, d, n_pages, Hkv, ps, flags = _paged_qkv(q, k_pages, v_pages)
+    n_seq, max_pages = _paged_batch(q, cu_q, seq_lens, page_table)
+    n_sel = pages.shape[2]
+    _dev(pages, torch.int32, "pages", (n, Hkv, n_sel))
+    _dev(counts, torch.int32, "counts", (n, Hkv))
+    with _On(q, stream, k_pages=k_pages, v_pages=v_pages, cu_q=cu_q, seq_lens=seq_lens,
+             page_table=page_table, pages=pages, counts=counts, o=o, lse=lse, workspace=workspace,
+             status=status) as on:
+        o = _paged_out(on, o, (n, Hq, d), q.dtype, "o")
+        if lse is not None or want_lse:
+            lse = _paged_out(on, lse, (n, Hq), torch.float32, "lse")
+        ws, nb = on.workspace(lib().ts_paged_selected_workspace_bytes(n, Hq, Hkv, d, ps, n_sel),
+                              workspace)
+        _check(lib().ts_paged_attention_selected(
+            _ptr(q), _ptr(k_pages), _ptr(v_pages), n, Hq, Hkv, d, _ptr(cu_q), _ptr(seq_lens),
+            n_seq, _ptr(page_table), max_pages, ps, n_pages, _ptr(pages), _ptr(counts), n_sel,
+            _ptr(o), _ptr(lse), _ptr(ws), nb, flags, _ptr(status), on.handle))
+    return o, lse
