@@ -3,6 +3,7 @@
 #include <cmath>
 
 #include "paged.cuh"
+#include "paged_tc.cuh"
 
 namespace ts {
 
@@ -58,6 +59,10 @@ int64_t bound_kv(int max_pages, int page_size, int64_t max_kv) {
   const int64_t cap = (int64_t)max_pages * page_size;
   return max_kv > 0 && max_kv < cap ? max_kv : cap;
 }
+
+// One block of 16 packed rows a KV head takes the row kernel, more take the
+// tensor-core tiles.
+bool few_rows(int max_q, int Hq, int Hkv) { return (int64_t)max_q * (Hq / Hkv) <= 16; }
 
 }  // namespace
 
@@ -174,9 +179,10 @@ size_t ts_paged_attention_workspace_bytes(int n, int n_seq, int Hq, int Hkv, int
   if (n < 1 || n_seq < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || max_pages < 1 || page_size < 1 ||
       max_q < 1)
     return 0;
-  return rows_plan((int64_t)n_seq * Hkv, n, Hq, max_q * (Hq / Hkv), d,
-                   bound_kv(max_pages, page_size, max_kv))
-      .ws_bytes;
+  const int64_t kv = bound_kv(max_pages, page_size, max_kv);
+  if (few_rows(max_q, Hq, Hkv))
+    return rows_plan((int64_t)n_seq * Hkv, n, Hq, max_q * (Hq / Hkv), d, kv).ws_bytes;
+  return tc_plan(n, n_seq, Hq, Hkv, d, max_q, kv).ws_bytes;
 }
 
 int ts_paged_attention(const void* q, const void* k_pages, const void* v_pages, int n, int Hq,
@@ -196,8 +202,16 @@ int ts_paged_attention(const void* q, const void* k_pages, const void* v_pages, 
   if (!q || !k_pages || !v_pages || !o) return fail(TS_ERR_INVALID_ARG, "%s: NULL tensor", W);
   for (const void* p : {q, k_pages, v_pages, (const void*)o})
     if (!aligned16(p)) return fail(TS_ERR_INVALID_ARG, "%s: a tensor is not 16-byte aligned", W);
-  const RowsPlan p = rows_plan((int64_t)n_seq * Hkv, n, Hq, max_q * (Hq / Hkv), d,
-                               bound_kv(max_pages, page_size, max_kv));
+  const int64_t kv = bound_kv(max_pages, page_size, max_kv);
+  if (!few_rows(max_q, Hq, Hkv)) {
+    const TcPlan p = tc_plan(n, n_seq, Hq, Hkv, d, max_q, kv);
+    rc = check_paged_ws(workspace, workspace_bytes, p.ws_bytes, W);
+    if (rc) return rc;
+    const TcArgs a{q, k_pages, v_pages, Hq, Hkv, max_q, o, lse};
+    return launch_paged_tc(b, a, p, d, (flags & TS_PAGED_FP16) != 0, workspace, status,
+                           static_cast<cudaStream_t>(stream));
+  }
+  const RowsPlan p = rows_plan((int64_t)n_seq * Hkv, n, Hq, max_q * (Hq / Hkv), d, kv);
   rc = check_paged_ws(workspace, workspace_bytes, p.ws_bytes, W);
   if (rc) return rc;
   RowsArgs a{};

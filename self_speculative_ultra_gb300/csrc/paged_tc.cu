@@ -1,0 +1,997 @@
+// Attention of chunks of new tokens over a paged cache on the 5th-generation
+// tensor cores (tcgen05).
+//
+//   s_ij = q_i . k_j / sqrt(d), j <= seq_len - q_len + i
+//   o_i = softmax_j(s) . v,  lse_i = ln sum_j exp(s_ij)
+//
+// The query rows of a KV head (row R = new token R / G, head kv * G + R % G)
+// are cut into tiles of 256, two groups of 128.  A chunk over a long cache is
+// bound by the tensor cores (4 d flops a row and key); what limits the rate is
+// the softmax between the two products, so the groups alternate: while one
+// group's scores are exponentiated the tensor core works for the other.
+//
+// Three launches.  The plan (one CTA) lists the work from the device-side
+// lengths: every tile's key range, cut into pieces where the tiles alone
+// would leave SMs idle, in order of falling cost.  The attention kernel keeps
+// one CTA a SM, which walks its share of the list forwards and backwards in
+// turn (so that costs even out), its copies running ahead across items.  The
+// third kernel joins the pieces of cut tiles.
+//
+// Per 128-key tile of an item:
+//   warp 0       copies K (2 stages) and V (3 stages), one box a page and
+//                64-column panel, each lane one box; 128-byte swizzle
+//   warp 1       S_g = Q_g K^T (M = N = 128, fp32 in TMEM); when the softmax
+//                has written P_g over S_g, O_g += P_g V with P read from TMEM
+//   warps 4..7   the item's query rows into shared memory; rows of V behind
+//                the sequence's last are cleared (0 * NaN would reach O)
+//   warps 8..15  softmax, one thread a row: all 128 scores in registers,
+//                P = 2^(s log2e / sqrt(d) - m) against a running maximum m that
+//                moves only when a tile's row sum of P exceeds 2^15; sums in
+//                fp32.  P is rounded once, to the type of V, since the tensor
+//                core takes both operands of a product in one 16-bit type: off
+//                by half a step a weight, as the output's own rounding is, and
+//                averaged over the keys.
+// At the end of an item the softmax warps write O / l (or the piece's O, m, l
+// in fp32); the next item's first scores are formed meanwhile.
+//
+// Every wait is bounded; on expiry the CTA reports TS_ERR_TIMEOUT, waits for
+// its own copies and products, frees its TMEM and returns.
+#include <cuda.h>
+
+#include "paged.cuh"
+#include "paged_tc.cuh"
+#include "tc_ptx.cuh"
+
+namespace ts {
+
+namespace {
+
+constexpr int kNk = 128;               // keys a tile
+constexpr int kM = kTcRows;            // query rows a tile
+constexpr int kSK = 2, kSV = 3;        // ring depths
+constexpr int kThreads = 512;
+constexpr int kRegsLow = 64, kRegsSoftmax = 192;
+static_assert(2 * 128 * kRegsLow + 2 * 128 * kRegsSoftmax == kThreads * 128,
+              "the register split must use exactly the launch's registers");
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kFastSum = 32768.0f;
+constexpr long long kDrainCycles = 1ll << 31;
+constexpr uint32_t kNegInf = 0xFF800000u;
+
+struct Header {
+  int n_entries;      // entries of the list; an entry is one item a KV head
+  int n_cut;          // cut tiles
+};
+
+// -------------------------------------------------------------------- plan
+constexpr int kPlanThreads = 1024;
+
+__device__ __forceinline__ int tile_steps(const SeqSpan& sp, int rows, int tile, int G) {
+  const int last = min((tile + 1) * kM, rows) - 1;
+  const int vis = sp.kl - sp.ql + last / G + 1;
+  return vis <= 0 ? 0 : (vis + kNk - 1) / kNk;
+}
+
+// Pieces of a tile of `steps` key tiles when a piece takes at most `per`.
+__device__ __forceinline__ int pieces_of(int steps, int per) {
+  return steps <= per ? 1 : (steps + per - 1) / per;
+}
+
+__global__ void __launch_bounds__(kPlanThreads)
+paged_plan_kernel(const PagedBatch b, int Hkv, int G, int max_q, int max_tiles, int max_entries,
+                  int max_slots, Header* hdr, int4* __restrict__ tiles, int4* __restrict__ entries,
+                  int* __restrict__ slots, int4* __restrict__ cuts, int32_t* status) {
+  __shared__ int first[kPlanThreads + 1];    // tiles before each sequence of the trip
+  __shared__ int seq_rows[kPlanThreads];
+  __shared__ int scan[32];
+  __shared__ int s_max;
+  __shared__ unsigned long long s_total;
+  __shared__ float est[32];
+  __shared__ int est_per[32];
+  __shared__ int hist[256];
+  __shared__ int s_slots, s_cut;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  griddep_wait();
+  griddep_launch_dependents();
+  if (tid == 0) {
+    s_max = 0;
+    s_total = 0;
+    s_slots = 0;
+    s_cut = 0;
+  }
+  for (int i = tid; i < 256; i += kPlanThreads) hist[i] = 0;
+  int n_tiles = 0;
+  for (int base = 0; base < b.n_seq; base += kPlanThreads) {
+    const int s = base + tid;
+    int cnt = 0, rows = 0;
+    if (s < b.n_seq) {
+      const SeqSpan sp = seq_span(b, s);
+      if (sp.bad || sp.ql > max_q) set_status(status, TS_ERR_INVALID_ARG);
+      rows = min(sp.ql, max_q) * G;
+      cnt = (rows + kM - 1) / kM;
+    }
+    int inc = cnt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    if (lane == 31) scan[warp] = inc;
+    __syncthreads();
+    int off = 0, total = 0;
+    for (int w = 0; w < 32; ++w) {
+      const int x = scan[w];
+      if (w < warp) off += x;
+      total += x;
+    }
+    first[tid] = off + inc - cnt;
+    seq_rows[tid] = rows;
+    if (tid == 0) first[kPlanThreads] = total;
+    __syncthreads();
+    unsigned long long mine = 0;
+    int top = 0;
+    for (int i = tid; i < total; i += kPlanThreads) {
+      // the last sequence of the trip that starts at or before tile i
+      int lo = 0, hi = kPlanThreads - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (first[mid] <= i) lo = mid;
+        else hi = mid - 1;
+      }
+      const int sq = base + lo, t = i - first[lo];
+      const int steps = tile_steps(seq_span(b, sq), seq_rows[lo], t, G);
+      if (n_tiles + i < max_tiles) tiles[n_tiles + i] = make_int4(sq, t, steps, 0);
+      mine += steps;
+      top = max(top, steps);
+    }
+    atomicAdd(&s_total, mine);
+    atomicMax(&s_max, top);
+    n_tiles += total;
+    __syncthreads();
+  }
+  n_tiles = min(n_tiles, max_tiles);
+  // How far to cut: the candidates are the longest tile in 1, 2, 3, ... equal
+  // parts; the estimate is in key steps, a piece costing kFixed more (its
+  // first copies, last product and epilogue) and a cut one its partial rows.
+  constexpr float kFixed = 3.f, kCut = 2.f;
+  const int longest = max(s_max, 1);
+  int per = longest;
+  if ((long long)n_tiles * Hkv < 16 * kGb300Sms && longest > 1) {
+    // 1..8 parts, then growing by about a fifth to about 1200
+    int parts = warp + 1;
+    if (warp >= 8) parts = (int)(8.f * exp2f((warp - 7) * 0.3f));
+    const int p = (longest + parts - 1) / parts;
+    int n_items = 0, n_full = 0, n_cut = 0;
+    for (int i = lane; i < n_tiles; i += 32) {
+      const int steps = tiles[i].z;
+      const int np = pieces_of(steps, p);
+      const int len = (steps + np - 1) / np;
+      n_items += np;
+      if (np > 1) n_cut += np;
+      if (len * 10 >= p * 9) n_full += (steps + len - 1) / len;
+    }
+    n_items = warp_sum_int(n_items);
+    n_full = warp_sum_int(n_full);
+    n_cut = warp_sum_int(n_cut);
+    const float waves = (float)((n_full * Hkv + kGb300Sms - 1) / kGb300Sms);
+    const float longest_chain = waves * (p + kFixed + (n_cut ? kCut : 0.f));
+    const float even = ((float)s_total * Hkv + (float)n_items * Hkv * kFixed +
+                        (float)n_cut * Hkv * kCut) / kGb300Sms;
+    float e = fmaxf(longest_chain, even) + (n_cut ? kCut : 0.f);
+    if ((long long)n_cut * Hkv > max_slots) e = INFINITY;
+    if (lane == 0) {
+      est[warp] = e;
+      est_per[warp] = p;
+    }
+    __syncthreads();
+    float best = est[0];
+    per = est_per[0];
+    for (int w = 1; w < 32; ++w)
+      if (est[w] < best) {
+        best = est[w];
+        per = est_per[w];
+      }
+  }
+  __syncthreads();
+  // entries by falling cost: count, place
+  auto bucket = [&](int len) { return 255 - min(255, (int)((long long)len * 255 / longest)); };
+  for (int i = tid; i < n_tiles; i += kPlanThreads) {
+    const int steps = tiles[i].z, np = pieces_of(steps, per), len = (steps + np - 1) / np;
+    for (int p = 0; p < np; ++p) atomicAdd(&hist[bucket(min(len, max(steps - p * len, 0)))], 1);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int c[8], sum = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      c[i] = hist[lane * 8 + i];
+      sum += c[i];
+    }
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    int at = inc - sum;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      hist[lane * 8 + i] = at;
+      at += c[i];
+    }
+    if (lane == 31) hdr->n_entries = min(inc, max_entries);
+  }
+  __syncthreads();
+  for (int i = tid; i < n_tiles; i += kPlanThreads) {
+    const int4 t = tiles[i];
+    const int np = pieces_of(t.z, per), len = (t.z + np - 1) / np;
+    int slot = -1;
+    if (np > 1) {
+      slot = atomicAdd(&s_slots, np);
+      cuts[atomicAdd(&s_cut, 1)] = make_int4(t.x, t.y, slot, np);
+    }
+    for (int p = 0; p < np; ++p) {
+      const int k0 = min(p * len, t.z), k1 = min(k0 + len, t.z);
+      const int at = atomicAdd(&hist[bucket(k1 - k0)], 1);
+      if (at < max_entries) {
+        entries[at] = make_int4(t.x, t.y, k0, k1);
+        slots[at] = slot < 0 ? -1 : slot + p;
+      }
+    }
+  }
+  __syncthreads();
+  if (tid == 0) hdr->n_cut = s_cut;
+}
+
+// -------------------------------------------------------------------- attention
+struct Aux {
+  uint64_t k_full[kSK], k_empty[kSK], v_full[kSV], v_empty[kSV];
+  // a V tile that reaches behind the sequence's rows lands on v_tail, and
+  // v_clear follows when the rows behind are cleared (v_full only counts it)
+  uint64_t v_tail[kSV], v_clear[kSV];
+  uint64_t q_full, q_empty, s_full[2], p_ready[2], o_full[2], drain;
+  uint32_t tmem_base;
+  volatile int32_t abort_flag;
+};
+
+template <int D>
+struct Layout {
+  static constexpr int kPanel = 128 * 128;
+  static constexpr int kTile = 128 * D * 2;
+  static constexpr int kQ = 0;
+  static constexpr int kK = kQ + 2 * kTile;
+  static constexpr int kV = kK + kSK * kTile;
+  static constexpr int kAux = kV + kSV * kTile;
+  static constexpr int kBytes = kAux + (int)sizeof(Aux);
+  static constexpr uint32_t kTmemCols = 512;
+  __host__ __device__ static constexpr uint32_t obase(int g) { return (uint32_t)(g * D); }
+  __host__ __device__ static constexpr uint32_t sbase(int g) { return (uint32_t)(2 * D + g * kNk); }
+};
+
+// One item: a tile's key steps [k0, k1) for one KV head.
+struct Item {
+  int s, kv, slot;
+  int q0, r0, rows;     // first token, the tile's first row, rows of the sequence
+  int see0;             // row R sees keys up to see0 + R / G
+  int kl;
+  int k0, n;            // first key step, steps
+  int n_g[2];           // steps each group needs
+};
+
+struct Work {
+  const Header* hdr;
+  const int4* entries;
+  const int* slots;
+};
+
+__device__ __forceinline__ Item load_item(const PagedBatch& b, const Work& w, int i, int Hkv, int G,
+                                          int max_q) {
+  Item it;
+  const int e = i / Hkv;
+  it.kv = i - e * Hkv;
+  const int4 x = __ldcg(&w.entries[e]);
+  it.slot = __ldcg(&w.slots[e]);
+  it.s = x.x;
+  const SeqSpan sp = seq_span(b, x.x);
+  it.q0 = sp.q0;
+  it.r0 = x.y * kM;
+  it.rows = min(sp.ql, max_q) * G;
+  it.see0 = sp.kl - sp.ql;
+  it.kl = sp.kl;
+  it.k0 = x.z;
+  it.n = x.w - x.z;
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    const int a = it.r0 + g * 128;
+    int steps = 0;
+    if (a < it.rows) {
+      const int vis = it.see0 + (min(a + 128, it.rows) - 1) / G + 1;
+      steps = vis <= 0 ? 0 : (vis + kNk - 1) / kNk;
+    }
+    it.n_g[g] = max(0, min(steps, x.w) - x.z);
+  }
+  return it;
+}
+
+// The i-th item of this CTA: the list in rounds of gridDim.x, every other
+// round backwards.
+__device__ __forceinline__ int item_index(int round) {
+  const int g = gridDim.x;
+  return round * g + ((round & 1) ? g - 1 - (int)blockIdx.x : (int)blockIdx.x);
+}
+
+__device__ __forceinline__ void give_up(Aux* aux, int32_t* status) {
+  aux->abort_flag = 1;
+  set_status(status, TS_ERR_TIMEOUT);
+}
+
+__device__ __forceinline__ float fmax32(const uint32_t* r) {
+  float a = ptx::max3(__uint_as_float(r[0]), __uint_as_float(r[1]), __uint_as_float(r[2]));
+  float c = ptx::max3(__uint_as_float(r[3]), __uint_as_float(r[4]), __uint_as_float(r[5]));
+#pragma unroll
+  for (int x = 6; x < 30; x += 4) {
+    a = ptx::max3(a, __uint_as_float(r[x]), __uint_as_float(r[x + 1]));
+    c = ptx::max3(c, __uint_as_float(r[x + 2]), __uint_as_float(r[x + 3]));
+  }
+  return ptx::max3(a, c, fmaxf(__uint_as_float(r[30]), __uint_as_float(r[31])));
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
+                const PagedBatch b, const T* __restrict__ q, int Hq, int Hkv, int max_q,
+                const Work work, T* __restrict__ o, float* __restrict__ lse,
+                float* __restrict__ part_o, float2* __restrict__ part_ml, long long wait_limit,
+                int32_t* status) {
+  using Ly = Layout<D>;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = Hq / Hkv;
+  if ((ptx::smem_u32(sm) & 1023u) != 0) {      // the swizzle needs 1024-byte aligned tiles
+    if (tid == 0) set_status(status, TS_ERR_CUDA);
+    return;
+  }
+  uint8_t* sq = sm + Ly::kQ;
+  uint8_t* sk = sm + Ly::kK;
+  uint8_t* sv = sm + Ly::kV;
+  Aux* aux = reinterpret_cast<Aux*>(sm + Ly::kAux);
+  if (tid == 0) {
+    for (int i = 0; i < kSK; ++i) {
+      ptx::mbar_init(&aux->k_full[i], 1);
+      ptx::mbar_init(&aux->k_empty[i], 1);
+    }
+    for (int i = 0; i < kSV; ++i) {
+      ptx::mbar_init(&aux->v_full[i], 1);
+      ptx::mbar_init(&aux->v_empty[i], 1);
+      ptx::mbar_init(&aux->v_tail[i], 1);
+      ptx::mbar_init(&aux->v_clear[i], 4);
+    }
+    ptx::mbar_init(&aux->q_full, 4);
+    ptx::mbar_init(&aux->q_empty, 1);
+    for (int g = 0; g < 2; ++g) {
+      ptx::mbar_init(&aux->s_full[g], 1);
+      ptx::mbar_init(&aux->p_ready[g], 4);
+      ptx::mbar_init(&aux->o_full[g], 1);
+    }
+    ptx::mbar_init(&aux->drain, 1);
+    aux->abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(&aux->tmem_base, Ly::kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = aux->tmem_base;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int n_items = __ldcg(&work.hdr->n_entries) * Hkv;
+  const int ps = 1 << b.page_shift;
+
+  if (warp < 8) {
+    ptx::regs_dec<kRegsLow>();
+    if (warp == 0) {
+      // ------------------------------------------------------------ copies
+      // lane: page `box` of the tile, both panels of K, then of V
+      const int boxes = kNk >> b.page_shift;
+      const uint64_t pol = ptx::l2_evict_first_policy();
+      uint32_t it = 0;                    // key tiles so far: ring positions
+      uint32_t kl_done = 0, vl_done = 0;  // copies issued (K, V), for the drain
+      uint32_t tail_on = 0, tail_par = 0; // a stage's v_tail was used; parity of its last use
+      bool ok = true;
+      auto ids = [&](const Item& w, int step) -> int64_t {
+        // the page of this lane's box, -1: behind the sequence
+        const int key = (w.k0 + step) * kNk + (lane << b.page_shift);
+        if (step >= w.n || lane >= boxes || key >= w.kl) return -1;
+        int64_t ph = b.table[(int64_t)w.s * b.max_pages + (key >> b.page_shift)];
+        if (ph < 0 || ph >= b.n_pages) {
+          set_status(status, TS_ERR_INVALID_ARG);
+          ph = 0;                          // any page: the sequence's outputs are unspecified
+        }
+        return ph;
+      };
+      for (int round = 0; ok; ++round) {
+        const int i = item_index(round);
+        if (i >= n_items) break;
+        const Item w = load_item(b, work, i, Hkv, G, max_q);
+        int64_t next = ids(w, 0);
+        for (int k = 0; ok && k < w.n; ++k, ++it) {
+          const int64_t ph = next;
+          next = ids(w, k + 1);
+          const int row = (int)(((ph < 0 ? 0 : ph) * Hkv + w.kv) << b.page_shift);
+          const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, ph >= 0)) *
+                                 (uint32_t)(ps * D * 2);
+          const int stK = it % kSK, stV = it % kSV;
+          if (it >= kSK)
+            ok = ptx::mbar_wait(&aux->k_empty[stK], (it / kSK - 1) & 1u, wait_limit);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane == 0) ptx::mbar_arrive_expect_tx(&aux->k_full[stK], bytes);
+          __syncwarp();
+          if (ph >= 0)
+            for (int p = 0; p < D / 64; ++p)
+              ptx::tma_load_2d(sk + stK * Ly::kTile + p * Ly::kPanel + lane * ps * 128, &tmap_k,
+                               &aux->k_full[stK], p * 64, row, pol);
+          ++kl_done;
+          if (it >= kSV)
+            ok = ptx::mbar_wait(&aux->v_empty[stV], (it / kSV - 1) & 1u, wait_limit);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const bool tail = (w.k0 + k + 1) * kNk > w.kl;
+          uint64_t* land = tail ? &aux->v_tail[stV] : &aux->v_full[stV];
+          if (tail) {
+            tail_par = (tail_on >> stV) & 1u ? tail_par ^ (1u << stV) : tail_par;
+            tail_on |= 1u << stV;
+          }
+          if (lane == 0) {
+            ptx::mbar_arrive_expect_tx(land, bytes);
+            if (tail) ptx::mbar_arrive(&aux->v_full[stV]);
+          }
+          __syncwarp();
+          if (ph >= 0)
+            for (int p = 0; p < D / 64; ++p)
+              ptx::tma_load_2d(sv + stV * Ly::kTile + p * Ly::kPanel + lane * ps * 128, &tmap_v,
+                               land, p * 64, row, pol);
+          ++vl_done;
+          ok = __all_sync(0xffffffffu, aux->abort_flag == 0);
+        }
+      }
+      if (!ok) give_up(aux, status);
+      // every copy issued must land before the CTA exits
+      if (lane == 0) {
+        for (uint32_t t = kl_done > kSK ? kl_done - kSK : 0; t < kl_done; ++t)
+          ptx::mbar_wait(&aux->k_full[t % kSK], (t / kSK) & 1u, kDrainCycles);
+        for (uint32_t t = vl_done > kSV ? vl_done - kSV : 0; t < vl_done; ++t)
+          ptx::mbar_wait(&aux->v_full[t % kSV], (t / kSV) & 1u, kDrainCycles);
+        for (int t = 0; t < kSV; ++t)
+          if ((tail_on >> t) & 1u)
+            ptx::mbar_wait(&aux->v_tail[t], (tail_par >> t) & 1u, kDrainCycles);
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------------ products
+      if (lane == 0) {
+        constexpr uint32_t idesc_qk = Pair<T>::kFp16 ? ptx::idesc_f16_f32(128, kNk, false)
+                                                     : ptx::idesc_bf16_f32(128, kNk, false);
+        constexpr uint32_t idesc_pv = Pair<T>::kFp16 ? ptx::idesc_f16_f32(128, D, true)
+                                                     : ptx::idesc_bf16_f32(128, D, true);
+        const uint64_t qd0 = ptx::sdesc_sw128(ptx::smem_u32(sq), 16, 1024);
+        const uint64_t kd0 = ptx::sdesc_sw128(ptx::smem_u32(sk), 16, 1024);
+        const uint64_t vd0 = ptx::sdesc_sw128(ptx::smem_u32(sv), Ly::kPanel, 1024);
+        constexpr uint32_t kTile16 = Ly::kTile >> 4;
+        uint32_t it = 0, items = 0, clear_par = 0;
+        uint32_t tiles_g[2] = {0, 0};
+        bool ok = true;
+        auto qk = [&](int g, uint32_t t) {
+          const uint64_t a0 = qd0 + (uint64_t)(g * kTile16);
+          const uint64_t b0 = kd0 + (uint64_t)((t % kSK) * kTile16);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t off = (ks >> 2) * (Ly::kPanel >> 4) + (ks & 3) * 2;
+            ptx::mma_ss(tmem + Ly::sbase(g), a0 + off, b0 + off, idesc_qk, ks > 0 ? 1u : 0u);
+          }
+          ptx::mma_commit(&aux->s_full[g]);
+        };
+        auto wait_k = [&](uint32_t t) {
+          if (!ptx::mbar_wait(&aux->k_full[t % kSK], (t / kSK) & 1u, wait_limit)) return false;
+          ptx::tc_fence_after();
+          return true;
+        };
+        for (int round = 0; ok; ++round) {
+          const int i = item_index(round);
+          if (i >= n_items) break;
+          const Item w = load_item(b, work, i, Hkv, G, max_q);
+          if (w.n == 0) continue;
+          ok = ptx::mbar_wait(&aux->q_full, items & 1u, wait_limit) && wait_k(it);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          for (int g = 0; g < 2; ++g)
+            if (w.n_g[g] > 0) qk(g, it);
+          ptx::mma_commit(&aux->k_empty[it % kSK]);
+          if (w.n == 1) ptx::mma_commit(&aux->q_empty);
+          for (int k = 0; ok && k < w.n; ++k) {
+            const uint32_t t = it + k;
+            ok = ptx::mbar_wait(&aux->v_full[t % kSV], (t / kSV) & 1u, wait_limit);
+            if (ok && (w.k0 + k + 1) * kNk > w.kl) {
+              ok = ptx::mbar_wait(&aux->v_clear[t % kSV], (clear_par >> (t % kSV)) & 1u, wait_limit);
+              clear_par ^= 1u << (t % kSV);
+            }
+            if (!ok) break;
+            bool have_k = false;
+            for (int g = 0; g < 2 && ok; ++g) {
+              if (k < w.n_g[g]) {
+                ok = ptx::mbar_wait(&aux->p_ready[g], tiles_g[g] & 1u, wait_limit);
+                if (!ok) break;
+                ++tiles_g[g];
+                ptx::tc_fence_after();
+                const uint64_t b0 = vd0 + (uint64_t)((t % kSV) * kTile16);
+#pragma unroll
+                for (int ks = 0; ks < kNk / 16; ++ks)
+                  ptx::mma_ts(tmem + Ly::obase(g), tmem + Ly::sbase(g) + 8 * ks,
+                              b0 + (uint64_t)(ks * 128), idesc_pv, (ks > 0 || k > 0) ? 1u : 0u);
+                if (k + 1 == w.n_g[g]) ptx::mma_commit(&aux->o_full[g]);
+              }
+              if (k + 1 < w.n_g[g]) {
+                if (!have_k) {
+                  ok = wait_k(t + 1);
+                  if (!ok) break;
+                  have_k = true;
+                }
+                qk(g, t + 1);
+              }
+            }
+            if (!ok) break;
+            ptx::mma_commit(&aux->v_empty[t % kSV]);
+            if (k + 1 < w.n) {
+              ptx::mma_commit(&aux->k_empty[(t + 1) % kSK]);
+              if (k + 2 == w.n) ptx::mma_commit(&aux->q_empty);
+            }
+          }
+          it += w.n;
+          ++items;
+        }
+        if (!ok) give_up(aux, status);
+        ptx::mma_commit(&aux->drain);       // this thread's products end before TMEM is freed
+        ptx::mbar_wait(&aux->drain, 0, kDrainCycles);
+      }
+    } else if (warp >= 4) {
+      // ------------------------------------------------------------ query rows, V tails
+      const int t = tid - 128;
+      constexpr int kCh = D / 8;
+      uint32_t it = 0, items = 0, tail_par = 0;
+      bool ok = true;
+      for (int round = 0; ok; ++round) {
+        const int i = item_index(round);
+        if (i >= n_items) break;
+        const Item w = load_item(b, work, i, Hkv, G, max_q);
+        if (w.n == 0) continue;
+        if (items > 0) ok = ptx::mbar_wait(&aux->q_empty, (items - 1) & 1u, wait_limit);
+        ok = __all_sync(0xffffffffu, ok && !aux->abort_flag);
+        if (!ok) break;
+#pragma unroll 4
+        for (int e = t; e < kM * kCh; e += 128) {
+          const int r = e / kCh, c = e % kCh, R = w.r0 + r;
+          const bool live = R < w.rows;
+          const int64_t row = live ? (int64_t)(w.q0 + R / G) * Hq + w.kv * G + R % G : 0;
+          const uint32_t dst = ptx::smem_u32(sq + (r >> 7) * Ly::kTile + (c >> 3) * Ly::kPanel +
+                                             (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4));
+          const int n = live ? 16 : 0;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+                       "l"(q + row * D + c * 8), "r"(n));
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&aux->q_full);
+        // the item's last tile, where it reaches behind the sequence's rows
+        const int last = w.k0 + w.n - 1;
+        if ((last + 1) * kNk > w.kl) {
+          const uint32_t st = (it + w.n - 1) % kSV;
+          ok = ptx::mbar_wait(&aux->v_tail[st], (tail_par >> st) & 1u, wait_limit);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tail_par ^= 1u << st;
+          const int keep = w.kl - last * kNk;      // rows [keep, 128) are cleared
+          for (int e = t; e < (kNk - keep) * kCh; e += 128) {
+            const int r = keep + e / kCh, c = e % kCh;
+            *reinterpret_cast<uint4*>(sv + st * Ly::kTile + (c >> 3) * Ly::kPanel +
+                                      r * 128 + ((c & 7) << 4)) = make_uint4(0, 0, 0, 0);
+          }
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&aux->v_clear[st]);
+        }
+        it += w.n;
+        ++items;
+      }
+      if (!ok) give_up(aux, status);
+    }
+  } else {
+    ptx::regs_inc<kRegsSoftmax>();
+    // ------------------------------------------------------------ softmax
+    const int g = (warp - 8) >> 2;
+    const int tr = (warp & 3) * 32 + lane;       // row of the group
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t s_addr = tmem + lane_off + Ly::sbase(g);
+    const uint32_t o_addr = tmem + lane_off + Ly::obase(g);
+    const float sl2 = kLog2e / sqrtf((float)D);
+    const uint64_t sl2x2 = ptx::f2(sl2, sl2);
+    uint32_t tiles = 0, outs = 0;
+    bool ok = true;
+    for (int round = 0; ok; ++round) {
+      const int i = item_index(round);
+      if (i >= n_items) break;
+      const Item w = load_item(b, work, i, Hkv, G, max_q);
+      const int wr0 = w.r0 + g * 128 + (warp & 3) * 32;     // the warp's first row
+      const bool warp_rows = wr0 < w.rows;
+      const int R = w.r0 + g * 128 + tr;
+      const bool valid = R < w.rows;
+      const int lim = w.see0 + (valid ? R : w.rows - 1) / G;   // last key this row sees
+      const int lim0 = w.see0 + min(wr0, w.rows - 1) / G;      // least of the warp
+      const int n_mine = g == 0 ? w.n_g[0] : w.n_g[1];
+      float m_used = -INFINITY, l = 0.f;
+      for (int k = 0; k < n_mine; ++k, ++tiles) {
+        bool got = !aux->abort_flag && ptx::mbar_wait(&aux->s_full[g], tiles & 1u, wait_limit);
+        if (!__all_sync(0xffffffffu, got)) {
+          ok = false;
+          break;
+        }
+        if (!warp_rows) {        // padding rows: their P feeds O rows that are never written
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&aux->p_ready[g]);
+          continue;
+        }
+        const int key0 = (w.k0 + k) * kNk;
+        const bool edge = key0 + kNk > lim0 + 1;    // warp-uniform
+        uint32_t r[kNk];
+        auto load_s = [&]() {
+          ptx::tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < kNk / 32; ++c)
+            ptx::tmem_ld32(s_addr + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(r + 32 * c));
+          ptx::tmem_ld_wait();
+          if (edge) {
+            const int vis = lim + 1 - key0;
+#pragma unroll
+            for (int x = 0; x < kNk; ++x)
+              if (x >= vis) r[x] = kNegInf;
+          }
+        };
+        load_s();
+        // P against mref, packed in place: the pair of keys 32c + 2i, 32c + 2i + 1
+        // in r[32c + i]; returns the row sum of P before rounding
+        auto exp_pack = [&](float mref) -> float {
+          const uint64_t negm = ptx::f2(-mref, -mref);
+          auto chunk_exp = [&](int c, float (&pe)[32]) {
+            const uint32_t* x = r + 32 * c;
+#pragma unroll
+            for (int y = 0; y < 16; ++y)
+              ptx::f2_split(ptx::fma2(ptx::f2(__uint_as_float(x[2 * y]), __uint_as_float(x[2 * y + 1])),
+                                      sl2x2, negm),
+                            pe[2 * y], pe[2 * y + 1]);
+#pragma unroll
+            for (int y = 0; y < 32; ++y) pe[y] = ptx::ex2(pe[y]);
+          };
+          uint64_t acc[2 * (kNk / 32)];
+          float pa[32], pb[32];
+          chunk_exp(0, pa);
+#pragma unroll
+          for (int c = 0; c < kNk / 32; ++c) {
+            float (&cur)[32] = (c & 1) ? pb : pa;
+            float (&nxt)[32] = (c & 1) ? pa : pb;
+            if (c + 1 < kNk / 32) chunk_exp(c + 1, nxt);
+            uint32_t* x = r + 32 * c;
+            uint64_t s0 = ptx::f2(cur[0], cur[1]), s1 = ptx::f2(cur[2], cur[3]);
+#pragma unroll
+            for (int y = 2; y < 16; y += 2) {
+              s0 = ptx::add2(s0, ptx::f2(cur[2 * y], cur[2 * y + 1]));
+              s1 = ptx::add2(s1, ptx::f2(cur[2 * y + 2], cur[2 * y + 3]));
+            }
+#pragma unroll
+            for (int y = 0; y < 16; ++y) x[y] = Pair<T>::pack(cur[2 * y], cur[2 * y + 1]);
+            acc[2 * c] = s0;
+            acc[2 * c + 1] = s1;
+          }
+          const uint64_t s = ptx::add2(ptx::add2(ptx::add2(acc[0], acc[1]), ptx::add2(acc[2], acc[3])),
+                                       ptx::add2(ptx::add2(acc[4], acc[5]), ptx::add2(acc[6], acc[7])));
+          float x, y;
+          ptx::f2_split(s, x, y);
+          return x + y;
+        };
+        // the running maximum moves only when it has to: a row sum of at most
+        // 2^15 means every P is at most 2^15, finite in either type
+        bool fast = m_used != -INFINITY;
+        float lt = 0.f;
+        if (__all_sync(0xffffffffu, fast)) {
+          lt = exp_pack(m_used);
+          fast = lt <= kFastSum;
+        } else {
+          fast = false;
+        }
+        bool raise = false;
+        float f = 1.f;
+        if (!__all_sync(0xffffffffu, fast)) {
+          load_s();
+          const float ms = fmaxf(fmaxf(fmax32(&r[0]), fmax32(&r[32])),
+                                 fmaxf(fmax32(&r[64]), fmax32(&r[96]))) * sl2;
+          raise = !fast && ms > m_used;
+          f = raise ? ptx::ex2(m_used - ms) : 1.f;
+          if (raise) {
+            l *= f;
+            m_used = ms;
+          }
+          lt = exp_pack(m_used == -INFINITY ? 0.f : m_used);   // nothing seen: 2^-inf = 0
+        }
+        l += lt;
+        {
+          uint32_t lo[32], hi[32];
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            lo[x] = r[x];
+            lo[16 + x] = r[32 + x];
+            hi[x] = r[64 + x];
+            hi[16 + x] = r[96 + x];
+          }
+          ptx::tmem_st32(s_addr, lo);
+          ptx::tmem_st32(s_addr + 32, hi);
+        }
+        ptx::tmem_st_wait();
+        if (k > 0 && __any_sync(0xffffffffu, raise)) {
+          // S of this tile complete means P V of the previous one is (products
+          // of one thread end in order): O may be rescaled
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t x[16];
+            ptx::tmem_ld16(o_addr + c * 16, x);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int y = 0; y < 16; ++y) x[y] = __float_as_uint(__uint_as_float(x[y]) * f);
+            ptx::tmem_st16(o_addr + c * 16, x);
+          }
+          ptx::tmem_st_wait();
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&aux->p_ready[g]);
+      }
+      if (!ok) break;
+      // ------------------------------------------------------------ the item's output
+      if (n_mine > 0) {
+        bool got = !aux->abort_flag && ptx::mbar_wait(&aux->o_full[g], outs & 1u, wait_limit);
+        if (!__all_sync(0xffffffffu, got)) {
+          ok = false;
+          break;
+        }
+        ++outs;
+        ptx::tc_fence_after();
+      }
+      if (!warp_rows) continue;
+      const int64_t row = (int64_t)(w.q0 + R / G) * Hq + w.kv * G + R % G;
+      const bool cut = w.slot >= 0;
+      const int64_t pr = ((int64_t)w.slot * Hkv + w.kv) * kM + g * 128 + tr;
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t x[32];
+        if (n_mine > 0) {
+          ptx::tmem_ld32(o_addr + c * 32, x);
+          ptx::tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int y = 0; y < 32; ++y) x[y] = 0u;
+        }
+        if (!valid) continue;
+        // a row that has seen nothing has P = 0 and l = 0: O = 0
+        if (cut) {
+          uint4* dst = reinterpret_cast<uint4*>(part_o + pr * D + c * 32);
+#pragma unroll
+          for (int y = 0; y < 8; ++y) dst[y] = make_uint4(x[4 * y], x[4 * y + 1], x[4 * y + 2], x[4 * y + 3]);
+        } else {
+          auto h2 = [&](int y) {
+            return Pair<T>::pack(__uint_as_float(x[y]) * inv, __uint_as_float(x[y + 1]) * inv);
+          };
+          uint4* dst = reinterpret_cast<uint4*>(o + row * D + c * 32);
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            dst[y] = make_uint4(h2(8 * y), h2(8 * y + 2), h2(8 * y + 4), h2(8 * y + 6));
+        }
+      }
+      if (valid) {
+        if (cut) part_ml[pr] = make_float2(m_used, l);
+        else if (lse) lse[row] = l > 0.f ? (m_used + log2f(l)) * kLn2 : -INFINITY;
+      }
+      // O has been read before this warp's next P is announced
+      ptx::tc_fence_before();
+    }
+    if (!ok) give_up(aux, status);
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, Ly::kTmemCols);
+  }
+}
+
+// -------------------------------------------------------------------- join
+// The rows of cut tiles, a warp a row, each lane D / 32 columns.
+template <typename T, int D>
+__global__ void __launch_bounds__(256)
+paged_tc_merge(const PagedBatch b, const Header* __restrict__ hdr, const int4* __restrict__ cuts,
+               int Hq, int Hkv, int max_q, const float* __restrict__ part_o,
+               const float2* __restrict__ part_ml, T* __restrict__ o, float* __restrict__ lse) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31, G = Hq / Hkv;
+  const int64_t total = (int64_t)__ldcg(&hdr->n_cut) * Hkv * kM;
+  constexpr int kPer = D / 32;
+  for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < total; u += (int64_t)gridDim.x * 8) {
+    const int r = (int)(u % kM), kv = (int)(u / kM % Hkv);
+    const int4 c = __ldcg(&cuts[u / kM / Hkv]);          // sequence, tile, first slot, pieces
+    const SeqSpan sp = seq_span(b, c.x);
+    const int R = c.y * kM + r;
+    if (R >= min(sp.ql, max_q) * G) continue;
+    const int64_t p0 = ((int64_t)c.z * Hkv + kv) * kM + r, step = (int64_t)Hkv * kM;
+    float m = -INFINITY;
+    for (int i = lane; i < c.w; i += 32) m = fmaxf(m, __ldcg(&part_ml[p0 + i * step]).x);
+    m = warp_max(m);
+    float acc[kPer], l = 0.f;
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) acc[x] = 0.f;
+    if (m != -INFINITY) {
+#pragma unroll 4
+      for (int i = 0; i < c.w; ++i) {
+        const float2 ml = __ldcg(&part_ml[p0 + i * step]);
+        const float f = exp2f(ml.x - m);                 // 0 for a piece that saw nothing
+        l += f * ml.y;
+        const float* p = part_o + (p0 + i * step) * D + lane * kPer;
+        if (kPer == 4) {
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(p));
+          acc[0] += f * v.x;
+          acc[1] += f * v.y;
+          acc[2 % kPer] += f * v.z;
+          acc[3 % kPer] += f * v.w;
+        } else {
+          const float2 v = __ldcg(reinterpret_cast<const float2*>(p));
+          acc[0] += f * v.x;
+          acc[1] += f * v.y;
+        }
+      }
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const int64_t row = (int64_t)(sp.q0 + R / G) * Hq + kv * G + R % G;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(o + row * D + lane * kPer);
+#pragma unroll
+    for (int x = 0; x < kPer / 2; ++x)
+      dst[x] = Pair<T>::pack(acc[2 * x] * inv, acc[2 * x + 1] * inv);
+    if (lse && lane == 0) lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  }
+}
+
+// -------------------------------------------------------------------- host side
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static const EncodeTiledFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult r{};
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiledFn>(p);
+  }();
+  return fn;
+}
+
+// The pool as rows of d: a box is one page's 64-column panel.
+int pool_map(CUtensorMap* map, const void* base, const PagedBatch& b, int Hkv, int d, bool fp16) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return fail(TS_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  const int ps = 1 << b.page_shift;
+  cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)b.n_pages * Hkv * ps};
+  cuuint64_t strides[1] = {(cuuint64_t)d * 2};
+  cuuint32_t box[2] = {64, (cuuint32_t)ps};
+  cuuint32_t estr[2] = {1, 1};
+  const CUresult r =
+      fn(map, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+         const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(TS_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return TS_OK;
+}
+
+template <typename T, int D>
+int go_tc(const PagedBatch& b, const TcArgs& a, const TcPlan& p, char* ws, int32_t* status,
+          cudaStream_t st) {
+  CUtensorMap mk, mv;
+  int rc = pool_map(&mk, a.k_pages, b, a.Hkv, D, Pair<T>::kFp16);
+  if (!rc) rc = pool_map(&mv, a.v_pages, b, a.Hkv, D, Pair<T>::kFp16);
+  if (rc) return rc;
+  auto kern = paged_tc_kernel<T, D>;
+  // the warps' register split adds up to 128 registers a thread at launch; any
+  // other count would leave the softmax warps waiting for registers
+  cudaFuncAttributes fa{};
+  if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess || fa.numRegs != 128)
+    return fail(TS_ERR_CUDA, "paged attention compiled to %d registers a thread; its register "
+                "split needs 128", fa.numRegs);
+  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kBytes);
+  Header* hdr = reinterpret_cast<Header*>(ws);
+  int4* tiles = reinterpret_cast<int4*>(ws + p.tiles_at);
+  int4* entries = reinterpret_cast<int4*>(ws + p.entries_at);
+  int* slots = reinterpret_cast<int*>(ws + p.slots_at);
+  int4* cuts = reinterpret_cast<int4*>(ws + p.cuts_at);
+  float* part_o = reinterpret_cast<float*>(ws + p.part_at);
+  float2* part_ml = reinterpret_cast<float2*>(ws + p.ml_at);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  pdl_config(&cfg, attr, dim3(1), dim3(kPlanThreads), 0, st);
+  cudaLaunchKernelEx(&cfg, paged_plan_kernel, b, a.Hkv, a.Hq / a.Hkv, a.max_q, p.max_tiles,
+                     p.max_entries, p.max_slots, hdr, tiles, entries, slots, cuts, status);
+  rc = launch_status("paged_plan_kernel");
+  if (rc) return rc;
+  const Work work{hdr, entries, slots};
+  pdl_config(&cfg, attr, dim3(p.grid), dim3(kThreads), Layout<D>::kBytes, st);
+  cudaLaunchKernelEx(&cfg, kern, mk, mv, b, static_cast<const T*>(a.q), a.Hq, a.Hkv, a.max_q, work,
+                     static_cast<T*>(a.o), a.lse, part_o, part_ml, wait_limit_cycles(), status);
+  rc = launch_status("paged_tc_kernel");
+  if (rc || p.max_slots == 0) return rc;
+  pdl_config(&cfg, attr, dim3(p.merge_grid), dim3(256), 0, st);
+  cudaLaunchKernelEx(&cfg, paged_tc_merge<T, D>, b, (const Header*)hdr, (const int4*)cuts, a.Hq,
+                     a.Hkv, a.max_q, (const float*)part_o, (const float2*)part_ml,
+                     static_cast<T*>(a.o), a.lse);
+  return launch_status("paged_tc_merge");
+}
+
+}  // namespace
+
+TcPlan tc_plan(int n, int n_seq, int Hq, int Hkv, int d, int max_q, int64_t max_kv) {
+  TcPlan p{};
+  const int64_t G = Hq / Hkv;
+  // tiles: a sequence's rows rounded up to whole tiles
+  const int64_t per_seq = (max_q * G + kM - 1) / kM;
+  const int64_t tiles = imin64(n * G / kM + n_seq, per_seq * n_seq);
+  // partial rows of cut tiles: at most four pieces a SM, and no more than the
+  // tiles have key steps
+  const int64_t steps = imax64(1, (max_kv + kNk - 1) / kNk);
+  int64_t slots = imin64(4 * kGb300Sms / Hkv, tiles * steps);
+  if (steps == 1 || tiles * Hkv >= 16 * kGb300Sms) slots = 0;
+  p.max_tiles = (int)tiles;
+  p.max_slots = (int)(slots * Hkv);
+  p.max_entries = (int)(tiles + slots);
+  p.grid = (int)imin64(kGb300Sms, (int64_t)p.max_entries * Hkv);
+  p.merge_grid = (int)imin64(4 * kGb300Sms, imax64(1, slots * Hkv * kM / 16));
+  size_t at = 256;
+  auto take = [&](size_t bytes) {
+    const size_t r = at;
+    at += align_up(bytes, 256);
+    return r;
+  };
+  p.tiles_at = take((size_t)tiles * sizeof(int4));
+  p.entries_at = take((size_t)p.max_entries * sizeof(int4));
+  p.slots_at = take((size_t)p.max_entries * sizeof(int));
+  p.cuts_at = take((size_t)(slots / 2 + 1) * sizeof(int4));
+  p.part_at = take((size_t)p.max_slots * kM * d * sizeof(float));
+  p.ml_at = take((size_t)p.max_slots * kM * sizeof(float2));
+  p.ws_bytes = at;
+  return p;
+}
+
+int launch_paged_tc(const PagedBatch& b, const TcArgs& a, const TcPlan& p, int d, bool fp16,
+                    void* ws, int32_t* status, cudaStream_t st) {
+  char* w = static_cast<char*>(ws);
+  if (fp16)
+    return d == 128 ? go_tc<__half, 128>(b, a, p, w, status, st)
+                    : go_tc<__half, 64>(b, a, p, w, status, st);
+  return d == 128 ? go_tc<__nv_bfloat16, 128>(b, a, p, w, status, st)
+                  : go_tc<__nv_bfloat16, 64>(b, a, p, w, status, st);
+}
+
+}  // namespace ts
