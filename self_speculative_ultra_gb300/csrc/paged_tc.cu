@@ -11,11 +11,11 @@
 // group's scores are exponentiated the tensor core works for the other.
 //
 // Three launches.  The plan (one CTA) lists the work from the device-side
-// lengths: every tile's key range, cut into pieces where the tiles alone
-// would leave SMs idle, in order of falling cost.  The attention kernel keeps
-// one CTA a SM, which walks its share of the list forwards and backwards in
-// turn (so that costs even out), its copies running ahead across items.  The
-// third kernel joins the pieces of cut tiles.
+// lengths in order of falling cost: the tiles of whole rounds over the SMs as
+// they are, the rest cut along the keys into pieces where it pays.  The
+// attention kernel keeps one CTA a SM; its copy warp takes the next item off
+// the list when the last copies of the one before are due, so that copies run
+// ahead across items.  The third kernel joins the pieces of cut tiles.
 //
 // Per 128-key tile of an item:
 //   warp 0       copies K (2 stages) and V (3 stages), one box a page and
@@ -62,6 +62,7 @@ constexpr uint32_t kNegInf = 0xFF800000u;
 struct Header {
   int n_entries;      // entries of the list; an entry is one item a KV head
   int n_cut;          // cut tiles
+  int taken;          // items taken off the list behind each CTA's first
 };
 
 // -------------------------------------------------------------------- plan
@@ -80,25 +81,23 @@ __device__ __forceinline__ int pieces_of(int steps, int per) {
 
 __global__ void __launch_bounds__(kPlanThreads)
 paged_plan_kernel(const PagedBatch b, int Hkv, int G, int max_q, int max_tiles, int max_entries,
-                  int max_slots, Header* hdr, int4* __restrict__ tiles, int4* __restrict__ entries,
-                  int* __restrict__ slots, int4* __restrict__ cuts, int32_t* status) {
+                  int max_slots, Header* hdr, int4* tiles, int4* sorted, int4* entries, int* slots,
+                  int4* cuts, int32_t* status) {
   __shared__ int first[kPlanThreads + 1];    // tiles before each sequence of the trip
   __shared__ int seq_rows[kPlanThreads];
   __shared__ int scan[32];
   __shared__ int s_max;
   __shared__ unsigned long long s_total;
   __shared__ float est[32];
-  __shared__ int est_per[32];
+  __shared__ int est_per[32], est_whole[32];
   __shared__ int hist[256];
-  __shared__ int s_slots, s_cut;
+  __shared__ int s_slots, s_cut, s_most;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   griddep_wait();
   griddep_launch_dependents();
   if (tid == 0) {
     s_max = 0;
     s_total = 0;
-    s_slots = 0;
-    s_cut = 0;
   }
   for (int i = tid; i < 256; i += kPlanThreads) hist[i] = 0;
   int n_tiles = 0;
@@ -151,55 +150,10 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int max_q, int max_tiles, 
     __syncthreads();
   }
   n_tiles = min(n_tiles, max_tiles);
-  // How far to cut: the candidates are the longest tile in 1, 2, 3, ... equal
-  // parts; the estimate is in key steps, a piece costing kFixed more (its
-  // first copies, last product and epilogue) and a cut one its partial rows.
-  constexpr float kFixed = 3.f, kCut = 2.f;
   const int longest = max(s_max, 1);
-  int per = longest;
-  if ((long long)n_tiles * Hkv < 16 * kGb300Sms && longest > 1) {
-    // 1..8 parts, then growing by about a fifth to about 1200
-    int parts = warp + 1;
-    if (warp >= 8) parts = (int)(8.f * exp2f((warp - 7) * 0.3f));
-    const int p = (longest + parts - 1) / parts;
-    int n_items = 0, n_full = 0, n_cut = 0;
-    for (int i = lane; i < n_tiles; i += 32) {
-      const int steps = tiles[i].z;
-      const int np = pieces_of(steps, p);
-      const int len = (steps + np - 1) / np;
-      n_items += np;
-      if (np > 1) n_cut += np;
-      if (len * 10 >= p * 9) n_full += (steps + len - 1) / len;
-    }
-    n_items = warp_sum_int(n_items);
-    n_full = warp_sum_int(n_full);
-    n_cut = warp_sum_int(n_cut);
-    const float waves = (float)((n_full * Hkv + kGb300Sms - 1) / kGb300Sms);
-    const float longest_chain = waves * (p + kFixed + (n_cut ? kCut : 0.f));
-    const float even = ((float)s_total * Hkv + (float)n_items * Hkv * kFixed +
-                        (float)n_cut * Hkv * kCut) / kGb300Sms;
-    float e = fmaxf(longest_chain, even) + (n_cut ? kCut : 0.f);
-    if ((long long)n_cut * Hkv > max_slots) e = INFINITY;
-    if (lane == 0) {
-      est[warp] = e;
-      est_per[warp] = p;
-    }
-    __syncthreads();
-    float best = est[0];
-    per = est_per[0];
-    for (int w = 1; w < 32; ++w)
-      if (est[w] < best) {
-        best = est[w];
-        per = est_per[w];
-      }
-  }
-  __syncthreads();
-  // entries by falling cost: count, place
-  auto bucket = [&](int len) { return 255 - min(255, (int)((long long)len * 255 / longest)); };
-  for (int i = tid; i < n_tiles; i += kPlanThreads) {
-    const int steps = tiles[i].z, np = pieces_of(steps, per), len = (steps + np - 1) / np;
-    for (int p = 0; p < np; ++p) atomicAdd(&hist[bucket(min(len, max(steps - p * len, 0)))], 1);
-  }
+  // tiles by falling cost (256 classes)
+  auto bucket = [&](int steps) { return 255 - (int)((long long)steps * 255 / longest); };
+  for (int i = tid; i < n_tiles; i += kPlanThreads) atomicAdd(&hist[bucket(tiles[i].z)], 1);
   __syncthreads();
   if (warp == 0) {
     int c[8], sum = 0;
@@ -220,39 +174,181 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int max_q, int max_tiles, 
       hist[lane * 8 + i] = at;
       at += c[i];
     }
-    if (lane == 31) hdr->n_entries = min(inc, max_entries);
   }
   __syncthreads();
   for (int i = tid; i < n_tiles; i += kPlanThreads) {
     const int4 t = tiles[i];
-    const int np = pieces_of(t.z, per), len = (t.z + np - 1) / np;
-    int slot = -1;
-    if (np > 1) {
-      slot = atomicAdd(&s_slots, np);
-      cuts[atomicAdd(&s_cut, 1)] = make_int4(t.x, t.y, slot, np);
-    }
-    for (int p = 0; p < np; ++p) {
-      const int k0 = min(p * len, t.z), k1 = min(k0 + len, t.z);
-      const int at = atomicAdd(&hist[bucket(k1 - k0)], 1);
-      if (at < max_entries) {
-        entries[at] = make_int4(t.x, t.y, k0, k1);
-        slots[at] = slot < 0 ? -1 : slot + p;
-      }
-    }
+    sorted[atomicAdd(&hist[bucket(t.z)], 1)] = t;
   }
   __syncthreads();
-  if (tid == 0) hdr->n_cut = s_cut;
+  // Which tiles to cut, and how far: the first `whole` of the order stay, the
+  // others go into pieces of at most `per` steps.  Candidates: no cut, and
+  // whole rounds over the SMs (none, all but one, all) x 30 piece lengths.
+  // A candidate's time in key steps is at least its work spread evenly, and at
+  // least what its longest chain takes.  Pieces of about one length go in
+  // rounds, behind the rounds of whole tiles; others end half a piece ragged.
+  // A piece costs kFixed steps more (first copies, last product, epilogue),
+  // a cut one kCut for its partial rows.
+  constexpr float kFixed = 3.f, kCut = 2.f;
+  const int C = kGb300Sms;
+  int whole = n_tiles, per = longest;
+  if ((long long)n_tiles * Hkv < 16 * C && longest > 1 && max_slots > 0) {
+    const int rounds = n_tiles * Hkv / C;
+    float best = INFINITY;
+    int best_whole = n_tiles, best_per = longest;
+    for (int cand = warp; cand < 96; cand += 32) {
+      const int kind = cand / 32, step = cand % 32;
+      int w = n_tiles, p = longest;
+      if (cand > 0) {
+        const int keep = kind == 0 ? 0 : kind == 1 ? rounds : rounds - 1;
+        if (keep < 0 || (kind > 0 && keep == 0)) continue;
+        w = min(n_tiles, keep * C / Hkv);
+        if (w == n_tiles) continue;
+        // 2 .. 12 parts, then growing by about a fifth to about 400
+        const int parts = step < 12 ? max(2, step + 1) : (int)(12.f * exp2f((step - 11) * 0.25f));
+        p = (sorted[w].z + parts - 1) / parts;
+      }
+      int n_pieces = 0, n_cut = 0, shortest = longest, widest = 0;
+      for (int i = w + lane; i < n_tiles; i += 32) {
+        const int steps = sorted[i].z, np = pieces_of(steps, p), len = (steps + np - 1) / np;
+        n_pieces += np;
+        if (np > 1) n_cut += np;
+        shortest = min(shortest, len);
+        widest = max(widest, len);
+      }
+      shortest = __reduce_min_sync(0xffffffffu, shortest);
+      widest = __reduce_max_sync(0xffffffffu, widest);
+      n_pieces = warp_sum_int(n_pieces);
+      n_cut = warp_sum_int(n_cut);
+      if ((long long)n_cut * Hkv > max_slots) continue;
+      const float cost = kFixed + (n_cut ? kCut : 0.f);
+      const float even = ((float)s_total * Hkv + (float)(n_pieces + w) * Hkv * kFixed +
+                          (float)n_cut * Hkv * kCut) / C;
+      // longest chain of whole tiles: k + 1 of them where the order's item
+      // k C is the k-th to follow
+      float chain = 0.f;
+      if (lane * C < w * Hkv) chain = (lane + 1) * (sorted[lane * C / Hkv].z + kFixed);
+      chain = warp_max(chain);
+      const float pieces = (float)((n_pieces * Hkv + C - 1) / C) * (widest + cost);
+      float e = fmaxf(even, chain) + (n_cut ? kCut : 0.f);
+      if (w < n_tiles) {
+        const bool equal = w == 0 || sorted[w - 1].z * 10 >= sorted[0].z * 9;
+        if (!equal || shortest * 10 < widest * 9)
+          e = fmaxf(e, even + 0.5f * widest);
+        else
+          e = fmaxf(e, (w ? (float)((w * Hkv + C - 1) / C) * (sorted[0].z + kFixed) : 0.f) + pieces);
+      }
+      if (e < best) {
+        best = e;
+        best_whole = w;
+        best_per = p;
+      }
+    }
+    if (lane == 0) {
+      est[warp] = best;
+      est_per[warp] = best_per;
+      est_whole[warp] = best_whole;
+    }
+    __syncthreads();
+    best = est[0];
+    whole = est_whole[0];
+    per = est_per[0];
+    for (int w = 1; w < 32; ++w)
+      if (est[w] < best) {
+        best = est[w];
+        whole = est_whole[w];
+        per = est_per[w];
+      }
+  }
+  // the list: whole tiles, then the others' pieces, first pieces first so
+  // that neighbours in time read the same keys
+  __syncthreads();
+  if (tid == 0) s_slots = s_cut = s_most = 0;
+  __syncthreads();
+  {
+    int np = 0;
+    for (int i = whole + tid; i < n_tiles; i += kPlanThreads) np = max(np, pieces_of(sorted[i].z, per));
+    atomicMax(&s_most, np);
+  }
+  for (int i = tid; i < whole; i += kPlanThreads) {
+    const int4 t = sorted[i];
+    if (i < max_entries) {
+      entries[i] = make_int4(t.x, t.y, 0, t.z);
+      slots[i] = -1;
+    }
+  }
+  int n_entries = whole;
+  __syncthreads();
+  const int most = s_most;
+  for (int p = 0; p < most; ++p) {
+    for (int base = whole; base < n_tiles; base += kPlanThreads) {
+      const int i = base + tid;
+      int4 t = make_int4(0, 0, 0, 0);
+      int np = 0;
+      if (i < n_tiles) {
+        t = sorted[i];
+        np = pieces_of(t.z, per);
+      }
+      const unsigned has = __ballot_sync(0xffffffffu, p < np);
+      if (lane == 0) scan[warp] = __popc(has);
+      __syncthreads();
+      int off = n_entries, total = 0;
+      for (int w = 0; w < 32; ++w) {
+        const int x = scan[w];
+        if (w < warp) off += x;
+        total += x;
+      }
+      off += __popc(has & ((1u << lane) - 1u));
+      if (p < np && off < max_entries) {
+        const int len = (t.z + np - 1) / np;
+        if (p == 0) {
+          // a cut tile's slots: its record holds the first, for the later pieces
+          int slot = -1;
+          if (np > 1) {
+            slot = atomicAdd(&s_slots, np);
+            cuts[atomicAdd(&s_cut, 1)] = make_int4(t.x, t.y, slot, np);
+          }
+          sorted[i].w = slot;
+          t.w = slot;
+        }
+        entries[off] = make_int4(t.x, t.y, min(p * len, t.z), min((p + 1) * len, t.z));
+        slots[off] = t.w < 0 ? -1 : t.w + p;
+      }
+      n_entries += total;
+      __syncthreads();
+    }
+  }
+  if (tid == 0) {
+    hdr->n_entries = min(n_entries, max_entries);
+    hdr->n_cut = s_cut;
+    hdr->taken = 0;
+  }
 }
 
 // -------------------------------------------------------------------- attention
+// One item: a tile's key steps [k0, k0 + n) for one KV head.
+struct Item {
+  int kv, slot;
+  int q0, r0, rows;     // first token, the tile's first row, rows of the sequence
+  int see0;             // row R sees keys up to see0 + R / G
+  int kl;
+  int k0, n;            // first key step, steps; n < 0: the list is at its end
+  int n_g[2];           // steps each group needs
+  int s;
+};
+
+constexpr int kNext = 4;
+
 struct Aux {
   uint64_t k_full[kSK], k_empty[kSK], v_full[kSV], v_empty[kSV];
   // a V tile that reaches behind the sequence's rows lands on v_tail, and
   // v_clear follows when the rows behind are cleared (v_full only counts it)
   uint64_t v_tail[kSV], v_clear[kSV];
   uint64_t q_full, q_empty, s_full[2], p_ready[2], o_full[2], drain;
+  uint64_t next_full[kNext], next_empty[kNext];   // items handed to the other warps
   uint32_t tmem_base;
   volatile int32_t abort_flag;
+  Item next[kNext];
 };
 
 template <int D>
@@ -269,18 +365,8 @@ struct Layout {
   __host__ __device__ static constexpr uint32_t sbase(int g) { return (uint32_t)(2 * D + g * kNk); }
 };
 
-// One item: a tile's key steps [k0, k1) for one KV head.
-struct Item {
-  int s, kv, slot;
-  int q0, r0, rows;     // first token, the tile's first row, rows of the sequence
-  int see0;             // row R sees keys up to see0 + R / G
-  int kl;
-  int k0, n;            // first key step, steps
-  int n_g[2];           // steps each group needs
-};
-
 struct Work {
-  const Header* hdr;
+  Header* hdr;
   const int4* entries;
   const int* slots;
 };
@@ -314,16 +400,22 @@ __device__ __forceinline__ Item load_item(const PagedBatch& b, const Work& w, in
   return it;
 }
 
-// The i-th item of this CTA: the list in rounds of gridDim.x, every other
-// round backwards.
-__device__ __forceinline__ int item_index(int round) {
-  const int g = gridDim.x;
-  return round * g + ((round & 1) ? g - 1 - (int)blockIdx.x : (int)blockIdx.x);
-}
-
 __device__ __forceinline__ void give_up(Aux* aux, int32_t* status) {
   aux->abort_flag = 1;
   set_status(status, TS_ERR_TIMEOUT);
+}
+
+// The next item as the copy warp handed it on; false: a wait ran out.
+__device__ __forceinline__ bool take_item(Aux* aux, uint32_t& count, Item& w, int lane,
+                                          long long limit) {
+  const uint32_t at = count % kNext;
+  const bool got = ptx::mbar_wait(&aux->next_full[at], (count / kNext) & 1u, limit);
+  if (!__all_sync(0xffffffffu, got)) return false;
+  w = aux->next[at];
+  __syncwarp();
+  if (lane == 0) ptx::mbar_arrive(&aux->next_empty[at]);
+  ++count;
+  return true;
 }
 
 __device__ __forceinline__ float fmax32(const uint32_t* r) {
@@ -375,6 +467,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       ptx::mbar_init(&aux->o_full[g], 1);
     }
     ptx::mbar_init(&aux->drain, 1);
+    for (int i = 0; i < kNext; ++i) {
+      ptx::mbar_init(&aux->next_full[i], 1);
+      ptx::mbar_init(&aux->next_empty[i], 1 + 4 + 8);   // warps 1, 4..7, 8..15
+    }
     aux->abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -413,12 +509,28 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
         }
         return ph;
       };
-      for (int round = 0; ok; ++round) {
-        const int i = item_index(round);
-        if (i >= n_items) break;
-        const Item w = load_item(b, work, i, Hkv, G, max_q);
+      int taken = blockIdx.x;             // the first item is the CTA's own
+      for (uint32_t count = 0; ok; ++count) {
+        const int i = __shfl_sync(0xffffffffu, taken, 0);
+        const uint32_t at = count % kNext;
+        if (count >= kNext)
+          ok = ptx::mbar_wait(&aux->next_empty[at], (count / kNext - 1) & 1u, wait_limit);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        Item w;
+        w.n = -1;
+        if (i < n_items) w = load_item(b, work, i, Hkv, G, max_q);
+        if (lane == 0) {
+          aux->next[at] = w;
+          ptx::mbar_arrive(&aux->next_full[at]);
+        }
+        if (w.n < 0) break;
         int64_t next = ids(w, 0);
+        if (w.n == 0 && lane == 0) taken = gridDim.x + atomicAdd(&work.hdr->taken, 1);
         for (int k = 0; ok && k < w.n; ++k, ++it) {
+          // the next item is taken as late as its latency allows
+          if (k == max(0, w.n - 2) && lane == 0)
+            taken = gridDim.x + atomicAdd(&work.hdr->taken, 1);
           const int64_t ph = next;
           next = ids(w, k + 1);
           const int row = (int)(((ph < 0 ? 0 : ph) * Hkv + w.kv) << b.page_shift);
@@ -472,100 +584,118 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       }
     } else if (warp == 1) {
       // ------------------------------------------------------------ products
-      if (lane == 0) {
-        constexpr uint32_t idesc_qk = Pair<T>::kFp16 ? ptx::idesc_f16_f32(128, kNk, false)
-                                                     : ptx::idesc_bf16_f32(128, kNk, false);
-        constexpr uint32_t idesc_pv = Pair<T>::kFp16 ? ptx::idesc_f16_f32(128, D, true)
-                                                     : ptx::idesc_bf16_f32(128, D, true);
-        const uint64_t qd0 = ptx::sdesc_sw128(ptx::smem_u32(sq), 16, 1024);
-        const uint64_t kd0 = ptx::sdesc_sw128(ptx::smem_u32(sk), 16, 1024);
-        const uint64_t vd0 = ptx::sdesc_sw128(ptx::smem_u32(sv), Ly::kPanel, 1024);
-        constexpr uint32_t kTile16 = Ly::kTile >> 4;
-        uint32_t it = 0, items = 0, clear_par = 0;
-        uint32_t tiles_g[2] = {0, 0};
-        bool ok = true;
-        auto qk = [&](int g, uint32_t t) {
-          const uint64_t a0 = qd0 + (uint64_t)(g * kTile16);
-          const uint64_t b0 = kd0 + (uint64_t)((t % kSK) * kTile16);
+      // The whole warp walks the loop and one elected lane issues.  Everything
+      // an instruction's operands come from is the same in all lanes, and is
+      // made so for the compiler too (broadcasts of lane 0): it then keeps them
+      // in uniform registers.  Issued by one lane of a divergent warp, every
+      // product paid ~100 cycles to move its operands there, 3.6 K a step.
+      constexpr uint32_t idesc_qk = Pair<T>::kFp16 ? ptx::idesc_f16_f32(128, kNk, false)
+                                                   : ptx::idesc_bf16_f32(128, kNk, false);
+      constexpr uint32_t idesc_pv = Pair<T>::kFp16 ? ptx::idesc_f16_f32(128, D, true)
+                                                   : ptx::idesc_bf16_f32(128, D, true);
+      auto same = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
+      const uint32_t base = same(ptx::smem_u32(sm));
+      const uint32_t tm = same(tmem);
+      const uint64_t qd0 = ptx::sdesc_sw128(base + Ly::kQ, 16, 1024);
+      const uint64_t kd0 = ptx::sdesc_sw128(base + Ly::kK, 16, 1024);
+      const uint64_t vd0 = ptx::sdesc_sw128(base + Ly::kV, Ly::kPanel, 1024);
+      constexpr uint32_t kTile16 = Ly::kTile >> 4;
+      uint32_t it = 0, items = 0, clear_par = 0, count = 0;
+      uint32_t tiles_g[2] = {0, 0};
+      bool ok = true;
+      auto qk = [&](int g, uint32_t t) {
+        const uint64_t a0 = qd0 + (uint64_t)(g * kTile16);
+        const uint64_t b0 = kd0 + (uint64_t)((t % kSK) * kTile16);
+        if (ptx::elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < D / 16; ++ks) {
             const uint32_t off = (ks >> 2) * (Ly::kPanel >> 4) + (ks & 3) * 2;
-            ptx::mma_ss(tmem + Ly::sbase(g), a0 + off, b0 + off, idesc_qk, ks > 0 ? 1u : 0u);
+            ptx::mma_ss(tm + Ly::sbase(g), a0 + off, b0 + off, idesc_qk, ks > 0 ? 1u : 0u);
           }
           ptx::mma_commit(&aux->s_full[g]);
-        };
-        auto wait_k = [&](uint32_t t) {
-          if (!ptx::mbar_wait(&aux->k_full[t % kSK], (t / kSK) & 1u, wait_limit)) return false;
-          ptx::tc_fence_after();
-          return true;
-        };
-        for (int round = 0; ok; ++round) {
-          const int i = item_index(round);
-          if (i >= n_items) break;
-          const Item w = load_item(b, work, i, Hkv, G, max_q);
-          if (w.n == 0) continue;
-          ok = ptx::mbar_wait(&aux->q_full, items & 1u, wait_limit) && wait_k(it);
-          if (!ok) break;
-          ptx::tc_fence_after();
-          for (int g = 0; g < 2; ++g)
-            if (w.n_g[g] > 0) qk(g, it);
-          ptx::mma_commit(&aux->k_empty[it % kSK]);
-          if (w.n == 1) ptx::mma_commit(&aux->q_empty);
-          for (int k = 0; ok && k < w.n; ++k) {
-            const uint32_t t = it + k;
-            ok = ptx::mbar_wait(&aux->v_full[t % kSV], (t / kSV) & 1u, wait_limit);
-            if (ok && (w.k0 + k + 1) * kNk > w.kl) {
-              ok = ptx::mbar_wait(&aux->v_clear[t % kSV], (clear_par >> (t % kSV)) & 1u, wait_limit);
-              clear_par ^= 1u << (t % kSV);
-            }
-            if (!ok) break;
-            bool have_k = false;
-            for (int g = 0; g < 2 && ok; ++g) {
-              if (k < w.n_g[g]) {
-                ok = ptx::mbar_wait(&aux->p_ready[g], tiles_g[g] & 1u, wait_limit);
-                if (!ok) break;
-                ++tiles_g[g];
-                ptx::tc_fence_after();
-                const uint64_t b0 = vd0 + (uint64_t)((t % kSV) * kTile16);
+        }
+        __syncwarp();
+      };
+      auto pv = [&](int g, uint32_t t, uint32_t acc, bool last) {
+        const uint64_t b0 = vd0 + (uint64_t)((t % kSV) * kTile16);
+        if (ptx::elect_one()) {
 #pragma unroll
-                for (int ks = 0; ks < kNk / 16; ++ks)
-                  ptx::mma_ts(tmem + Ly::obase(g), tmem + Ly::sbase(g) + 8 * ks,
-                              b0 + (uint64_t)(ks * 128), idesc_pv, (ks > 0 || k > 0) ? 1u : 0u);
-                if (k + 1 == w.n_g[g]) ptx::mma_commit(&aux->o_full[g]);
-              }
-              if (k + 1 < w.n_g[g]) {
-                if (!have_k) {
-                  ok = wait_k(t + 1);
-                  if (!ok) break;
-                  have_k = true;
+          for (int ks = 0; ks < kNk / 16; ++ks)
+            ptx::mma_ts(tm + Ly::obase(g), tm + Ly::sbase(g) + 8 * ks, b0 + (uint64_t)(ks * 128),
+                        idesc_pv, ks > 0 ? 1u : acc);
+          if (last) ptx::mma_commit(&aux->o_full[g]);
+        }
+        __syncwarp();
+      };
+      auto release = [&](uint64_t* bar) {
+        if (ptx::elect_one()) ptx::mma_commit(bar);
+        __syncwarp();
+      };
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        const bool got = __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity & 1u, wait_limit));
+        ptx::tc_fence_after();
+        return got;
+      };
+      while (ok) {
+        Item w;
+        ok = take_item(aux, count, w, lane, wait_limit);
+        if (!ok) break;
+        const int n = (int)same(w.n), n0 = (int)same(w.n_g[0]), n1 = (int)same(w.n_g[1]);
+        const bool tail = same((w.k0 + w.n) * kNk > w.kl) != 0;   // of the item's last tile
+        if (n < 0) break;
+        if (n == 0) continue;
+        ok = wait(&aux->q_full, items) && wait(&aux->k_full[it % kSK], it / kSK);
+        if (!ok) break;
+        if (n0 > 0) qk(0, it);
+        if (n1 > 0) qk(1, it);
+        release(&aux->k_empty[it % kSK]);
+        if (n == 1) release(&aux->q_empty);
+        for (int k = 0; k < n; ++k) {
+          const uint32_t t = it + k, stV = t % kSV;
+          ok = wait(&aux->v_full[stV], t / kSV);
+          if (ok && tail && k + 1 == n) {
+            ok = wait(&aux->v_clear[stV], clear_par >> stV);
+            clear_par ^= 1u << stV;
+          }
+          if (!ok) break;
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const int ng = g == 0 ? n0 : n1;
+            if (ok && k < ng) {
+              ok = wait(&aux->p_ready[g], tiles_g[g]);
+              if (ok) {
+                ++tiles_g[g];
+                pv(g, t, k > 0 ? 1u : 0u, k + 1 == ng);
+                if (k + 1 < ng) {
+                  ok = wait(&aux->k_full[(t + 1) % kSK], (t + 1) / kSK);
+                  if (ok) qk(g, t + 1);
                 }
-                qk(g, t + 1);
               }
-            }
-            if (!ok) break;
-            ptx::mma_commit(&aux->v_empty[t % kSV]);
-            if (k + 1 < w.n) {
-              ptx::mma_commit(&aux->k_empty[(t + 1) % kSK]);
-              if (k + 2 == w.n) ptx::mma_commit(&aux->q_empty);
             }
           }
-          it += w.n;
-          ++items;
+          if (!ok) break;
+          release(&aux->v_empty[stV]);
+          if (k + 1 < n) {
+            release(&aux->k_empty[(t + 1) % kSK]);
+            if (k + 2 == n) release(&aux->q_empty);
+          }
         }
-        if (!ok) give_up(aux, status);
-        ptx::mma_commit(&aux->drain);       // this thread's products end before TMEM is freed
-        ptx::mbar_wait(&aux->drain, 0, kDrainCycles);
+        it += n;
+        ++items;
       }
+      if (!ok) give_up(aux, status);
+      release(&aux->drain);               // this warp's products end before TMEM is freed
+      ptx::mbar_wait(&aux->drain, 0, kDrainCycles);
     } else if (warp >= 4) {
       // ------------------------------------------------------------ query rows, V tails
       const int t = tid - 128;
       constexpr int kCh = D / 8;
-      uint32_t it = 0, items = 0, tail_par = 0;
+      uint32_t it = 0, items = 0, tail_par = 0, count = 0;
       bool ok = true;
-      for (int round = 0; ok; ++round) {
-        const int i = item_index(round);
-        if (i >= n_items) break;
-        const Item w = load_item(b, work, i, Hkv, G, max_q);
+      while (ok) {
+        Item w;
+        ok = take_item(aux, count, w, lane, wait_limit);
+        if (!ok || w.n < 0) break;
         if (w.n == 0) continue;
         if (items > 0) ok = ptx::mbar_wait(&aux->q_empty, (items - 1) & 1u, wait_limit);
         ok = __all_sync(0xffffffffu, ok && !aux->abort_flag);
@@ -618,12 +748,12 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
     const uint32_t o_addr = tmem + lane_off + Ly::obase(g);
     const float sl2 = kLog2e / sqrtf((float)D);
     const uint64_t sl2x2 = ptx::f2(sl2, sl2);
-    uint32_t tiles = 0, outs = 0;
+    uint32_t tiles = 0, outs = 0, count = 0;
     bool ok = true;
-    for (int round = 0; ok; ++round) {
-      const int i = item_index(round);
-      if (i >= n_items) break;
-      const Item w = load_item(b, work, i, Hkv, G, max_q);
+    while (ok) {
+      Item w;
+      ok = take_item(aux, count, w, lane, wait_limit);
+      if (!ok || w.n < 0) break;
       const int wr0 = w.r0 + g * 128 + (warp & 3) * 32;     // the warp's first row
       const bool warp_rows = wr0 < w.rows;
       const int R = w.r0 + g * 128 + tr;
@@ -925,6 +1055,7 @@ int go_tc(const PagedBatch& b, const TcArgs& a, const TcPlan& p, char* ws, int32
   cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kBytes);
   Header* hdr = reinterpret_cast<Header*>(ws);
   int4* tiles = reinterpret_cast<int4*>(ws + p.tiles_at);
+  int4* sorted = tiles + p.max_tiles;
   int4* entries = reinterpret_cast<int4*>(ws + p.entries_at);
   int* slots = reinterpret_cast<int*>(ws + p.slots_at);
   int4* cuts = reinterpret_cast<int4*>(ws + p.cuts_at);
@@ -934,7 +1065,7 @@ int go_tc(const PagedBatch& b, const TcArgs& a, const TcPlan& p, char* ws, int32
   cudaLaunchAttribute attr[1];
   pdl_config(&cfg, attr, dim3(1), dim3(kPlanThreads), 0, st);
   cudaLaunchKernelEx(&cfg, paged_plan_kernel, b, a.Hkv, a.Hq / a.Hkv, a.max_q, p.max_tiles,
-                     p.max_entries, p.max_slots, hdr, tiles, entries, slots, cuts, status);
+                     p.max_entries, p.max_slots, hdr, tiles, sorted, entries, slots, cuts, status);
   rc = launch_status("paged_plan_kernel");
   if (rc) return rc;
   const Work work{hdr, entries, slots};
@@ -958,10 +1089,10 @@ TcPlan tc_plan(int n, int n_seq, int Hq, int Hkv, int d, int max_q, int64_t max_
   // tiles: a sequence's rows rounded up to whole tiles
   const int64_t per_seq = (max_q * G + kM - 1) / kM;
   const int64_t tiles = imin64(n * G / kM + n_seq, per_seq * n_seq);
-  // partial rows of cut tiles: at most four pieces a SM, and no more than the
+  // partial rows of cut tiles: at most six pieces a SM, and no more than the
   // tiles have key steps
   const int64_t steps = imax64(1, (max_kv + kNk - 1) / kNk);
-  int64_t slots = imin64(4 * kGb300Sms / Hkv, tiles * steps);
+  int64_t slots = imin64(6 * kGb300Sms / Hkv, tiles * steps);
   if (steps == 1 || tiles * Hkv >= 16 * kGb300Sms) slots = 0;
   p.max_tiles = (int)tiles;
   p.max_slots = (int)(slots * Hkv);
@@ -974,7 +1105,7 @@ TcPlan tc_plan(int n, int n_seq, int Hq, int Hkv, int d, int max_q, int64_t max_
     at += align_up(bytes, 256);
     return r;
   };
-  p.tiles_at = take((size_t)tiles * sizeof(int4));
+  p.tiles_at = take((size_t)tiles * 2 * sizeof(int4));
   p.entries_at = take((size_t)p.max_entries * sizeof(int4));
   p.slots_at = take((size_t)p.max_entries * sizeof(int));
   p.cuts_at = take((size_t)(slots / 2 + 1) * sizeof(int4));
