@@ -67,6 +67,8 @@ struct Header {
 
 // -------------------------------------------------------------------- plan
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanTiles = 2048;
+constexpr int kPlanParts = 512;      // more than a tile is ever cut into
 
 __device__ __forceinline__ int tile_steps(const SeqSpan& sp, int rows, int tile, int G) {
   const int last = min((tile + 1) * kM, rows) - 1;
@@ -81,8 +83,13 @@ __device__ __forceinline__ int pieces_of(int steps, int per) {
 
 __global__ void __launch_bounds__(kPlanThreads)
 paged_plan_kernel(const PagedBatch b, int Hkv, int G, int max_q, int max_tiles, int max_entries,
-                  int max_slots, Header* hdr, int4* tiles, int4* sorted, int4* entries, int* slots,
-                  int4* cuts, int32_t* status) {
+                  int max_slots, Header* hdr, int4* tiles, int4* entries, int* slots, int4* cuts,
+                  int32_t* status) {
+  // the tiles as found and in order: in shared memory where they fit (every
+  // pass over them otherwise waits for L2, and the plan is all latency)
+  extern __shared__ int4 near_tiles[];
+  if (max_tiles <= kPlanTiles) tiles = near_tiles;
+  int4* sorted = tiles + max_tiles;
   __shared__ int first[kPlanThreads + 1];    // tiles before each sequence of the trip
   __shared__ int seq_rows[kPlanThreads];
   __shared__ int scan[32];
@@ -91,7 +98,8 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int max_q, int max_tiles, 
   __shared__ float est[32];
   __shared__ int est_per[32], est_whole[32];
   __shared__ int hist[256];
-  __shared__ int s_slots, s_cut, s_most;
+  __shared__ int at[kPlanParts];
+  __shared__ int s_slots, s_cut, s_most, s_entries;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   griddep_wait();
   griddep_launch_dependents();
@@ -118,12 +126,9 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int max_q, int max_tiles, 
     }
     if (lane == 31) scan[warp] = inc;
     __syncthreads();
-    int off = 0, total = 0;
-    for (int w = 0; w < 32; ++w) {
-      const int x = scan[w];
-      if (w < warp) off += x;
-      total += x;
-    }
+    const int mine_w = scan[lane];
+    const int total = warp_sum_int(mine_w);
+    const int off = warp_sum_int(lane < warp ? mine_w : 0);
     first[tid] = off + inc - cnt;
     seq_rows[tid] = rows;
     if (tid == 0) first[kPlanThreads] = total;
@@ -144,8 +149,13 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int max_q, int max_tiles, 
       mine += steps;
       top = max(top, steps);
     }
-    atomicAdd(&s_total, mine);
-    atomicMax(&s_max, top);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) {
+      atomicAdd(&s_total, mine);
+      atomicMax(&s_max, top);
+    }
     n_tiles += total;
     __syncthreads();
   }
@@ -196,17 +206,20 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int max_q, int max_tiles, 
     const int rounds = n_tiles * Hkv / C;
     float best = INFINITY;
     int best_whole = n_tiles, best_per = longest;
-    for (int cand = warp; cand < 96; cand += 32) {
-      const int kind = cand / 32, step = cand % 32;
+    for (int cand = warp; cand < 64; cand += 32) {
       int w = n_tiles, p = longest;
       if (cand > 0) {
+        // 32 piece lengths without whole tiles, 16 behind all and all but one round
+        const int kind = cand < 32 ? 0 : 1 + (cand & 1), step = cand < 32 ? cand : (cand - 32) / 2;
         const int keep = kind == 0 ? 0 : kind == 1 ? rounds : rounds - 1;
         if (keep < 0 || (kind > 0 && keep == 0)) continue;
         w = min(n_tiles, keep * C / Hkv);
         if (w == n_tiles) continue;
-        // 2 .. 12 parts, then growing by about a fifth to about 400
-        const int parts = step < 12 ? max(2, step + 1) : (int)(12.f * exp2f((step - 11) * 0.25f));
-        p = (sorted[w].z + parts - 1) / parts;
+        // 2 .. 12 parts, then growing by about a fifth to 384
+        const int parts = step < 11 ? step + 2 : (int)(12.f * exp2f((step - 11) * 0.25f));
+        // no tile of the rest is longer than its first's class
+        const int top = min(longest, sorted[w].z + longest / 255 + 1);
+        p = (top + parts - 1) / parts;
       }
       int n_pieces = 0, n_cut = 0, shortest = longest, widest = 0;
       for (int i = w + lane; i < n_tiles; i += 32) {
@@ -260,66 +273,81 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int max_q, int max_tiles, 
         per = est_per[w];
       }
   }
-  // the list: whole tiles, then the others' pieces, first pieces first so
-  // that neighbours in time read the same keys
+  // The list: whole tiles, then the others' pieces, first pieces first, so that
+  // neighbours in time read the same keys.  at[p]: where the p-th pieces go.
   __syncthreads();
+  if (tid < kPlanParts) at[tid] = 0;
   if (tid == 0) s_slots = s_cut = s_most = 0;
   __syncthreads();
-  {
-    int np = 0;
-    for (int i = whole + tid; i < n_tiles; i += kPlanThreads) np = max(np, pieces_of(sorted[i].z, per));
-    atomicMax(&s_most, np);
-  }
-  for (int i = tid; i < whole; i += kPlanThreads) {
+  for (int i = tid; i < n_tiles; i += kPlanThreads) {
     const int4 t = sorted[i];
-    if (i < max_entries) {
-      entries[i] = make_int4(t.x, t.y, 0, t.z);
-      slots[i] = -1;
+    if (i < whole) {
+      if (i < max_entries) {
+        entries[i] = make_int4(t.x, t.y, 0, t.z);
+        slots[i] = -1;
+      }
+      continue;
     }
+    const int np = pieces_of(t.z, per);
+    atomicAdd(&at[np - 1], 1);          // tiles of np pieces, for now
+    atomicMax(&s_most, np);
+    int slot = -1;
+    if (np > 1) {
+      slot = atomicAdd(&s_slots, np);
+      cuts[atomicAdd(&s_cut, 1)] = make_int4(t.x, t.y, slot, np);
+    }
+    sorted[i].w = slot;
   }
-  int n_entries = whole;
   __syncthreads();
   const int most = s_most;
-  for (int p = 0; p < most; ++p) {
-    for (int base = whole; base < n_tiles; base += kPlanThreads) {
-      const int i = base + tid;
-      int4 t = make_int4(0, 0, 0, 0);
-      int np = 0;
-      if (i < n_tiles) {
-        t = sorted[i];
-        np = pieces_of(t.z, per);
-      }
-      const unsigned has = __ballot_sync(0xffffffffu, p < np);
-      if (lane == 0) scan[warp] = __popc(has);
-      __syncthreads();
-      int off = n_entries, total = 0;
-      for (int w = 0; w < 32; ++w) {
-        const int x = scan[w];
-        if (w < warp) off += x;
-        total += x;
-      }
-      off += __popc(has & ((1u << lane) - 1u));
-      if (p < np && off < max_entries) {
-        const int len = (t.z + np - 1) / np;
-        if (p == 0) {
-          // a cut tile's slots: its record holds the first, for the later pieces
-          int slot = -1;
-          if (np > 1) {
-            slot = atomicAdd(&s_slots, np);
-            cuts[atomicAdd(&s_cut, 1)] = make_int4(t.x, t.y, slot, np);
-          }
-          sorted[i].w = slot;
-          t.w = slot;
-        }
-        entries[off] = make_int4(t.x, t.y, min(p * len, t.z), min((p + 1) * len, t.z));
-        slots[off] = t.w < 0 ? -1 : t.w + p;
-      }
-      n_entries += total;
-      __syncthreads();
+  if (warp == 0) {
+    // tiles that have a p-th piece: sums from the back; then where they start
+    int n_p[kPlanParts / 32], sum = 0;
+#pragma unroll
+    for (int x = kPlanParts / 32 - 1; x >= 0; --x) {
+      sum += at[lane * (kPlanParts / 32) + x];
+      n_p[x] = sum;
+    }
+    int behind = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_down_sync(0xffffffffu, behind, o);
+      if (lane + o < 32) behind += x;
+    }
+    behind -= sum;                      // tiles whose last piece is a later lane's
+    sum = 0;
+#pragma unroll
+    for (int x = 0; x < kPlanParts / 32; ++x) {
+      n_p[x] += behind;
+      sum += n_p[x];
+    }
+    int before = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += x;
+    }
+    if (lane == 31) s_entries = whole + before;
+    before += whole - sum;
+#pragma unroll
+    for (int x = 0; x < kPlanParts / 32; ++x) {
+      at[lane * (kPlanParts / 32) + x] = before;
+      before += n_p[x];
     }
   }
+  __syncthreads();
+  for (int u = tid; u < (n_tiles - whole) * most; u += kPlanThreads) {
+    const int i = whole + u / most, p = u % most;
+    const int4 t = sorted[i];
+    const int np = pieces_of(t.z, per);
+    if (p >= np) continue;
+    const int len = (t.z + np - 1) / np, e = atomicAdd(&at[p], 1);
+    if (e >= max_entries) continue;
+    entries[e] = make_int4(t.x, t.y, min(p * len, t.z), min((p + 1) * len, t.z));
+    slots[e] = t.w < 0 ? -1 : t.w + p;
+  }
   if (tid == 0) {
-    hdr->n_entries = min(n_entries, max_entries);
+    hdr->n_entries = min(s_entries, max_entries);
     hdr->n_cut = s_cut;
     hdr->taken = 0;
   }
@@ -947,57 +975,63 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
 }
 
 // -------------------------------------------------------------------- join
-// The rows of cut tiles, a warp a row, each lane D / 32 columns.
+// The rows of cut tiles: a warp takes four neighbouring rows, 8 lanes a row,
+// D / 8 columns a lane, so that the loads of four rows are in flight together.
 template <typename T, int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 4)
 paged_tc_merge(const PagedBatch b, const Header* __restrict__ hdr, const int4* __restrict__ cuts,
                int Hq, int Hkv, int max_q, const float* __restrict__ part_o,
                const float2* __restrict__ part_ml, T* __restrict__ o, float* __restrict__ lse) {
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31, G = Hq / Hkv;
-  const int64_t total = (int64_t)__ldcg(&hdr->n_cut) * Hkv * kM;
-  constexpr int kPer = D / 32;
-  for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < total; u += (int64_t)gridDim.x * 8) {
-    const int r = (int)(u % kM), kv = (int)(u / kM % Hkv);
-    const int4 c = __ldcg(&cuts[u / kM / Hkv]);          // sequence, tile, first slot, pieces
+  const int lane = threadIdx.x & 31, sub = lane & 7, G = Hq / Hkv;
+  const int64_t total = (int64_t)__ldcg(&hdr->n_cut) * Hkv * (kM / 4);
+  constexpr int kQuads = D / 32;          // 16-byte columns a lane
+  for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < total;
+       u += (int64_t)gridDim.x * 8) {
+    const int r = (int)(u % (kM / 4)) * 4 + (lane >> 3), kv = (int)(u / (kM / 4) % Hkv);
+    const int4 c = __ldcg(&cuts[u / (kM / 4) / Hkv]);    // sequence, tile, first slot, pieces
     const SeqSpan sp = seq_span(b, c.x);
     const int R = c.y * kM + r;
-    if (R >= min(sp.ql, max_q) * G) continue;
+    const bool live = R < min(sp.ql, max_q) * G;         // the same for a row's 8 lanes
+    if (!__any_sync(0xffffffffu, live)) continue;
     const int64_t p0 = ((int64_t)c.z * Hkv + kv) * kM + r, step = (int64_t)Hkv * kM;
+    const int np = live ? c.w : 0;
     float m = -INFINITY;
-    for (int i = lane; i < c.w; i += 32) m = fmaxf(m, __ldcg(&part_ml[p0 + i * step]).x);
-    m = warp_max(m);
-    float acc[kPer], l = 0.f;
+    for (int i = sub; i < np; i += 8) m = fmaxf(m, __ldcg(&part_ml[p0 + i * step]).x);
 #pragma unroll
-    for (int x = 0; x < kPer; ++x) acc[x] = 0.f;
-    if (m != -INFINITY) {
-#pragma unroll 4
-      for (int i = 0; i < c.w; ++i) {
-        const float2 ml = __ldcg(&part_ml[p0 + i * step]);
-        const float f = exp2f(ml.x - m);                 // 0 for a piece that saw nothing
-        l += f * ml.y;
-        const float* p = part_o + (p0 + i * step) * D + lane * kPer;
-        if (kPer == 4) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(p));
-          acc[0] += f * v.x;
-          acc[1] += f * v.y;
-          acc[2 % kPer] += f * v.z;
-          acc[3 % kPer] += f * v.w;
-        } else {
-          const float2 v = __ldcg(reinterpret_cast<const float2*>(p));
-          acc[0] += f * v.x;
-          acc[1] += f * v.y;
-        }
+    for (int x = 1; x < 8; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+    float4 acc[kQuads];
+    float l = 0.f;
+#pragma unroll
+    for (int x = 0; x < kQuads; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int n_sum = m == -INFINITY ? 0 : np;           // no piece saw a key: O = 0
+#pragma unroll 2
+    for (int i = 0; i < n_sum; ++i) {
+      const float2 ml = __ldcg(&part_ml[p0 + i * step]);
+      const float4* p = reinterpret_cast<const float4*>(part_o + (p0 + i * step) * D) + sub;
+      float4 v[kQuads];
+#pragma unroll
+      for (int x = 0; x < kQuads; ++x) v[x] = __ldcg(p + 8 * x);
+      const float f = exp2f(ml.x - m);                   // 0 for a piece that saw nothing
+      l += f * ml.y;
+#pragma unroll
+      for (int x = 0; x < kQuads; ++x) {
+        acc[x].x += f * v[x].x;
+        acc[x].y += f * v[x].y;
+        acc[x].z += f * v[x].z;
+        acc[x].w += f * v[x].w;
       }
     }
+    if (!live) continue;
     const float inv = l > 0.f ? 1.f / l : 0.f;
     const int64_t row = (int64_t)(sp.q0 + R / G) * Hq + kv * G + R % G;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(o + row * D + lane * kPer);
+    uint2* dst = reinterpret_cast<uint2*>(o + row * D) + sub;
 #pragma unroll
-    for (int x = 0; x < kPer / 2; ++x)
-      dst[x] = Pair<T>::pack(acc[2 * x] * inv, acc[2 * x + 1] * inv);
-    if (lse && lane == 0) lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    for (int x = 0; x < kQuads; ++x)
+      dst[8 * x] = make_uint2(Pair<T>::pack(acc[x].x * inv, acc[x].y * inv),
+                              Pair<T>::pack(acc[x].z * inv, acc[x].w * inv));
+    if (lse && sub == 0) lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
   }
 }
 
@@ -1055,7 +1089,6 @@ int go_tc(const PagedBatch& b, const TcArgs& a, const TcPlan& p, char* ws, int32
   cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::kBytes);
   Header* hdr = reinterpret_cast<Header*>(ws);
   int4* tiles = reinterpret_cast<int4*>(ws + p.tiles_at);
-  int4* sorted = tiles + p.max_tiles;
   int4* entries = reinterpret_cast<int4*>(ws + p.entries_at);
   int* slots = reinterpret_cast<int*>(ws + p.slots_at);
   int4* cuts = reinterpret_cast<int4*>(ws + p.cuts_at);
@@ -1063,9 +1096,12 @@ int go_tc(const PagedBatch& b, const TcArgs& a, const TcPlan& p, char* ws, int32
   float2* part_ml = reinterpret_cast<float2*>(ws + p.ml_at);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  pdl_config(&cfg, attr, dim3(1), dim3(kPlanThreads), 0, st);
+  const size_t near = p.max_tiles <= kPlanTiles ? (size_t)p.max_tiles * 2 * sizeof(int4) : 0;
+  cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                       kPlanTiles * 2 * sizeof(int4));
+  pdl_config(&cfg, attr, dim3(1), dim3(kPlanThreads), near, st);
   cudaLaunchKernelEx(&cfg, paged_plan_kernel, b, a.Hkv, a.Hq / a.Hkv, a.max_q, p.max_tiles,
-                     p.max_entries, p.max_slots, hdr, tiles, sorted, entries, slots, cuts, status);
+                     p.max_entries, p.max_slots, hdr, tiles, entries, slots, cuts, status);
   rc = launch_status("paged_plan_kernel");
   if (rc) return rc;
   const Work work{hdr, entries, slots};
@@ -1098,7 +1134,8 @@ TcPlan tc_plan(int n, int n_seq, int Hq, int Hkv, int d, int max_q, int64_t max_
   p.max_slots = (int)(slots * Hkv);
   p.max_entries = (int)(tiles + slots);
   p.grid = (int)imin64(kGb300Sms, (int64_t)p.max_entries * Hkv);
-  p.merge_grid = (int)imin64(4 * kGb300Sms, imax64(1, slots * Hkv * kM / 16));
+  // four rows a warp, eight warps a CTA; a cut tile has at least two pieces
+  p.merge_grid = (int)imin64(8 * kGb300Sms, imax64(1, slots * Hkv * kM / 64));
   size_t at = 256;
   auto take = [&](size_t bytes) {
     const size_t r = at;
