@@ -18,7 +18,7 @@
 // ahead across items.  The third kernel joins the pieces of cut tiles.
 //
 // Per 128-key tile of an item:
-//   warp 0       copies K (2 stages) and V (3 stages), one box a page and
+//   warps 0, 2   copy K (2 stages) and V (3 stages), one box a page and
 //                64-column panel, each lane one box; 128-byte swizzle
 //   warp 1       S_g = Q_g K^T (M = N = 128, fp32 in TMEM); when the softmax
 //                has written P_g over S_g, O_g += P_g V with P read from TMEM
@@ -497,7 +497,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
     ptx::mbar_init(&aux->drain, 1);
     for (int i = 0; i < kNext; ++i) {
       ptx::mbar_init(&aux->next_full[i], 1);
-      ptx::mbar_init(&aux->next_empty[i], 1 + 4 + 8);   // warps 1, 4..7, 8..15
+      ptx::mbar_init(&aux->next_empty[i], 2 + 4 + 8);   // warps 1, 2, 4..7, 8..15
     }
     aux->abort_flag = 0;
     ptx::fence_mbar_init();
@@ -517,13 +517,20 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
 
   if (warp < 8) {
     ptx::regs_dec<kRegsLow>();
-    if (warp == 0) {
+    if (warp == 0 || warp == 2) {
       // ------------------------------------------------------------ copies
-      // lane: page `box` of the tile, both panels of K, then of V
+      // warp 0 copies K, warp 2 V; lane: page `box` of the tile, both panels.
+      // (Small pages make many boxes, and a box costs its warp's lanes a turn
+      // each: one warp for both took 7 % longer at pages of 16 rows.)
+      const bool is_k = warp == 0;
+      const uint32_t depth = is_k ? kSK : kSV;
+      const CUtensorMap* map = is_k ? &tmap_k : &tmap_v;
+      uint64_t* full = is_k ? aux->k_full : aux->v_full;
+      uint64_t* empty = is_k ? aux->k_empty : aux->v_empty;
+      const uint32_t ring = ptx::smem_u32(is_k ? sk : sv);
       const int boxes = kNk >> b.page_shift;
       const uint64_t pol = ptx::l2_evict_first_policy();
-      uint32_t it = 0;                    // key tiles so far: ring positions
-      uint32_t kl_done = 0, vl_done = 0;  // copies issued (K, V), for the drain
+      uint32_t it = 0, done = 0;          // key tiles so far; copies issued
       uint32_t tail_on = 0, tail_par = 0; // a stage's v_tail was used; parity of its last use
       bool ok = true;
       auto ids = [&](const Item& w, int step) -> int64_t {
@@ -537,75 +544,65 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
         }
         return ph;
       };
-      int taken = blockIdx.x;             // the first item is the CTA's own
-      for (uint32_t count = 0; ok; ++count) {
-        const int i = __shfl_sync(0xffffffffu, taken, 0);
-        const uint32_t at = count % kNext;
-        if (count >= kNext)
-          ok = ptx::mbar_wait(&aux->next_empty[at], (count / kNext - 1) & 1u, wait_limit);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+      int taken = blockIdx.x;             // warp 0: the next item; the first is the CTA's own
+      for (uint32_t count = 0; ok;) {
         Item w;
-        w.n = -1;
-        if (i < n_items) w = load_item(b, work, i, Hkv, G, max_q);
-        if (lane == 0) {
-          aux->next[at] = w;
-          ptx::mbar_arrive(&aux->next_full[at]);
+        if (is_k) {
+          const int i = __shfl_sync(0xffffffffu, taken, 0);
+          const uint32_t at = count % kNext;
+          if (count >= kNext)
+            ok = ptx::mbar_wait(&aux->next_empty[at], (count / kNext - 1) & 1u, wait_limit);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          w.n = -1;
+          if (i < n_items) w = load_item(b, work, i, Hkv, G, max_q);
+          if (lane == 0) {
+            aux->next[at] = w;
+            ptx::mbar_arrive(&aux->next_full[at]);
+          }
+          ++count;
+        } else {
+          ok = take_item(aux, count, w, lane, wait_limit);
         }
-        if (w.n < 0) break;
+        if (!ok || w.n < 0) break;
         int64_t next = ids(w, 0);
-        if (w.n == 0 && lane == 0) taken = gridDim.x + atomicAdd(&work.hdr->taken, 1);
+        if (w.n == 0 && lane == 0 && is_k) taken = gridDim.x + atomicAdd(&work.hdr->taken, 1);
         for (int k = 0; ok && k < w.n; ++k, ++it) {
           // the next item is taken as late as its latency allows
-          if (k == max(0, w.n - 2) && lane == 0)
+          if (is_k && k == max(0, w.n - 2) && lane == 0)
             taken = gridDim.x + atomicAdd(&work.hdr->taken, 1);
           const int64_t ph = next;
           next = ids(w, k + 1);
           const int row = (int)(((ph < 0 ? 0 : ph) * Hkv + w.kv) << b.page_shift);
           const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, ph >= 0)) *
                                  (uint32_t)(ps * D * 2);
-          const int stK = it % kSK, stV = it % kSV;
-          if (it >= kSK)
-            ok = ptx::mbar_wait(&aux->k_empty[stK], (it / kSK - 1) & 1u, wait_limit);
-          ok = __all_sync(0xffffffffu, ok);
+          const uint32_t st = it % depth;
+          if (it >= depth) ok = ptx::mbar_wait(&empty[st], (it / depth - 1) & 1u, wait_limit);
+          ok = __all_sync(0xffffffffu, ok && aux->abort_flag == 0);
           if (!ok) break;
-          if (lane == 0) ptx::mbar_arrive_expect_tx(&aux->k_full[stK], bytes);
-          __syncwarp();
-          if (ph >= 0)
-            for (int p = 0; p < D / 64; ++p)
-              ptx::tma_load_2d(sk + stK * Ly::kTile + p * Ly::kPanel + lane * ps * 128, &tmap_k,
-                               &aux->k_full[stK], p * 64, row, pol);
-          ++kl_done;
-          if (it >= kSV)
-            ok = ptx::mbar_wait(&aux->v_empty[stV], (it / kSV - 1) & 1u, wait_limit);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          const bool tail = (w.k0 + k + 1) * kNk > w.kl;
-          uint64_t* land = tail ? &aux->v_tail[stV] : &aux->v_full[stV];
+          const bool tail = !is_k && (w.k0 + k + 1) * kNk > w.kl;
+          uint64_t* land = tail ? &aux->v_tail[st] : &full[st];
           if (tail) {
-            tail_par = (tail_on >> stV) & 1u ? tail_par ^ (1u << stV) : tail_par;
-            tail_on |= 1u << stV;
+            tail_par = (tail_on >> st) & 1u ? tail_par ^ (1u << st) : tail_par;
+            tail_on |= 1u << st;
           }
           if (lane == 0) {
             ptx::mbar_arrive_expect_tx(land, bytes);
-            if (tail) ptx::mbar_arrive(&aux->v_full[stV]);
+            if (tail) ptx::mbar_arrive(&full[st]);
           }
           __syncwarp();
           if (ph >= 0)
             for (int p = 0; p < D / 64; ++p)
-              ptx::tma_load_2d(sv + stV * Ly::kTile + p * Ly::kPanel + lane * ps * 128, &tmap_v,
-                               land, p * 64, row, pol);
-          ++vl_done;
-          ok = __all_sync(0xffffffffu, aux->abort_flag == 0);
+              ptx::tma_load_2d_at(ring + st * Ly::kTile + p * Ly::kPanel + lane * ps * 128, map,
+                                  land, p * 64, row, pol);
+          ++done;
         }
       }
       if (!ok) give_up(aux, status);
       // every copy issued must land before the CTA exits
       if (lane == 0) {
-        for (uint32_t t = kl_done > kSK ? kl_done - kSK : 0; t < kl_done; ++t)
-          ptx::mbar_wait(&aux->k_full[t % kSK], (t / kSK) & 1u, kDrainCycles);
-        for (uint32_t t = vl_done > kSV ? vl_done - kSV : 0; t < vl_done; ++t)
-          ptx::mbar_wait(&aux->v_full[t % kSV], (t / kSV) & 1u, kDrainCycles);
+        for (uint32_t t = done > depth ? done - depth : 0; t < done; ++t)
+          ptx::mbar_wait(&full[t % depth], (t / depth) & 1u, kDrainCycles);
         for (int t = 0; t < kSV; ++t)
           if ((tail_on >> t) & 1u)
             ptx::mbar_wait(&aux->v_tail[t], (tail_par >> t) & 1u, kDrainCycles);
