@@ -9,6 +9,7 @@ There is no CPU fallback: if the library is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -632,63 +633,90 @@ def ts_rope_frequencies(rot_dim, base=10000.0, scaling="plain", factor=1.0, orig
     return torch.tensor(list(host), dtype=torch.float64).to(device), scale.value
 
 
-class _On:
-    """The device and stream of one paged call: every tensor on one device,
-    which is made current for the launch; memory the call takes from the
-    allocator is tied to the stream it is used on."""
+# the current stream's handle without building a Stream object
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_PAGED_DTYPES = (torch.bfloat16, torch.float16)
 
-    __slots__ = ("device", "stream", "given", "guard")
 
-    def __init__(self, first, stream, **tensors):
-        self.device = first.device
-        for name, t in tensors.items():
-            if t is not None and t.device != self.device:
-                raise ValueError(f"{name} is on {t.device}, q is on {self.device}")
-        self.given = stream is not None
-        self.stream = torch.cuda.current_stream(self.device) if stream is None else stream
-        self.guard = None if self.device.index == torch.cuda.current_device() \
-            else torch.cuda.device(self.device)
+def _need(t, dtype, shape, dev, name):
+    """The address of tensor `t` after its checks (None stays None)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not dtype or \
+            t.shape != shape or not t.is_contiguous():
+        _dev(t, dtype, name, shape)
+        raise ValueError(f"{name} is on {t.device}, q is on cuda:{dev}")
+    return t.data_ptr()
 
-    def __enter__(self):
-        if self.guard is not None:
+
+def _paged_q(q):
+    """(n, Hq, d, device index, flags) of a call's queries."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        raise TypeError("q must be a CUDA tensor")
+    if q.dtype not in _PAGED_DTYPES:
+        raise TypeError(f"q must be {_PAGED_DTYPES}, got {q.dtype}")
+    if q.dim() != 3:
+        raise ValueError(f"q has shape {tuple(q.shape)}, expected (n, Hq, d)")
+    n, Hq, d = q.shape
+    return n, Hq, d, q.get_device(), TS_PAGED_FP16 if q.dtype is torch.float16 else 0
+
+
+def _paged_batch(cu_q, seq_lens, page_table, dev):
+    """(n_seq, max_pages, the three addresses) of a call's batch."""
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be a tensor [n_seq, pages]")
+    n_seq, max_pages = page_table.shape
+    i32 = torch.int32
+    return (n_seq, max_pages, _need(cu_q, i32, (n_seq + 1,), dev, "cu_q"),
+            _need(seq_lens, i32, (n_seq,), dev, "seq_lens"),
+            _need(page_table, i32, (n_seq, max_pages), dev, "page_table"))
+
+
+class _Launch:
+    """Device and stream of one paged call.  The tensors' device is current
+    during the call; memory that the call takes from the allocator for a stream
+    other than the current one is tied to it."""
+
+    __slots__ = ("dev", "stream", "guard")
+
+    def __init__(self, dev, stream):
+        self.dev, self.stream = dev, stream
+        self.guard = None
+        if _raw_device() != dev:
+            self.guard = torch.cuda.device(dev)
             self.guard.__enter__()
-        return self
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+    def handle(self):
+        return _raw_stream(self.dev) if self.stream is None else self.stream.cuda_stream
 
     def empty(self, shape, dtype):
-        t = torch.empty(shape, dtype=dtype, device=self.device)
-        if self.given:
+        t = torch.empty(shape, dtype=dtype, device="cuda")
+        if self.stream is not None:
             t.record_stream(self.stream)
         return t
 
     def workspace(self, nbytes, workspace):
-        if workspace is None and nbytes:
+        """(tensor to keep, address, bytes) of the call's workspace."""
+        if workspace is None:
+            if nbytes == 0:
+                return None, None, 0
             workspace = self.empty(nbytes, torch.uint8)
-        return _workspace(nbytes, self.device, workspace)
+        elif workspace.get_device() != self.dev:
+            raise ValueError(f"workspace is on {workspace.device}, q is on cuda:{self.dev}")
+        have = workspace.numel() * workspace.element_size()
+        if have < nbytes:
+            raise ValueError(f"workspace too small: {nbytes} bytes needed")
+        return workspace, workspace.data_ptr(), have
 
-    @property
-    def handle(self):
-        return ctypes.c_void_p(self.stream.cuda_stream)
-
-
-_PAGED_DTYPES = (torch.bfloat16, torch.float16)
-
-
-def _paged_batch(q, cu_q, seq_lens, page_table):
-    _dev(cu_q, torch.int32, "cu_q")
-    n_seq = cu_q.numel() - 1
-    _dev(seq_lens, torch.int32, "seq_lens", (n_seq,))
-    _dev(page_table, torch.int32, "page_table")
-    if page_table.dim() != 2 or page_table.shape[0] != n_seq:
-        raise ValueError(f"page_table has shape {tuple(page_table.shape)}, expected ({n_seq}, pages)")
-    return n_seq, page_table.shape[1]
+    def done(self):
+        if self.guard is not None:
+            self.guard.__exit__(None, None, None)
 
 
-def _paged_out(on, t, shape, dtype, name):
-    return on.empty(shape, dtype) if t is None else _dev(t, dtype, name, shape)
+def _paged_status(status, dev):
+    return None if status is None else _need(status, torch.int32, status.shape, dev, "status")
 
 
 def ts_paged_rope_append(q, k, v, cu_q, seq_lens, page_table, k_pages, v_pages, freqs,
@@ -700,57 +728,54 @@ def ts_paged_rope_append(q, k, v, cu_q, seq_lens, page_table, k_pages, v_pages, 
     Hkv, page_size, d], freqs [rot_dim / 2] fp64 (see ts_rope_frequencies).
     key_min, key_max [n_pages, Hkv, d]: the pages' key bounds, updated.
     Returns the rotated queries [n, Hq, d]."""
-    n, Hq, d = q.shape
-    n_pages, Hkv, ps = k_pages.shape[:3]
+    n, Hq, d, dev, flags = _paged_q(q)
     dt = q.dtype
+    n_pages, Hkv, ps = k_pages.shape[:3]
+    strides = []
     for t, name, heads in ((q, "q", Hq), (k, "k", Hkv), (v, "v", Hkv)):
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{name} must be a CUDA tensor")
-        if t.dtype not in _PAGED_DTYPES or t.dtype != dt:
-            raise TypeError(f"{name} must be {dt if dt in _PAGED_DTYPES else _PAGED_DTYPES}, "
-                            f"got {t.dtype}")
-        if tuple(t.shape) != (n, heads, d):
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(n, heads, d)}")
-        if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
+        if t.dtype is not dt:
+            raise TypeError(f"{name} must be {dt}, got {t.dtype}")
+        if t.shape != (n, heads, d) or t.get_device() != dev:
+            raise ValueError(f"{name} has shape {tuple(t.shape)} on {t.device}, expected "
+                             f"{(n, heads, d)} on cuda:{dev}")
+        row, head, one = t.stride()
+        if n and (one != 1 or (heads > 1 and head != d)):
             raise ValueError(f"{name}: the heads of a token must be dense")
-    n_seq, max_pages = _paged_batch(q, cu_q, seq_lens, page_table)
-    _dev(k_pages, dt, "k_pages", (n_pages, Hkv, ps, d))
-    _dev(v_pages, dt, "v_pages", (n_pages, Hkv, ps, d))
-    _dev(freqs, torch.float64, "freqs")
-    if positions is not None:
-        _dev(positions, torch.int32, "positions", (n,))
-    for t, name in ((key_min, "key_min"), (key_max, "key_max")):
-        if t is not None:
-            _dev(t, dt, name, (n_pages, Hkv, d))
-    # a single token's stride is never walked; a view may report any
-    stride = lambda t, heads: t.stride(0) if n > 1 else heads * d  # noqa: E731
-    flags = (TS_PAGED_FP16 if dt == torch.float16 else 0) | (TS_ROPE_INTERLEAVED if interleaved else 0)
-    with _On(q, stream, k=k, v=v, cu_q=cu_q, seq_lens=seq_lens, page_table=page_table,
-             k_pages=k_pages, v_pages=v_pages, freqs=freqs, positions=positions, key_min=key_min,
-             key_max=key_max, q_out=q_out, status=status) as on:
-        q_out = _paged_out(on, q_out, (n, Hq, d), dt, "q_out")
-        _check(lib().ts_paged_rope_append(
-            _ptr(q), _ptr(k), _ptr(v), stride(q, Hq), stride(k, Hkv), stride(v, Hkv), n, Hq, Hkv,
-            d, _ptr(cu_q), _ptr(seq_lens), n_seq, _ptr(page_table), max_pages, ps, n_pages,
-            _ptr(positions), _ptr(freqs), 2 * freqs.numel(), rope_scale, _ptr(q_out),
-            _ptr(k_pages), _ptr(v_pages), _ptr(key_min), _ptr(key_max), flags, _ptr(status),
-            on.handle))
+        # a single token's stride is never walked; a view may report any
+        strides.append(row if n > 1 else heads * d)
+    if interleaved:
+        flags |= TS_ROPE_INTERLEAVED
+    n_seq, max_pages, cu, lens, table = _paged_batch(cu_q, seq_lens, page_table, dev)
+    kp = _need(k_pages, dt, (n_pages, Hkv, ps, d), dev, "k_pages")
+    vp = _need(v_pages, dt, (n_pages, Hkv, ps, d), dev, "v_pages")
+    fr = _need(freqs, torch.float64, freqs.shape, dev, "freqs")
+    pos = _need(positions, torch.int32, (n,), dev, "positions")
+    mn = _need(key_min, dt, (n_pages, Hkv, d), dev, "key_min")
+    mx = _need(key_max, dt, (n_pages, Hkv, d), dev, "key_max")
+    st = _paged_status(status, dev)
+    out = _need(q_out, dt, (n, Hq, d), dev, "q_out")
+    on = _Launch(dev, stream)
+    try:
+        if q_out is None:
+            q_out = on.empty((n, Hq, d), dt)
+            out = q_out.data_ptr()
+        rc = lib().ts_paged_rope_append(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), strides[0], strides[1], strides[2], n, Hq,
+            Hkv, d, cu, lens, n_seq, table, max_pages, ps, n_pages, pos, fr, 2 * freqs.numel(),
+            rope_scale, out, kp, vp, mn, mx, flags, st, on.handle())
+    finally:
+        on.done()
+    _check(rc)
     return q_out
 
 
+@functools.lru_cache(maxsize=4096)
 def ts_paged_attention_workspace_bytes(n, n_seq, Hq, Hkv, d, max_pages, page_size, max_q,
                                        max_kv=0) -> int:
     return lib().ts_paged_attention_workspace_bytes(n, n_seq, Hq, Hkv, d, max_pages, page_size,
                                                     max_q, max_kv)
-
-
-def _paged_qkv(q, k_pages, v_pages):
-    n, Hq, d = q.shape
-    n_pages, Hkv, ps = k_pages.shape[:3]
-    _dev(q, _PAGED_DTYPES, "q")
-    _dev(k_pages, q.dtype, "k_pages", (n_pages, Hkv, ps, d))
-    _dev(v_pages, q.dtype, "v_pages", (n_pages, Hkv, ps, d))
-    return n, Hq, d, n_pages, Hkv, ps, TS_PAGED_FP16 if q.dtype == torch.float16 else 0
 
 
 def ts_paged_attention(q, k_pages, v_pages, cu_q, seq_lens, page_table, max_q, max_kv=0, o=None,
@@ -760,22 +785,36 @@ def ts_paged_attention(q, k_pages, v_pages, cu_q, seq_lens, page_table, max_q, m
     k_pages, v_pages [n_pages, Hkv, page_size, d]; max_q bounds the sequences'
     new tokens, max_kv (0: the page table's width) is the longest sequence as
     far as the host knows.  Returns (o [n, Hq, d], lse [n, Hq] fp32)."""
-    n, Hq, d, n_pages, Hkv, ps, flags = _paged_qkv(q, k_pages, v_pages)
-    n_seq, max_pages = _paged_batch(q, cu_q, seq_lens, page_table)
-    with _On(q, stream, k_pages=k_pages, v_pages=v_pages, cu_q=cu_q, seq_lens=seq_lens,
-             page_table=page_table, o=o, lse=lse, workspace=workspace, status=status) as on:
-        o = _paged_out(on, o, (n, Hq, d), q.dtype, "o")
-        if lse is not None or want_lse:
-            lse = _paged_out(on, lse, (n, Hq), torch.float32, "lse")
-        ws, nb = on.workspace(lib().ts_paged_attention_workspace_bytes(
+    n, Hq, d, dev, flags = _paged_q(q)
+    dt = q.dtype
+    n_pages, Hkv, ps = k_pages.shape[:3]
+    n_seq, max_pages, cu, lens, table = _paged_batch(cu_q, seq_lens, page_table, dev)
+    qp = _need(q, dt, (n, Hq, d), dev, "q")
+    kp = _need(k_pages, dt, (n_pages, Hkv, ps, d), dev, "k_pages")
+    vp = _need(v_pages, dt, (n_pages, Hkv, ps, d), dev, "v_pages")
+    st = _paged_status(status, dev)
+    out = _need(o, dt, (n, Hq, d), dev, "o")
+    ls = _need(lse, torch.float32, (n, Hq), dev, "lse")
+    on = _Launch(dev, stream)
+    try:
+        if o is None:
+            o = on.empty((n, Hq, d), dt)
+            out = o.data_ptr()
+        if lse is None and want_lse:
+            lse = on.empty((n, Hq), torch.float32)
+            ls = lse.data_ptr()
+        keep, ws, nb = on.workspace(ts_paged_attention_workspace_bytes(
             n, n_seq, Hq, Hkv, d, max_pages, ps, max_q, max_kv), workspace)
-        _check(lib().ts_paged_attention(
-            _ptr(q), _ptr(k_pages), _ptr(v_pages), n, Hq, Hkv, d, _ptr(cu_q), _ptr(seq_lens),
-            n_seq, _ptr(page_table), max_pages, ps, n_pages, max_q, max_kv, _ptr(o), _ptr(lse),
-            _ptr(ws), nb, flags, _ptr(status), on.handle))
+        rc = lib().ts_paged_attention(
+            qp, kp, vp, n, Hq, Hkv, d, cu, lens, n_seq, table, max_pages, ps, n_pages, max_q,
+            max_kv, out, ls, ws, nb, flags, st, on.handle())
+    finally:
+        on.done()
+    _check(rc)
     return o, lse
 
 
+@functools.lru_cache(maxsize=4096)
 def ts_paged_select_workspace_bytes(n, Hkv, max_pages) -> int:
     return lib().ts_paged_select_workspace_bytes(n, Hkv, max_pages)
 
@@ -788,26 +827,36 @@ def ts_paged_select_pages(q, key_min, key_max, cu_q, seq_lens, page_table, page_
     q [n, Hq, d] rotated, key_min, key_max [n_pages, Hkv, d].  Returns
     (pages [n, Hkv, n_sink + n_top + n_recent], counts [n, Hkv]) int32:
     ascending positions in the page table's row, -1 behind the last."""
-    n, Hq, d = q.shape
+    n, Hq, d, dev, flags = _paged_q(q)
+    dt = q.dtype
     n_pages, Hkv = key_min.shape[:2]
-    _dev(q, _PAGED_DTYPES, "q")
-    _dev(key_min, q.dtype, "key_min", (n_pages, Hkv, d))
-    _dev(key_max, q.dtype, "key_max", (n_pages, Hkv, d))
-    n_seq, max_pages = _paged_batch(q, cu_q, seq_lens, page_table)
-    flags = TS_PAGED_FP16 if q.dtype == torch.float16 else 0
-    with _On(q, stream, key_min=key_min, key_max=key_max, cu_q=cu_q, seq_lens=seq_lens,
-             page_table=page_table, pages=pages, counts=counts, workspace=workspace,
-             status=status) as on:
-        pages = _paged_out(on, pages, (n, Hkv, n_sink + n_top + n_recent), torch.int32, "pages")
-        counts = _paged_out(on, counts, (n, Hkv), torch.int32, "counts")
-        ws, nb = on.workspace(lib().ts_paged_select_workspace_bytes(n, Hkv, max_pages), workspace)
-        _check(lib().ts_paged_select_pages(
-            _ptr(q), _ptr(key_min), _ptr(key_max), n, Hq, Hkv, d, _ptr(cu_q), _ptr(seq_lens),
-            n_seq, _ptr(page_table), max_pages, page_size, n_pages, n_top, n_sink, n_recent,
-            _ptr(pages), _ptr(counts), _ptr(ws), nb, flags, _ptr(status), on.handle))
+    n_seq, max_pages, cu, lens, table = _paged_batch(cu_q, seq_lens, page_table, dev)
+    qp = _need(q, dt, (n, Hq, d), dev, "q")
+    mn = _need(key_min, dt, (n_pages, Hkv, d), dev, "key_min")
+    mx = _need(key_max, dt, (n_pages, Hkv, d), dev, "key_max")
+    n_sel = n_sink + n_top + n_recent
+    st = _paged_status(status, dev)
+    pg = _need(pages, torch.int32, (n, Hkv, n_sel), dev, "pages")
+    ct = _need(counts, torch.int32, (n, Hkv), dev, "counts")
+    on = _Launch(dev, stream)
+    try:
+        if pages is None:
+            pages = on.empty((n, Hkv, max(n_sel, 0)), torch.int32)
+            pg = pages.data_ptr()
+        if counts is None:
+            counts = on.empty((n, Hkv), torch.int32)
+            ct = counts.data_ptr()
+        keep, ws, nb = on.workspace(ts_paged_select_workspace_bytes(n, Hkv, max_pages), workspace)
+        rc = lib().ts_paged_select_pages(
+            qp, mn, mx, n, Hq, Hkv, d, cu, lens, n_seq, table, max_pages, page_size, n_pages,
+            n_top, n_sink, n_recent, pg, ct, ws, nb, flags, st, on.handle())
+    finally:
+        on.done()
+    _check(rc)
     return pages, counts
 
 
+@functools.lru_cache(maxsize=4096)
 def ts_paged_selected_workspace_bytes(n, Hq, Hkv, d, page_size, n_sel) -> int:
     return lib().ts_paged_selected_workspace_bytes(n, Hq, Hkv, d, page_size, n_sel)
 
@@ -818,21 +867,33 @@ def ts_paged_attention_selected(q, k_pages, v_pages, cu_q, seq_lens, page_table,
     """ts_paged_attention over each token's chosen pages (pages [n, Hkv,
     n_sel], counts [n, Hkv] int32, as ts_paged_select_pages returns them).
     Returns (o [n, Hq, d], lse [n, Hq] fp32)."""
-    n, Hq, d, n_pages, Hkv, ps, flags = _paged_qkv(q, k_pages, v_pages)
-    n_seq, max_pages = _paged_batch(q, cu_q, seq_lens, page_table)
-    n_sel = pages.shape[2]
-    _dev(pages, torch.int32, "pages", (n, Hkv, n_sel))
-    _dev(counts, torch.int32, "counts", (n, Hkv))
-    with _On(q, stream, k_pages=k_pages, v_pages=v_pages, cu_q=cu_q, seq_lens=seq_lens,
-             page_table=page_table, pages=pages, counts=counts, o=o, lse=lse, workspace=workspace,
-             status=status) as on:
-        o = _paged_out(on, o, (n, Hq, d), q.dtype, "o")
-        if lse is not None or want_lse:
-            lse = _paged_out(on, lse, (n, Hq), torch.float32, "lse")
-        ws, nb = on.workspace(lib().ts_paged_selected_workspace_bytes(n, Hq, Hkv, d, ps, n_sel),
-                              workspace)
-        _check(lib().ts_paged_attention_selected(
-            _ptr(q), _ptr(k_pages), _ptr(v_pages), n, Hq, Hkv, d, _ptr(cu_q), _ptr(seq_lens),
-            n_seq, _ptr(page_table), max_pages, ps, n_pages, _ptr(pages), _ptr(counts), n_sel,
-            _ptr(o), _ptr(lse), _ptr(ws), nb, flags, _ptr(status), on.handle))
+    n, Hq, d, dev, flags = _paged_q(q)
+    dt = q.dtype
+    n_pages, Hkv, ps = k_pages.shape[:3]
+    n_seq, max_pages, cu, lens, table = _paged_batch(cu_q, seq_lens, page_table, dev)
+    qp = _need(q, dt, (n, Hq, d), dev, "q")
+    kp = _need(k_pages, dt, (n_pages, Hkv, ps, d), dev, "k_pages")
+    vp = _need(v_pages, dt, (n_pages, Hkv, ps, d), dev, "v_pages")
+    n_sel = pages.shape[-1]
+    pg = _need(pages, torch.int32, (n, Hkv, n_sel), dev, "pages")
+    ct = _need(counts, torch.int32, (n, Hkv), dev, "counts")
+    st = _paged_status(status, dev)
+    out = _need(o, dt, (n, Hq, d), dev, "o")
+    ls = _need(lse, torch.float32, (n, Hq), dev, "lse")
+    on = _Launch(dev, stream)
+    try:
+        if o is None:
+            o = on.empty((n, Hq, d), dt)
+            out = o.data_ptr()
+        if lse is None and want_lse:
+            lse = on.empty((n, Hq), torch.float32)
+            ls = lse.data_ptr()
+        keep, ws, nb = on.workspace(
+            ts_paged_selected_workspace_bytes(n, Hq, Hkv, d, ps, n_sel), workspace)
+        rc = lib().ts_paged_attention_selected(
+            qp, kp, vp, n, Hq, Hkv, d, cu, lens, n_seq, table, max_pages, ps, n_pages, pg, ct,
+            n_sel, out, ls, ws, nb, flags, st, on.handle())
+    finally:
+        on.done()
+    _check(rc)
     return o, lse
