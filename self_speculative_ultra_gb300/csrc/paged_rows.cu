@@ -25,6 +25,7 @@ namespace ts {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kCtas = 1;                   // CTAs a SM
 constexpr int kThreads = kWarps * 32;
 constexpr int kTileKeys = 32;              // keys of a warp's tile
 constexpr int kStep = kWarps * kTileKeys;  // keys a CTA takes per trip
@@ -92,7 +93,7 @@ __device__ __forceinline__ uint32_t chunk_off(int r, int c) {
 // Partials of row (t, head) and split s: O (fp32, scaled to the split's own
 // maximum) at ((t * Hq + head) * n_split + s) * D, (m, l) likewise.
 template <typename T, int D, bool kSparse>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kCtas)
 paged_rows_kernel(const PagedBatch b, const RowsArgs a, int n_rb, int n_split, int keys_per_split,
                   float* __restrict__ part_o, float2* __restrict__ part_ml, int32_t* status) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -207,24 +208,43 @@ paged_rows_kernel(const PagedBatch b, const RowsArgs a, int n_rb, int n_split, i
     };
     constexpr int kCh = D / 8;                       // 16-byte chunks a row
     constexpr int kRowsPer = 32 / kCh;               // rows a warp copies at once
+    // a lane copies 16-byte chunk lane % kCh of rows lane / kCh + x * kRowsPer;
+    // within a page its addresses are one base and constant steps
+    const uint32_t lane_bytes = (lane / kCh) * (D * 2) + (lane % kCh) * 16;
+    const char* kbase = static_cast<const char*>(a.k_pages) + lane_bytes;
+    const char* vbase = static_cast<const char*>(a.v_pages) + lane_bytes;
+    const int64_t page_bytes = (int64_t)a.Hkv * ps * (D * 2);
+    const int64_t head_bytes = (int64_t)kv * ps * (D * 2);
     auto fetch = [&](int i, const Tile& t) {
       if (i < n_tiles) {
         const int j = j0 + i * kStep + warp * kTileKeys;
         const uint32_t st = ring + (i % kStages) * R::kStage;
-        const int c = lane % kCh;
+        const int in_page = j & (ps - 1);
+        // rows behind the last visible one are filled with zeros: whatever
+        // their page holds there must not reach P.V
+        int live0 = t.ph0 < 0 ? 0 : j1 - j, live1 = t.ph1 < 0 ? 0 : j1 - j;
+        if (kSparse) {
+          live0 = min(live0, see0 + 1 - (t.lp0 << b.page_shift) - in_page);
+          live1 = min(live1, see0 + 1 - (t.lp1 << b.page_shift) - in_page +
+                                 (b.page_shift == 4 ? 16 : 0));
+        }
+        const int64_t o0 = max(t.ph0, (int64_t)0) * page_bytes + head_bytes + in_page * (D * 2);
+        // rows 16.. of the tile: the next 16 of the page, or the second page's
+        const int64_t o1 = b.page_shift == 4
+                               ? max(t.ph1, (int64_t)0) * page_bytes + head_bytes - 16 * (D * 2)
+                               : o0;
+        const int r0l = lane / kCh;
 #pragma unroll
         for (int x = 0; x < kTileKeys / kRowsPer; ++x) {
-          const int r = x * kRowsPer + lane / kCh;
-          const int64_t ph = r < 16 ? t.ph0 : t.ph1;
-          const int lp = r < 16 ? t.lp0 : t.lp1;
-          const int in_page = (j + r) & (ps - 1);
-          // rows behind the last visible one are filled with zeros: whatever
-          // their page holds there must not reach P.V
-          const bool live = j + r < j1 && ph >= 0 && (!kSparse || (lp << b.page_shift) + in_page <= see0);
-          const int64_t row = live ? ((ph * a.Hkv + kv) << b.page_shift) + in_page : 0;
-          const uint32_t off = chunk_off<D>(r, c);
-          cp16(st + off, static_cast<const T*>(a.k_pages) + row * D + c * 8, live);
-          cp16(st + R::kTile + off, static_cast<const T*>(a.v_pages) + row * D + c * 8, live);
+          const int r = x * kRowsPer + r0l;
+          const bool second = x * kRowsPer >= 16;
+          const bool live = r < (second ? live1 : live0);
+          // a row that is not read still needs a valid address
+          const int64_t off = (second ? o1 : o0) + x * (kRowsPer * D * 2);
+          const int64_t at = live ? off : -(int64_t)lane_bytes;
+          const uint32_t dst = chunk_off<D>(r, lane % kCh);
+          cp16(st + dst, kbase + at, live);
+          cp16(st + R::kTile + dst, vbase + at, live);
         }
       }
       cp_commit();
@@ -405,50 +425,65 @@ paged_rows_kernel(const PagedBatch b, const RowsArgs a, int n_rb, int n_split, i
   }
 }
 
-// Joins the splits of every row: a warp a row, each lane D/32 columns.
+// Joins the splits of every row: a warp a row, each lane D/32 columns.  The
+// lanes hold one split's weight each; the loads of O do not wait for one
+// another.
 template <typename T, int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(128)
 paged_rows_merge(const PagedBatch b, const float* __restrict__ part_o,
                  const float2* __restrict__ part_ml, int Hq, int n_split, int max_q, T* o,
                  float* lse) {
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int t = (int)(row / Hq);
   if (t >= b.n) return;
+  const float2* ml = part_ml + row * n_split;
+  const float2 first = lane < n_split ? ml[lane] : make_float2(-INFINITY, 0.f);
   const int s = warp_find_seq(b, t, lane);
   if (s < 0) return;
   if (max_q > 0 && t - seq_span(b, s).q0 >= max_q) return;   // no partials were made
-  const float2* ml = part_ml + row * n_split;
-  float m = -INFINITY;
-  for (int i = lane; i < n_split; i += 32) m = fmaxf(m, ml[i].x);
+  float m = first.x;
+  for (int i = lane + 32; i < n_split; i += 32) m = fmaxf(m, ml[i].x);
   m = warp_max(m);
   constexpr int kPer = D / 32;
   float acc[kPer], l = 0.f;
 #pragma unroll
   for (int x = 0; x < kPer; ++x) acc[x] = 0.f;
   if (m != -INFINITY) {
-#pragma unroll 4
-    for (int i = 0; i < n_split; ++i) {
-      const float2 x = ml[i];
-      if (!(x.y > 0.f)) continue;         // an empty split left no O
-      const float f = exp2f(x.x - m);
-      l += f * x.y;
-      const float* p = part_o + (row * n_split + i) * D + lane * kPer;
-      if (kPer == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(p);
-        acc[0] += f * v.x;
-        acc[1] += f * v.y;
-        acc[2 % kPer] += f * v.z;
-        acc[3 % kPer] += f * v.w;
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(p);
-        acc[0] += f * v.x;
-        acc[1] += f * v.y;
+    const float* po = part_o + row * n_split * D + lane * kPer;
+    for (int base = 0; base < n_split; base += 32) {
+      const float2 x = base == 0 ? first
+                                 : base + lane < n_split ? ml[base + lane] : make_float2(-INFINITY, 0.f);
+      const float w = x.y > 0.f ? exp2f(x.x - m) : 0.f;      // an empty split left no O
+      l += w * x.y;
+      const int n = min(32, n_split - base);
+#pragma unroll 8
+      for (int i = 0; i < n; ++i) {
+        const float f = __shfl_sync(0xffffffffu, w, i);
+        float v[kPer];
+#pragma unroll
+        for (int y = 0; y < kPer; ++y) v[y] = 0.f;
+        if (f > 0.f) {
+          if (kPer == 4) {
+            const float4 u = *reinterpret_cast<const float4*>(po + (int64_t)(base + i) * D);
+            v[0] = u.x;
+            v[1] = u.y;
+            v[2 % kPer] = u.z;
+            v[3 % kPer] = u.w;
+          } else {
+            const float2 u = *reinterpret_cast<const float2*>(po + (int64_t)(base + i) * D);
+            v[0] = u.x;
+            v[1] = u.y;
+          }
+        }
+#pragma unroll
+        for (int y = 0; y < kPer; ++y) acc[y] += f * v[y];
       }
     }
   }
+  l = warp_sum(l);
   const float inv = l > 0.f ? 1.f / l : 0.f;
   uint32_t* dst = reinterpret_cast<uint32_t*>(o + row * D + lane * kPer);
 #pragma unroll
@@ -461,7 +496,7 @@ paged_rows_merge(const PagedBatch b, const float* __restrict__ part_o,
 // units x 16-row blocks x splits CTAs, one a SM (their rings fill its shared
 // memory): the split count that minimises waves x (trips + a fixed cost).
 RowsPlan rows_plan(int64_t units, int n, int Hq, int rows, int d, int64_t max_keys) {
-  constexpr double kFixedTrips = 6.0;
+  constexpr double kFixedTrips = 6.0;  // ~2 us
   RowsPlan p{};
   p.n_rb = (rows + 15) / 16;
   const int64_t base = units * p.n_rb;
@@ -471,7 +506,7 @@ RowsPlan rows_plan(int64_t units, int n, int Hq, int rows, int d, int64_t max_ke
   for (int64_t ns = 1; ns <= imin64(trips, 256); ++ns) {
     const int64_t per = (trips + ns - 1) / ns;
     const int64_t used = (trips + per - 1) / per;
-    const int64_t waves = (base * used + kGb300Sms - 1) / kGb300Sms;
+    const int64_t waves = (base * used + kCtas * kGb300Sms - 1) / (kCtas * kGb300Sms);
     const double cost = (double)waves * ((double)per + kFixedTrips);
     if (cost < best - 1e-9) {
       best = cost;
@@ -506,7 +541,7 @@ static int go_rows(const PagedBatch& b, const RowsArgs& a, const RowsPlan& p, vo
   int rc = launch_status("paged_rows_kernel");
   if (rc || p.n_split == 1) return rc;
   const int64_t rows = (int64_t)b.n * a.Hq;
-  pdl_config(&cfg, attr, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, st);
+  pdl_config(&cfg, attr, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st);
   cudaLaunchKernelEx(&cfg, paged_rows_merge<T, D>, b, (const float*)part_o, (const float2*)part_ml,
                      a.Hq, p.n_split, sparse ? 0 : a.max_q, static_cast<T*>(a.o), a.lse);
   return launch_status("paged_rows_merge");
