@@ -110,11 +110,11 @@ int launch_paged_append(const PagedBatch& b, const AppendArgs& a, int d, bool fp
 // CTAs, and its sparse form over per-token page lists.
 struct RowsPlan {
   int n_rb;            // blocks of 16 query rows
-  int n_split;         // key splits
-  int keys_per_split;  // a multiple of 128
-  size_t part_bytes, ml_bytes, ws_bytes;
+  int unit_trips;      // trips of 128 keys a unit, by the host's bound
+  int grid;
+  size_t cuts_bytes, part_bytes, ws_bytes;
 };
-RowsPlan rows_plan(int64_t units, int n, int Hq, int rows, int d, int64_t max_keys);
+RowsPlan rows_plan(int64_t units, int rows, int d, int64_t max_keys);
 struct RowsArgs {
   const void *q, *k_pages, *v_pages;
   const int32_t *pages, *counts;   // sparse form: [n, Hkv, n_sel], [n, Hkv]; else NULL

@@ -181,7 +181,7 @@ size_t ts_paged_attention_workspace_bytes(int n, int n_seq, int Hq, int Hkv, int
     return 0;
   const int64_t kv = bound_kv(max_pages, page_size, max_kv);
   if (few_rows(max_q, Hq, Hkv))
-    return rows_plan((int64_t)n_seq * Hkv, n, Hq, max_q * (Hq / Hkv), d, kv).ws_bytes;
+    return rows_plan((int64_t)n_seq * Hkv, max_q * (Hq / Hkv), d, kv).ws_bytes;
   return tc_plan(n, n_seq, Hq, Hkv, d, max_q, kv).ws_bytes;
 }
 
@@ -211,7 +211,7 @@ int ts_paged_attention(const void* q, const void* k_pages, const void* v_pages, 
     return launch_paged_tc(b, a, p, d, (flags & TS_PAGED_FP16) != 0, workspace, status,
                            static_cast<cudaStream_t>(stream));
   }
-  const RowsPlan p = rows_plan((int64_t)n_seq * Hkv, n, Hq, max_q * (Hq / Hkv), d, kv);
+  const RowsPlan p = rows_plan((int64_t)n_seq * Hkv, max_q * (Hq / Hkv), d, kv);
   rc = check_paged_ws(workspace, workspace_bytes, p.ws_bytes, W);
   if (rc) return rc;
   RowsArgs a{};
@@ -263,7 +263,7 @@ int ts_paged_select_pages(const void* q, const void* key_min, const void* key_ma
 
 size_t ts_paged_selected_workspace_bytes(int n, int Hq, int Hkv, int d, int page_size, int n_sel) {
   if (n < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || page_size < 1 || n_sel < 1) return 0;
-  return rows_plan((int64_t)n * Hkv, n, Hq, Hq / Hkv, d, (int64_t)n_sel * page_size).ws_bytes;
+  return rows_plan((int64_t)n * Hkv, Hq / Hkv, d, (int64_t)n_sel * page_size).ws_bytes;
 }
 
 int ts_paged_attention_selected(const void* q, const void* k_pages, const void* v_pages, int n,
@@ -288,7 +288,7 @@ int ts_paged_attention_selected(const void* q, const void* k_pages, const void* 
   for (const void* p : {q, k_pages, v_pages, (const void*)o})
     if (!aligned16(p)) return fail(TS_ERR_INVALID_ARG, "%s: a tensor is not 16-byte aligned", W);
   const RowsPlan p =
-      rows_plan((int64_t)n * Hkv, n, Hq, Hq / Hkv, d, (int64_t)n_sel * page_size);
+      rows_plan((int64_t)n * Hkv, Hq / Hkv, d, (int64_t)n_sel * page_size);
   rc = check_paged_ws(workspace, workspace_bytes, p.ws_bytes, W);
   if (rc) return rc;
   RowsArgs a{};

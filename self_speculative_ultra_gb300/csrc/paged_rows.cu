@@ -9,11 +9,14 @@
 //
 // Memory bound: K and V are read once, 4 d bytes a key and KV head.  The
 // query rows of a KV head (new tokens x group) are packed into blocks of 16,
-// so a key tile is read once for all of them; the keys are split over CTAs.
-// A CTA's four warps work on their own 32-key tiles: each warp streams its
-// tiles through its own ring of asynchronous copies and runs the online
-// softmax by itself, without a CTA-wide barrier in the loop; the four states
-// are joined at the end in shared memory, the splits by a second kernel.
+// so a key tile is read once for all of them.  A unit is one block of rows of
+// one KV head; all units' keys, in trips of 128, form one line of work that is
+// cut into equal stretches, one a SM, whatever the lengths: a unit that a cut
+// falls into is joined by a second kernel.  A CTA's four warps work on their
+// own 32-key tiles of a trip: each streams its tiles through its own ring of
+// asynchronous copies, which runs on across units, and runs the online softmax
+// by itself, without a CTA-wide barrier; the four states are joined at the
+// unit's end in shared memory.
 // Q.K^T and P.V use 16x8x16 matrix instructions: 16 rows never fill a tensor
 // core tile, so the copy engine's 128-row tiles would only pad.  P is split
 // into a 16-bit value and its 16-bit remainder (two products), so P.V sees P
@@ -25,11 +28,11 @@ namespace ts {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kCtas = 1;                   // CTAs a SM
 constexpr int kThreads = kWarps * 32;
 constexpr int kTileKeys = 32;              // keys of a warp's tile
 constexpr int kStep = kWarps * kTileKeys;  // keys a CTA takes per trip
 constexpr int kStages = 3;
+constexpr int kMinTrips = 2;               // trips a CTA takes at least
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -38,7 +41,8 @@ struct Ring {
   static constexpr int kRow = D * 2;
   static constexpr int kTile = kTileKeys * kRow;
   static constexpr int kStage = 2 * kTile;                 // K tile, V tile
-  static constexpr int kBytes = kWarps * kStages * kStage;
+  static constexpr int kStates = kWarps * kStages * kStage;  // the warps' states at a unit's end
+  static constexpr int kBytes = kStates + kWarps * 16 * (D + 2) * 4;
 };
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
@@ -90,77 +94,304 @@ __device__ __forceinline__ uint32_t chunk_off(int r, int c) {
   return (uint32_t)(r * (D * 2) + ((c ^ (r & 7)) << 4));
 }
 
-// Partials of row (t, head) and split s: O (fp32, scaled to the split's own
-// maximum) at ((t * Hq + head) * n_split + s) * D, (m, l) likewise.
-template <typename T, int D, bool kSparse>
-__global__ void __launch_bounds__(kThreads, kCtas)
-paged_rows_kernel(const PagedBatch b, const RowsArgs a, int n_rb, int n_split, int keys_per_split,
-                  float* __restrict__ part_o, float2* __restrict__ part_ml, int32_t* status) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  using R = Ring<D>;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int split = blockIdx.x % n_split;
-  const int unit = blockIdx.x / n_split;       // sequence (dense) or token (sparse)
-  const int kv = blockIdx.y / n_rb, rb = blockIdx.y % n_rb;
+// What the first kernel leaves for the second: unit `first of a stretch's last,
+// cut unit`, its rows, and how many stretches hold a part of it.
+struct CutUnit {
+  int tok0, kv, r0, nr;
+  int parts;             // 0: the stretch ends with a whole unit
+  int pad[3];
+};
+
+// A unit: a block of 16 packed rows of one KV head, and the keys it walks.
+struct Unit {
+  int s, kv, r0, nr;     // nr = 0: nothing to do
+  int tok0, see0;        // row R is token tok0 + R / G and sees rows up to see0 + R / G
+  int n_keys;            // in list order
+  const int32_t* list;   // sparse: the listed pages
+};
+
+template <bool kSparse>
+__device__ __forceinline__ Unit make_unit(const PagedBatch& b, const RowsArgs& a, int owner, int kv,
+                                          int rb, int lane, int32_t* status) {
+  Unit u;
   const int G = a.Hq / a.Hkv;
-  const int ps = 1 << b.page_shift;
-  griddep_wait();
-  griddep_launch_dependents();
-  const int s = kSparse ? warp_find_seq(b, unit, lane) : unit;
-  if (s < 0) return;                           // a token behind the last sequence
-  const SeqSpan sp = seq_span(b, s);
-  const bool first_cta = split == 0 && blockIdx.y == 0 && tid == 0;
-  if (first_cta && (sp.bad || (!kSparse && sp.ql > a.max_q)))
-    set_status(status, TS_ERR_INVALID_ARG);
-  // rows of this block: R = r0 .. r0 + nr - 1; row R is token tok0 + R / G,
-  // head kv * G + R % G, and sees rows up to see0 + R / G
-  const int tok0 = kSparse ? unit : sp.q0;
-  const int see0 = kSparse ? sp.kl - sp.ql + (unit - sp.q0) : sp.kl - sp.ql;
+  u.kv = kv;
+  u.r0 = rb * 16;
+  u.list = nullptr;
+  u.nr = 0;
+  u.n_keys = 0;
+  u.tok0 = u.see0 = 0;
+  u.s = kSparse ? warp_find_seq(b, owner, lane) : owner;
+  if (u.s < 0) return u;                     // a token behind the last sequence
+  const SeqSpan sp = seq_span(b, u.s);
+  u.tok0 = kSparse ? owner : sp.q0;
+  u.see0 = sp.kl - sp.ql + (kSparse ? owner - sp.q0 : 0);
   const int rows = kSparse ? G : min(sp.ql, a.max_q) * G;
-  const int r0 = rb * 16;
-  if (r0 >= rows) return;
-  const int nr = min(16, rows - r0);
-  const int32_t* list = nullptr;
-  int n_keys;                                  // keys to walk, in list order
+  u.nr = max(0, min(16, rows - u.r0));
+  if (u.nr == 0) return u;
   if (kSparse) {
-    int cnt = a.counts[(int64_t)unit * a.Hkv + kv];
+    int cnt = a.counts[(int64_t)owner * a.Hkv + kv];
     if (cnt < 0 || cnt > a.n_sel) {
-      if (split == 0 && rb == 0 && tid == 0) set_status(status, TS_ERR_INVALID_ARG);
+      set_status(status, TS_ERR_INVALID_ARG);
       cnt = cnt < 0 ? 0 : a.n_sel;
     }
-    list = a.pages + ((int64_t)unit * a.Hkv + kv) * a.n_sel;
-    n_keys = see0 < 0 ? 0 : cnt << b.page_shift;
+    u.list = a.pages + ((int64_t)owner * a.Hkv + kv) * a.n_sel;
+    u.n_keys = u.see0 < 0 ? 0 : cnt << b.page_shift;
   } else {
-    n_keys = max(0, see0 + (r0 + nr - 1) / G + 1);
+    u.n_keys = max(0, u.see0 + (u.r0 + u.nr - 1) / G + 1);
   }
-  const int j0 = (int)imin64((int64_t)split * keys_per_split, n_keys);
-  // the last split takes whatever the host's bound on the lengths left out
-  const int j1 = split == n_split - 1 ? n_keys : (int)imin64((int64_t)j0 + keys_per_split, n_keys);
+  return u;
+}
+
+// Trips a sequence's units take each in the dense form (at least one where
+// there are tokens: rows without a key are written too).
+__device__ __forceinline__ int seq_trips(const SeqSpan& sp) {
+  return sp.ql > 0 ? max(1, (sp.kl + kStep - 1) / kStep) : 0;
+}
+
+// Stretches a line of `total` trips is cut into: all of the grid's CTAs, as far
+// as each gets kMinTrips.
+__device__ __forceinline__ int stretches(long long total) {
+  const long long n = total / kMinTrips;
+  return (int)(n < 1 ? 1 : n < gridDim.x ? n : gridDim.x);
+}
+
+template <typename T, int D, bool kSparse>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_rows_kernel(const PagedBatch b, const RowsArgs a, int n_rb, int unit_trips,
+                  float* __restrict__ part_o, float2* __restrict__ part_ml,
+                  CutUnit* __restrict__ cuts, int32_t* status) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ long long s_sum[kWarps];
+  __shared__ long long s_before;
+  __shared__ int s_first;
+  using R = Ring<D>;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = a.Hq / a.Hkv;
+  const int ps = 1 << b.page_shift;
+  const int c = blockIdx.x;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  // ------------------------------------------------------ this CTA's stretch
+  // Trips [w0, w1) of the line; `owner` (sequence or token), KV head and row
+  // block of its first unit, and the unit's first trip on the line.
+  long long total, w0, w1, unit_at;
+  int C, owner, sub;                           // sub = kv * n_rb + row block
+  const int subs = a.Hkv * n_rb;
+  if (kSparse) {
+    total = (long long)b.n * subs * unit_trips;
+    C = stretches(total);
+    w0 = total * c / C;
+    w1 = total * (c + 1) / C;
+    const long long u = w0 / unit_trips;
+    owner = (int)(u / subs);
+    sub = (int)(u % subs);
+    unit_at = u * unit_trips;
+    if (c == 0)
+      for (int s = tid; s < b.n_seq; s += kThreads)
+        if (seq_span(b, s).bad) set_status(status, TS_ERR_INVALID_ARG);
+  } else {
+    long long mine = 0;
+    for (int s = tid; s < b.n_seq; s += kThreads) {
+      const SeqSpan sp = seq_span(b, s);
+      if (c == 0 && (sp.bad || sp.ql > a.max_q)) set_status(status, TS_ERR_INVALID_ARG);
+      mine += seq_trips(sp);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0) s_sum[warp] = mine;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) total += s_sum[w];
+    total *= subs;
+    C = stretches(total);
+    w0 = total * c / C;
+    w1 = total * (c + 1) / C;
+    // the sequence that holds trip w0: one warp walks the running count
+    if (warp == 0) {
+      long long before = 0;
+      for (int base = 0; base < b.n_seq; base += 32) {
+        const int s = base + lane;
+        const long long t = s < b.n_seq ? (long long)seq_trips(seq_span(b, s)) * subs : 0;
+        long long inc = t;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += x;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, w0 < before + inc && c < C);
+        if (hit) {
+          const int f = __ffs(hit) - 1;
+          if (lane == f) {
+            s_first = s;
+            s_before = before + inc - t;
+          }
+          break;
+        }
+        before += __shfl_sync(0xffffffffu, inc, 31);
+      }
+    }
+    __syncthreads();
+    owner = sub = 0;
+    unit_at = 0;
+    if (c < C && w0 < w1) {
+      owner = s_first;
+      unit_trips = seq_trips(seq_span(b, owner));
+      sub = (int)((w0 - s_before) / unit_trips);
+      unit_at = s_before + (long long)sub * unit_trips;
+    }
+  }
+  if (tid == 0) cuts[c].parts = 0;
+  if (c >= C || w0 >= w1) return;
   const float sl2 = kLog2e / sqrtf((float)D);
 
-  // the two rows of this thread's accumulators
-  const int ra = lane >> 2, rb8 = ra + 8;
-  const int lim_a = ra < nr ? see0 + (r0 + ra) / G : -1;
-  const int lim_b = rb8 < nr ? see0 + (r0 + rb8) / G : -1;
-  // below this key every live row sees everything (rows without a query only
-  // ever feed accumulators that are not written)
-  const int free_to = see0 + r0 / G + 1;
+  // A place on the line: a unit, and the trips [k, k1) of it in this stretch.
+  struct Place {
+    int owner, sub, trips;
+    long long at;          // the unit's first trip on the line
+    Unit u;
+    int k, k1;
+  };
+  auto enter = [&](Place& p) {
+    p.u = make_unit<kSparse>(b, a, p.owner, p.sub / n_rb, p.sub % n_rb, lane, status);
+    p.k = (int)(w0 > p.at ? w0 - p.at : 0);
+    p.k1 = (int)imin64(p.trips, w1 - p.at);
+  };
+  // the next unit of the stretch (false: its end)
+  auto leave = [&](Place& p) -> bool {
+    p.at += p.trips;
+    if (p.at >= w1) return false;
+    if (++p.sub == subs) {
+      p.sub = 0;
+      ++p.owner;
+      if (!kSparse) {
+        // sequences without new tokens take no trips
+        while ((p.trips = seq_trips(seq_span(b, p.owner))) == 0) ++p.owner;
+      }
+    }
+    enter(p);
+    return true;
+  };
 
-  float oacc[D / 8][4];
+  const uint32_t ring = smem_addr(smem) + warp * (kStages * R::kStage);
+  constexpr int kCh = D / 8;                       // 16-byte chunks a row
+  constexpr int kRowsPer = 32 / kCh;               // rows a warp copies at once
+  // A 32-key tile lies in one page, or in two of 16 rows: where they are
+  // (-1: not there) and which pages of the sequence.
+  struct Tile {
+    int64_t ph0, ph1;
+    int lp0, lp1;
+  };
+  auto page_at = [&](const Unit& u, int j, int& logical) -> int64_t {
+    logical = -1;
+    if (j >= u.n_keys) return -1;
+    const int lp = kSparse ? u.list[j >> b.page_shift] : j >> b.page_shift;
+    if (kSparse && (lp < 0 || lp > (u.see0 >> b.page_shift))) {
+      set_status(status, TS_ERR_INVALID_ARG);
+      return -1;
+    }
+    const int64_t ph = b.table[(int64_t)u.s * b.max_pages + lp];
+    if (ph < 0 || ph >= b.n_pages) {
+      set_status(status, TS_ERR_INVALID_ARG);
+      return -1;
+    }
+    logical = lp;
+    return ph;
+  };
+  auto look = [&](const Unit& u, int k) {
+    Tile t;
+    const int j = k * kStep + warp * kTileKeys;
+    t.ph0 = page_at(u, j, t.lp0);
+    t.ph1 = t.ph0;
+    t.lp1 = t.lp0;
+    if (b.page_shift == 4) t.ph1 = page_at(u, j + 16, t.lp1);
+    return t;
+  };
+  // a lane copies 16-byte chunk lane % kCh of rows lane / kCh + x * kRowsPer;
+  // within a page its addresses are one base and constant steps
+  const uint32_t lane_bytes = (lane / kCh) * (D * 2) + (lane % kCh) * 16;
+  const char* kbase = static_cast<const char*>(a.k_pages) + lane_bytes;
+  const char* vbase = static_cast<const char*>(a.v_pages) + lane_bytes;
+  const int64_t page_bytes = (int64_t)a.Hkv * ps * (D * 2);
+  auto fetch = [&](const Unit& u, int k, const Tile& t, uint32_t stage) {
+    const int j = k * kStep + warp * kTileKeys;
+    const uint32_t st = ring + stage * R::kStage;
+    const int in_page = j & (ps - 1);
+    const int64_t head_bytes = (int64_t)u.kv * ps * (D * 2);
+    // rows behind the last visible one are filled with zeros: whatever their
+    // page holds there must not reach P.V
+    int live0 = t.ph0 < 0 ? 0 : u.n_keys - j, live1 = t.ph1 < 0 ? 0 : u.n_keys - j;
+    if (kSparse) {
+      live0 = min(live0, u.see0 + 1 - (t.lp0 << b.page_shift) - in_page);
+      live1 = min(live1, u.see0 + 1 - (t.lp1 << b.page_shift) - in_page +
+                             (b.page_shift == 4 ? 16 : 0));
+    }
+    const int64_t o0 = imax64(t.ph0, 0) * page_bytes + head_bytes + in_page * (D * 2);
+    // rows 16.. of the tile: the next 16 of the page, or the second page's
+    const int64_t o1 =
+        b.page_shift == 4 ? imax64(t.ph1, 0) * page_bytes + head_bytes - 16 * (D * 2) : o0;
+    const int r0l = lane / kCh;
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-    for (int x = 0; x < 4; ++x) oacc[i][x] = 0.f;
-  float ma = -INFINITY, mb = -INFINITY, la = 0.f, lb = 0.f;
+    for (int x = 0; x < kTileKeys / kRowsPer; ++x) {
+      const int r = x * kRowsPer + r0l;
+      const bool second = x * kRowsPer >= 16;
+      const bool live = r < (second ? live1 : live0);
+      // a row that is not read still needs a valid address
+      const int64_t off = (second ? o1 : o0) + x * (kRowsPer * D * 2);
+      const int64_t at = live ? off : -(int64_t)lane_bytes;
+      const uint32_t dst = chunk_off<D>(r, lane % kCh);
+      cp16(st + dst, kbase + at, live);
+      cp16(st + R::kTile + dst, vbase + at, live);
+    }
+  };
 
-  if (j0 < j1) {
+  // The copies run kStages - 1 trips ahead of the products, on their own place;
+  // the pages of the trip behind them are looked up one trip earlier still.
+  Place ahead{owner, sub, unit_trips, unit_at, {}, 0, 0};
+  enter(ahead);
+  Place now = ahead;
+  bool more = true;
+  Tile held[kStages];           // tiles whose copies are on their way, oldest first
+  Tile next = look(ahead.u, ahead.k);
+  uint32_t put = 0, got = 0;    // trips copied, trips used
+  auto push = [&](Tile& into) {
+    if (more) {
+      into = next;
+      fetch(ahead.u, ahead.k, next, put % kStages);
+      ++put;
+      if (++ahead.k == ahead.k1) more = leave(ahead);
+      if (more) next = look(ahead.u, ahead.k);
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) push(held[i]);
+
+  const int ra = lane >> 2, rb8 = ra + 8;      // the rows of this thread's accumulators
+  float* so = reinterpret_cast<float*>(smem + R::kStates);          // [warp][16][D]
+  float2* sml = reinterpret_cast<float2*>(so + kWarps * 16 * D);    // [warp][16]
+  while (true) {
+    const Unit& u = now.u;
+    const int lim_a = ra < u.nr ? u.see0 + (u.r0 + ra) / G : -1;
+    const int lim_b = rb8 < u.nr ? u.see0 + (u.r0 + rb8) / G : -1;
+    // below this key every live row sees everything (rows without a query only
+    // ever feed accumulators that are not written)
+    const int free_to = u.see0 + u.r0 / G + 1;
+    float oacc[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) oacc[i][x] = 0.f;
+    float ma = -INFINITY, mb = -INFINITY, la = 0.f, lb = 0.f;
     // query fragments (16 x 16 blocks), straight from global memory
     uint32_t qf[D / 16][4];
     {
       auto row_ptr = [&](int r) {
-        const int RR = r0 + min(r, nr - 1);
+        const int RR = u.r0 + max(0, min(r, u.nr - 1));
         return reinterpret_cast<const uint32_t*>(
-            static_cast<const T*>(a.q) + ((int64_t)(tok0 + RR / G) * a.Hq + kv * G + RR % G) * D);
+            static_cast<const T*>(a.q) + ((int64_t)(u.tok0 + RR / G) * a.Hq + u.kv * G + RR % G) * D);
       };
       const uint32_t* pa = row_ptr(ra);
       const uint32_t* pb = row_ptr(rb8);
@@ -172,104 +403,17 @@ paged_rows_kernel(const PagedBatch b, const RowsArgs a, int n_rb, int n_split, i
         qf[ks][3] = pb[ks * 8 + 4 + (lane & 3)];
       }
     }
-    const uint32_t ring = smem_addr(smem) + warp * (kStages * R::kStage);
-    const int n_tiles = (j1 - j0 + kStep - 1) / kStep;
-    const int32_t* trow = b.table + (int64_t)s * b.max_pages;
-    // page of list position j: logical page and where its rows start (-1: none)
-    auto page_at = [&](int j, int& logical) -> int64_t {
-      logical = -1;
-      if (j >= j1) return -1;
-      const int lp = kSparse ? list[j >> b.page_shift] : j >> b.page_shift;
-      if (kSparse && (lp < 0 || lp > (see0 >> b.page_shift))) {
-        set_status(status, TS_ERR_INVALID_ARG);
-        return -1;
-      }
-      const int64_t ph = trow[lp];
-      if (ph < 0 || ph >= b.n_pages) {
-        set_status(status, TS_ERR_INVALID_ARG);
-        return -1;
-      }
-      logical = lp;
-      return ph;
-    };
-    // A 32-key tile lies in one page, or in two of 16 rows.
-    struct Tile {
-      int64_t ph0, ph1;
-      int lp0, lp1;
-    };
-    auto look = [&](int i) {
-      Tile t;
-      const int j = j0 + i * kStep + warp * kTileKeys;
-      t.ph0 = page_at(j, t.lp0);
-      t.ph1 = t.ph0;
-      t.lp1 = t.lp0;
-      if (b.page_shift == 4) t.ph1 = page_at(j + 16, t.lp1);
-      return t;
-    };
-    constexpr int kCh = D / 8;                       // 16-byte chunks a row
-    constexpr int kRowsPer = 32 / kCh;               // rows a warp copies at once
-    // a lane copies 16-byte chunk lane % kCh of rows lane / kCh + x * kRowsPer;
-    // within a page its addresses are one base and constant steps
-    const uint32_t lane_bytes = (lane / kCh) * (D * 2) + (lane % kCh) * 16;
-    const char* kbase = static_cast<const char*>(a.k_pages) + lane_bytes;
-    const char* vbase = static_cast<const char*>(a.v_pages) + lane_bytes;
-    const int64_t page_bytes = (int64_t)a.Hkv * ps * (D * 2);
-    const int64_t head_bytes = (int64_t)kv * ps * (D * 2);
-    auto fetch = [&](int i, const Tile& t) {
-      if (i < n_tiles) {
-        const int j = j0 + i * kStep + warp * kTileKeys;
-        const uint32_t st = ring + (i % kStages) * R::kStage;
-        const int in_page = j & (ps - 1);
-        // rows behind the last visible one are filled with zeros: whatever
-        // their page holds there must not reach P.V
-        int live0 = t.ph0 < 0 ? 0 : j1 - j, live1 = t.ph1 < 0 ? 0 : j1 - j;
-        if (kSparse) {
-          live0 = min(live0, see0 + 1 - (t.lp0 << b.page_shift) - in_page);
-          live1 = min(live1, see0 + 1 - (t.lp1 << b.page_shift) - in_page +
-                                 (b.page_shift == 4 ? 16 : 0));
-        }
-        const int64_t o0 = max(t.ph0, (int64_t)0) * page_bytes + head_bytes + in_page * (D * 2);
-        // rows 16.. of the tile: the next 16 of the page, or the second page's
-        const int64_t o1 = b.page_shift == 4
-                               ? max(t.ph1, (int64_t)0) * page_bytes + head_bytes - 16 * (D * 2)
-                               : o0;
-        const int r0l = lane / kCh;
-#pragma unroll
-        for (int x = 0; x < kTileKeys / kRowsPer; ++x) {
-          const int r = x * kRowsPer + r0l;
-          const bool second = x * kRowsPer >= 16;
-          const bool live = r < (second ? live1 : live0);
-          // a row that is not read still needs a valid address
-          const int64_t off = (second ? o1 : o0) + x * (kRowsPer * D * 2);
-          const int64_t at = live ? off : -(int64_t)lane_bytes;
-          const uint32_t dst = chunk_off<D>(r, lane % kCh);
-          cp16(st + dst, kbase + at, live);
-          cp16(st + R::kTile + dst, vbase + at, live);
-        }
-      }
-      cp_commit();
-    };
-    // tiles in flight, and the logical pages of the tile in hand
-    Tile ahead[kStages];
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
-      ahead[i] = look(i);
-      fetch(i, ahead[i]);
-    }
-    Tile next = look(kStages - 1);
-    for (int i = 0; i < n_tiles; ++i) {
-      const Tile cur = ahead[0];
+    for (; now.k < now.k1; ++now.k, ++got) {
       __syncwarp();                       // every lane is done with the stage refilled now
-      fetch(i + kStages - 1, next);
+      push(held[kStages - 1]);
+      const Tile cur = held[0];
 #pragma unroll
-      for (int x = 0; x + 2 < kStages; ++x) ahead[x] = ahead[x + 1];
-      ahead[kStages - 2] = next;
-      next = look(i + kStages);
+      for (int x = 0; x + 1 < kStages; ++x) held[x] = held[x + 1];
       cp_wait<kStages - 1>();
       __syncwarp();
-      const int j = j0 + i * kStep + warp * kTileKeys;
-      if (j >= j1) continue;              // this warp's share of the last trip is empty
-      const uint32_t kt = ring + (i % kStages) * R::kStage, vt = kt + R::kTile;
+      const int j = now.k * kStep + warp * kTileKeys;
+      if (j >= u.n_keys) continue;        // nothing of this trip is this warp's
+      const uint32_t kt = ring + (got % kStages) * R::kStage, vt = kt + R::kTile;
       // S = Q K^T: 16 rows x 32 keys
       float c[4][4];
 #pragma unroll
@@ -290,14 +434,14 @@ paged_rows_kernel(const PagedBatch b, const RowsArgs a, int n_rb, int n_split, i
       // in a page that could not be read
       const bool bad = cur.ph0 < 0 || cur.ph1 < 0;
       const int top = kSparse ? (max(cur.lp0, cur.lp1) << b.page_shift) + ps : j + kTileKeys;
-      if (bad || top > free_to || j + kTileKeys > j1) {
+      if (bad || top > free_to || j + kTileKeys > u.n_keys) {
 #pragma unroll
         for (int nb = 0; nb < 4; ++nb)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const int r = nb * 8 + (lane & 3) * 2 + x;
             int key = j + r;
-            bool none = key >= j1 || (nb < 2 ? cur.ph0 : cur.ph1) < 0;
+            const bool none = key >= u.n_keys || (nb < 2 ? cur.ph0 : cur.ph1) < 0;
             if (kSparse) key = ((nb < 2 ? cur.lp0 : cur.lp1) << b.page_shift) + (key & (ps - 1));
             if (none || key > lim_a) c[nb][x] = -INFINITY;
             if (none || key > lim_b) c[nb][2 + x] = -INFINITY;
@@ -365,185 +509,158 @@ paged_rows_kernel(const PagedBatch b, const RowsArgs a, int n_rb, int n_split, i
         }
       }
     }
-    cp_wait<0>();
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
       la += __shfl_xor_sync(0xffffffffu, la, o);
       lb += __shfl_xor_sync(0xffffffffu, lb, o);
     }
-  }
-
-  // ---------------------------------------------------------- join the warps
-  __syncthreads();
-  float* so = reinterpret_cast<float*>(smem);                       // [warp][16][D]
-  float2* sml = reinterpret_cast<float2*>(so + kWarps * 16 * D);    // [warp][16]
-  static_assert(kWarps * 16 * (D + 2) * 4 <= R::kBytes, "the states must fit the ring");
+    // -------------------------------------------------------- join the warps
 #pragma unroll
-  for (int n = 0; n < D / 8; ++n) {
-    const int col = n * 8 + (lane & 3) * 2;
-    *reinterpret_cast<float2*>(so + (warp * 16 + ra) * D + col) = make_float2(oacc[n][0], oacc[n][1]);
-    *reinterpret_cast<float2*>(so + (warp * 16 + rb8) * D + col) = make_float2(oacc[n][2], oacc[n][3]);
-  }
-  if ((lane & 3) == 0) {
-    sml[warp * 16 + ra] = make_float2(ma, la);
-    sml[warp * 16 + rb8] = make_float2(mb, lb);
-  }
-  __syncthreads();
-  constexpr int kQuads = D / 4;
-  for (int e = tid; e < nr * kQuads; e += kThreads) {
-    const int r = e / kQuads, c4 = e % kQuads;
-    float m = -INFINITY;
+    for (int n = 0; n < D / 8; ++n) {
+      const int col = n * 8 + (lane & 3) * 2;
+      *reinterpret_cast<float2*>(so + (warp * 16 + ra) * D + col) = make_float2(oacc[n][0], oacc[n][1]);
+      *reinterpret_cast<float2*>(so + (warp * 16 + rb8) * D + col) = make_float2(oacc[n][2], oacc[n][3]);
+    }
+    if ((lane & 3) == 0) {
+      sml[warp * 16 + ra] = make_float2(ma, la);
+      sml[warp * 16 + rb8] = make_float2(mb, lb);
+    }
+    __syncthreads();
+    const bool starts = now.at >= w0, ends = now.at + now.trips <= w1;
+    // a part that does not hold the unit's first trip takes the stretch's slot
+    // 0, one that does slot 1; the latter's stretch says what is to be joined
+    const int64_t slot = (int64_t)c * 2 + (starts ? 1 : 0);
+    constexpr int kQuads = D / 4;
+    for (int e = tid; e < u.nr * kQuads; e += kThreads) {
+      const int r = e / kQuads, c4 = e % kQuads;
+      float m = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sml[w * 16 + r].x);
-    float l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (m != -INFINITY) {
+      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sml[w * 16 + r].x);
+      float l = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (m != -INFINITY) {
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float2 x = sml[w * 16 + r];
-        const float f = ex2(x.x - m);
-        const float4 v = *reinterpret_cast<const float4*>(so + (w * 16 + r) * D + c4 * 4);
-        l += f * x.y;
-        acc.x += f * v.x;
-        acc.y += f * v.y;
-        acc.z += f * v.z;
-        acc.w += f * v.w;
+        for (int w = 0; w < kWarps; ++w) {
+          const float2 x = sml[w * 16 + r];
+          const float f = ex2(x.x - m);
+          const float4 v = *reinterpret_cast<const float4*>(so + (w * 16 + r) * D + c4 * 4);
+          l += f * x.y;
+          acc.x += f * v.x;
+          acc.y += f * v.y;
+          acc.z += f * v.z;
+          acc.w += f * v.w;
+        }
+      }
+      if (starts && ends) {
+        const int RR = u.r0 + r;
+        const int64_t row = (int64_t)(u.tok0 + RR / G) * a.Hq + u.kv * G + RR % G;
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + row * D + c4 * 4) =
+            make_uint2(Pair<T>::pack(acc.x * inv, acc.y * inv), Pair<T>::pack(acc.z * inv, acc.w * inv));
+        if (a.lse && c4 == 0) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+      } else {
+        *reinterpret_cast<float4*>(part_o + (slot * 16 + r) * D + c4 * 4) = acc;
+        if (c4 == 0) part_ml[slot * 16 + r] = make_float2(m, l);
       }
     }
-    const int RR = r0 + r;
-    const int64_t row = (int64_t)(tok0 + RR / G) * a.Hq + kv * G + RR % G;
-    if (n_split == 1) {
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + row * D + c4 * 4) =
-          make_uint2(Pair<T>::pack(acc.x * inv, acc.y * inv), Pair<T>::pack(acc.z * inv, acc.w * inv));
-      if (a.lse && c4 == 0) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
-    } else {
-      const int64_t at = row * n_split + split;
-      if (l > 0.f) *reinterpret_cast<float4*>(part_o + at * D + c4 * 4) = acc;
-      if (c4 == 0) part_ml[at] = make_float2(m, l);
+    if (tid == 0 && starts && !ends && u.nr > 0) {
+      CutUnit x{};
+      x.tok0 = u.tok0;
+      x.kv = u.kv;
+      x.r0 = u.r0;
+      x.nr = u.nr;
+      // the stretch that holds the unit's last trip z: the last whose start is
+      // at or before z
+      const long long z = now.at + now.trips - 1;
+      int q = (int)((z * C) / total);
+      while (q + 1 < C && total * (q + 1) / C <= z) ++q;
+      while (total * q / C > z) --q;
+      x.parts = q - c + 1;
+      cuts[c] = x;
     }
+    if (!leave(now)) break;
+    __syncthreads();                      // the states are read before the next unit's
   }
+  cp_wait<0>();
 }
 
-// Joins the splits of every row: a warp a row, each lane D/32 columns.  The
-// lanes hold one split's weight each; the loads of O do not wait for one
-// another.
+// Joins cut units: CTA c the one that stretch c starts and does not end.  Four
+// columns of a row a thread; the loads of O do not wait for one another.
 template <typename T, int D>
-__global__ void __launch_bounds__(128)
-paged_rows_merge(const PagedBatch b, const float* __restrict__ part_o,
-                 const float2* __restrict__ part_ml, int Hq, int n_split, int max_q, T* o,
-                 float* lse) {
+__global__ void __launch_bounds__(512)
+paged_rows_merge(const CutUnit* __restrict__ cuts, const float* __restrict__ part_o,
+                 const float2* __restrict__ part_ml, int Hq, int Hkv, T* o, float* lse) {
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int t = (int)(row / Hq);
-  if (t >= b.n) return;
-  const float2* ml = part_ml + row * n_split;
-  const float2 first = lane < n_split ? ml[lane] : make_float2(-INFINITY, 0.f);
-  const int s = warp_find_seq(b, t, lane);
-  if (s < 0) return;
-  if (max_q > 0 && t - seq_span(b, s).q0 >= max_q) return;   // no partials were made
-  float m = first.x;
-  for (int i = lane + 32; i < n_split; i += 32) m = fmaxf(m, ml[i].x);
-  m = warp_max(m);
-  constexpr int kPer = D / 32;
-  float acc[kPer], l = 0.f;
-#pragma unroll
-  for (int x = 0; x < kPer; ++x) acc[x] = 0.f;
-  if (m != -INFINITY) {
-    const float* po = part_o + row * n_split * D + lane * kPer;
-    for (int base = 0; base < n_split; base += 32) {
-      const float2 x = base == 0 ? first
-                                 : base + lane < n_split ? ml[base + lane] : make_float2(-INFINITY, 0.f);
-      const float w = x.y > 0.f ? exp2f(x.x - m) : 0.f;      // an empty split left no O
-      l += w * x.y;
-      const int n = min(32, n_split - base);
+  const int c = blockIdx.x, G = Hq / Hkv;
+  const CutUnit x = cuts[c];
+  constexpr int kQuads = D / 4;
+  if (x.parts == 0 || threadIdx.x >= x.nr * kQuads) return;
+  const int r = threadIdx.x / kQuads, c4 = threadIdx.x % kQuads;
+  // part i: stretch c's slot 1, then slot 0 of the stretches behind it
+  auto at = [&](int i) { return ((int64_t)(i == 0 ? 2 * c + 1 : 2 * (c + i))) * 16 + r; };
+  float m = -INFINITY;
 #pragma unroll 8
-      for (int i = 0; i < n; ++i) {
-        const float f = __shfl_sync(0xffffffffu, w, i);
-        float v[kPer];
-#pragma unroll
-        for (int y = 0; y < kPer; ++y) v[y] = 0.f;
-        if (f > 0.f) {
-          if (kPer == 4) {
-            const float4 u = *reinterpret_cast<const float4*>(po + (int64_t)(base + i) * D);
-            v[0] = u.x;
-            v[1] = u.y;
-            v[2 % kPer] = u.z;
-            v[3 % kPer] = u.w;
-          } else {
-            const float2 u = *reinterpret_cast<const float2*>(po + (int64_t)(base + i) * D);
-            v[0] = u.x;
-            v[1] = u.y;
-          }
-        }
-#pragma unroll
-        for (int y = 0; y < kPer; ++y) acc[y] += f * v[y];
-      }
+  for (int i = 0; i < x.parts; ++i) m = fmaxf(m, part_ml[at(i)].x);
+  float l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (m != -INFINITY) {
+#pragma unroll 8
+    for (int i = 0; i < x.parts; ++i) {
+      const float2 ml = part_ml[at(i)];
+      const float4 v = *reinterpret_cast<const float4*>(part_o + at(i) * D + c4 * 4);
+      const float f = exp2f(ml.x - m);              // 0 for a part without a key
+      l += f * ml.y;
+      acc.x += f * v.x;
+      acc.y += f * v.y;
+      acc.z += f * v.z;
+      acc.w += f * v.w;
     }
   }
-  l = warp_sum(l);
+  const int RR = x.r0 + r;
+  const int64_t row = (int64_t)(x.tok0 + RR / G) * Hq + x.kv * G + RR % G;
   const float inv = l > 0.f ? 1.f / l : 0.f;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(o + row * D + lane * kPer);
-#pragma unroll
-  for (int x = 0; x < kPer / 2; ++x) dst[x] = Pair<T>::pack(acc[2 * x] * inv, acc[2 * x + 1] * inv);
-  if (lse && lane == 0) lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  *reinterpret_cast<uint2*>(o + row * D + c4 * 4) =
+      make_uint2(Pair<T>::pack(acc.x * inv, acc.y * inv), Pair<T>::pack(acc.z * inv, acc.w * inv));
+  if (lse && c4 == 0) lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
 }  // namespace
 
-// units x 16-row blocks x splits CTAs, one a SM (their rings fill its shared
-// memory): the split count that minimises waves x (trips + a fixed cost).
-RowsPlan rows_plan(int64_t units, int n, int Hq, int rows, int d, int64_t max_keys) {
-  constexpr double kFixedTrips = 6.0;  // ~2 us
+// One CTA a SM (the rings fill its shared memory), fewer where a stretch would
+// fall below kMinTrips trips of 128 keys.
+RowsPlan rows_plan(int64_t units, int rows, int d, int64_t max_keys) {
   RowsPlan p{};
   p.n_rb = (rows + 15) / 16;
-  const int64_t base = units * p.n_rb;
-  const int64_t trips = imax64(1, (max_keys + kStep - 1) / kStep);
-  double best = 1e300;
-  int64_t best_per = trips;
-  for (int64_t ns = 1; ns <= imin64(trips, 256); ++ns) {
-    const int64_t per = (trips + ns - 1) / ns;
-    const int64_t used = (trips + per - 1) / per;
-    const int64_t waves = (base * used + kCtas * kGb300Sms - 1) / (kCtas * kGb300Sms);
-    const double cost = (double)waves * ((double)per + kFixedTrips);
-    if (cost < best - 1e-9) {
-      best = cost;
-      best_per = per;
-    }
-  }
-  p.keys_per_split = (int)(best_per * kStep);
-  p.n_split = (int)((trips + best_per - 1) / best_per);
-  if (p.n_split > 1) {
-    p.part_bytes = align_up((size_t)n * Hq * p.n_split * d * sizeof(float), 256);
-    p.ml_bytes = align_up((size_t)n * Hq * p.n_split * sizeof(float2), 256);
-  }
-  p.ws_bytes = p.part_bytes + p.ml_bytes;
+  p.unit_trips = (int)imax64(1, (max_keys + kStep - 1) / kStep);
+  const int64_t trips = units * p.n_rb * p.unit_trips;
+  p.grid = (int)imax64(1, imin64(kGb300Sms, trips / kMinTrips));
+  p.cuts_bytes = align_up((size_t)p.grid * sizeof(CutUnit), 256);
+  p.part_bytes = (size_t)p.grid * 2 * 16 * d * sizeof(float);
+  p.ws_bytes = p.cuts_bytes + p.part_bytes + align_up((size_t)p.grid * 2 * 16 * sizeof(float2), 256);
   return p;
 }
 
 template <typename T, int D>
 static int go_rows(const PagedBatch& b, const RowsArgs& a, const RowsPlan& p, void* ws,
                    int32_t* status, cudaStream_t st) {
-  float* part_o = static_cast<float*>(ws);
-  float2* part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + p.part_bytes);
+  char* w = static_cast<char*>(ws);
+  CutUnit* cuts = reinterpret_cast<CutUnit*>(w);
+  float* part_o = reinterpret_cast<float*>(w + p.cuts_bytes);
+  float2* part_ml = reinterpret_cast<float2*>(w + p.cuts_bytes + p.part_bytes);
   const bool sparse = a.pages != nullptr;
-  const int units = sparse ? b.n : b.n_seq;
   auto kern = sparse ? paged_rows_kernel<T, D, true> : paged_rows_kernel<T, D, false>;
   cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<D>::kBytes);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  pdl_config(&cfg, attr, dim3((unsigned)units * p.n_split, a.Hkv * p.n_rb), dim3(kThreads),
-             Ring<D>::kBytes, st);
-  cudaLaunchKernelEx(&cfg, kern, b, a, p.n_rb, p.n_split, p.keys_per_split, part_o, part_ml,
-                     status);
+  pdl_config(&cfg, attr, dim3(p.grid), dim3(kThreads), Ring<D>::kBytes, st);
+  cudaLaunchKernelEx(&cfg, kern, b, a, p.n_rb, p.unit_trips, part_o, part_ml, cuts, status);
   int rc = launch_status("paged_rows_kernel");
-  if (rc || p.n_split == 1) return rc;
-  const int64_t rows = (int64_t)b.n * a.Hq;
-  pdl_config(&cfg, attr, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, st);
-  cudaLaunchKernelEx(&cfg, paged_rows_merge<T, D>, b, (const float*)part_o, (const float2*)part_ml,
-                     a.Hq, p.n_split, sparse ? 0 : a.max_q, static_cast<T*>(a.o), a.lse);
+  // sparse units are cut by the host's numbers: none where the CTAs divide them
+  if (rc || p.grid == 1 || (sparse && (int64_t)b.n * a.Hkv * p.n_rb % p.grid == 0)) return rc;
+  pdl_config(&cfg, attr, dim3(p.grid), dim3(16 * (D / 4)), 0, st);
+  cudaLaunchKernelEx(&cfg, paged_rows_merge<T, D>, (const CutUnit*)cuts, (const float*)part_o,
+                     (const float2*)part_ml, a.Hq, a.Hkv, static_cast<T*>(a.o), a.lse);
   return launch_status("paged_rows_merge");
 }
 
