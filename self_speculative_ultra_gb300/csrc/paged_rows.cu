@@ -31,7 +31,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTileKeys = 32;              // keys of a warp's tile
 constexpr int kStep = kWarps * kTileKeys;  // keys a CTA takes per trip
-constexpr int kStages = 3;
+constexpr int kStages = 2;
 constexpr int kMinTrips = 2;               // trips a CTA takes at least
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -278,36 +278,68 @@ paged_rows_kernel(const PagedBatch b, const RowsArgs a, int n_rb, int unit_trips
   const uint32_t ring = smem_addr(smem) + warp * (kStages * R::kStage);
   constexpr int kCh = D / 8;                       // 16-byte chunks a row
   constexpr int kRowsPer = 32 / kCh;               // rows a warp copies at once
-  // A 32-key tile lies in one page, or in two of 16 rows: where they are
-  // (-1: not there) and which pages of the sequence.
-  struct Tile {
-    int64_t ph0, ph1;
-    int lp0, lp1;
+  // The pages a unit walks, 32 at a time, one a lane: `lp` in the sequence, `ph`
+  // in the pool (-1: not there).  The window behind is on its way meanwhile:
+  // its list entries are asked for when a window begins, its table entries one
+  // trip later, and neither is looked at before it is needed.
+  struct Pages {
+    int lp, ph, lp2, ph2;
+    int base;               // first page of the window
+    bool half;              // lp2 asked for, ph2 not yet
+  } pg;
+  auto ask_lp = [&](const Unit& u, int base) -> int {
+    const int i = base + lane;
+    if (i >= (u.n_keys + ps - 1) >> b.page_shift) return -1;
+    return kSparse ? u.list[i] : i;
   };
-  auto page_at = [&](const Unit& u, int j, int& logical) -> int64_t {
-    logical = -1;
-    if (j >= u.n_keys) return -1;
-    const int lp = kSparse ? u.list[j >> b.page_shift] : j >> b.page_shift;
-    if (kSparse && (lp < 0 || lp > (u.see0 >> b.page_shift))) {
+  auto seen_lp = [&](const Unit& u, int base, int lp) -> int {
+    // in the sparse form a listed page may lie anywhere
+    if (kSparse && base + lane < (u.n_keys + ps - 1) >> b.page_shift &&
+        (lp < 0 || lp > (u.see0 >> b.page_shift))) {
       set_status(status, TS_ERR_INVALID_ARG);
       return -1;
     }
-    const int64_t ph = b.table[(int64_t)u.s * b.max_pages + lp];
-    if (ph < 0 || ph >= b.n_pages) {
+    return lp;
+  };
+  auto ask_ph = [&](const Unit& u, int lp) -> int {
+    return lp < 0 ? -1 : b.table[(int64_t)u.s * b.max_pages + lp];
+  };
+  auto seen_ph = [&](int lp, int ph) -> int {
+    if (lp >= 0 && (ph < 0 || ph >= b.n_pages)) {
       set_status(status, TS_ERR_INVALID_ARG);
       return -1;
     }
-    logical = lp;
     return ph;
   };
-  auto look = [&](const Unit& u, int k) {
-    Tile t;
-    const int j = k * kStep + warp * kTileKeys;
-    t.ph0 = page_at(u, j, t.lp0);
-    t.ph1 = t.ph0;
-    t.lp1 = t.lp0;
-    if (b.page_shift == 4) t.ph1 = page_at(u, j + 16, t.lp1);
-    return t;
+  auto window_at = [&](const Unit& u, int k) { return (k * kStep >> b.page_shift) & ~31; };
+  auto open_pages = [&](const Unit& u, int k) {
+    pg.base = window_at(u, k);
+    pg.lp = seen_lp(u, pg.base, ask_lp(u, pg.base));
+    pg.lp2 = ask_lp(u, pg.base + 32);
+    pg.ph = seen_ph(pg.lp, ask_ph(u, pg.lp));
+    pg.half = true;
+  };
+  auto second_half = [&](const Unit& u) {
+    pg.lp2 = seen_lp(u, pg.base + 32, pg.lp2);
+    pg.ph2 = ask_ph(u, pg.lp2);
+    pg.half = false;
+  };
+  // the window of trip k (the trips of a unit come in order)
+  auto pages_for = [&](const Unit& u, int k) {
+    if (window_at(u, k) != pg.base) {
+      if (pg.half) second_half(u);
+      pg.base += 32;
+      pg.lp = pg.lp2;
+      pg.ph = seen_ph(pg.lp2, pg.ph2);
+      pg.lp2 = ask_lp(u, pg.base + 32);
+      pg.half = true;
+    } else if (pg.half) {
+      second_half(u);
+    }
+  };
+  // A warp's 32-key tile lies in one page, or in two of 16 rows.
+  struct Tile {
+    int lp0, lp1;           // pages in the sequence; -1: not readable
   };
   // a lane copies 16-byte chunk lane % kCh of rows lane / kCh + x * kRowsPer;
   // within a page its addresses are one base and constant steps
@@ -315,23 +347,32 @@ paged_rows_kernel(const PagedBatch b, const RowsArgs a, int n_rb, int unit_trips
   const char* kbase = static_cast<const char*>(a.k_pages) + lane_bytes;
   const char* vbase = static_cast<const char*>(a.v_pages) + lane_bytes;
   const int64_t page_bytes = (int64_t)a.Hkv * ps * (D * 2);
-  auto fetch = [&](const Unit& u, int k, const Tile& t, uint32_t stage) {
+  auto fetch = [&](const Unit& u, int k, uint32_t stage) -> Tile {
     const int j = k * kStep + warp * kTileKeys;
+    const int src = (j >> b.page_shift) - pg.base;
+    const int two = b.page_shift == 4 ? src + 1 : src;
+    const int ph0 = __shfl_sync(0xffffffffu, pg.ph, src);
+    const int ph1 = __shfl_sync(0xffffffffu, pg.ph, two & 31);
+    Tile t;
+    t.lp0 = __shfl_sync(0xffffffffu, pg.lp, src);
+    t.lp1 = __shfl_sync(0xffffffffu, pg.lp, two & 31);
+    if (ph0 < 0) t.lp0 = -1;
+    if (ph1 < 0) t.lp1 = -1;
     const uint32_t st = ring + stage * R::kStage;
     const int in_page = j & (ps - 1);
     const int64_t head_bytes = (int64_t)u.kv * ps * (D * 2);
     // rows behind the last visible one are filled with zeros: whatever their
     // page holds there must not reach P.V
-    int live0 = t.ph0 < 0 ? 0 : u.n_keys - j, live1 = t.ph1 < 0 ? 0 : u.n_keys - j;
+    int live0 = t.lp0 < 0 ? 0 : u.n_keys - j, live1 = t.lp1 < 0 ? 0 : u.n_keys - j;
     if (kSparse) {
       live0 = min(live0, u.see0 + 1 - (t.lp0 << b.page_shift) - in_page);
       live1 = min(live1, u.see0 + 1 - (t.lp1 << b.page_shift) - in_page +
                              (b.page_shift == 4 ? 16 : 0));
     }
-    const int64_t o0 = imax64(t.ph0, 0) * page_bytes + head_bytes + in_page * (D * 2);
+    const int64_t o0 = (int64_t)max(ph0, 0) * page_bytes + head_bytes + in_page * (D * 2);
     // rows 16.. of the tile: the next 16 of the page, or the second page's
     const int64_t o1 =
-        b.page_shift == 4 ? imax64(t.ph1, 0) * page_bytes + head_bytes - 16 * (D * 2) : o0;
+        b.page_shift == 4 ? (int64_t)max(ph1, 0) * page_bytes + head_bytes - 16 * (D * 2) : o0;
     const int r0l = lane / kCh;
 #pragma unroll
     for (int x = 0; x < kTileKeys / kRowsPer; ++x) {
@@ -345,24 +386,26 @@ paged_rows_kernel(const PagedBatch b, const RowsArgs a, int n_rb, int unit_trips
       cp16(st + dst, kbase + at, live);
       cp16(st + R::kTile + dst, vbase + at, live);
     }
+    return t;
   };
 
-  // The copies run kStages - 1 trips ahead of the products, on their own place;
-  // the pages of the trip behind them are looked up one trip earlier still.
+  // The copies run kStages - 1 trips ahead of the products, on their own place.
   Place ahead{owner, sub, unit_trips, unit_at, {}, 0, 0};
   enter(ahead);
   Place now = ahead;
   bool more = true;
   Tile held[kStages];           // tiles whose copies are on their way, oldest first
-  Tile next = look(ahead.u, ahead.k);
+  open_pages(ahead.u, ahead.k);
   uint32_t put = 0, got = 0;    // trips copied, trips used
   auto push = [&](Tile& into) {
     if (more) {
-      into = next;
-      fetch(ahead.u, ahead.k, next, put % kStages);
+      pages_for(ahead.u, ahead.k);
+      into = fetch(ahead.u, ahead.k, put % kStages);
       ++put;
-      if (++ahead.k == ahead.k1) more = leave(ahead);
-      if (more) next = look(ahead.u, ahead.k);
+      if (++ahead.k == ahead.k1) {
+        more = leave(ahead);
+        if (more) open_pages(ahead.u, ahead.k);
+      }
     }
     cp_commit();
   };
@@ -432,7 +475,7 @@ paged_rows_kernel(const PagedBatch b, const RowsArgs a, int n_rb, int unit_trips
         }
       // keys a row does not see: behind its own position, behind the range, or
       // in a page that could not be read
-      const bool bad = cur.ph0 < 0 || cur.ph1 < 0;
+      const bool bad = cur.lp0 < 0 || cur.lp1 < 0;
       const int top = kSparse ? (max(cur.lp0, cur.lp1) << b.page_shift) + ps : j + kTileKeys;
       if (bad || top > free_to || j + kTileKeys > u.n_keys) {
 #pragma unroll
@@ -441,7 +484,7 @@ paged_rows_kernel(const PagedBatch b, const RowsArgs a, int n_rb, int unit_trips
           for (int x = 0; x < 2; ++x) {
             const int r = nb * 8 + (lane & 3) * 2 + x;
             int key = j + r;
-            const bool none = key >= u.n_keys || (nb < 2 ? cur.ph0 : cur.ph1) < 0;
+            const bool none = key >= u.n_keys || (nb < 2 ? cur.lp0 : cur.lp1) < 0;
             if (kSparse) key = ((nb < 2 ? cur.lp0 : cur.lp1) << b.page_shift) + (key & (ps - 1));
             if (none || key > lim_a) c[nb][x] = -INFINITY;
             if (none || key > lim_b) c[nb][2 + x] = -INFINITY;
@@ -593,29 +636,53 @@ paged_rows_merge(const CutUnit* __restrict__ cuts, const float* __restrict__ par
   griddep_wait();
   griddep_launch_dependents();
   const int c = blockIdx.x, G = Hq / Hkv;
-  const CutUnit x = cuts[c];
-  constexpr int kQuads = D / 4;
-  if (x.parts == 0 || threadIdx.x >= x.nr * kQuads) return;
+  constexpr int kQuads = D / 4, kAtOnce = 8;
   const int r = threadIdx.x / kQuads, c4 = threadIdx.x % kQuads;
-  // part i: stretch c's slot 1, then slot 0 of the stretches behind it
+  // part i: stretch c's slot 1, then slot 0 of the stretches behind it.  The
+  // first parts are asked for before their number is known (every slot up to
+  // the grid's is there to be read): one round trip for most units.
   auto at = [&](int i) { return ((int64_t)(i == 0 ? 2 * c + 1 : 2 * (c + i))) * 16 + r; };
-  float m = -INFINITY;
-#pragma unroll 8
-  for (int i = 0; i < x.parts; ++i) m = fmaxf(m, part_ml[at(i)].x);
-  float l = 0.f;
+  const int most = min(kAtOnce, (int)gridDim.x - c);
+  float2 ml[kAtOnce];
+  float4 v[kAtOnce];
+  auto ask = [&](int i0, int n) {
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i)
+      if (i < n) {
+        ml[i] = part_ml[at(i0 + i)];
+        v[i] = *reinterpret_cast<const float4*>(part_o + at(i0 + i) * D + c4 * 4);
+      }
+  };
+  ask(0, most);
+  const CutUnit x = cuts[c];
+  if (r >= x.nr || x.parts == 0) return;
+  float m = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (m != -INFINITY) {
-#pragma unroll 8
-    for (int i = 0; i < x.parts; ++i) {
-      const float2 ml = part_ml[at(i)];
-      const float4 v = *reinterpret_cast<const float4*>(part_o + at(i) * D + c4 * 4);
-      const float f = exp2f(ml.x - m);              // 0 for a part without a key
-      l += f * ml.y;
-      acc.x += f * v.x;
-      acc.y += f * v.y;
-      acc.z += f * v.z;
-      acc.w += f * v.w;
-    }
+  for (int i0 = 0; i0 < x.parts; i0 += kAtOnce) {
+    const int n = min(kAtOnce, x.parts - i0);
+    if (i0 > 0) ask(i0, n);
+    float mn = m;
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i)
+      if (i < n) mn = fmaxf(mn, ml[i].x);
+    if (mn == -INFINITY) continue;                  // no key so far
+    const float f0 = exp2f(m - mn);
+    l *= f0;
+    acc.x *= f0;
+    acc.y *= f0;
+    acc.z *= f0;
+    acc.w *= f0;
+#pragma unroll
+    for (int i = 0; i < kAtOnce; ++i)
+      if (i < n) {
+        const float f = exp2f(ml[i].x - mn);        // 0 for a part without a key
+        l += f * ml[i].y;
+        acc.x += f * v[i].x;
+        acc.y += f * v[i].y;
+        acc.z += f * v[i].z;
+        acc.w += f * v[i].w;
+      }
+    m = mn;
   }
   const int RR = x.r0 + r;
   const int64_t row = (int64_t)(x.tok0 + RR / G) * Hq + x.kv * G + RR % G;
