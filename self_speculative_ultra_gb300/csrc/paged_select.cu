@@ -27,8 +27,9 @@ namespace ts {
 namespace {
 
 constexpr int kScoreThreads = 128;
-constexpr int kPagesPerBlock = 64;
 constexpr int kPickThreads = 512;
+constexpr int kBinBits = 11, kBins = 1 << kBinBits;
+static_assert(kPickThreads / 32 <= 32, "one warp scans the warps' sums");
 constexpr int kPickSmemKeys = 48 * 1024;     // larger candidate lists stay in the workspace
 constexpr uint32_t kLowest = 0x007FFFFFu;    // float_key(-inf)
 
@@ -68,7 +69,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kScoreThreads)
 paged_score_kernel(const PagedBatch b, const T* __restrict__ q, const T* __restrict__ key_min,
                    const T* __restrict__ key_max, int Hq, int Hkv, int n_top, int n_sink,
-                   int n_recent, uint32_t* __restrict__ keys, int32_t* status) {
+                   int n_recent, int per_block, uint32_t* __restrict__ keys, int32_t* status) {
   // query sums: [positive, negative][12-bit part, rest][column]
   __shared__ __align__(16) float qs[2][2][D];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -80,8 +81,8 @@ paged_score_kernel(const PagedBatch b, const T* __restrict__ q, const T* __restr
   const SeqSpan sp = seq_span(b, s);
   if (blockIdx.x == 0 && kv == 0 && tid == 0 && sp.bad) set_status(status, TS_ERR_INVALID_ARG);
   const Span w = span_of(sp, t, b.page_shift, n_top, n_sink, n_recent);
-  const int p0 = max(w.lo, (int)blockIdx.x * kPagesPerBlock);
-  const int p1 = min(w.hi, ((int)blockIdx.x + 1) * kPagesPerBlock);
+  const int p0 = w.lo + (int)blockIdx.x * per_block;
+  const int p1 = min(w.hi, p0 + per_block);
   if (p0 >= p1) return;
   for (int c = tid; c < D; c += kScoreThreads) {
     float up = 0.f, upe = 0.f, dn = 0.f, dne = 0.f;
@@ -115,40 +116,58 @@ paged_score_kernel(const PagedBatch b, const T* __restrict__ q, const T* __restr
     }
   const int32_t* trow = b.table + (int64_t)s * b.max_pages;
   uint32_t* out = keys + ((int64_t)t * Hkv + kv) * b.max_pages;
-#pragma unroll 2
-  for (int i = 0; i < kPagesPerBlock / 16; ++i) {
-    const int pg = (int)blockIdx.x * kPagesPerBlock + i * 16 + warp * 4 + (lane >> 3);
-    const bool in = pg >= p0 && pg < p1;
-    int64_t ph = in ? trow[pg] : 0;
-    bool ok = in;
+  // a page's rows are on their way while the page before is summed, its pool
+  // page while the one before that is
+  struct Rows {
+    uint4 mx[kCh], mn[kCh];
+    bool ok;
+  };
+  auto pool_page = [&](int pg) { return pg < p1 ? trow[pg] : 0; };
+  auto ask = [&](int pg, int ph) {
+    Rows r;
+    r.ok = pg < p1;
     if (ph < 0 || ph >= b.n_pages) {
       if (sub == 0) set_status(status, TS_ERR_INVALID_ARG);
-      ok = false;
+      r.ok = false;
     }
-    if (!ok) ph = 0;
-    const uint4* mx = reinterpret_cast<const uint4*>(key_max + (ph * Hkv + kv) * D);
-    const uint4* mn = reinterpret_cast<const uint4*>(key_min + (ph * Hkv + kv) * D);
-    uint4 vx[kCh], vn[kCh];
+    const int64_t row = ((int64_t)(r.ok ? ph : 0) * Hkv + kv) * (D / 8);
+    const uint4* mx = reinterpret_cast<const uint4*>(key_max) + row;
+    const uint4* mn = reinterpret_cast<const uint4*>(key_min) + row;
 #pragma unroll
     for (int x = 0; x < kCh; ++x) {
-      vx[x] = __ldg(mx + sub + 8 * x);
-      vn[x] = __ldg(mn + sub + 8 * x);
+      r.mx[x] = __ldg(mx + sub + 8 * x);
+      r.mn[x] = __ldg(mn + sub + 8 * x);
     }
-    uint64_t sum = 0, err = 0;
+    return r;
+  };
+  const int first = p0 + warp * 4 + (lane >> 3);
+  constexpr int kEach = kScoreThreads / 8;           // pages a trip
+  Rows next = ask(first, pool_page(first));
+  int ph_next = pool_page(first + kEach);
+  for (int base = p0; base < p1; base += kEach) {    // the same trips for every lane
+    const int pg = base + (first - p0);
+    const Rows r = next;
+    if (base + kEach < p1) {
+      next = ask(pg + kEach, ph_next);
+      ph_next = pool_page(pg + 2 * kEach);
+    }
+    uint64_t sum = 0, err = 0, sum2 = 0, err2 = 0;
 #pragma unroll
     for (int x = 0; x < kCh; ++x) {
-      const uint32_t wx[4] = {vx[x].x, vx[x].y, vx[x].z, vx[x].w};
-      const uint32_t wn[4] = {vn[x].x, vn[x].y, vn[x].z, vn[x].w};
+      const uint32_t wx[4] = {r.mx[x].x, r.mx[x].y, r.mx[x].z, r.mx[x].w};
+      const uint32_t wn[4] = {r.mn[x].x, r.mn[x].y, r.mn[x].z, r.mn[x].w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float2 fx = Pair<T>::unpack(wx[k]), fn = Pair<T>::unpack(wn[k]);
         const uint64_t px = ptx::f2(fx.x, fx.y), pn = ptx::f2(fn.x, fn.y);
         two_sum(sum, err, ptx::mul2(uh[x][k], px));
         err = ptx::fma2(ul[x][k], px, err);
-        two_sum(sum, err, ptx::mul2(dh[x][k], pn));
-        err = ptx::fma2(dl[x][k], pn, err);
+        two_sum(sum2, err2, ptx::mul2(dh[x][k], pn));
+        err2 = ptx::fma2(dl[x][k], pn, err2);
       }
     }
+    two_sum(sum, err, sum2);
+    err = ptx::add2(err, err2);
     float s0, s1, e0, e1;
     ptx::f2_split(sum, s0, s1);
     ptx::f2_split(err, e0, e1);
@@ -162,8 +181,8 @@ paged_score_kernel(const PagedBatch b, const T* __restrict__ q, const T* __restr
       two_sum1(s0, e0, so);
     }
     const float score = s0 + e0;
-    if (sub == 0 && in)
-      out[pg] = ok && isfinite(score) ? float_key(score) : kLowest;   // not finite: last
+    if (sub == 0 && pg < p1)
+      out[pg] = r.ok && isfinite(score) ? float_key(score) : kLowest;   // not finite: last
   }
 }
 
@@ -172,10 +191,10 @@ paged_pick_kernel(const PagedBatch b, const uint32_t* __restrict__ keys, int Hkv
                   int n_sink, int n_recent, int smem_keys, int32_t* __restrict__ pages,
                   int32_t* __restrict__ counts) {
   extern __shared__ uint32_t held[];
-  __shared__ int hist[256];
+  __shared__ int hist[kBins];
   __shared__ int scan_gt[kPickThreads / 32], scan_eq[kPickThreads / 32];
-  __shared__ uint32_t s_prefix;
-  __shared__ int s_need;
+  __shared__ uint32_t s_low, s_high, s_bin;
+  __shared__ int s_need, s_in;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int t = blockIdx.x, kv = blockIdx.y;
   const int N = n_sink + n_top + n_recent;
@@ -198,61 +217,97 @@ paged_pick_kernel(const PagedBatch b, const uint32_t* __restrict__ keys, int Hkv
   const int m = w.hi - w.lo;                       // candidates; m > n_top
   const uint32_t* src = keys + ((int64_t)t * Hkv + kv) * b.max_pages + w.lo;
   const uint32_t* key = src;
-  if (m <= smem_keys) {
-    for (int i = tid; i < m; i += kPickThreads) held[i] = src[i];
-    key = held;
+  if (tid == 0) {
+    s_low = 0xFFFFFFFFu;
+    s_high = 0u;
   }
-  // the n_top-th largest key, one byte a pass: `prefix` holds the bytes found
-  uint32_t prefix = 0, mask = 0;
-  int need = n_top;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256; i += kPickThreads) hist[i] = 0;
+  __syncthreads();
+  uint32_t low = 0xFFFFFFFFu, high = 0u;
+  for (int i = tid; i < m; i += kPickThreads) {
+    const uint32_t x = src[i];
+    if (m <= smem_keys) held[i] = x;
+    low = min(low, x);
+    high = max(high, x);
+  }
+  if (m <= smem_keys) key = held;
+  low = __reduce_min_sync(0xffffffffu, low);
+  high = __reduce_max_sync(0xffffffffu, high);
+  if (lane == 0) {
+    atomicMin(&s_low, low);
+    atomicMax(&s_high, high);
+  }
+  __syncthreads();
+  // The n_top-th largest key, 11 bits a pass from the highest bit in which the
+  // keys differ (scores share sign and exponent: their leading bits would put
+  // them all in one bin).  The keys x - low of the bin found so far lie in
+  // [at, at + 2^shift); `need` of them are kept, and all if there are no more.
+  low = s_low;
+  int shift = 32 - __clz(s_high - low);              // 0: all keys are equal
+  uint32_t at = 0;
+  int need = n_top, in_bin = m;
+  while (shift > 0 && need < in_bin) {
+    const int step = min(shift, kBinBits), down = shift - step;
+    for (int i = tid; i < kBins; i += kPickThreads) hist[i] = 0;
     __syncthreads();
     for (int i = tid; i < m; i += kPickThreads) {
-      const uint32_t x = key[i];
-      if ((x & mask) == prefix) atomicAdd(&hist[(x >> shift) & 255], 1);
+      const uint32_t d = key[i] - low - at;          // wraps for smaller keys
+      if (shift == 32 || d >> shift == 0) atomicAdd(&hist[d >> down], 1);
     }
     __syncthreads();
-    if (warp == 0) {
-      // lane: bins 255 - 8 lane .. 248 - 8 lane, largest first
-      int c[8], sum = 0;
+    // thread: four bins, largest first
+    int c[kBins / kPickThreads], sum = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        c[i] = hist[255 - 8 * lane - i];
-        sum += c[i];
-      }
-      int inc = sum;
+    for (int i = 0; i < kBins / kPickThreads; ++i) {
+      c[i] = hist[kBins - 1 - (tid * (kBins / kPickThreads) + i)];
+      sum += c[i];
+    }
+    int inc = sum;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += x;
-      }
-      int above = inc - sum;
-      if (above < need && need <= inc) {
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    if (lane == 31) scan_gt[warp] = inc;
+    __syncthreads();
+    int above = inc - sum;
+    {
+      const int x = lane < warp ? scan_gt[lane] : 0;
+      above += warp_sum_int(x);
+    }
+    if (above < need && need <= above + sum) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (above < need && need <= above + c[i]) {
-            s_prefix = prefix | ((uint32_t)(255 - 8 * lane - i) << shift);
-            s_need = need - above;
-          }
-          above += c[i];
+      for (int i = 0; i < kBins / kPickThreads; ++i) {
+        if (above < need && need <= above + c[i]) {
+          s_bin = kBins - 1 - (tid * (kBins / kPickThreads) + i);
+          s_need = need - above;
+          s_in = c[i];
         }
+        above += c[i];
       }
     }
     __syncthreads();
-    prefix = s_prefix;
+    at += s_bin << down;
     need = s_need;
-    mask |= 255u << shift;
+    in_bin = s_in;
+    shift = down;
   }
-  // keys above `prefix` are kept, and the first `need` that equal it; thread
-  // tid owns a run of candidates, so ranks follow from one scan
+  // kept: keys above the bin, and the bin's first `need` (of equal keys, or all
+  // of it); thread tid owns a run of candidates, so ranks follow from one scan
+  auto above_bin = [&](uint32_t x) {
+    const uint32_t d = x - low;
+    return d >= at && shift < 32 && (d - at) >> shift != 0;
+  };
+  auto of_bin = [&](uint32_t x) {
+    const uint32_t d = x - low;
+    return d >= at && (shift == 32 || (d - at) >> shift == 0);
+  };
   const int per = (m + kPickThreads - 1) / kPickThreads;
   const int i0 = min(tid * per, m), i1 = min(i0 + per, m);
   int gt = 0, eq = 0;
   for (int i = i0; i < i1; ++i) {
     const uint32_t x = key[i];
-    gt += x > prefix;
-    eq += x == prefix;
+    gt += above_bin(x);
+    eq += of_bin(x);
   }
   int ig = gt, ie = eq;
 #pragma unroll
@@ -269,15 +324,13 @@ paged_pick_kernel(const PagedBatch b, const uint32_t* __restrict__ keys, int Hkv
   }
   __syncthreads();
   int g = ig - gt, q = ie - eq;                    // before this thread's run
-  for (int x = 0; x < warp; ++x) {
-    g += scan_gt[x];
-    q += scan_eq[x];
-  }
+  g += warp_sum_int(lane < warp ? scan_gt[lane] : 0);
+  q += warp_sum_int(lane < warp ? scan_eq[lane] : 0);
   for (int i = i0; i < i1; ++i) {
     const uint32_t x = key[i];
-    const bool same = x == prefix;
-    if (x > prefix || (same && q < need)) out[n_sink + g + min(q, need)] = w.lo + i;
-    g += x > prefix;
+    const bool over = above_bin(x), same = of_bin(x);
+    if (over || (same && q < need)) out[n_sink + g + min(q, need)] = w.lo + i;
+    g += over;
     q += same;
   }
 }
@@ -293,16 +346,22 @@ int launch_paged_select(const PagedBatch& b, const void* q, const void* key_min,
                         int n_sink, int n_recent, int32_t* pages, int32_t* counts, void* ws,
                         int32_t* status, cudaStream_t st) {
   uint32_t* keys = static_cast<uint32_t*>(ws);
+  // pages a block: enough that the query sums and the first loads' latency are
+  // spread over several trips of 16 pages, while the SMs have blocks to overlap
+  int per_block = 256;
+  while (per_block > 32 &&
+         (int64_t)b.n * Hkv * ((b.max_pages + per_block - 1) / per_block) < 4 * kGb300Sms)
+    per_block >>= 1;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   auto score = [&](auto kern, auto* type) {
     using T = std::remove_pointer_t<decltype(type)>;
     pdl_config(&cfg, attr,
-               dim3((b.max_pages + kPagesPerBlock - 1) / kPagesPerBlock, b.n, Hkv),
-               dim3(kScoreThreads), 0, st);
+               dim3((b.max_pages + per_block - 1) / per_block, b.n, Hkv), dim3(kScoreThreads), 0,
+               st);
     cudaLaunchKernelEx(&cfg, kern, b, static_cast<const T*>(q), static_cast<const T*>(key_min),
-                       static_cast<const T*>(key_max), Hq, Hkv, n_top, n_sink, n_recent, keys,
-                       status);
+                       static_cast<const T*>(key_max), Hq, Hkv, n_top, n_sink, n_recent, per_block,
+                       keys, status);
   };
   if (fp16)
     d == 128 ? score(paged_score_kernel<__half, 128>, (__half*)nullptr)
