@@ -4,8 +4,7 @@
 //   (x, y) -> ((x cos a - y sin a) * scale, (y cos a + x sin a) * scale).
 // The angle is kept in turns: f_c / 2 pi as a sum of two floats, p as a sum of
 // two exact floats, each product with its rounding error, so only the
-// fraction of a turn is ever rounded and far positions lose nothing
-// (cos(2 pi r) then comes from the half-turn functions).
+// fraction of a turn is ever rounded and far positions lose nothing.
 //
 // Memory bound: every element is read and written once.  One launch; block
 // roles by index:
@@ -15,7 +14,7 @@
 //                handled by one block, so its bounds need no atomics.
 //   query blocks 16 tokens x 8 query heads.
 // cos/sin are formed once per (token, pair) in shared memory and used by all
-// of the block's heads.
+// of the block's heads, while the rows they turn are on their way to registers.
 #include "paged.cuh"
 
 namespace ts {
@@ -23,17 +22,19 @@ namespace ts {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kSub = 32;        // tokens of a page block per trip
+constexpr int kSub = 32;        // most tokens of a page block per trip
 constexpr int kQTok = 16;       // tokens of a query block
-constexpr int kQHeads = 8;      // heads of a query block
+constexpr int kQHeads = 8;      // heads of a query block, at d = 128
 
 struct Smem {
   union {
-    float2 cs[kSub][64];                 // (cos, sin) * scale
+    // (cos, sin) * scale of pair c: half c % 2 of cs[.][c % 8 / 2][c / 8], so
+    // that neighbouring units read neighbouring 16-byte words
+    float4 cs[kSub][4][8];
     uint4 red[kThreads][4];              // bounds: minimum (2), maximum (2)
   };
   float2 turn[64];                       // f / 2 pi = x + y
-  int pos[kSub];
+  int pos[kQTok];
   int scan[kThreads / 32];
   int seq, page;
 };
@@ -43,51 +44,53 @@ __device__ __forceinline__ float2 sincos_turns(int pos, float2 f, float scale) {
   const float lo = (float)(pos & 4095), hi = (float)(pos - (pos & 4095));
   const float p1 = hi * f.x, p2 = lo * f.x;
   const float e = fmaf(hi, f.x, -p1) + fmaf(lo, f.x, -p2) + (hi + lo) * f.y;
-  const float r = (p1 - rintf(p1)) + (p2 - rintf(p2)) + e;
+  const float r0 = (p1 - rintf(p1)) + (p2 - rintf(p2)) + e;
+  // within half a turn the hardware's sine and cosine are good to 2^-21, far
+  // below half a step of a 16-bit output; the exact ones took 10 of 54 us of a
+  // 12,000-token append
   float s, c;
-  sincospif(2.f * r, &s, &c);
+  __sincosf((r0 - rintf(r0)) * 6.283185307179586f, &s, &c);
   return make_float2(c * scale, s * scale);
 }
 
-// Rotate the unit (two 16-byte chunks a, b of one head row) in place.  In the
+// Rotate unit u (two 16-byte chunks a, b of one head row) in place.  In the
 // half layout chunk a holds first members and b second members of 8 pairs
-// starting at pair c0; interleaved, a and b hold pairs c0..c0+3, c0+4..c0+7.
+// starting at pair 8 u; interleaved, a and b hold pairs 8 u .. + 3, + 4 .. + 7.
 template <typename T>
-__device__ __forceinline__ void rotate(uint4& a, uint4& b, const float2* cs, bool inter) {
+__device__ __forceinline__ void rotate(uint4& a, uint4& b, const float4 (*cs)[8], int u, bool inter) {
   uint32_t* wa = reinterpret_cast<uint32_t*>(&a);
   uint32_t* wb = reinterpret_cast<uint32_t*>(&b);
+  const float4 t[4] = {cs[0][u], cs[1][u], cs[2][u], cs[3][u]};
   if (inter) {
+    auto turn = [](uint32_t w, float c, float s) {
+      const float2 x = Pair<T>::unpack(w);
+      return Pair<T>::pack(x.x * c - x.y * s, x.y * c + x.x * s);
+    };
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 x = Pair<T>::unpack(wa[i]), y = Pair<T>::unpack(wb[i]);
-      const float2 t = cs[i], u = cs[4 + i];
-      wa[i] = Pair<T>::pack(x.x * t.x - x.y * t.y, x.y * t.x + x.x * t.y);
-      wb[i] = Pair<T>::pack(y.x * u.x - y.y * u.y, y.y * u.x + y.x * u.y);
+    for (int i = 0; i < 2; ++i) {
+      wa[2 * i] = turn(wa[2 * i], t[i].x, t[i].y);
+      wa[2 * i + 1] = turn(wa[2 * i + 1], t[i].z, t[i].w);
+      wb[2 * i] = turn(wb[2 * i], t[2 + i].x, t[2 + i].y);
+      wb[2 * i + 1] = turn(wb[2 * i + 1], t[2 + i].z, t[2 + i].w);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 x = Pair<T>::unpack(wa[i]), y = Pair<T>::unpack(wb[i]);
-      const float2 t = cs[2 * i], u = cs[2 * i + 1];
-      wa[i] = Pair<T>::pack(x.x * t.x - y.x * t.y, x.y * u.x - y.y * u.y);
-      wb[i] = Pair<T>::pack(y.x * t.x + x.x * t.y, y.y * u.x + x.y * u.y);
+      wa[i] = Pair<T>::pack(x.x * t[i].x - y.x * t[i].y, x.y * t[i].z - y.y * t[i].w);
+      wb[i] = Pair<T>::pack(y.x * t[i].x + x.x * t[i].y, y.y * t[i].z + x.y * t[i].w);
     }
   }
 }
 
-// Chunk indices of unit u (0 .. D/16 - 1) of a head row, and its first pair
-// (-1: the unit lies behind the rotated part).
-__device__ __forceinline__ void unit_chunks(int u, int rot, bool inter, int& ca, int& cb, int& c0) {
+// Chunk indices of unit u (0 .. D/16 - 1) of a head row; false: the unit lies
+// behind the rotated part.
+__device__ __forceinline__ bool unit_chunks(int u, int rot, bool inter, int& ca, int& cb) {
   const int nr = rot / 16;
-  if (u < nr) {
-    ca = inter ? 2 * u : u;
-    cb = inter ? 2 * u + 1 : u + nr;
-    c0 = 8 * u;
-  } else {
-    ca = 2 * u;
-    cb = 2 * u + 1;
-    c0 = -1;
-  }
+  const bool turned = u < nr;
+  ca = turned && !inter ? u : 2 * u;
+  cb = turned && !inter ? u + nr : 2 * u + 1;
+  return turned;
 }
 
 template <typename T>
@@ -104,7 +107,7 @@ __device__ __forceinline__ void fold(uint4& lo, uint4& hi, const uint4& v) {
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, 3)
 paged_append_kernel(const PagedBatch b, const AppendArgs a, int n_page_blocks, int heads_per_block,
                     int32_t* status) {
   __shared__ Smem sm;
@@ -126,9 +129,26 @@ paged_append_kernel(const PagedBatch b, const AppendArgs a, int n_page_blocks, i
   if ((int)blockIdx.x >= n_page_blocks) {
     // ------------------------------------------------------------ queries
     const int qb = blockIdx.x - n_page_blocks;
-    const int n_hc = (a.Hq + kQHeads - 1) / kQHeads;
-    const int t0 = qb / n_hc * kQTok, h0 = qb % n_hc * kQHeads;
-    const int nh = min(kQHeads, a.Hq - h0);
+    constexpr int kHeads = kQHeads * 128 / D;
+    const int n_hc = (a.Hq + kHeads - 1) / kHeads;
+    const int t0 = qb / n_hc * kQTok, h0 = qb % n_hc * kHeads;
+    const int nh = min(kHeads, a.Hq - h0);
+    // a thread's rows, asked for first (a token of no sequence has a row too)
+    constexpr int kEach = kQTok * kQHeads * 8 / kThreads;   // units a thread
+    const int n_units = kQTok * nh * kUnits;
+    uint4 xa[kEach], xb[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int e = tid + i * kThreads;
+      const int u = e % kUnits, h = e / kUnits % nh, t = t0 + e / (kUnits * nh);
+      if (e < n_units && t < b.n) {
+        int ca, cb;
+        const bool turned = unit_chunks(u, a.rot, inter, ca, cb);
+        const uint4* src = reinterpret_cast<const uint4*>(q + t * a.q_stride + (int64_t)(h0 + h) * D);
+        xa[i] = src[ca];
+        xb[i] = src[cb];
+      }
+    }
     // positions of the block's tokens: each thread looks at its sequences
     if (tid < kQTok) sm.pos[tid] = INT_MIN;
     __syncthreads();
@@ -140,23 +160,22 @@ paged_append_kernel(const PagedBatch b, const AppendArgs a, int n_page_blocks, i
     __syncthreads();
     for (int e = tid; e < kQTok * half; e += kThreads) {
       const int i = e / half, c = e - i * half;
-      sm.cs[i][c] = sincos_turns(sm.pos[i], sm.turn[c], a.rope_scale);
+      reinterpret_cast<float2*>(&sm.cs[i][(c & 7) >> 1][c >> 3])[c & 1] =
+          sincos_turns(sm.pos[i], sm.turn[c], a.rope_scale);
     }
     __syncthreads();
     T* out = static_cast<T*>(a.q_out);
-#pragma unroll 2
-    for (int e = tid; e < kQTok * nh * kUnits; e += kThreads) {
-      const int u = e % kUnits, h = e / kUnits % nh, i = e / (kUnits * nh);
-      const int t = t0 + i;
-      if (t >= b.n || sm.pos[i] == INT_MIN) continue;   // behind the last sequence
-      int ca, cb, c0;
-      unit_chunks(u, a.rot, inter, ca, cb, c0);
-      const uint4* src = reinterpret_cast<const uint4*>(q + t * a.q_stride + (int64_t)(h0 + h) * D);
-      uint4 x = src[ca], y = src[cb];
-      if (c0 >= 0) rotate<T>(x, y, &sm.cs[i][c0], inter);
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int e = tid + i * kThreads;
+      const int u = e % kUnits, h = e / kUnits % nh, at = e / (kUnits * nh), t = t0 + at;
+      if (e >= n_units || t >= b.n || sm.pos[at] == INT_MIN) continue;   // of no sequence
+      int ca, cb;
+      const bool turned = unit_chunks(u, a.rot, inter, ca, cb);
+      if (turned) rotate<T>(xa[i], xb[i], sm.cs[at], u, inter);
       uint4* dst = reinterpret_cast<uint4*>(out + ((int64_t)t * a.Hq + h0 + h) * D);
-      dst[ca] = x;
-      dst[cb] = y;
+      dst[ca] = xa[i];
+      dst[cb] = xb[i];
     }
     return;
   }
@@ -223,51 +242,61 @@ paged_append_kernel(const PagedBatch b, const AppendArgs a, int n_page_blocks, i
   const int combos = heads_per_block * kUnits;
   const int combo = tid % combos, tl = tid / combos, n_tl = kThreads / combos;
   const int h = combo / kUnits, u = combo % kUnits;
-  int ca, cb, c0;
-  unit_chunks(u, a.rot, inter, ca, cb, c0);
+  int ca, cb;
+  const bool turned = unit_chunks(u, a.rot, inter, ca, cb);
   uint4 loa, lob, hia, hib;
   bool any = false;
-  for (int t0 = r0; t0 < r1; t0 += kSub) {
-    const int m = min(kSub, r1 - t0);
-    if (tid < m) {
-      const int t = sp.q0 + (t0 + tid - a0);
-      sm.pos[tid] = a.positions ? a.positions[t] : t0 + tid;
-    }
-    __syncthreads();
-    for (int e = tid; e < m * half; e += kThreads) {
-      const int i = e / half, c = e - i * half;
-      sm.cs[i][c] = sincos_turns(sm.pos[i], sm.turn[c], a.rope_scale);
-    }
-    __syncthreads();
-    if (h < nh) {
-#pragma unroll 2
-      for (int i = tl; i < m; i += n_tl) {
+  constexpr int kEach = 2;               // tokens of a trip a thread
+  const int per_trip = min(kSub, kEach * n_tl);
+  for (int t0 = r0; t0 < r1; t0 += per_trip) {
+    const int m = min(per_trip, r1 - t0);
+    uint4 kx[kEach], ky[kEach], vx[kEach], vy[kEach];
+#pragma unroll
+    for (int x = 0; x < kEach; ++x) {
+      const int i = tl + x * n_tl;
+      if (h < nh && i < m) {
         const int64_t t = sp.q0 + (t0 + i - a0);
         const uint4* ks = reinterpret_cast<const uint4*>(k + t * a.k_stride + (int64_t)(h0 + h) * D);
         const uint4* vs = reinterpret_cast<const uint4*>(v + t * a.v_stride + (int64_t)(h0 + h) * D);
-        uint4 x = ks[ca], y = ks[cb];
-        const uint4 va = vs[2 * u], vb = vs[2 * u + 1];
-        if (c0 >= 0) rotate<T>(x, y, &sm.cs[i][c0], inter);
+        kx[x] = ks[ca];
+        ky[x] = ks[cb];
+        vx[x] = vs[2 * u];
+        vy[x] = vs[2 * u + 1];
+      }
+    }
+    __syncthreads();                     // the trip before is done with cos/sin
+    for (int e = tid; e < m * half; e += kThreads) {
+      const int i = e / half, c = e - i * half;
+      const int pos = a.positions ? a.positions[sp.q0 + (t0 + i - a0)] : t0 + i;
+      reinterpret_cast<float2*>(&sm.cs[i][(c & 7) >> 1][c >> 3])[c & 1] =
+          sincos_turns(pos, sm.turn[c], a.rope_scale);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < kEach; ++x) {
+      const int i = tl + x * n_tl;
+      if (h < nh && i < m) {
+        if (turned) rotate<T>(kx[x], ky[x], sm.cs[i], u, inter);
         const int64_t row = ((phys * a.Hkv + h0 + h) << b.page_shift) + ((t0 + i) & (ps - 1));
         uint4* kd = reinterpret_cast<uint4*>(kp + row * D);
         uint4* vd = reinterpret_cast<uint4*>(vp + row * D);
-        kd[ca] = x;
-        kd[cb] = y;
-        vd[2 * u] = va;
-        vd[2 * u + 1] = vb;
+        kd[ca] = kx[x];
+        kd[cb] = ky[x];
+        vd[2 * u] = vx[x];
+        vd[2 * u + 1] = vy[x];
         if (!any) {
-          loa = hia = x;
-          lob = hib = y;
+          loa = hia = kx[x];
+          lob = hib = ky[x];
           any = true;
         } else {
-          fold<T>(loa, hia, x);
-          fold<T>(lob, hib, y);
+          fold<T>(loa, hia, kx[x]);
+          fold<T>(lob, hib, ky[x]);
         }
       }
     }
-    __syncthreads();
   }
   if (!a.key_min) return;
+  __syncthreads();
   // token lanes beyond the page's rows hold nothing; lane 0 always does
   sm.red[tid][0] = loa;
   sm.red[tid][1] = lob;
@@ -275,8 +304,7 @@ paged_append_kernel(const PagedBatch b, const AppendArgs a, int n_page_blocks, i
   sm.red[tid][3] = hib;
   __syncthreads();
   if (tid < combos && h < nh) {
-    // lanes that saw a row: the longest trip had min(kSub, rows) tokens
-    const int live = min(n_tl, min(kSub, r1 - r0));
+    const int live = min(n_tl, min(per_trip, r1 - r0));   // lanes that saw a row
     for (int j = 1; j < live; ++j) {
       const uint4* o = sm.red[j * combos + tid];
       fold<T>(loa, hia, o[0]);
@@ -307,11 +335,12 @@ int launch_paged_append(const PagedBatch& b, const AppendArgs& a, int d, bool fp
   const int64_t slots = imin64(b.n, (b.n >> b.page_shift) + 2 * (int64_t)b.n_seq);
   // KV heads of a page block: more heads share the block's cos/sin, fewer
   // heads fill the SMs when few pages are touched
-  int hpb = 4;
+  int hpb = 4 * 128 / d;
   while (hpb > 1 && (hpb > a.Hkv || slots * ((a.Hkv + hpb - 1) / hpb) < 4 * kGb300Sms)) hpb >>= 1;
   const int64_t page_blocks = slots * ((a.Hkv + hpb - 1) / hpb);
+  const int q_heads = kQHeads * 128 / d;
   const int64_t q_blocks =
-      (int64_t)((b.n + kQTok - 1) / kQTok) * ((a.Hq + kQHeads - 1) / kQHeads);
+      (int64_t)((b.n + kQTok - 1) / kQTok) * ((a.Hq + q_heads - 1) / q_heads);
   const int64_t blocks = page_blocks + q_blocks;
   if (blocks > INT32_MAX)
     return fail(TS_ERR_UNSUPPORTED, "ts_paged_rope_append: %lld blocks in one launch",

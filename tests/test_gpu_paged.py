@@ -116,6 +116,12 @@ def test_append_head_counts(ts, Hq, Hkv, ps):
     _append_case(ts, [1, 17, 200], [33, 17, 1000], Hq, Hkv, 128, ps, BF, 128, False, seed=3)
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (8, 8), (32, 4)])
+def test_append_small_heads_in_long_pages(ts, Hq, Hkv):
+    """Few units a head row: a thread's token lanes outnumber a trip's tokens."""
+    _append_case(ts, [130, 128, 1], [130, 300, 128], Hq, Hkv, 64, 128, BF, 64, False, seed=4)
+
+
 @pytest.mark.parametrize("n_seq", [1, 255, 256, 700])
 def test_append_many_single_tokens(ts, n_seq):
     kv = [(37 * s) % 50 + 1 for s in range(n_seq)]
