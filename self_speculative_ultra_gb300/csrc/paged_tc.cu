@@ -37,6 +37,7 @@
 // Every wait is bounded; on expiry the CTA reports TS_ERR_TIMEOUT, waits for
 // its own copies and products, frees its TMEM and returns.
 #include <cuda.h>
+#include <cstddef>
 
 #include "paged.cuh"
 #include "paged_tc.cuh"
@@ -48,7 +49,7 @@ namespace {
 
 constexpr int kNk = 128;               // keys a tile
 constexpr int kM = kTcRows;            // query rows a tile
-constexpr int kSK = 2, kSV = 3;        // ring depths
+constexpr int kRing = 4;               // barriers in turn for a group's tiles
 constexpr int kThreads = 512;
 constexpr int kRegsLow = 64, kRegsSoftmax = 192;
 static_assert(2 * 128 * kRegsLow + 2 * 128 * kRegsSoftmax == kThreads * 128,
@@ -367,12 +368,17 @@ struct Item {
 
 constexpr int kNext = 4;
 
+constexpr int kMostStages = 4;
+
 struct Aux {
-  uint64_t k_full[kSK], k_empty[kSK], v_full[kSV], v_empty[kSV];
+  uint64_t k_full[kMostStages], k_empty[kMostStages], v_full[kMostStages], v_empty[kMostStages];
   // a V tile that reaches behind the sequence's rows lands on v_tail, and
   // v_clear follows when the rows behind are cleared (v_full only counts it)
-  uint64_t v_tail[kSV], v_clear[kSV];
-  uint64_t q_full, q_empty, s_full[2], p_ready[2], o_full[2], drain;
+  uint64_t v_tail[kMostStages], v_clear[kMostStages];
+  // a group's tiles take these in turn: a tile's turn comes again only when
+  // every waiter has seen its last
+  uint64_t s_full[2][kRing], p_ready[2][kRing], o_done[2][kRing];
+  uint64_t q_full, q_empty, drain;
   uint64_t next_full[kNext], next_empty[kNext];   // items handed to the other warps
   uint32_t tmem_base;
   volatile int32_t abort_flag;
@@ -383,6 +389,9 @@ template <int D>
 struct Layout {
   static constexpr int kPanel = 128 * 128;
   static constexpr int kTile = 128 * D * 2;
+  static constexpr int kSK = D == 64 ? 4 : 2, kSV = D == 64 ? 4 : 3;   // ring depths
+  // score tiles in TMEM beside the two O tiles (512 columns in all)
+  static constexpr int kScores = D == 64 ? 3 : 2;
   static constexpr int kQ = 0;
   static constexpr int kK = kQ + 2 * kTile;
   static constexpr int kV = kK + kSK * kTile;
@@ -390,7 +399,7 @@ struct Layout {
   static constexpr int kBytes = kAux + (int)sizeof(Aux);
   static constexpr uint32_t kTmemCols = 512;
   __host__ __device__ static constexpr uint32_t obase(int g) { return (uint32_t)(g * D); }
-  __host__ __device__ static constexpr uint32_t sbase(int g) { return (uint32_t)(2 * D + g * kNk); }
+  __host__ __device__ static constexpr uint32_t sbase(int i) { return (uint32_t)(2 * D + i * kNk); }
 };
 
 struct Work {
@@ -465,6 +474,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
                 float* __restrict__ part_o, float2* __restrict__ part_ml, long long wait_limit,
                 int32_t* status) {
   using Ly = Layout<D>;
+  constexpr int kSK = Ly::kSK, kSV = Ly::kSV, kScores = Ly::kScores;
   extern __shared__ __align__(1024) uint8_t sm[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = Hq / Hkv;
@@ -490,9 +500,11 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
     ptx::mbar_init(&aux->q_full, 4);
     ptx::mbar_init(&aux->q_empty, 1);
     for (int g = 0; g < 2; ++g) {
-      ptx::mbar_init(&aux->s_full[g], 1);
-      ptx::mbar_init(&aux->p_ready[g], 4);
-      ptx::mbar_init(&aux->o_full[g], 1);
+      for (int i = 0; i < kRing; ++i) {
+        ptx::mbar_init(&aux->s_full[g][i], 1);
+        ptx::mbar_init(&aux->p_ready[g][i], 4);
+        ptx::mbar_init(&aux->o_done[g][i], 1);
+      }
     }
     ptx::mbar_init(&aux->drain, 1);
     for (int i = 0; i < kNext; ++i) {
@@ -609,11 +621,14 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       }
     } else if (warp == 1) {
       // ------------------------------------------------------------ products
-      // The whole warp walks the loop and one elected lane issues.  Everything
-      // an instruction's operands come from is the same in all lanes, and is
-      // made so for the compiler too (broadcasts of lane 0): it then keeps them
-      // in uniform registers.  Issued by one lane of a divergent warp, every
-      // product paid ~100 cycles to move its operands there, 3.6 K a step.
+      // The whole warp walks the loop, and one lane issues under a predicate.
+      // Everything an instruction's operands come from is the same in all lanes,
+      // and is made so for the compiler too (broadcasts of lane 0): it then keeps
+      // them in uniform registers.  The queue in front of the tensor core is
+      // short, so what this warp spends between products leaves it idle: issued
+      // by one lane of a divergent warp a step took 3.6 K cycles, in a branch of
+      // the elected lane 2.9 K (2182 us for 2048 tokens over 100K rows, 8B
+      // shape), under a predicate 2.6 K (1974 us).
       constexpr uint32_t idesc_qk = Pair<T>::kFp16 ? ptx::idesc_f16_f32(128, kNk, false)
                                                    : ptx::idesc_bf16_f32(128, kNk, false);
       constexpr uint32_t idesc_pv = Pair<T>::kFp16 ? ptx::idesc_f16_f32(128, D, true)
@@ -621,41 +636,17 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       auto same = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
       const uint32_t base = same(ptx::smem_u32(sm));
       const uint32_t tm = same(tmem);
+      const uint32_t lead = ptx::elect_one() ? 1u : 0u;
+      const uint32_t bars = base + Ly::kAux;
       const uint64_t qd0 = ptx::sdesc_sw128(base + Ly::kQ, 16, 1024);
       const uint64_t kd0 = ptx::sdesc_sw128(base + Ly::kK, 16, 1024);
       const uint64_t vd0 = ptx::sdesc_sw128(base + Ly::kV, Ly::kPanel, 1024);
       constexpr uint32_t kTile16 = Ly::kTile >> 4;
       uint32_t it = 0, items = 0, clear_par = 0, count = 0;
-      uint32_t tiles_g[2] = {0, 0};
+      uint32_t scores_g[2] = {0, 0}, tiles_g[2] = {0, 0};   // S and P V products issued
+      uint32_t outs_g[2] = {0, 0};                          // items ended
       bool ok = true;
-      auto qk = [&](int g, uint32_t t) {
-        const uint64_t a0 = qd0 + (uint64_t)(g * kTile16);
-        const uint64_t b0 = kd0 + (uint64_t)((t % kSK) * kTile16);
-        if (ptx::elect_one()) {
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint32_t off = (ks >> 2) * (Ly::kPanel >> 4) + (ks & 3) * 2;
-            ptx::mma_ss(tm + Ly::sbase(g), a0 + off, b0 + off, idesc_qk, ks > 0 ? 1u : 0u);
-          }
-          ptx::mma_commit(&aux->s_full[g]);
-        }
-        __syncwarp();
-      };
-      auto pv = [&](int g, uint32_t t, uint32_t acc, bool last) {
-        const uint64_t b0 = vd0 + (uint64_t)((t % kSV) * kTile16);
-        if (ptx::elect_one()) {
-#pragma unroll
-          for (int ks = 0; ks < kNk / 16; ++ks)
-            ptx::mma_ts(tm + Ly::obase(g), tm + Ly::sbase(g) + 8 * ks, b0 + (uint64_t)(ks * 128),
-                        idesc_pv, ks > 0 ? 1u : acc);
-          if (last) ptx::mma_commit(&aux->o_full[g]);
-        }
-        __syncwarp();
-      };
-      auto release = [&](uint64_t* bar) {
-        if (ptx::elect_one()) ptx::mma_commit(bar);
-        __syncwarp();
-      };
+      auto commit = [&](uint32_t off) { ptx::mma_commit_if(lead, bars + off); };
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         const bool got = __all_sync(0xffffffffu, ptx::mbar_wait(bar, parity & 1u, wait_limit));
         ptx::tc_fence_after();
@@ -669,47 +660,146 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
         const bool tail = same((w.k0 + w.n) * kNk > w.kl) != 0;   // of the item's last tile
         if (n < 0) break;
         if (n == 0) continue;
-        ok = wait(&aux->q_full, items) && wait(&aux->k_full[it % kSK], it / kSK);
-        if (!ok) break;
-        if (n0 > 0) qk(0, it);
-        if (n1 > 0) qk(1, it);
-        release(&aux->k_empty[it % kSK]);
-        if (n == 1) release(&aux->q_empty);
-        for (int k = 0; k < n; ++k) {
-          const uint32_t t = it + k, stV = t % kSV;
-          ok = wait(&aux->v_full[stV], t / kSV);
-          if (ok && tail && k + 1 == n) {
-            ok = wait(&aux->v_clear[stV], clear_par >> stV);
-            clear_par ^= 1u << stV;
-          }
-          if (!ok) break;
+        ok = wait(&aux->q_full, items);
+        if constexpr (kScores == 2) {
+          // S tile g is group g's: its next scores go behind its P V.  (The loop
+          // of three S tiles below costs more between the products than it gives
+          // here: 2079 us for 1974 on 2048 tokens over 100K rows.)
+          auto scores = [&](int g, uint32_t t) {
+            const uint64_t a0 = qd0 + (uint64_t)(g * kTile16);
+            const uint64_t b0 = kd0 + (uint64_t)((t % kSK) * kTile16);
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const int ng = g == 0 ? n0 : n1;
-            if (ok && k < ng) {
-              ok = wait(&aux->p_ready[g], tiles_g[g]);
-              if (ok) {
-                ++tiles_g[g];
-                pv(g, t, k > 0 ? 1u : 0u, k + 1 == ng);
-                if (k + 1 < ng) {
-                  ok = wait(&aux->k_full[(t + 1) % kSK], (t + 1) / kSK);
-                  if (ok) qk(g, t + 1);
+            for (int ks = 0; ks < D / 16; ++ks) {
+              const uint32_t off = (ks >> 2) * (Ly::kPanel >> 4) + (ks & 3) * 2;
+              ptx::mma_ss_if(lead, tm + Ly::sbase(g), a0 + off, b0 + off, idesc_qk, ks > 0 ? 1u : 0u);
+            }
+            commit(offsetof(Aux, s_full) + (g * kRing + scores_g[g]++ % kRing) * 8);
+          };
+          ok = ok && wait(&aux->k_full[it % kSK], it / kSK);
+          if (!ok) break;
+          if (n0 > 0) scores(0, it);
+          if (n1 > 0) scores(1, it);
+          commit(offsetof(Aux, k_empty) + it % kSK * 8);
+          if (n == 1) commit(offsetof(Aux, q_empty));
+          for (int k = 0; k < n; ++k) {
+            const uint32_t t = it + k, stV = t % kSV;
+            ok = wait(&aux->v_full[stV], t / kSV);
+            if (ok && tail && k + 1 == n) {
+              ok = wait(&aux->v_clear[stV], clear_par >> stV);
+              clear_par ^= 1u << stV;
+            }
+            if (!ok) break;
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              const int ng = g == 0 ? n0 : n1;
+              if (ok && k < ng) {
+                const uint32_t turn = tiles_g[g]++;
+                ok = wait(&aux->p_ready[g][turn % kRing], turn / kRing);
+                if (ok) {
+                  const uint64_t b0 = vd0 + (uint64_t)(stV * kTile16);
+#pragma unroll
+                  for (int ks = 0; ks < kNk / 16; ++ks)
+                    ptx::mma_ts_if(lead, tm + Ly::obase(g), tm + Ly::sbase(g) + 8 * ks,
+                                   b0 + (uint64_t)(ks * 128), idesc_pv, (ks > 0 || k > 0) ? 1u : 0u);
+                  if (k + 1 == ng) commit(offsetof(Aux, o_done) + (g * kRing + outs_g[g]++ % kRing) * 8);
+                  if (k + 1 < ng) {
+                    ok = wait(&aux->k_full[(t + 1) % kSK], (t + 1) / kSK);
+                    if (ok) scores(g, t + 1);
+                  }
                 }
               }
             }
+            if (!ok) break;
+            commit(offsetof(Aux, v_empty) + stV * 8);
+            if (k + 1 < n) {
+              commit(offsetof(Aux, k_empty) + (t + 1) % kSK * 8);
+              if (k + 2 == n) commit(offsetof(Aux, q_empty));
+            }
           }
-          if (!ok) break;
-          release(&aux->v_empty[stV]);
-          if (k + 1 < n) {
-            release(&aux->k_empty[(t + 1) % kSK]);
-            if (k + 2 == n) release(&aux->q_empty);
+        } else {
+          // The item's products in pairs, by tile and group: op i writes its scores
+          // to S tile i % kScores and, once they are P, multiplies them by V.  The
+          // scores of op i + kScores go behind the P V of op i, so every group has
+          // its next scores while it works on these.
+          struct Op {
+            int g, k;
+          };
+          auto step = [&](Op& x) {
+            do {
+              x.k += x.g;
+              x.g ^= 1;
+            } while (x.k < n && x.k >= (x.g == 0 ? n0 : n1));
+          };
+          const int total = n0 + n1;
+          Op a{n0 > 0 ? 0 : 1, 0}, p = a;
+          int ka = -1, kp = -1, sa = 0, sp_ = 0;     // tiles waited for; S tiles of the next ops
+          auto scores = [&]() {
+            const uint32_t t = it + a.k;
+            if (a.k != ka) {
+              ka = a.k;
+              ok = wait(&aux->k_full[t % kSK], t / kSK);
+              if (!ok) return;
+            }
+            const uint64_t a0 = qd0 + (uint64_t)(a.g * kTile16);
+            const uint64_t b0 = kd0 + (uint64_t)((t % kSK) * kTile16);
+            const uint32_t d0 = tm + Ly::sbase(sa);
+            const uint32_t turn = (a.g == 0 ? scores_g[0]++ : scores_g[1]++) % kRing;
+            const Op at = a;
+            step(a);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+              const uint32_t off = (ks >> 2) * (Ly::kPanel >> 4) + (ks & 3) * 2;
+              ptx::mma_ss_if(lead, d0, a0 + off, b0 + off, idesc_qk, ks > 0 ? 1u : 0u);
+            }
+            commit(offsetof(Aux, s_full) + (at.g * kRing + turn) * 8);
+            if (a.k != at.k) commit(offsetof(Aux, k_empty) + t % kSK * 8);
+            if (a.k >= n) commit(offsetof(Aux, q_empty));
+            sa = sa + 1 == kScores ? 0 : sa + 1;
+          };
+          for (int i = 0; ok && i < min(kScores, total); ++i) scores();
+          for (int i = 0; ok && i < total; ++i) {
+            const uint32_t t = it + p.k, stV = t % kSV;
+            if (p.k != kp) {
+              kp = p.k;
+              ok = wait(&aux->v_full[stV], t / kSV);
+              if (ok && tail && p.k + 1 == n) {
+                ok = wait(&aux->v_clear[stV], clear_par >> stV);
+                clear_par ^= 1u << stV;
+              }
+            }
+            const uint32_t turn = p.g == 0 ? tiles_g[0]++ : tiles_g[1]++;
+            ok = ok && wait(&aux->p_ready[p.g][turn % kRing], turn / kRing);
+            if (!ok) break;
+            const uint64_t b0 = vd0 + (uint64_t)(stV * kTile16);
+            const uint32_t s0 = tm + Ly::sbase(sp_), d0 = tm + Ly::obase(p.g);
+            const uint32_t acc = p.k > 0 ? 1u : 0u;
+            const Op at = p;
+            step(p);
+#pragma unroll
+            for (int ks = 0; ks < kNk / 16; ++ks)
+              ptx::mma_ts_if(lead, d0, s0 + 8 * ks, b0 + (uint64_t)(ks * 128), idesc_pv,
+                             ks > 0 ? 1u : acc);
+            commit(offsetof(Aux, o_done) + (at.g * kRing + turn % kRing) * 8);
+            if (p.k != at.k) commit(offsetof(Aux, v_empty) + stV * 8);
+            sp_ = sp_ + 1 == kScores ? 0 : sp_ + 1;
+            if (i + kScores < total) scores();
           }
         }
         it += n;
         ++items;
       }
       if (!ok) give_up(aux, status);
-      release(&aux->drain);               // this warp's products end before TMEM is freed
+      // This warp's products end before TMEM is freed.  (How this last commit is
+      // written decides how the compiler arranges the loops above: by measurement
+      // under the predicate for two S tiles, 1990 us against 2125 for 2048 tokens
+      // over 100K rows, and in a branch for three, 124 against 137 for 9 mixed
+      // streams at d = 64.)
+      if constexpr (kScores == 2) {
+        commit(offsetof(Aux, drain));
+      } else {
+        if (ptx::elect_one()) ptx::mma_commit(&aux->drain);
+        __syncwarp();
+      }
       ptx::mbar_wait(&aux->drain, 0, kDrainCycles);
     } else if (warp >= 4) {
       // ------------------------------------------------------------ query rows, V tails
@@ -769,7 +859,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
     const int g = (warp - 8) >> 2;
     const int tr = (warp & 3) * 32 + lane;       // row of the group
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t s_addr = tmem + lane_off + Ly::sbase(g);
     const uint32_t o_addr = tmem + lane_off + Ly::obase(g);
     const float sl2 = kLog2e / sqrtf((float)D);
     const uint64_t sl2x2 = ptx::f2(sl2, sl2);
@@ -788,16 +877,21 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       const int n_mine = g == 0 ? w.n_g[0] : w.n_g[1];
       float m_used = -INFINITY, l = 0.f;
       for (int k = 0; k < n_mine; ++k, ++tiles) {
-        bool got = !aux->abort_flag && ptx::mbar_wait(&aux->s_full[g], tiles & 1u, wait_limit);
+        bool got = !aux->abort_flag && ptx::mbar_wait(&aux->s_full[g][tiles % kRing], (tiles / kRing) & 1u, wait_limit);
         if (!__all_sync(0xffffffffu, got)) {
           ok = false;
           break;
         }
         if (!warp_rows) {        // padding rows: their P feeds O rows that are never written
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&aux->p_ready[g]);
+          if (lane == 0) ptx::mbar_arrive(&aux->p_ready[g][tiles % kRing]);
           continue;
         }
+        // this tile's place among the item's products
+        const int op = kScores == 2 ? g
+                                    : min(k, w.n_g[0]) + min(k, w.n_g[1]) +
+                                          (g == 1 && k < w.n_g[0] ? 1 : 0);
+        const uint32_t s_addr = tmem + lane_off + Ly::sbase(op % kScores);
         const int key0 = (w.k0 + k) * kNk;
         const bool edge = key0 + kNk > lim0 + 1;    // warp-uniform
         uint32_t r[kNk];
@@ -894,8 +988,17 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
         }
         ptx::tmem_st_wait();
         if (k > 0 && __any_sync(0xffffffffu, raise)) {
-          // S of this tile complete means P V of the previous one is (products
-          // of one thread end in order): O may be rescaled
+          // O may be rescaled once the P V of the tile before is complete.  With
+          // an S tile a group this tile's scores went behind it; else it is asked
+          if constexpr (kScores > 2) {
+            const uint32_t last = tiles - 1;
+            bool done = ptx::mbar_wait(&aux->o_done[g][last % kRing], (last / kRing) & 1u, wait_limit);
+            if (!__all_sync(0xffffffffu, done)) {
+              ok = false;
+              break;
+            }
+            ptx::tc_fence_after();
+          }
 #pragma unroll 1
           for (int c = 0; c < D / 16; ++c) {
             uint32_t x[16];
@@ -909,17 +1012,19 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
         }
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&aux->p_ready[g]);
+        if (lane == 0) ptx::mbar_arrive(&aux->p_ready[g][tiles % kRing]);
       }
       if (!ok) break;
       // ------------------------------------------------------------ the item's output
       if (n_mine > 0) {
-        bool got = !aux->abort_flag && ptx::mbar_wait(&aux->o_full[g], outs & 1u, wait_limit);
+        // with an S tile a group, o_done counts items, not tiles
+        const uint32_t last = kScores > 2 ? tiles - 1 : outs++;
+        bool got = !aux->abort_flag &&
+                   ptx::mbar_wait(&aux->o_done[g][last % kRing], (last / kRing) & 1u, wait_limit);
         if (!__all_sync(0xffffffffu, got)) {
           ok = false;
           break;
         }
-        ++outs;
         ptx::tc_fence_after();
       }
       if (!warp_rows) continue;
