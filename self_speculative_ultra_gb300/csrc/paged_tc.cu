@@ -222,18 +222,26 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int max_q, int max_tiles, 
         const int top = min(longest, sorted[w].z + longest / 255 + 1);
         p = (top + parts - 1) / parts;
       }
-      int n_pieces = 0, n_cut = 0, shortest = longest, widest = 0;
+      // pieces_of without its division (the quotient put right, as the slots are
+      // counted by it); the lengths only feed the estimate
+      const float inv = 1.f / p;
+      int n_pieces = 0, n_cut = 0;
+      float low = longest, high = 0.f;
       for (int i = w + lane; i < n_tiles; i += 32) {
-        const int steps = sorted[i].z, np = pieces_of(steps, p), len = (steps + np - 1) / np;
+        const int steps = sorted[i].z;
+        int np = (int)(steps * inv);
+        np += np * p < steps;
+        np -= (np - 1) * p >= steps;
+        np = max(np, 1);
         n_pieces += np;
         if (np > 1) n_cut += np;
-        shortest = min(shortest, len);
-        widest = max(widest, len);
+        const float len = __fdividef((float)steps, (float)np);
+        low = fminf(low, len);
+        high = fmaxf(high, len);
       }
-      shortest = __reduce_min_sync(0xffffffffu, shortest);
-      widest = __reduce_max_sync(0xffffffffu, widest);
-      n_pieces = warp_sum_int(n_pieces);
-      n_cut = warp_sum_int(n_cut);
+      const float shortest = -warp_max(-low), widest = warp_max(high);
+      n_pieces = __reduce_add_sync(0xffffffffu, n_pieces);
+      n_cut = __reduce_add_sync(0xffffffffu, n_cut);
       if ((long long)n_cut * Hkv > max_slots) continue;
       const float cost = kFixed + (n_cut ? kCut : 0.f);
       const float even = ((float)s_total * Hkv + (float)(n_pieces + w) * Hkv * kFixed +
@@ -247,7 +255,7 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int max_q, int max_tiles, 
       float e = fmaxf(even, chain) + (n_cut ? kCut : 0.f);
       if (w < n_tiles) {
         const bool equal = w == 0 || sorted[w - 1].z * 10 >= sorted[0].z * 9;
-        if (!equal || shortest * 10 < widest * 9)
+        if (!equal || shortest * 10.f < widest * 9.f)
           e = fmaxf(e, even + 0.5f * widest);
         else
           e = fmaxf(e, (w ? (float)((w * Hkv + C - 1) / C) * (sorted[0].z + kFixed) : 0.f) + pieces);
@@ -264,15 +272,20 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int max_q, int max_tiles, 
       est_whole[warp] = best_whole;
     }
     __syncthreads();
-    best = est[0];
-    whole = est_whole[0];
-    per = est_per[0];
-    for (int w = 1; w < 32; ++w)
-      if (est[w] < best) {
-        best = est[w];
-        whole = est_whole[w];
-        per = est_per[w];
+    // the least, of equals the first warp's
+    best = est[lane];
+    int from = lane;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float x = __shfl_xor_sync(0xffffffffu, best, o);
+      const int f = __shfl_xor_sync(0xffffffffu, from, o);
+      if (x < best || (x == best && f < from)) {
+        best = x;
+        from = f;
       }
+    }
+    whole = est_whole[from];
+    per = est_per[from];
   }
   // The list: whole tiles, then the others' pieces, first pieces first, so that
   // neighbours in time read the same keys.  at[p]: where the p-th pieces go.
@@ -1077,52 +1090,75 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
 }
 
 // -------------------------------------------------------------------- join
-// The rows of cut tiles: a warp takes four neighbouring rows, 8 lanes a row,
-// D / 8 columns a lane, so that the loads of four rows are in flight together.
+// The rows of cut tiles, four neighbouring rows at a time: 8 lanes a row, D / 8
+// columns a lane, so that the loads of four rows are in flight together.  Where
+// there are CTAs enough, a CTA takes four rows and its warps share the pieces
+// (48 tokens in 76 pieces: 50 us with a warp alone on them); else a warp does.
 template <typename T, int D>
 __global__ void __launch_bounds__(256, 4)
 paged_tc_merge(const PagedBatch b, const Header* __restrict__ hdr, const int4* __restrict__ cuts,
                int Hq, int Hkv, int max_q, const float* __restrict__ part_o,
                const float2* __restrict__ part_ml, T* __restrict__ o, float* __restrict__ lse) {
+  constexpr int kWarps = 8;
+  __shared__ float4 s_o[kWarps][4][D / 4];
+  __shared__ float2 s_ml[kWarps][4];
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31, sub = lane & 7, G = Hq / Hkv;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & 7, G = Hq / Hkv;
   const int64_t total = (int64_t)__ldcg(&hdr->n_cut) * Hkv * (kM / 4);
   constexpr int kQuads = D / 32;          // 16-byte columns a lane
-  for (int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u < total;
-       u += (int64_t)gridDim.x * 8) {
+  const bool shared = total <= gridDim.x;
+  const int64_t first = shared ? blockIdx.x : (int64_t)blockIdx.x * kWarps + warp;
+  const int64_t hop = shared ? gridDim.x : (int64_t)gridDim.x * kWarps;
+  for (int64_t u = first; u < total; u += hop) {
     const int r = (int)(u % (kM / 4)) * 4 + (lane >> 3), kv = (int)(u / (kM / 4) % Hkv);
     const int4 c = __ldcg(&cuts[u / (kM / 4) / Hkv]);    // sequence, tile, first slot, pieces
     const SeqSpan sp = seq_span(b, c.x);
     const int R = c.y * kM + r;
     const bool live = R < min(sp.ql, max_q) * G;         // the same for a row's 8 lanes
-    if (!__any_sync(0xffffffffu, live)) continue;
+    if (!__any_sync(0xffffffffu, live)) continue;        // and for the CTA's warps, if shared
     const int64_t p0 = ((int64_t)c.z * Hkv + kv) * kM + r, step = (int64_t)Hkv * kM;
     const int np = live ? c.w : 0;
-    float m = -INFINITY;
-    for (int i = sub; i < np; i += 8) m = fmaxf(m, __ldcg(&part_ml[p0 + i * step]).x);
-#pragma unroll
-    for (int x = 1; x < 8; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+    const int i0 = shared ? warp : 0, di = shared ? kWarps : 1;
     float4 acc[kQuads];
-    float l = 0.f;
+    float l = 0.f, m = -INFINITY;
 #pragma unroll
     for (int x = 0; x < kQuads; ++x) acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int n_sum = m == -INFINITY ? 0 : np;           // no piece saw a key: O = 0
+    auto add = [&](float mi, float li, const float4 (&v)[kQuads]) {
+      const float mn = fmaxf(m, mi);
+      if (mn == -INFINITY) return;                       // no key so far
+      const float f0 = exp2f(m - mn), f = exp2f(mi - mn);
+      l = l * f0 + f * li;
+#pragma unroll
+      for (int x = 0; x < kQuads; ++x) {
+        acc[x].x = acc[x].x * f0 + f * v[x].x;
+        acc[x].y = acc[x].y * f0 + f * v[x].y;
+        acc[x].z = acc[x].z * f0 + f * v[x].z;
+        acc[x].w = acc[x].w * f0 + f * v[x].w;
+      }
+      m = mn;
+    };
 #pragma unroll 2
-    for (int i = 0; i < n_sum; ++i) {
+    for (int i = i0; i < np; i += di) {
       const float2 ml = __ldcg(&part_ml[p0 + i * step]);
       const float4* p = reinterpret_cast<const float4*>(part_o + (p0 + i * step) * D) + sub;
       float4 v[kQuads];
 #pragma unroll
       for (int x = 0; x < kQuads; ++x) v[x] = __ldcg(p + 8 * x);
-      const float f = exp2f(ml.x - m);                   // 0 for a piece that saw nothing
-      l += f * ml.y;
+      add(ml.x, ml.y, v);
+    }
+    if (shared) {
 #pragma unroll
-      for (int x = 0; x < kQuads; ++x) {
-        acc[x].x += f * v[x].x;
-        acc[x].y += f * v[x].y;
-        acc[x].z += f * v[x].z;
-        acc[x].w += f * v[x].w;
+      for (int x = 0; x < kQuads; ++x) s_o[warp][lane >> 3][sub + 8 * x] = acc[x];
+      if (sub == 0) s_ml[warp][lane >> 3] = make_float2(m, l);
+      __syncthreads();
+      if (warp > 0) continue;                            // one unit a CTA: no trip follows
+      for (int w = 1; w < kWarps; ++w) {
+        float4 v[kQuads];
+#pragma unroll
+        for (int x = 0; x < kQuads; ++x) v[x] = s_o[w][lane >> 3][sub + 8 * x];
+        const float2 ml = s_ml[w][lane >> 3];
+        add(ml.x, ml.y, v);
       }
     }
     if (!live) continue;
