@@ -60,9 +60,17 @@ int64_t bound_kv(int max_pages, int page_size, int64_t max_kv) {
   return max_kv > 0 && max_kv < cap ? max_kv : cap;
 }
 
-// One block of 16 packed rows a KV head takes the row kernel, more take the
-// tensor-core tiles.
-bool few_rows(int max_q, int Hq, int Hkv) { return (int64_t)max_q * (Hq / Hkv) <= 16; }
+// Which kernel takes a dense call.  The row kernel reads the keys once a block
+// of 16 packed rows of a KV head, the tensor-core tiles once for 256 rows but
+// after a plan and with a join (~20 us in all): one block always takes the row
+// kernel, up to four where they are at most 13 trips of 128 keys a SM in all.
+// Measured: 24 rows of 2 KV heads over 32K rows 22.6 us against 26.9; 32 rows of
+// 8 KV heads over 100K rows 127 against 83.
+bool few_rows(int n_seq, int max_q, int Hq, int Hkv, int64_t kv) {
+  const int64_t blocks = ((int64_t)max_q * (Hq / Hkv) + 15) / 16;
+  return blocks <= 1 ||
+         (blocks <= 4 && (int64_t)n_seq * Hkv * blocks * ((kv + 127) / 128) <= 13 * kGb300Sms);
+}
 
 }  // namespace
 
@@ -180,7 +188,7 @@ size_t ts_paged_attention_workspace_bytes(int n, int n_seq, int Hq, int Hkv, int
       max_q < 1)
     return 0;
   const int64_t kv = bound_kv(max_pages, page_size, max_kv);
-  if (few_rows(max_q, Hq, Hkv))
+  if (few_rows(n_seq, max_q, Hq, Hkv, kv))
     return rows_plan((int64_t)n_seq * Hkv, max_q * (Hq / Hkv), d, kv).ws_bytes;
   return tc_plan(n, n_seq, Hq, Hkv, d, max_q, kv).ws_bytes;
 }
@@ -203,7 +211,7 @@ int ts_paged_attention(const void* q, const void* k_pages, const void* v_pages, 
   for (const void* p : {q, k_pages, v_pages, (const void*)o})
     if (!aligned16(p)) return fail(TS_ERR_INVALID_ARG, "%s: a tensor is not 16-byte aligned", W);
   const int64_t kv = bound_kv(max_pages, page_size, max_kv);
-  if (!few_rows(max_q, Hq, Hkv)) {
+  if (!few_rows(n_seq, max_q, Hq, Hkv, kv)) {
     const TcPlan p = tc_plan(n, n_seq, Hq, Hkv, d, max_q, kv);
     rc = check_paged_ws(workspace, workspace_bytes, p.ws_bytes, W);
     if (rc) return rc;

@@ -128,7 +128,10 @@ __device__ __forceinline__ Unit make_unit(const PagedBatch& b, const RowsArgs& a
   u.see0 = sp.kl - sp.ql + (kSparse ? owner - sp.q0 : 0);
   const int rows = kSparse ? G : min(sp.ql, a.max_q) * G;
   u.nr = max(0, min(16, rows - u.r0));
-  if (u.nr == 0) return u;
+  if (u.nr == 0) {                           // a shorter sequence: no row, nothing to walk
+    u.tok0 = u.r0 = 0;
+    return u;
+  }
   if (kSparse) {
     int cnt = a.counts[(int64_t)owner * a.Hkv + kv];
     if (cnt < 0 || cnt > a.n_sel) {
