@@ -644,79 +644,82 @@ def _need(t, dtype, shape, dev, name):
     """The address of tensor `t` after its checks (None stays None)."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev or t.dtype is not dtype or \
-            t.shape != shape or not t.is_contiguous():
-        _dev(t, dtype, name, shape)
-        raise ValueError(f"{name} is on {t.device}, q is on cuda:{dev}")
-    return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dev(t, dtype, name, shape)
+    raise ValueError(f"{name} is on {t.device}, q is on cuda:{dev}")
 
 
 def _paged_q(q):
-    """(n, Hq, d, device index, flags) of a call's queries."""
+    """(n, Hq, d, type, device index, flags) of a call's queries."""
     if not isinstance(q, torch.Tensor) or not q.is_cuda:
         raise TypeError("q must be a CUDA tensor")
-    if q.dtype not in _PAGED_DTYPES:
-        raise TypeError(f"q must be {_PAGED_DTYPES}, got {q.dtype}")
+    dt = q.dtype
+    if dt not in _PAGED_DTYPES:
+        raise TypeError(f"q must be {_PAGED_DTYPES}, got {dt}")
     if q.dim() != 3:
         raise ValueError(f"q has shape {tuple(q.shape)}, expected (n, Hq, d)")
     n, Hq, d = q.shape
-    return n, Hq, d, q.get_device(), TS_PAGED_FP16 if q.dtype is torch.float16 else 0
+    return n, Hq, d, dt, q.get_device(), TS_PAGED_FP16 if dt is torch.float16 else 0
 
 
 def _paged_batch(cu_q, seq_lens, page_table, dev):
     """(n_seq, max_pages, the three addresses) of a call's batch."""
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must be a tensor [n_seq, pages]")
-    n_seq, max_pages = page_table.shape
+    n_seq, max_pages = shape = page_table.shape
     i32 = torch.int32
     return (n_seq, max_pages, _need(cu_q, i32, (n_seq + 1,), dev, "cu_q"),
             _need(seq_lens, i32, (n_seq,), dev, "seq_lens"),
-            _need(page_table, i32, (n_seq, max_pages), dev, "page_table"))
+            _need(page_table, i32, shape, dev, "page_table"))
 
 
-class _Launch:
-    """Device and stream of one paged call.  The tensors' device is current
-    during the call; memory that the call takes from the allocator for a stream
-    other than the current one is tied to it."""
-
-    __slots__ = ("dev", "stream", "guard")
-
-    def __init__(self, dev, stream):
-        self.dev, self.stream = dev, stream
-        self.guard = None
-        if _raw_device() != dev:
-            self.guard = torch.cuda.device(dev)
-            self.guard.__enter__()
-
-    def handle(self):
-        return _raw_stream(self.dev) if self.stream is None else self.stream.cuda_stream
-
-    def empty(self, shape, dtype):
-        t = torch.empty(shape, dtype=dtype, device="cuda")
-        if self.stream is not None:
-            t.record_stream(self.stream)
-        return t
-
-    def workspace(self, nbytes, workspace):
-        """(tensor to keep, address, bytes) of the call's workspace."""
-        if workspace is None:
-            if nbytes == 0:
-                return None, None, 0
-            workspace = self.empty(nbytes, torch.uint8)
-        elif workspace.get_device() != self.dev:
-            raise ValueError(f"workspace is on {workspace.device}, q is on cuda:{self.dev}")
-        have = workspace.numel() * workspace.element_size()
-        if have < nbytes:
-            raise ValueError(f"workspace too small: {nbytes} bytes needed")
-        return workspace, workspace.data_ptr(), have
-
-    def done(self):
-        if self.guard is not None:
-            self.guard.__exit__(None, None, None)
+def _paged_call(fn, dev, stream, taken, args):
+    """One library call with the tensors' device current.  `taken`: memory that
+    the binding allocated for it, tied to `stream` where that is not the current
+    one."""
+    if _raw_device() == dev:
+        rc = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if stream is not None:
+        for t in taken:
+            t.record_stream(stream)
+    if rc:
+        _check(rc)
 
 
-def _paged_status(status, dev):
-    return None if status is None else _need(status, torch.int32, status.shape, dev, "status")
+def _given_workspace(workspace, nbytes, dev):
+    """(address, bytes) of a caller's workspace."""
+    if workspace.get_device() != dev:
+        raise ValueError(f"workspace is on {workspace.device}, q is on cuda:{dev}")
+    have = workspace.numel() * workspace.element_size()
+    if have < nbytes:
+        raise ValueError(f"workspace too small: {nbytes} bytes needed")
+    return workspace.data_ptr(), have
+
+
+def _new_rows(t, name, n, heads, d, dt, dev):
+    """(address, token stride) of a strided [n, heads, d] input of the append."""
+    try:
+        if t.dtype is dt and t.shape == (n, heads, d) and t.get_device() == dev:
+            row, head, one = t.stride()
+            if n == 0 or (one == 1 and (head == d or heads == 1)):
+                # a single token's stride is never walked; a view may report any
+                return t.data_ptr(), row if n > 1 else heads * d
+            raise ValueError(f"{name}: the heads of a token must be dense")
+    except AttributeError:
+        pass
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype is not dt:
+        raise TypeError(f"{name} must be {dt}, got {t.dtype}")
+    raise ValueError(f"{name} has shape {tuple(t.shape)} on {t.device}, expected {(n, heads, d)} "
+                     f"on cuda:{dev}")
 
 
 def ts_paged_rope_append(q, k, v, cu_q, seq_lens, page_table, k_pages, v_pages, freqs,
@@ -728,46 +731,37 @@ def ts_paged_rope_append(q, k, v, cu_q, seq_lens, page_table, k_pages, v_pages, 
     Hkv, page_size, d], freqs [rot_dim / 2] fp64 (see ts_rope_frequencies).
     key_min, key_max [n_pages, Hkv, d]: the pages' key bounds, updated.
     Returns the rotated queries [n, Hq, d]."""
-    n, Hq, d, dev, flags = _paged_q(q)
-    dt = q.dtype
-    n_pages, Hkv, ps = k_pages.shape[:3]
-    strides = []
-    for t, name, heads in ((q, "q", Hq), (k, "k", Hkv), (v, "v", Hkv)):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise TypeError(f"{name} must be a CUDA tensor")
-        if t.dtype is not dt:
-            raise TypeError(f"{name} must be {dt}, got {t.dtype}")
-        if t.shape != (n, heads, d) or t.get_device() != dev:
-            raise ValueError(f"{name} has shape {tuple(t.shape)} on {t.device}, expected "
-                             f"{(n, heads, d)} on cuda:{dev}")
-        row, head, one = t.stride()
-        if n and (one != 1 or (heads > 1 and head != d)):
-            raise ValueError(f"{name}: the heads of a token must be dense")
-        # a single token's stride is never walked; a view may report any
-        strides.append(row if n > 1 else heads * d)
+    n, Hq, d, dt, dev, flags = _paged_q(q)
+    n_pages, Hkv, ps, _ = pool = k_pages.shape
+    qp, q_stride = _new_rows(q, "q", n, Hq, d, dt, dev)
+    kr, k_stride = _new_rows(k, "k", n, Hkv, d, dt, dev)
+    vr, v_stride = _new_rows(v, "v", n, Hkv, d, dt, dev)
     if interleaved:
         flags |= TS_ROPE_INTERLEAVED
     n_seq, max_pages, cu, lens, table = _paged_batch(cu_q, seq_lens, page_table, dev)
-    kp = _need(k_pages, dt, (n_pages, Hkv, ps, d), dev, "k_pages")
-    vp = _need(v_pages, dt, (n_pages, Hkv, ps, d), dev, "v_pages")
+    if pool[3] != d:
+        raise ValueError(f"k_pages has shape {tuple(pool)}, expected head dim {d}")
+    kp = _need(k_pages, dt, pool, dev, "k_pages")
+    vp = _need(v_pages, dt, pool, dev, "v_pages")
     fr = _need(freqs, torch.float64, freqs.shape, dev, "freqs")
-    pos = _need(positions, torch.int32, (n,), dev, "positions")
-    mn = _need(key_min, dt, (n_pages, Hkv, d), dev, "key_min")
-    mx = _need(key_max, dt, (n_pages, Hkv, d), dev, "key_max")
-    st = _paged_status(status, dev)
-    out = _need(q_out, dt, (n, Hq, d), dev, "q_out")
-    on = _Launch(dev, stream)
-    try:
-        if q_out is None:
-            q_out = on.empty((n, Hq, d), dt)
-            out = q_out.data_ptr()
-        rc = lib().ts_paged_rope_append(
-            q.data_ptr(), k.data_ptr(), v.data_ptr(), strides[0], strides[1], strides[2], n, Hq,
-            Hkv, d, cu, lens, n_seq, table, max_pages, ps, n_pages, pos, fr, 2 * freqs.numel(),
-            rope_scale, out, kp, vp, mn, mx, flags, st, on.handle())
-    finally:
-        on.done()
-    _check(rc)
+    pos = mn = mx = st = None
+    if positions is not None:
+        pos = _need(positions, torch.int32, (n,), dev, "positions")
+    if key_min is not None:
+        mn = _need(key_min, dt, (n_pages, Hkv, d), dev, "key_min")
+    if key_max is not None:
+        mx = _need(key_max, dt, (n_pages, Hkv, d), dev, "key_max")
+    if status is not None:
+        st = _need(status, torch.int32, status.shape, dev, "status")
+    taken = ()
+    if q_out is None:
+        q_out = torch.empty((n, Hq, d), dtype=dt, device=q.device)
+        out, taken = q_out.data_ptr(), (q_out,)
+    else:
+        out = _need(q_out, dt, (n, Hq, d), dev, "q_out")
+    _paged_call(lib().ts_paged_rope_append, dev, stream, taken, (
+        qp, kr, vr, q_stride, k_stride, v_stride, n, Hq, Hkv, d, cu, lens, n_seq, table, max_pages,
+        ps, n_pages, pos, fr, 2 * freqs.numel(), rope_scale, out, kp, vp, mn, mx, flags, st))
     return q_out
 
 
@@ -778,6 +772,36 @@ def ts_paged_attention_workspace_bytes(n, n_seq, Hq, Hkv, d, max_pages, page_siz
                                                     max_q, max_kv)
 
 
+def _attend(fn, q, pools, o, lse, want_lse, nbytes, workspace, status, stream, head):
+    """Outputs, workspace and launch that the two attention calls share; head: the
+    arguments in front of (o, lse, workspace, bytes, flags, status, stream)."""
+    n, Hq, d, dt, dev, flags = pools
+    taken = []
+    if o is None:
+        o = torch.empty((n, Hq, d), dtype=dt, device=q.device)
+        out = o.data_ptr()
+        taken.append(o)
+    else:
+        out = _need(o, dt, (n, Hq, d), dev, "o")
+    ls = None
+    if lse is not None:
+        ls = _need(lse, torch.float32, (n, Hq), dev, "lse")
+    elif want_lse:
+        lse = torch.empty((n, Hq), dtype=torch.float32, device=q.device)
+        ls = lse.data_ptr()
+        taken.append(lse)
+    ws, nb = None, nbytes
+    if workspace is not None:
+        ws, nb = _given_workspace(workspace, nbytes, dev)
+    elif nbytes:
+        scratch = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        ws = scratch.data_ptr()
+        taken.append(scratch)
+    st = None if status is None else _need(status, torch.int32, status.shape, dev, "status")
+    _paged_call(fn, dev, stream, taken, head + (out, ls, ws, nb, flags, st))
+    return o, lse
+
+
 def ts_paged_attention(q, k_pages, v_pages, cu_q, seq_lens, page_table, max_q, max_kv=0, o=None,
                        lse=None, want_lse=True, workspace=None, status=None, stream=None):
     """Causal attention of new tokens (prompts, chunks, single tokens) over a
@@ -785,33 +809,17 @@ def ts_paged_attention(q, k_pages, v_pages, cu_q, seq_lens, page_table, max_q, m
     k_pages, v_pages [n_pages, Hkv, page_size, d]; max_q bounds the sequences'
     new tokens, max_kv (0: the page table's width) is the longest sequence as
     far as the host knows.  Returns (o [n, Hq, d], lse [n, Hq] fp32)."""
-    n, Hq, d, dev, flags = _paged_q(q)
-    dt = q.dtype
-    n_pages, Hkv, ps = k_pages.shape[:3]
+    n, Hq, d, dt, dev, _ = what = _paged_q(q)
+    n_pages, Hkv, ps, _ = k_pages.shape
+    pool = (n_pages, Hkv, ps, d)
     n_seq, max_pages, cu, lens, table = _paged_batch(cu_q, seq_lens, page_table, dev)
-    qp = _need(q, dt, (n, Hq, d), dev, "q")
-    kp = _need(k_pages, dt, (n_pages, Hkv, ps, d), dev, "k_pages")
-    vp = _need(v_pages, dt, (n_pages, Hkv, ps, d), dev, "v_pages")
-    st = _paged_status(status, dev)
-    out = _need(o, dt, (n, Hq, d), dev, "o")
-    ls = _need(lse, torch.float32, (n, Hq), dev, "lse")
-    on = _Launch(dev, stream)
-    try:
-        if o is None:
-            o = on.empty((n, Hq, d), dt)
-            out = o.data_ptr()
-        if lse is None and want_lse:
-            lse = on.empty((n, Hq), torch.float32)
-            ls = lse.data_ptr()
-        keep, ws, nb = on.workspace(ts_paged_attention_workspace_bytes(
-            n, n_seq, Hq, Hkv, d, max_pages, ps, max_q, max_kv), workspace)
-        rc = lib().ts_paged_attention(
-            qp, kp, vp, n, Hq, Hkv, d, cu, lens, n_seq, table, max_pages, ps, n_pages, max_q,
-            max_kv, out, ls, ws, nb, flags, st, on.handle())
-    finally:
-        on.done()
-    _check(rc)
-    return o, lse
+    return _attend(
+        lib().ts_paged_attention, q, what, o, lse, want_lse,
+        ts_paged_attention_workspace_bytes(n, n_seq, Hq, Hkv, d, max_pages, ps, max_q, max_kv),
+        workspace, status, stream,
+        (_need(q, dt, (n, Hq, d), dev, "q"), _need(k_pages, dt, pool, dev, "k_pages"),
+         _need(v_pages, dt, pool, dev, "v_pages"), n, Hq, Hkv, d, cu, lens, n_seq, table,
+         max_pages, ps, n_pages, max_q, max_kv))
 
 
 @functools.lru_cache(maxsize=4096)
@@ -827,32 +835,39 @@ def ts_paged_select_pages(q, key_min, key_max, cu_q, seq_lens, page_table, page_
     q [n, Hq, d] rotated, key_min, key_max [n_pages, Hkv, d].  Returns
     (pages [n, Hkv, n_sink + n_top + n_recent], counts [n, Hkv]) int32:
     ascending positions in the page table's row, -1 behind the last."""
-    n, Hq, d, dev, flags = _paged_q(q)
-    dt = q.dtype
-    n_pages, Hkv = key_min.shape[:2]
+    n, Hq, d, dt, dev, flags = _paged_q(q)
+    n_pages, Hkv, _ = key_min.shape
+    bounds = (n_pages, Hkv, d)
     n_seq, max_pages, cu, lens, table = _paged_batch(cu_q, seq_lens, page_table, dev)
     qp = _need(q, dt, (n, Hq, d), dev, "q")
-    mn = _need(key_min, dt, (n_pages, Hkv, d), dev, "key_min")
-    mx = _need(key_max, dt, (n_pages, Hkv, d), dev, "key_max")
-    n_sel = n_sink + n_top + n_recent
-    st = _paged_status(status, dev)
-    pg = _need(pages, torch.int32, (n, Hkv, n_sel), dev, "pages")
-    ct = _need(counts, torch.int32, (n, Hkv), dev, "counts")
-    on = _Launch(dev, stream)
-    try:
-        if pages is None:
-            pages = on.empty((n, Hkv, max(n_sel, 0)), torch.int32)
-            pg = pages.data_ptr()
-        if counts is None:
-            counts = on.empty((n, Hkv), torch.int32)
-            ct = counts.data_ptr()
-        keep, ws, nb = on.workspace(ts_paged_select_workspace_bytes(n, Hkv, max_pages), workspace)
-        rc = lib().ts_paged_select_pages(
-            qp, mn, mx, n, Hq, Hkv, d, cu, lens, n_seq, table, max_pages, page_size, n_pages,
-            n_top, n_sink, n_recent, pg, ct, ws, nb, flags, st, on.handle())
-    finally:
-        on.done()
-    _check(rc)
+    mn = _need(key_min, dt, bounds, dev, "key_min")
+    mx = _need(key_max, dt, bounds, dev, "key_max")
+    n_sel = max(n_sink + n_top + n_recent, 0)
+    taken = []
+    if pages is None:
+        pages = torch.empty((n, Hkv, n_sel), dtype=torch.int32, device=q.device)
+        pg = pages.data_ptr()
+        taken.append(pages)
+    else:
+        pg = _need(pages, torch.int32, (n, Hkv, n_sel), dev, "pages")
+    if counts is None:
+        counts = torch.empty((n, Hkv), dtype=torch.int32, device=q.device)
+        ct = counts.data_ptr()
+        taken.append(counts)
+    else:
+        ct = _need(counts, torch.int32, (n, Hkv), dev, "counts")
+    nb = ts_paged_select_workspace_bytes(n, Hkv, max_pages)
+    ws = None
+    if workspace is not None:
+        ws, nb = _given_workspace(workspace, nb, dev)
+    elif nb:
+        scratch = torch.empty(nb, dtype=torch.uint8, device=q.device)
+        ws = scratch.data_ptr()
+        taken.append(scratch)
+    st = None if status is None else _need(status, torch.int32, status.shape, dev, "status")
+    _paged_call(lib().ts_paged_select_pages, dev, stream, taken, (
+        qp, mn, mx, n, Hq, Hkv, d, cu, lens, n_seq, table, max_pages, page_size, n_pages, n_top,
+        n_sink, n_recent, pg, ct, ws, nb, flags, st))
     return pages, counts
 
 
@@ -867,33 +882,15 @@ def ts_paged_attention_selected(q, k_pages, v_pages, cu_q, seq_lens, page_table,
     """ts_paged_attention over each token's chosen pages (pages [n, Hkv,
     n_sel], counts [n, Hkv] int32, as ts_paged_select_pages returns them).
     Returns (o [n, Hq, d], lse [n, Hq] fp32)."""
-    n, Hq, d, dev, flags = _paged_q(q)
-    dt = q.dtype
-    n_pages, Hkv, ps = k_pages.shape[:3]
+    n, Hq, d, dt, dev, _ = what = _paged_q(q)
+    n_pages, Hkv, ps, _ = k_pages.shape
+    pool = (n_pages, Hkv, ps, d)
     n_seq, max_pages, cu, lens, table = _paged_batch(cu_q, seq_lens, page_table, dev)
-    qp = _need(q, dt, (n, Hq, d), dev, "q")
-    kp = _need(k_pages, dt, (n_pages, Hkv, ps, d), dev, "k_pages")
-    vp = _need(v_pages, dt, (n_pages, Hkv, ps, d), dev, "v_pages")
     n_sel = pages.shape[-1]
-    pg = _need(pages, torch.int32, (n, Hkv, n_sel), dev, "pages")
-    ct = _need(counts, torch.int32, (n, Hkv), dev, "counts")
-    st = _paged_status(status, dev)
-    out = _need(o, dt, (n, Hq, d), dev, "o")
-    ls = _need(lse, torch.float32, (n, Hq), dev, "lse")
-    on = _Launch(dev, stream)
-    try:
-        if o is None:
-            o = on.empty((n, Hq, d), dt)
-            out = o.data_ptr()
-        if lse is None and want_lse:
-            lse = on.empty((n, Hq), torch.float32)
-            ls = lse.data_ptr()
-        keep, ws, nb = on.workspace(
-            ts_paged_selected_workspace_bytes(n, Hq, Hkv, d, ps, n_sel), workspace)
-        rc = lib().ts_paged_attention_selected(
-            qp, kp, vp, n, Hq, Hkv, d, cu, lens, n_seq, table, max_pages, ps, n_pages, pg, ct,
-            n_sel, out, ls, ws, nb, flags, st, on.handle())
-    finally:
-        on.done()
-    _check(rc)
-    return o, lse
+    return _attend(
+        lib().ts_paged_attention_selected, q, what, o, lse, want_lse,
+        ts_paged_selected_workspace_bytes(n, Hq, Hkv, d, ps, n_sel), workspace, status, stream,
+        (_need(q, dt, (n, Hq, d), dev, "q"), _need(k_pages, dt, pool, dev, "k_pages"),
+         _need(v_pages, dt, pool, dev, "v_pages"), n, Hq, Hkv, d, cu, lens, n_seq, table,
+         max_pages, ps, n_pages, _need(pages, torch.int32, (n, Hkv, n_sel), dev, "pages"),
+         _need(counts, torch.int32, (n, Hkv), dev, "counts"), n_sel))
