@@ -112,6 +112,7 @@ struct RowsPlan {
   int n_rb;            // blocks of 16 query rows
   int unit_trips;      // trips of 128 keys a unit, by the host's bound
   int grid;
+  int cluster;         // CTAs a unit, joined on chip (0: stretches of the line)
   size_t cuts_bytes, part_bytes, ws_bytes;
 };
 RowsPlan rows_plan(int64_t units, int rows, int d, int64_t max_keys);

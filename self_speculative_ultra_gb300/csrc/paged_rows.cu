@@ -33,6 +33,7 @@ constexpr int kTileKeys = 32;              // keys of a warp's tile
 constexpr int kStep = kWarps * kTileKeys;  // keys a CTA takes per trip
 constexpr int kStages = 2;
 constexpr int kMinTrips = 2;               // trips a CTA takes at least
+constexpr int kMostCluster = 8;            // CTAs of a cluster
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -159,9 +160,72 @@ __device__ __forceinline__ int stretches(long long total) {
   return (int)(n < 1 ? 1 : n < gridDim.x ? n : gridDim.x);
 }
 
+// Four columns of row r over the warps' states.
+template <int D>
+__device__ __forceinline__ float4 join_warps(const float* so, const float2* sml, int r, int c4,
+                                             float& m, float& l) {
+  m = -INFINITY;
+  l = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sml[w * 16 + r].x);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (m != -INFINITY) {
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float2 x = sml[w * 16 + r];
+      const float f = ex2(x.x - m);
+      const float4 v = *reinterpret_cast<const float4*>(so + (w * 16 + r) * D + c4 * 4);
+      l += f * x.y;
+      acc.x += f * v.x;
+      acc.y += f * v.y;
+      acc.z += f * v.z;
+      acc.w += f * v.w;
+    }
+  }
+  return acc;
+}
+
+template <typename T, int D>
+__device__ __forceinline__ void write_row(const RowsArgs& a, const Unit& u, int r, int c4,
+                                          const float4& acc, float m, float l) {
+  const int G = a.Hq / a.Hkv, R = u.r0 + r;
+  const int64_t row = (int64_t)(u.tok0 + R / G) * a.Hq + u.kv * G + R % G;
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + row * D + c4 * 4) =
+      make_uint2(Pair<T>::pack(acc.x * inv, acc.y * inv), Pair<T>::pack(acc.z * inv, acc.w * inv));
+  if (a.lse && c4 == 0) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+}
+
+// Clusters: the barrier, and loads from the shared memory of CTA `rank`.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::
+                   : "memory");
+}
+__device__ __forceinline__ uint32_t far_addr(const void* p, int rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 far_float4(const void* p, int rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(far_addr(p, rank))
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 far_float2(const void* p, int rank) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];"
+               : "=f"(v.x), "=f"(v.y)
+               : "r"(far_addr(p, rank))
+               : "memory");
+  return v;
+}
+
 template <typename T, int D, bool kSparse>
 __global__ void __launch_bounds__(kThreads, 1)
-paged_rows_kernel(const PagedBatch b, const RowsArgs a, int n_rb, int unit_trips,
+paged_rows_kernel(const PagedBatch b, const RowsArgs a, int n_rb, int unit_trips, int cluster,
                   float* __restrict__ part_o, float2* __restrict__ part_ml,
                   CutUnit* __restrict__ cuts, int32_t* status) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -180,9 +244,28 @@ paged_rows_kernel(const PagedBatch b, const RowsArgs a, int n_rb, int unit_trips
   // Trips [w0, w1) of the line; `owner` (sequence or token), KV head and row
   // block of its first unit, and the unit's first trip on the line.
   long long total, w0, w1, unit_at;
+  // (With `cluster` > 0 the line is one unit and its CTAs are a cluster.)
   int C, owner, sub;                           // sub = kv * n_rb + row block
   const int subs = a.Hkv * n_rb;
-  if (kSparse) {
+  if (cluster > 0) {
+    const int u = c / cluster, rank = c % cluster;
+    owner = u / subs;
+    sub = u % subs;
+    C = gridDim.x;
+    unit_at = 0;
+    const SeqSpan sp = kSparse ? SeqSpan{} : seq_span(b, owner);
+    if (!kSparse) {
+      unit_trips = seq_trips(sp);
+      if (sub == 0 && rank == 0 && tid == 0 && (sp.bad || sp.ql > a.max_q))
+        set_status(status, TS_ERR_INVALID_ARG);
+    } else if (c == 0) {
+      for (int s = tid; s < b.n_seq; s += kThreads)
+        if (seq_span(b, s).bad) set_status(status, TS_ERR_INVALID_ARG);
+    }
+    total = unit_trips;
+    w0 = total * rank / cluster;
+    w1 = total * (rank + 1) / cluster;
+  } else if (kSparse) {
     total = (long long)b.n * subs * unit_trips;
     C = stretches(total);
     w0 = total * c / C;
@@ -246,8 +329,12 @@ paged_rows_kernel(const PagedBatch b, const RowsArgs a, int n_rb, int unit_trips
       unit_at = s_before + (long long)sub * unit_trips;
     }
   }
-  if (tid == 0) cuts[c].parts = 0;
-  if (c >= C || w0 >= w1) return;
+  if (cluster == 0) {
+    if (tid == 0) cuts[c].parts = 0;
+    if (c >= C || w0 >= w1) return;
+  } else if (total == 0) {
+    return;                                    // the whole cluster
+  }
   const float sl2 = kLog2e / sqrtf((float)D);
 
   // A place on the line: a unit, and the trips [k, k1) of it in this stretch.
@@ -396,9 +483,10 @@ paged_rows_kernel(const PagedBatch b, const RowsArgs a, int n_rb, int unit_trips
   Place ahead{owner, sub, unit_trips, unit_at, {}, 0, 0};
   enter(ahead);
   Place now = ahead;
-  bool more = true;
+  bool more = w0 < w1;                  // a cluster may have more CTAs than trips
+  if (!more) now.k1 = now.k;
   Tile held[kStages];           // tiles whose copies are on their way, oldest first
-  open_pages(ahead.u, ahead.k);
+  if (more) open_pages(ahead.u, ahead.k);
   uint32_t put = 0, got = 0;    // trips copied, trips used
   auto push = [&](Tile& into) {
     if (more) {
@@ -573,37 +661,65 @@ paged_rows_kernel(const PagedBatch b, const RowsArgs a, int n_rb, int unit_trips
     }
     __syncthreads();
     const bool starts = now.at >= w0, ends = now.at + now.trips <= w1;
+    if (cluster > 0) {
+      // ------------------------------------------------- join the cluster's CTAs
+      // Each leaves its state where its ring was; then each reads the others'
+      // for its share of the columns.
+      cp_wait<0>();
+      __syncthreads();
+      float* jo = reinterpret_cast<float*>(smem);                      // [16][D]
+      float2* jml = reinterpret_cast<float2*>(jo + 16 * D);            // [16]
+      for (int e = tid; e < u.nr * (D / 4); e += kThreads) {
+        const int r = e / (D / 4), c4 = e % (D / 4);
+        float m, l;
+        const float4 acc = join_warps<D>(so, sml, r, c4, m, l);
+        *reinterpret_cast<float4*>(jo + r * D + c4 * 4) = acc;
+        if (c4 == 0) jml[r] = make_float2(m, l);
+      }
+      cluster_sync();
+      const int rank = c % cluster;
+      for (int e = tid * cluster + rank; e < u.nr * (D / 4); e += kThreads * cluster) {
+        const int r = e / (D / 4), c4 = e % (D / 4);
+        float2 ml[kMostCluster];
+        float4 v[kMostCluster];
+#pragma unroll
+        for (int i = 0; i < kMostCluster; ++i)
+          if (i < cluster) {
+            ml[i] = far_float2(jml + r, i);
+            v[i] = far_float4(jo + r * D + c4 * 4, i);
+          }
+        float m = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int i = 0; i < kMostCluster; ++i)
+          if (i < cluster) m = fmaxf(m, ml[i].x);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (m != -INFINITY) {
+#pragma unroll
+          for (int i = 0; i < kMostCluster; ++i)
+            if (i < cluster) {
+              const float f = ex2(ml[i].x - m);
+              l += f * ml[i].y;
+              acc.x += f * v[i].x;
+              acc.y += f * v[i].y;
+              acc.z += f * v[i].z;
+              acc.w += f * v[i].w;
+            }
+        }
+        write_row<T, D>(a, u, r, c4, acc, m, l);
+      }
+      cluster_sync();                     // nobody leaves while its state is read
+      return;
+    }
     // a part that does not hold the unit's first trip takes the stretch's slot
     // 0, one that does slot 1; the latter's stretch says what is to be joined
     const int64_t slot = (int64_t)c * 2 + (starts ? 1 : 0);
     constexpr int kQuads = D / 4;
     for (int e = tid; e < u.nr * kQuads; e += kThreads) {
       const int r = e / kQuads, c4 = e % kQuads;
-      float m = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, sml[w * 16 + r].x);
-      float l = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (m != -INFINITY) {
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float2 x = sml[w * 16 + r];
-          const float f = ex2(x.x - m);
-          const float4 v = *reinterpret_cast<const float4*>(so + (w * 16 + r) * D + c4 * 4);
-          l += f * x.y;
-          acc.x += f * v.x;
-          acc.y += f * v.y;
-          acc.z += f * v.z;
-          acc.w += f * v.w;
-        }
-      }
+      float m, l;
+      const float4 acc = join_warps<D>(so, sml, r, c4, m, l);
       if (starts && ends) {
-        const int RR = u.r0 + r;
-        const int64_t row = (int64_t)(u.tok0 + RR / G) * a.Hq + u.kv * G + RR % G;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + row * D + c4 * 4) =
-            make_uint2(Pair<T>::pack(acc.x * inv, acc.y * inv), Pair<T>::pack(acc.z * inv, acc.w * inv));
-        if (a.lse && c4 == 0) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        write_row<T, D>(a, u, r, c4, acc, m, l);
       } else {
         *reinterpret_cast<float4*>(part_o + (slot * 16 + r) * D + c4 * 4) = acc;
         if (c4 == 0) part_ml[slot * 16 + r] = make_float2(m, l);
@@ -697,13 +813,25 @@ paged_rows_merge(const CutUnit* __restrict__ cuts, const float* __restrict__ par
 
 }  // namespace
 
-// One CTA a SM (the rings fill its shared memory), fewer where a stretch would
-// fall below kMinTrips trips of 128 keys.
+// One CTA a SM (the rings fill its shared memory).  Few units of few trips take
+// a cluster of CTAs each, which join in shared memory: no second kernel and no
+// workspace, worth ~4 trips (3 streams of up to 4096 rows: 9.0 -> 6 us).  Else
+// the line of all units is cut into stretches of at least kMinTrips.
 RowsPlan rows_plan(int64_t units, int rows, int d, int64_t max_keys) {
+  constexpr int64_t kJoinTrips = 4;
   RowsPlan p{};
   p.n_rb = (rows + 15) / 16;
   p.unit_trips = (int)imax64(1, (max_keys + kStep - 1) / kStep);
-  const int64_t trips = units * p.n_rb * p.unit_trips;
+  units *= p.n_rb;
+  const int64_t trips = units * p.unit_trips;
+  int64_t size = kMostCluster;
+  while (size > 1 && (units * size > kGb300Sms || size > p.unit_trips)) size >>= 1;
+  if (units * size <= kGb300Sms &&
+      (p.unit_trips + size - 1) / size <= imax64(trips / kGb300Sms, kMinTrips) + kJoinTrips) {
+    p.cluster = (int)size;
+    p.grid = (int)(units * size);
+    return p;
+  }
   p.grid = (int)imax64(1, imin64(kGb300Sms, trips / kMinTrips));
   p.cuts_bytes = align_up((size_t)p.grid * sizeof(CutUnit), 256);
   p.part_bytes = (size_t)p.grid * 2 * 16 * d * sizeof(float);
@@ -722,10 +850,18 @@ static int go_rows(const PagedBatch& b, const RowsArgs& a, const RowsPlan& p, vo
   auto kern = sparse ? paged_rows_kernel<T, D, true> : paged_rows_kernel<T, D, false>;
   cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<D>::kBytes);
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   pdl_config(&cfg, attr, dim3(p.grid), dim3(kThreads), Ring<D>::kBytes, st);
-  cudaLaunchKernelEx(&cfg, kern, b, a, p.n_rb, p.unit_trips, part_o, part_ml, cuts, status);
+  if (p.cluster > 1) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
+  cudaLaunchKernelEx(&cfg, kern, b, a, p.n_rb, p.unit_trips, p.cluster, part_o, part_ml, cuts,
+                     status);
   int rc = launch_status("paged_rows_kernel");
+  if (rc || p.cluster > 0) return rc;
   // sparse units are cut by the host's numbers: none where the CTAs divide them
   if (rc || p.grid == 1 || (sparse && (int64_t)b.n * a.Hkv * p.n_rb % p.grid == 0)) return rc;
   pdl_config(&cfg, attr, dim3(p.grid), dim3(16 * (D / 4)), 0, st);
