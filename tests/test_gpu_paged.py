@@ -255,7 +255,7 @@ def test_tokens_without_a_key_get_zero(ts):
     _check_attend(ts, b)
 
 
-@pytest.mark.parametrize("q", [1, 50])
+@pytest.mark.parametrize("q", [1, 50, 150])
 def test_large_scores(ts, q):
     """Scores of hundreds: the running maximum moves, old sums rescale."""
     b = pu.Batch([q, q], [700, 90], 4, 2, 128, 32, BF, seed=9, scale=30.0)
@@ -264,14 +264,14 @@ def test_large_scores(ts, q):
     _check_attend(ts, b)
 
 
-@pytest.mark.parametrize("q", [1, 30])
+@pytest.mark.parametrize("q", [1, 30, 200])
 def test_host_bound_on_lengths_is_only_a_hint(ts, q):
     b = pu.Batch([q] * 2, [3000, 40], 4, 2, 128, 16, BF, seed=11)
     o, lse = _check_attend(ts, b, max_kv=64)
     o2, lse2 = _check_attend(ts, b, max_kv=2999)
 
 
-@pytest.mark.parametrize("q", [1, 33])
+@pytest.mark.parametrize("q", [1, 33, 150])
 def test_without_lse_and_with_a_workspace(ts, q):
     b = pu.Batch([q] * 3, [900, 33, 2000], 8, 2, 64, 64, FP, seed=12)
     o, lse = _attend(ts, b)
@@ -283,7 +283,7 @@ def test_without_lse_and_with_a_workspace(ts, q):
     assert none is None and torch.equal(o, o2)
 
 
-@pytest.mark.parametrize("q", [1, 40])
+@pytest.mark.parametrize("q", [1, 40, 150])
 def test_attention_reports_a_bad_page(ts, q):
     b = pu.Batch([q, q], [300, 300], 4, 2, 128, 16, BF, seed=13)
     ref = b.oracle()
@@ -303,7 +303,7 @@ def test_more_new_tokens_than_announced_is_reported(ts):
     assert status_of(b) == 1
 
 
-@pytest.mark.parametrize("q", [1, 24])
+@pytest.mark.parametrize("q", [1, 24, 150])
 def test_replay_sees_new_lengths(ts, q):
     """A captured call reads lengths, offsets and tables when it is replayed,
     and two graphs may run after one another on one workspace."""
@@ -323,7 +323,7 @@ def test_replay_sees_new_lengths(ts, q):
     for g in graphs:
         with torch.cuda.graph(g):
             call()
-    for lens in ([1500, 700], [q, 1], [333, 64]):
+    for lens in ([1500, 700], [q, 1], [333, 164]):
         b.kv_lens = lens
         b.lens.copy_(torch.tensor(lens, dtype=torch.int32))
         for g in graphs:
@@ -333,15 +333,79 @@ def test_replay_sees_new_lengths(ts, q):
             pu.check_attention(o, lse, b.oracle(), BF, 128, p_round=P_ROUND[BF])
 
 
-@pytest.mark.parametrize("q", [1, 40])
+@pytest.mark.parametrize("q", [1, 40, 300])
 def test_another_stream_and_repeatability(ts, q):
-    b = pu.Batch([q, q, q], [2100, 64, 800], 8, 2, 128, 32, BF, seed=16)
+    b = pu.Batch([q, q, q], [2100, max(q, 64), 800], 8, 2, 128, 32, BF, seed=16)
     o, lse = _attend(ts, b)
     st = torch.cuda.Stream()
     st.wait_stream(torch.cuda.current_stream())
     o2, lse2 = ts.ts_paged_attention(b.q, b.k, b.v, b.cu_q, b.lens, b.table, q, stream=st)
     st.synchronize()
     assert torch.equal(o, o2) and torch.equal(lse, lse2)      # same bits every time
+
+
+@pytest.mark.parametrize("q,Hq,Hkv,d", [(1, 2, 1, 64), (40, 2, 1, 64), (1, 5, 1, 128), (33, 4, 1, 128)])
+def test_long_cache(ts, q, Hq, Hkv, d):
+    """Hundreds of thousands of rows: many splits, pieces and partial sums."""
+    b = pu.Batch([q], [260_003], Hq, Hkv, d, 64, BF, seed=17)
+    _check_attend(ts, b)
+
+
+@pytest.mark.parametrize("q", [1, 30, 130])
+def test_pool_beyond_32_bit_offsets(ts, q):
+    """Pages whose bytes lie past 2^32: offsets are 64-bit in every kernel."""
+    b = pu.Batch([q], [500], 8, 8, 128, 128, BF, seed=18)
+    n_pages = (1 << 32) // (8 * 128 * 128 * 2) + 40            # 4.3 GB a tensor
+    k = torch.zeros(n_pages, 8, 128, 128, dtype=BF, device="cuda")
+    v = torch.zeros_like(k)
+    far = torch.arange(n_pages - 4, n_pages, device="cuda")
+    near = b.table[0, :4].long()
+    k[far], v[far] = b.k[near], b.v[near]
+    table = b.table.clone()
+    table[0, :4] = far.int()
+    ref = b.oracle()
+    o, lse = ts.ts_paged_attention(b.q, k, v, b.cu_q, b.lens, table, q, status=b.status)
+    assert status_of(b) == 0
+    pu.check_attention(o, lse, ref, BF, 128, p_round=P_ROUND[BF])
+    pages = torch.arange(4, dtype=torch.int32, device="cuda").expand(q, 8, 4).contiguous()
+    counts = torch.full((q, 8), 4, dtype=torch.int32, device="cuda")
+    rows = torch.arange(500 - q, 500, device="cuda")
+    counts = (rows // 128 + 1).int()[:, None].expand(q, 8).contiguous()
+    o, lse = ts.ts_paged_attention_selected(b.q, k, v, b.cu_q, b.lens, table, pages, counts,
+                                            status=b.status)
+    assert status_of(b) == 0
+    pu.check_attention(o, lse, ref, BF, 128)
+    mn, mx = k[far].amin(2), k[far].amax(2)
+    kmin, kmax = (torch.zeros(n_pages, 8, 128, dtype=BF, device="cuda") for _ in range(2))
+    freqs, _ = ts.ts_rope_frequencies(128)
+    x = torch.randn(q, 8, 128, device="cuda").to(BF)
+    ts.ts_paged_rope_append(b.q, x, x, b.cu_q, b.lens, table, k, v, freqs, key_min=kmin,
+                            key_max=kmax, status=b.status)
+    assert status_of(b) == 0
+    slot = torch.arange(500 - q, 500, device="cuda")
+    assert torch.equal(v[far[slot // 128], :, slot % 128], x)
+    assert (kmax[far[3]] >= k[far[3], :, :500 - 384].amax(1)).all() or q < 116
+
+
+def test_batch_of_nothing(ts):
+    """No new token anywhere, and no sequence at all."""
+    b = pu.Batch([0, 0], [40, 0], 4, 2, 64, 16, BF, extra=3)
+    o = torch.full_like(b.q, 5.0)
+    ts.ts_paged_attention(b.q, b.k, b.v, b.cu_q, b.lens, b.table, 1, o=o, want_lse=False,
+                          status=b.status)
+    ts.ts_paged_attention(b.q, b.k, b.v, b.cu_q, b.lens, b.table, 3, o=o, want_lse=False,
+                          status=b.status)
+    x = torch.zeros(3, 2, 64, dtype=BF, device="cuda")
+    k0 = b.k.clone()
+    freqs, _ = ts.ts_rope_frequencies(64)
+    ts.ts_paged_rope_append(b.q, x, x, b.cu_q, b.lens, b.table, b.k, b.v, freqs, q_out=o,
+                            status=b.status)
+    assert status_of(b) == 0
+    assert (o == 5.0).all() and torch.equal(k0.view(torch.int16), b.k.view(torch.int16))
+    none = b.q[:0]
+    o, lse = ts.ts_paged_attention(none, b.k, b.v, torch.zeros(1, dtype=torch.int32, device="cuda"),
+                                   b.lens[:0], b.table[:0], 1)
+    assert o.shape == (0, 4, 64) and lse.shape == (0, 4)
 
 
 # ------------------------------------------------------------------ choice of pages
