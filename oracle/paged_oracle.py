@@ -132,7 +132,8 @@ def select_pages(q, key_min, key_max, cu_q, seq_lens, table, ps, n_top, n_sink, 
                     qs = q[t, kv * G:(kv + 1) * G]
                     with np.errstate(all="ignore"):
                         x = np.float32(np.maximum(qs * mn, qs * mx).sum())
-                    score[j] = x if np.isfinite(x) else np.float32(-np.inf)
+                    good = np.isfinite(x) and np.isfinite(mn).all() and np.isfinite(mx).all()
+                    score[j] = x if good else np.float32(-np.inf)
                 best = sorted(score, key=lambda j: (-score[j], j))[:n_top]
                 kept = list(range(n_sink)) + sorted(best) + list(range(vis - n_recent, vis))
             counts[t, kv] = len(kept)

@@ -9,16 +9,22 @@
 // Kept: the first n_sink and the last n_recent pages a token sees and the
 // n_top best between them, by (score desc, page asc).
 //
-// The scores decide which whole numbers come out, so they must not depend on
-// the order of a sum: they are formed to about 2^-45 and rounded to fp32
-// once.  Query sums are split into a part of 12 bits, whose product with a
-// 16-bit element is exact in fp32, and the rest; the exact products are added
-// with the rounding error of every addition kept beside the sum (Knuth's
-// two-sum).
-//
-// Two launches: scores (memory bound: 4 d bytes a page and KV head; 8 lanes a
-// page, packed fp32 pairs), then per (token, KV head) a radix selection of
-// the n_top-th key and an ordered write.
+// The scores decide which whole numbers come out, so the choice must not hang
+// on the order of a sum: it is that of the sums formed to about 2^-45 and
+// rounded to fp32 once.  But only pages near the cut need them so well:
+//   scores  every page's sum in plain fp32 (memory bound: 4 d bytes a page and
+//           KV head; 8 lanes a page, packed fp32 pairs), and its largest bound
+//           |m|: the sum is off by less than (20 + G) 2^-24 sum|u| max|m|.
+//   pick    per (token, KV head) the n_top-th largest of them, T.  With delta
+//           the largest such error, a page above T + 3 delta is kept and one
+//           below T - 3 delta is not, whatever the errors; when more are left
+//           than places, the pages between are formed well (query sums split
+//           into a part of 12 bits, whose product with a 16-bit element is
+//           exact in fp32, and the rest; the rounding error of every addition
+//           kept beside the sum, Knuth's two-sum) and ranked again.  With
+//           scores that are not made to tie that is rarely a page.
+// Forming every page's sum well made the first kernel bound by fp32 arithmetic:
+// 39 us for 16 streams of up to 3200 pages (8 KV heads, d = 128).
 #include "paged.cuh"
 #include "tc_ptx.cuh"
 
@@ -28,23 +34,24 @@ namespace {
 
 constexpr int kScoreThreads = 128;
 constexpr int kPickThreads = 512;
+constexpr int kPickWarps = kPickThreads / 32;
 constexpr int kBinBits = 11, kBins = 1 << kBinBits;
-static_assert(kPickThreads / 32 <= 32, "one warp scans the warps' sums");
 constexpr int kPickSmemKeys = 48 * 1024;     // larger candidate lists stay in the workspace
 constexpr uint32_t kLowest = 0x007FFFFFu;    // float_key(-inf)
+constexpr uint32_t kKept = 0xFFFFFFFFu, kDropped = 0u;   // beyond every score's key
+constexpr int kPickList = 64;                // close pages ranked against each other
+static_assert(kPickWarps <= 32, "one warp scans the warps' sums");
 
 // s + e += p, the sum's rounding error kept in e
-__device__ __forceinline__ void two_sum(uint64_t& s, uint64_t& e, uint64_t p) {
-  const uint64_t t = ptx::add2(s, p);
-  const uint64_t bb = ptx::sub2(t, s);
-  e = ptx::add2(e, ptx::add2(ptx::sub2(s, ptx::sub2(t, bb)), ptx::sub2(p, bb)));
-  s = t;
-}
-__device__ __forceinline__ void two_sum1(float& s, float& e, float p) {
+__device__ __forceinline__ void two_sum(float& s, float& e, float p) {
   const float t = __fadd_rn(s, p);
   const float bb = __fsub_rn(t, s);
   e = __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, bb)), __fsub_rn(p, bb)));
   s = t;
+}
+
+__device__ __forceinline__ float key_float(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
 // What one token chooses from: pages [lo, hi) compete for n_top places (none
@@ -65,13 +72,15 @@ __device__ __forceinline__ Span span_of(const SeqSpan& sp, int t, int shift, int
   return r;
 }
 
+// Per page: .x the score's key, .y the largest |bound| (fp32 bits).  Per
+// (token, KV head): weight = sum |u|.
 template <typename T, int D>
 __global__ void __launch_bounds__(kScoreThreads)
 paged_score_kernel(const PagedBatch b, const T* __restrict__ q, const T* __restrict__ key_min,
                    const T* __restrict__ key_max, int Hq, int Hkv, int n_top, int n_sink,
-                   int n_recent, int per_block, uint32_t* __restrict__ keys, int32_t* status) {
-  // query sums: [positive, negative][12-bit part, rest][column]
-  __shared__ __align__(16) float qs[2][2][D];
+                   int n_recent, int per_block, uint2* __restrict__ scores,
+                   float* __restrict__ weight, int32_t* status) {
+  __shared__ __align__(16) float us[2][D];      // query sums: positive, negative parts
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int t = blockIdx.y, kv = blockIdx.z, G = Hq / Hkv;
   griddep_wait();
@@ -85,39 +94,39 @@ paged_score_kernel(const PagedBatch b, const T* __restrict__ q, const T* __restr
   const int p1 = min(w.hi, p0 + per_block);
   if (p0 >= p1) return;
   for (int c = tid; c < D; c += kScoreThreads) {
-    float up = 0.f, upe = 0.f, dn = 0.f, dne = 0.f;
+    float up = 0.f, dn = 0.f;
     for (int g = 0; g < G; ++g) {
       const float x = Pair<T>::one(q[((int64_t)t * Hq + kv * G + g) * D + c]);
-      two_sum1(up, upe, fmaxf(x, 0.f));
-      two_sum1(dn, dne, fminf(x, 0.f));
+      up += fmaxf(x, 0.f);
+      dn += fminf(x, 0.f);
     }
-    // 12 leading bits: the product with an 11-bit element is exact
-    const float uh = __uint_as_float(__float_as_uint(up) & 0xFFFFF000u);
-    const float dh = __uint_as_float(__float_as_uint(dn) & 0xFFFFF000u);
-    qs[0][0][c] = uh;
-    qs[0][1][c] = (up - uh) + upe;
-    qs[1][0][c] = dh;
-    qs[1][1][c] = (dn - dh) + dne;
+    us[0][c] = up;
+    us[1][c] = dn;
   }
   __syncthreads();
+  if (blockIdx.x == 0 && warp == 0) {
+    float sum = 0.f;
+    for (int c = lane; c < D; c += 32) sum += us[0][c] - us[1][c];
+    sum = warp_sum(sum);
+    if (lane == 0) weight[(int64_t)t * Hkv + kv] = sum;
+  }
   // lane: page lane / 8 of the warp's four, 16-byte chunks sub and sub + 8
   constexpr int kCh = D / 64;
   const int sub = lane & 7;
-  uint64_t uh[kCh][4], ul[kCh][4], dh[kCh][4], dl[kCh][4];
+  uint64_t up[kCh][4], dn[kCh][4];
 #pragma unroll
   for (int x = 0; x < kCh; ++x)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int c = (sub + 8 * x) * 8 + 2 * i;
-      uh[x][i] = *reinterpret_cast<const uint64_t*>(&qs[0][0][c]);
-      ul[x][i] = *reinterpret_cast<const uint64_t*>(&qs[0][1][c]);
-      dh[x][i] = *reinterpret_cast<const uint64_t*>(&qs[1][0][c]);
-      dl[x][i] = *reinterpret_cast<const uint64_t*>(&qs[1][1][c]);
+      up[x][i] = *reinterpret_cast<const uint64_t*>(&us[0][c]);
+      dn[x][i] = *reinterpret_cast<const uint64_t*>(&us[1][c]);
     }
   const int32_t* trow = b.table + (int64_t)s * b.max_pages;
-  uint32_t* out = keys + ((int64_t)t * Hkv + kv) * b.max_pages;
-  // a page's rows are on their way while the page before is summed, its pool
-  // page while the one before that is
+  uint2* out = scores + ((int64_t)t * Hkv + kv) * b.max_pages;
+  // the rows of kDeep trips are on their way while a page is summed, the pool
+  // pages of the trip behind them too
+  constexpr int kDeep = 2;
   struct Rows {
     uint4 mx[kCh], mn[kCh];
     bool ok;
@@ -126,6 +135,7 @@ paged_score_kernel(const PagedBatch b, const T* __restrict__ q, const T* __restr
   auto ask = [&](int pg, int ph) {
     Rows r;
     r.ok = pg < p1;
+    if (!r.ok) return r;
     if (ph < 0 || ph >= b.n_pages) {
       if (sub == 0) set_status(status, TS_ERR_INVALID_ARG);
       r.ok = false;
@@ -142,16 +152,23 @@ paged_score_kernel(const PagedBatch b, const T* __restrict__ q, const T* __restr
   };
   const int first = p0 + warp * 4 + (lane >> 3);
   constexpr int kEach = kScoreThreads / 8;           // pages a trip
-  Rows next = ask(first, pool_page(first));
-  int ph_next = pool_page(first + kEach);
+  Rows next[kDeep];
+  int ph = pool_page(first);
+#pragma unroll
+  for (int x = 0; x < kDeep; ++x) {
+    const int behind = pool_page(first + (x + 1) * kEach);
+    next[x] = ask(first + x * kEach, ph);
+    ph = behind;
+  }
   for (int base = p0; base < p1; base += kEach) {    // the same trips for every lane
     const int pg = base + (first - p0);
-    const Rows r = next;
-    if (base + kEach < p1) {
-      next = ask(pg + kEach, ph_next);
-      ph_next = pool_page(pg + 2 * kEach);
-    }
-    uint64_t sum = 0, err = 0, sum2 = 0, err2 = 0;
+    const Rows r = next[0];
+#pragma unroll
+    for (int x = 0; x + 1 < kDeep; ++x) next[x] = next[x + 1];
+    next[kDeep - 1] = ask(pg + kDeep * kEach, ph);
+    ph = pool_page(pg + (kDeep + 1) * kEach);
+    uint64_t s1 = 0, s2 = 0;
+    uint32_t top = 0;                                // largest |bound| of either half, as bits
 #pragma unroll
     for (int x = 0; x < kCh; ++x) {
       const uint32_t wx[4] = {r.mx[x].x, r.mx[x].y, r.mx[x].z, r.mx[x].w};
@@ -159,44 +176,152 @@ paged_score_kernel(const PagedBatch b, const T* __restrict__ q, const T* __restr
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float2 fx = Pair<T>::unpack(wx[k]), fn = Pair<T>::unpack(wn[k]);
-        const uint64_t px = ptx::f2(fx.x, fx.y), pn = ptx::f2(fn.x, fn.y);
-        two_sum(sum, err, ptx::mul2(uh[x][k], px));
-        err = ptx::fma2(ul[x][k], px, err);
-        two_sum(sum2, err2, ptx::mul2(dh[x][k], pn));
-        err2 = ptx::fma2(dl[x][k], pn, err2);
+        s1 = ptx::fma2(up[x][k], ptx::f2(fx.x, fx.y), s1);
+        s2 = ptx::fma2(dn[x][k], ptx::f2(fn.x, fn.y), s2);
+        top = __vimax3_u16x2(top, wx[k] & 0x7FFF7FFFu, wn[k] & 0x7FFF7FFFu);
       }
     }
-    two_sum(sum, err, sum2);
-    err = ptx::add2(err, err2);
-    float s0, s1, e0, e1;
-    ptx::f2_split(sum, s0, s1);
-    ptx::f2_split(err, e0, e1);
-    e0 += e1;
-    two_sum1(s0, e0, s1);
+    float a0, a1;
+    ptx::f2_split(ptx::add2(s1, s2), a0, a1);
+    float score = a0 + a1;
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) {
-      const float so = __shfl_xor_sync(0xffffffffu, s0, o);
-      const float eo = __shfl_xor_sync(0xffffffffu, e0, o);
-      e0 += eo;
-      two_sum1(s0, e0, so);
+      score += __shfl_xor_sync(0xffffffffu, score, o);
+      top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
     }
-    const float score = s0 + e0;
-    if (sub == 0 && pg < p1)
-      out[pg] = r.ok && isfinite(score) ? float_key(score) : kLowest;   // not finite: last
+    if (sub == 0 && pg < p1) {
+      const uint32_t m16 = max(top & 0xFFFFu, top >> 16);
+      const float m = Pair<T>::unpack(m16).x;
+      const bool good = r.ok && isfinite(score) && isfinite(m);     // the others rank last
+      out[pg] = make_uint2(good ? float_key(score) : kLowest, good ? __float_as_uint(m) : 0u);
+    }
   }
 }
 
+// The candidates' keys: in shared memory, or in the workspace (stride 2).
+struct Keys {
+  uint32_t* p;
+  int stride;
+  __device__ __forceinline__ uint32_t get(int i) const { return p[(int64_t)i * stride]; }
+  __device__ __forceinline__ void set(int i, uint32_t x) const { p[(int64_t)i * stride] = x; }
+};
+
+// Where the n_top-th largest key lies: the keys x with x - low in [at, at +
+// 2^shift) are the last bin, of which `need` are kept (all when it holds no
+// more).
+struct Cut {
+  uint32_t low, at;
+  int shift, need;
+  __device__ __forceinline__ bool above(uint32_t x) const {
+    const uint32_t d = x - low;
+    return d >= at && shift < 32 && (d - at) >> shift != 0;
+  }
+  __device__ __forceinline__ bool in(uint32_t x) const {
+    const uint32_t d = x - low;
+    return d >= at && (shift == 32 || (d - at) >> shift == 0);
+  }
+};
+
+struct PickSmem {
+  int hist[kBins];
+  int scan_a[kPickWarps], scan_b[kPickWarps];
+  uint32_t low, high, bin, widest;
+  int need, in;
+  int listed, list[kPickList];               // close pages, and their keys formed well
+  uint32_t listed_key[kPickList];
+};
+
+// Selection 11 bits a pass from the highest bit in which the keys differ
+// (scores share sign and exponent: their leading bits would put them all in one
+// bin).  Whole block; low and high: the block's least and largest key.
+__device__ Cut find_cut(PickSmem& sm, const Keys& keys, int m, int n_top, uint32_t low,
+                        uint32_t high) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  Cut c{low, 0, 32 - __clz(high - low), n_top};     // shift 0: all keys are equal
+  int in_bin = m;
+  while (c.shift > 0 && c.need < in_bin) {
+    const int step = min(c.shift, kBinBits), down = c.shift - step;
+    for (int i = tid; i < kBins; i += kPickThreads) sm.hist[i] = 0;
+    __syncthreads();
+    for (int i = tid; i < m; i += kPickThreads) {
+      const uint32_t d = keys.get(i) - low - c.at;  // wraps for smaller keys
+      if (c.shift == 32 || d >> c.shift == 0) atomicAdd(&sm.hist[d >> down], 1);
+    }
+    __syncthreads();
+    // thread: its bins, largest first
+    constexpr int kOwn = kBins / kPickThreads;
+    int cnt[kOwn], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+      cnt[i] = sm.hist[kBins - 1 - (tid * kOwn + i)];
+      sum += cnt[i];
+    }
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    if (lane == 31) sm.scan_a[warp] = inc;
+    __syncthreads();
+    int above = inc - sum + warp_sum_int(lane < warp ? sm.scan_a[lane] : 0);
+    if (above < c.need && c.need <= above + sum) {
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i) {
+        if (above < c.need && c.need <= above + cnt[i]) {
+          sm.bin = kBins - 1 - (tid * kOwn + i);
+          sm.need = c.need - above;
+          sm.in = cnt[i];
+        }
+        above += cnt[i];
+      }
+    }
+    __syncthreads();
+    c.at += sm.bin << down;
+    c.need = sm.need;
+    in_bin = sm.in;
+    c.shift = down;
+  }
+  return c;
+}
+
+// The score's key formed well, by a warp (all lanes return it).  qs: query sums
+// [positive, negative][12-bit part, rest][column].
+template <typename T, int D>
+__device__ uint32_t exact_key(const float (*qs)[2][D], const T* mn, const T* mx, int lane) {
+  float s = 0.f, e = 0.f;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    const int c = lane + 32 * i;
+    const float x = Pair<T>::one(mx[c]), n = Pair<T>::one(mn[c]);
+    two_sum(s, e, __fmul_rn(qs[0][0][c], x));
+    e = fmaf(qs[0][1][c], x, e);
+    two_sum(s, e, __fmul_rn(qs[1][0][c], n));
+    e = fmaf(qs[1][1][c], n, e);
+  }
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float so = __shfl_xor_sync(0xffffffffu, s, o), eo = __shfl_xor_sync(0xffffffffu, e, o);
+    e += eo;
+    two_sum(s, e, so);
+  }
+  const float score = s + e;
+  const uint32_t k = isfinite(score) ? float_key(score) : kLowest;
+  return __shfl_sync(0xffffffffu, k, 0);      // the lanes' sums may differ in the last place
+}
+
+template <typename T, int D>
 __global__ void __launch_bounds__(kPickThreads)
-paged_pick_kernel(const PagedBatch b, const uint32_t* __restrict__ keys, int Hkv, int n_top,
-                  int n_sink, int n_recent, int smem_keys, int32_t* __restrict__ pages,
+paged_pick_kernel(const PagedBatch b, const T* __restrict__ q, const T* __restrict__ key_min,
+                  const T* __restrict__ key_max, uint2* __restrict__ scores,
+                  const float* __restrict__ weight, int Hq, int Hkv, int n_top, int n_sink,
+                  int n_recent, int smem_keys, int32_t* __restrict__ pages,
                   int32_t* __restrict__ counts) {
   extern __shared__ uint32_t held[];
-  __shared__ int hist[kBins];
-  __shared__ int scan_gt[kPickThreads / 32], scan_eq[kPickThreads / 32];
-  __shared__ uint32_t s_low, s_high, s_bin;
-  __shared__ int s_need, s_in;
+  __shared__ PickSmem sm;
+  __shared__ float qs[2][2][D];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int t = blockIdx.x, kv = blockIdx.y;
+  const int t = blockIdx.x, kv = blockIdx.y, G = Hq / Hkv;
   const int N = n_sink + n_top + n_recent;
   griddep_wait();
   griddep_launch_dependents();
@@ -204,8 +329,9 @@ paged_pick_kernel(const PagedBatch b, const uint32_t* __restrict__ keys, int Hkv
   if (s < 0) return;
   const SeqSpan sp = seq_span(b, s);
   const Span w = span_of(sp, t, b.page_shift, n_top, n_sink, n_recent);
-  int32_t* out = pages + ((int64_t)t * Hkv + kv) * N;
-  if (tid == 0) counts[(int64_t)t * Hkv + kv] = min(w.vis, N);
+  const int64_t unit = (int64_t)t * Hkv + kv;
+  int32_t* out = pages + unit * N;
+  if (tid == 0) counts[unit] = min(w.vis, N);
   if (w.lo == w.hi) {
     // every visible page fits (w.hi > w.lo otherwise: vis > N)
     for (int i = tid; i < N; i += kPickThreads) out[i] = i < w.vis ? i : -1;
@@ -215,99 +341,153 @@ paged_pick_kernel(const PagedBatch b, const uint32_t* __restrict__ keys, int Hkv
   for (int i = tid; i < n_recent; i += kPickThreads) out[n_sink + n_top + i] = w.hi + i;
   if (n_top == 0) return;
   const int m = w.hi - w.lo;                       // candidates; m > n_top
-  const uint32_t* src = keys + ((int64_t)t * Hkv + kv) * b.max_pages + w.lo;
-  const uint32_t* key = src;
-  if (tid == 0) {
-    s_low = 0xFFFFFFFFu;
-    s_high = 0u;
-  }
-  __syncthreads();
-  uint32_t low = 0xFFFFFFFFu, high = 0u;
+  uint2* src = scores + unit * b.max_pages + w.lo;
+  const bool near = m <= smem_keys;
+  const Keys keys{near ? held : reinterpret_cast<uint32_t*>(src), near ? 1 : 2};
+  auto bounds = [&](uint32_t low, uint32_t high, uint32_t widest) {
+    low = __reduce_min_sync(0xffffffffu, low);
+    high = __reduce_max_sync(0xffffffffu, high);
+    widest = __reduce_max_sync(0xffffffffu, widest);
+    __syncthreads();
+    if (tid == 0) {
+      sm.low = 0xFFFFFFFFu;
+      sm.high = sm.widest = 0u;
+    }
+    __syncthreads();
+    if (lane == 0) {
+      atomicMin(&sm.low, low);
+      atomicMax(&sm.high, high);
+      atomicMax(&sm.widest, widest);
+    }
+    __syncthreads();
+  };
+  uint32_t low = 0xFFFFFFFFu, high = 0u, widest = 0u;
   for (int i = tid; i < m; i += kPickThreads) {
-    const uint32_t x = src[i];
-    if (m <= smem_keys) held[i] = x;
-    low = min(low, x);
-    high = max(high, x);
+    const uint2 x = src[i];
+    if (near) held[i] = x.x;
+    low = min(low, x.x);
+    high = max(high, x.x);
+    widest = max(widest, x.y);                     // magnitudes order as their bits
   }
-  if (m <= smem_keys) key = held;
-  low = __reduce_min_sync(0xffffffffu, low);
-  high = __reduce_max_sync(0xffffffffu, high);
+  const float u = weight[unit];
+  // the query sums, should a page have to be formed well
+  for (int c = tid; c < D; c += kPickThreads) {
+    float up = 0.f, upe = 0.f, dn = 0.f, dne = 0.f;
+#pragma unroll 4
+    for (int g = 0; g < G; ++g) {
+      const float x = Pair<T>::one(q[((int64_t)t * Hq + kv * G + g) * D + c]);
+      two_sum(up, upe, fmaxf(x, 0.f));
+      two_sum(dn, dne, fminf(x, 0.f));
+    }
+    // 12 leading bits: the product with an 11-bit element is exact
+    const float uh = __uint_as_float(__float_as_uint(up) & 0xFFFFF000u);
+    const float dh = __uint_as_float(__float_as_uint(dn) & 0xFFFFF000u);
+    qs[0][0][c] = uh;
+    qs[0][1][c] = (up - uh) + upe;
+    qs[1][0][c] = dh;
+    qs[1][1][c] = (dn - dh) + dne;
+  }
+  if (tid == 0) sm.listed = 0;
+  bounds(low, high, widest);
+  Cut cut = find_cut(sm, keys, m, n_top, sm.low, sm.high);
+  // pages that may be on either side of the cut
+  const float delta = 3.f * (20.f + G) * 5.9604645e-8f * u * __uint_as_float(sm.widest);
+  const uint32_t bin0 = cut.low + cut.at;
+  const uint32_t bin1 = cut.shift == 32 ? 0xFFFFFFFFu : bin0 + ((1u << cut.shift) - 1u);
+  const float from = key_float(bin0) - delta, to = key_float(min(bin1, sm.high)) + delta;
+  auto side = [&](uint32_t x) {                    // 2: kept, 1: near the cut, 0: not kept
+    const float f = key_float(x);
+    return f > to ? 2 : f < from ? 0 : 1;
+  };
+  int over = 0, close = 0;
+  for (int i = tid; i < m; i += kPickThreads) {
+    const int x = side(keys.get(i));
+    over += x == 2;
+    if (x == 1) {
+      ++close;
+      const int at = atomicAdd(&sm.listed, 1);
+      if (at < kPickList) sm.list[at] = i;
+    }
+  }
+  over = __reduce_add_sync(0xffffffffu, over);
+  close = __reduce_add_sync(0xffffffffu, close);
+  __syncthreads();                                 // the sums' places were read in find_cut
   if (lane == 0) {
-    atomicMin(&s_low, low);
-    atomicMax(&s_high, high);
+    sm.scan_a[warp] = over;
+    sm.scan_b[warp] = close;
   }
   __syncthreads();
-  // The n_top-th largest key, 11 bits a pass from the highest bit in which the
-  // keys differ (scores share sign and exponent: their leading bits would put
-  // them all in one bin).  The keys x - low of the bin found so far lie in
-  // [at, at + 2^shift); `need` of them are kept, and all if there are no more.
-  low = s_low;
-  int shift = 32 - __clz(s_high - low);              // 0: all keys are equal
-  uint32_t at = 0;
-  int need = n_top, in_bin = m;
-  while (shift > 0 && need < in_bin) {
-    const int step = min(shift, kBinBits), down = shift - step;
-    for (int i = tid; i < kBins; i += kPickThreads) hist[i] = 0;
-    __syncthreads();
-    for (int i = tid; i < m; i += kPickThreads) {
-      const uint32_t d = key[i] - low - at;          // wraps for smaller keys
-      if (shift == 32 || d >> shift == 0) atomicAdd(&hist[d >> down], 1);
+  over = warp_sum_int(lane < kPickWarps ? sm.scan_a[lane] : 0);
+  close = warp_sum_int(lane < kPickWarps ? sm.scan_b[lane] : 0);
+  const int32_t* trow = b.table + (int64_t)s * b.max_pages + w.lo;
+  auto formed = [&](int i) {
+    const int64_t row = ((int64_t)trow[i] * Hkv + kv) * D;
+    return exact_key<T, D>(qs, key_min + row, key_max + row, lane);
+  };
+  const bool all_close = over + close <= n_top;
+  const bool few = !all_close && close <= kPickList;
+  if (few) {
+    // rank the close ones against each other: the best take the places left
+    for (int a = warp; a < close; a += kPickWarps) {
+      const int i = sm.list[a];
+      const uint32_t x = keys.get(i);
+      // a page that ranks last has no score to form
+      const uint32_t k = x == kLowest ? x : formed(i);
+      if (lane == 0) sm.listed_key[a] = k;
     }
     __syncthreads();
-    // thread: four bins, largest first
-    int c[kBins / kPickThreads], sum = 0;
-#pragma unroll
-    for (int i = 0; i < kBins / kPickThreads; ++i) {
-      c[i] = hist[kBins - 1 - (tid * (kBins / kPickThreads) + i)];
-      sum += c[i];
+    bool best = false;
+    int mine = 0;
+    if (tid < close) {
+      mine = sm.list[tid];
+      const uint32_t k = sm.listed_key[tid];
+      int before = 0;
+      for (int a = 0; a < close; ++a)
+        before += sm.listed_key[a] > k || (sm.listed_key[a] == k && sm.list[a] < mine);
+      best = before < n_top - over;
     }
-    int inc = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += x;
-    }
-    if (lane == 31) scan_gt[warp] = inc;
     __syncthreads();
-    int above = inc - sum;
-    {
-      const int x = lane < warp ? scan_gt[lane] : 0;
-      above += warp_sum_int(x);
-    }
-    if (above < need && need <= above + sum) {
-#pragma unroll
-      for (int i = 0; i < kBins / kPickThreads; ++i) {
-        if (above < need && need <= above + c[i]) {
-          s_bin = kBins - 1 - (tid * (kBins / kPickThreads) + i);
-          s_need = need - above;
-          s_in = c[i];
-        }
-        above += c[i];
+    if (tid < close) keys.set(mine, best ? kKept : kDropped);
+    __syncthreads();
+  } else if (!all_close) {
+    // form all close ones well and rank everything again: kept pages first, the
+    // others last
+    low = 0xFFFFFFFFu;
+    high = 0u;
+    for (int base = warp * 32; base < m; base += kPickThreads) {
+      const int i = base + lane;
+      uint32_t x = i < m ? keys.get(i) : kDropped;
+      const int where = i < m ? side(x) : 0;
+      if (where != 1) x = where == 2 ? kKept : kDropped;
+      unsigned todo = __ballot_sync(0xffffffffu, where == 1 && x != kLowest);
+      while (todo) {
+        const int l = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const uint32_t k = formed(base + l);
+        if (lane == l) x = k;
+      }
+      if (i < m) {
+        keys.set(i, x);
+        low = min(low, x);
+        high = max(high, x);
       }
     }
-    __syncthreads();
-    at += s_bin << down;
-    need = s_need;
-    in_bin = s_in;
-    shift = down;
+    bounds(low, high, 0u);
+    cut = find_cut(sm, keys, m, n_top, sm.low, sm.high);
   }
-  // kept: keys above the bin, and the bin's first `need` (of equal keys, or all
-  // of it); thread tid owns a run of candidates, so ranks follow from one scan
-  auto above_bin = [&](uint32_t x) {
-    const uint32_t d = x - low;
-    return d >= at && shift < 32 && (d - at) >> shift != 0;
-  };
-  auto of_bin = [&](uint32_t x) {
-    const uint32_t d = x - low;
-    return d >= at && (shift == 32 || (d - at) >> shift == 0);
+  // ordered write; thread tid owns a run of candidates, so ranks follow from
+  // one scan: all close pages where they fit, else what the second cut says
+  const bool ranked = !all_close && !few;
+  auto kept = [&](uint32_t x) {
+    return ranked ? cut.above(x) : few ? x == kKept || (x != kDropped && side(x) == 2) : side(x) != 0;
   };
   const int per = (m + kPickThreads - 1) / kPickThreads;
   const int i0 = min(tid * per, m), i1 = min(i0 + per, m);
   int gt = 0, eq = 0;
   for (int i = i0; i < i1; ++i) {
-    const uint32_t x = key[i];
-    gt += above_bin(x);
-    eq += of_bin(x);
+    const uint32_t x = keys.get(i);
+    gt += kept(x);
+    eq += ranked && cut.in(x);
   }
   int ig = gt, ie = eq;
 #pragma unroll
@@ -318,34 +498,45 @@ paged_pick_kernel(const PagedBatch b, const uint32_t* __restrict__ keys, int Hkv
       ie += y;
     }
   }
+  __syncthreads();
   if (lane == 31) {
-    scan_gt[warp] = ig;
-    scan_eq[warp] = ie;
+    sm.scan_a[warp] = ig;
+    sm.scan_b[warp] = ie;
   }
   __syncthreads();
-  int g = ig - gt, q = ie - eq;                    // before this thread's run
-  g += warp_sum_int(lane < warp ? scan_gt[lane] : 0);
-  q += warp_sum_int(lane < warp ? scan_eq[lane] : 0);
+  // kept and in the bin before this thread's run
+  int g = ig - gt + warp_sum_int(lane < warp ? sm.scan_a[lane] : 0);
+  int e = ie - eq + warp_sum_int(lane < warp ? sm.scan_b[lane] : 0);
+  const int need = ranked ? cut.need : 0;
   for (int i = i0; i < i1; ++i) {
-    const uint32_t x = key[i];
-    const bool over = above_bin(x), same = of_bin(x);
-    if (over || (same && q < need)) out[n_sink + g + min(q, need)] = w.lo + i;
-    g += over;
-    q += same;
+    const uint32_t x = keys.get(i);
+    const bool is_over = kept(x), same = ranked && cut.in(x);
+    if (is_over || (same && e < need)) out[n_sink + g + min(e, need)] = w.lo + i;
+    g += is_over;
+    e += same;
   }
+}
+
+size_t scores_bytes(int n, int Hkv, int max_pages) {
+  return align_up((size_t)n * Hkv * max_pages * sizeof(uint2), 256);
 }
 
 }  // namespace
 
 size_t paged_select_ws_bytes(int n, int Hkv, int max_pages) {
-  return align_up((size_t)n * Hkv * max_pages * sizeof(uint32_t), 256);
+  return scores_bytes(n, Hkv, max_pages) + align_up((size_t)n * Hkv * sizeof(float), 256);
 }
 
-int launch_paged_select(const PagedBatch& b, const void* q, const void* key_min,
-                        const void* key_max, int Hq, int Hkv, int d, bool fp16, int n_top,
-                        int n_sink, int n_recent, int32_t* pages, int32_t* counts, void* ws,
-                        int32_t* status, cudaStream_t st) {
-  uint32_t* keys = static_cast<uint32_t*>(ws);
+template <typename T, int D>
+static int go_select(const PagedBatch& b, const void* q, const void* key_min, const void* key_max,
+                     int Hq, int Hkv, int n_top, int n_sink, int n_recent, int32_t* pages,
+                     int32_t* counts, void* ws, int32_t* status, cudaStream_t st) {
+  uint2* scores = static_cast<uint2*>(ws);
+  float* weight =
+      reinterpret_cast<float*>(static_cast<char*>(ws) + scores_bytes(b.n, Hkv, b.max_pages));
+  const T* qt = static_cast<const T*>(q);
+  const T* mn = static_cast<const T*>(key_min);
+  const T* mx = static_cast<const T*>(key_max);
   // pages a block: enough that the query sums and the first loads' latency are
   // spread over several trips of 16 pages, while the SMs have blocks to overlap
   int per_block = 256;
@@ -354,30 +545,31 @@ int launch_paged_select(const PagedBatch& b, const void* q, const void* key_min,
     per_block >>= 1;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  auto score = [&](auto kern, auto* type) {
-    using T = std::remove_pointer_t<decltype(type)>;
-    pdl_config(&cfg, attr,
-               dim3((b.max_pages + per_block - 1) / per_block, b.n, Hkv), dim3(kScoreThreads), 0,
-               st);
-    cudaLaunchKernelEx(&cfg, kern, b, static_cast<const T*>(q), static_cast<const T*>(key_min),
-                       static_cast<const T*>(key_max), Hq, Hkv, n_top, n_sink, n_recent, per_block,
-                       keys, status);
-  };
-  if (fp16)
-    d == 128 ? score(paged_score_kernel<__half, 128>, (__half*)nullptr)
-             : score(paged_score_kernel<__half, 64>, (__half*)nullptr);
-  else
-    d == 128 ? score(paged_score_kernel<__nv_bfloat16, 128>, (__nv_bfloat16*)nullptr)
-             : score(paged_score_kernel<__nv_bfloat16, 64>, (__nv_bfloat16*)nullptr);
+  pdl_config(&cfg, attr, dim3((b.max_pages + per_block - 1) / per_block, b.n, Hkv),
+             dim3(kScoreThreads), 0, st);
+  cudaLaunchKernelEx(&cfg, paged_score_kernel<T, D>, b, qt, mn, mx, Hq, Hkv, n_top, n_sink,
+                     n_recent, per_block, scores, weight, status);
   int rc = launch_status("paged_score_kernel");
   if (rc) return rc;
   const int smem_keys = b.max_pages < kPickSmemKeys ? b.max_pages : kPickSmemKeys;
-  cudaFuncSetAttribute(paged_pick_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaFuncSetAttribute(paged_pick_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                        kPickSmemKeys * 4);
   pdl_config(&cfg, attr, dim3(b.n, Hkv), dim3(kPickThreads), (size_t)smem_keys * 4, st);
-  cudaLaunchKernelEx(&cfg, paged_pick_kernel, b, (const uint32_t*)keys, Hkv, n_top, n_sink,
-                     n_recent, smem_keys, pages, counts);
+  cudaLaunchKernelEx(&cfg, paged_pick_kernel<T, D>, b, qt, mn, mx, scores, (const float*)weight, Hq,
+                     Hkv, n_top, n_sink, n_recent, smem_keys, pages, counts);
   return launch_status("paged_pick_kernel");
+}
+
+int launch_paged_select(const PagedBatch& b, const void* q, const void* key_min,
+                        const void* key_max, int Hq, int Hkv, int d, bool fp16, int n_top,
+                        int n_sink, int n_recent, int32_t* pages, int32_t* counts, void* ws,
+                        int32_t* status, cudaStream_t st) {
+  auto go = [&](auto run) {
+    return run(b, q, key_min, key_max, Hq, Hkv, n_top, n_sink, n_recent, pages, counts, ws, status,
+               st);
+  };
+  if (fp16) return d == 128 ? go(go_select<__half, 128>) : go(go_select<__half, 64>);
+  return d == 128 ? go(go_select<__nv_bfloat16, 128>) : go(go_select<__nv_bfloat16, 64>);
 }
 
 }  // namespace ts

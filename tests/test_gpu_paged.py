@@ -452,6 +452,30 @@ def test_select_ties_go_to_the_lowest_page(ts):
     _check_select(ts, b, 9, 1, 2, zero, zero)  # every score equal
 
 
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_select_scores_close_to_the_cut(ts, dtype, d):
+    """Pages that differ from one another by a step of one bound: the sums lie
+    within fp32's rounding of each other, and only well formed ones rank them."""
+    b = pu.Batch([1, 2], [6000, 2500], 6, 2, d, 16, dtype, seed=34)
+    mn, mx = _bounds(b, 35)
+    g = torch.Generator().manual_seed(36)
+    one = mx[:1].clone()
+    mx[:] = one
+    mn[:] = mn[:1].clone()
+    # every page: one column of the maximum a step or two away
+    col = torch.randint(0, d, (b.n_pages, 2), generator=g).cuda()
+    step = (1 + torch.randint(0, 2, (b.n_pages, 2), generator=g).cuda()).to(torch.int16)
+    bits = mx.view(torch.int16)
+    pg = torch.arange(b.n_pages, device="cuda")[:, None].expand(-1, 2)
+    hd = torch.arange(2, device="cuda")[None, :].expand(b.n_pages, -1)
+    bits[pg, hd, col] = bits[pg, hd, col] + step
+    small = (b.q.float() * 0.003).to(dtype)
+    b.q = torch.where(torch.rand(b.q.shape, generator=g).cuda() < 0.7, small, b.q)
+    for top in (1, 30, 100):
+        _check_select(ts, b, top, 1, 1, mn, mx)
+
+
 def test_select_scores_that_cancel(ts):
     """Sums of large terms that cancel to small scores: a plain fp32 sum would
     order many pages differently."""
@@ -470,8 +494,7 @@ def test_select_scores_that_are_not_finite_rank_last(ts):
     b = pu.Batch([1], [1600], 4, 1, 64, 16, BF, seed=26)
     mn, mx = _bounds(b, 27)
     for i, x in ((3, float("nan")), (17, float("inf")), (40, float("-inf"))):
-        mx[int(b.table_host[0, i]), 0, 5] = x
-        mn[int(b.table_host[0, i]), 0, 5] = x
+        (mn if i == 40 else mx)[int(b.table_host[0, i]), 0, 5] = x
     pages, _ = _check_select(ts, b, 30, 1, 1, mn, mx)
     assert not {3, 17, 40} & set(pages[0, 0].tolist())
     # chosen only when nothing better is left, lowest first
