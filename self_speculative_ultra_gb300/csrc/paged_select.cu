@@ -323,12 +323,31 @@ paged_pick_kernel(const PagedBatch b, const T* __restrict__ q, const T* __restri
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int t = blockIdx.x, kv = blockIdx.y, G = Hq / Hkv;
   const int N = n_sink + n_top + n_recent;
+  // The score kernel lets this one start only when all that came before is
+  // complete, so what it reads as well may be read ahead of its end.
+  const int s = warp_find_seq(b, t, lane);
+  const SeqSpan sp = seq_span(b, max(s, 0));
+  const Span w = span_of(sp, t, b.page_shift, n_top, n_sink, n_recent);
+  // the query sums, should a page have to be formed well
+  for (int c = tid; c < D; c += kPickThreads) {
+    float up = 0.f, upe = 0.f, dn = 0.f, dne = 0.f;
+#pragma unroll 4
+    for (int g = 0; g < G; ++g) {
+      const float x = Pair<T>::one(q[((int64_t)t * Hq + kv * G + g) * D + c]);
+      two_sum(up, upe, fmaxf(x, 0.f));
+      two_sum(dn, dne, fminf(x, 0.f));
+    }
+    // 12 leading bits: the product with an 11-bit element is exact
+    const float uh = __uint_as_float(__float_as_uint(up) & 0xFFFFF000u);
+    const float dh = __uint_as_float(__float_as_uint(dn) & 0xFFFFF000u);
+    qs[0][0][c] = uh;
+    qs[0][1][c] = (up - uh) + upe;
+    qs[1][0][c] = dh;
+    qs[1][1][c] = (dn - dh) + dne;
+  }
   griddep_wait();
   griddep_launch_dependents();
-  const int s = warp_find_seq(b, t, lane);
   if (s < 0) return;
-  const SeqSpan sp = seq_span(b, s);
-  const Span w = span_of(sp, t, b.page_shift, n_top, n_sink, n_recent);
   const int64_t unit = (int64_t)t * Hkv + kv;
   int32_t* out = pages + unit * N;
   if (tid == 0) counts[unit] = min(w.vis, N);
@@ -362,6 +381,7 @@ paged_pick_kernel(const PagedBatch b, const T* __restrict__ q, const T* __restri
     __syncthreads();
   };
   uint32_t low = 0xFFFFFFFFu, high = 0u, widest = 0u;
+#pragma unroll 8
   for (int i = tid; i < m; i += kPickThreads) {
     const uint2 x = src[i];
     if (near) held[i] = x.x;
@@ -370,23 +390,6 @@ paged_pick_kernel(const PagedBatch b, const T* __restrict__ q, const T* __restri
     widest = max(widest, x.y);                     // magnitudes order as their bits
   }
   const float u = weight[unit];
-  // the query sums, should a page have to be formed well
-  for (int c = tid; c < D; c += kPickThreads) {
-    float up = 0.f, upe = 0.f, dn = 0.f, dne = 0.f;
-#pragma unroll 4
-    for (int g = 0; g < G; ++g) {
-      const float x = Pair<T>::one(q[((int64_t)t * Hq + kv * G + g) * D + c]);
-      two_sum(up, upe, fmaxf(x, 0.f));
-      two_sum(dn, dne, fminf(x, 0.f));
-    }
-    // 12 leading bits: the product with an 11-bit element is exact
-    const float uh = __uint_as_float(__float_as_uint(up) & 0xFFFFF000u);
-    const float dh = __uint_as_float(__float_as_uint(dn) & 0xFFFFF000u);
-    qs[0][0][c] = uh;
-    qs[0][1][c] = (up - uh) + upe;
-    qs[1][0][c] = dh;
-    qs[1][1][c] = (dn - dh) + dne;
-  }
   if (tid == 0) sm.listed = 0;
   bounds(low, high, widest);
   Cut cut = find_cut(sm, keys, m, n_top, sm.low, sm.high);
