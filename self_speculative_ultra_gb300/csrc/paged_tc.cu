@@ -828,16 +828,29 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
         if (items > 0) ok = ptx::mbar_wait(&aux->q_empty, (items - 1) & 1u, wait_limit);
         ok = __all_sync(0xffffffffu, ok && !aux->abort_flag);
         if (!ok) break;
-#pragma unroll 4
-        for (int e = t; e < kM * kCh; e += 128) {
-          const int r = e / kCh, c = e % kCh, R = w.r0 + r;
+        // thread: 16-byte chunk c of every kHop-th row; (token, head) of its row
+        // advance without a division a row
+        constexpr int kHop = 128 / kCh;
+        const int c = t % kCh;
+        int R = w.r0 + t / kCh, tok = R / G, head = R - tok * G;
+        const int dt = kHop / G, dh = kHop - dt * G;
+        const T* src = q + ((int64_t)w.q0 * Hq + w.kv * G) * D + c * 8;
+        const uint32_t dst = ptx::smem_u32(sq) + (c >> 3) * Ly::kPanel;
+#pragma unroll 8
+        for (int r = t / kCh; r < kM; r += kHop) {
           const bool live = R < w.rows;
-          const int64_t row = live ? (int64_t)(w.q0 + R / G) * Hq + w.kv * G + R % G : 0;
-          const uint32_t dst = ptx::smem_u32(sq + (r >> 7) * Ly::kTile + (c >> 3) * Ly::kPanel +
-                                             (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4));
+          const T* from = live ? src + ((int64_t)tok * Hq + head) * D : q;
           const int n = live ? 16 : 0;
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
-                       "l"(q + row * D + c * 8), "r"(n));
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                           dst + (r >> 7) * Ly::kTile + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4)),
+                       "l"(from), "r"(n));
+          R += kHop;
+          tok += dt;
+          head += dh;
+          if (head >= G) {
+            head -= G;
+            ++tok;
+          }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         ptx::fence_proxy_async_smem();
@@ -1043,7 +1056,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       if (!warp_rows) continue;
       const int64_t row = (int64_t)(w.q0 + R / G) * Hq + w.kv * G + R % G;
       const bool cut = w.slot >= 0;
-      const int64_t pr = ((int64_t)w.slot * Hkv + w.kv) * kM + g * 128 + tr;
+      const int64_t piece = (int64_t)w.slot * Hkv + w.kv;
       const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
@@ -1058,9 +1071,11 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
         if (!valid) continue;
         // a row that has seen nothing has P = 0 and l = 0: O = 0
         if (cut) {
-          uint4* dst = reinterpret_cast<uint4*>(part_o + pr * D + c * 32);
+          // a piece's O by column quads, rows inside: a warp's stores are contiguous
+          uint4* dst = reinterpret_cast<uint4*>(part_o) + piece * (kM * D / 4) + (c * 8) * kM + g * 128 + tr;
 #pragma unroll
-          for (int y = 0; y < 8; ++y) dst[y] = make_uint4(x[4 * y], x[4 * y + 1], x[4 * y + 2], x[4 * y + 3]);
+          for (int y = 0; y < 8; ++y)
+            dst[y * kM] = make_uint4(x[4 * y], x[4 * y + 1], x[4 * y + 2], x[4 * y + 3]);
         } else {
           auto h2 = [&](int y) {
             return Pair<T>::pack(__uint_as_float(x[y]) * inv, __uint_as_float(x[y + 1]) * inv);
@@ -1072,7 +1087,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
         }
       }
       if (valid) {
-        if (cut) part_ml[pr] = make_float2(m_used, l);
+        if (cut) part_ml[piece * kM + g * 128 + tr] = make_float2(m_used, l);
         else if (lse) lse[row] = l > 0.f ? (m_used + log2f(l)) * kLn2 : -INFINITY;
       }
       // O has been read before this warp's next P is announced
@@ -1090,35 +1105,34 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
 }
 
 // -------------------------------------------------------------------- join
-// The rows of cut tiles, four neighbouring rows at a time: 8 lanes a row, D / 8
-// columns a lane, so that the loads of four rows are in flight together.  Where
-// there are CTAs enough, a CTA takes four rows and its warps share the pieces
-// (48 tokens in 76 pieces: 50 us with a warp alone on them); else a warp does.
+// The rows of cut tiles, 32 neighbouring rows at a time, a row a lane and
+// kPart columns a thread: a piece's O lies by column quads, rows inside, so a
+// warp's loads are contiguous.  A CTA's warps take the D / kPart column parts of
+// the rows, or where there are CTAs enough, the pieces of one part among them.
 template <typename T, int D>
 __global__ void __launch_bounds__(256, 4)
 paged_tc_merge(const PagedBatch b, const Header* __restrict__ hdr, const int4* __restrict__ cuts,
                int Hq, int Hkv, int max_q, const float* __restrict__ part_o,
                const float2* __restrict__ part_ml, T* __restrict__ o, float* __restrict__ lse) {
-  constexpr int kWarps = 8;
-  __shared__ float4 s_o[kWarps][4][D / 4];
-  __shared__ float2 s_ml[kWarps][4];
+  constexpr int kWarps = 8, kPart = 16, kQuads = kPart / 4, kParts = D / kPart;
+  __shared__ float4 s_o[kWarps][kQuads][32];
+  __shared__ float2 s_ml[kWarps][32];
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & 7, G = Hq / Hkv;
-  const int64_t total = (int64_t)__ldcg(&hdr->n_cut) * Hkv * (kM / 4);
-  constexpr int kQuads = D / 32;          // 16-byte columns a lane
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = Hq / Hkv;
+  // units: (cut tile, KV head, 32 rows, part)
+  const int64_t total = (int64_t)__ldcg(&hdr->n_cut) * Hkv * (kM / 32) * kParts;
   const bool shared = total <= gridDim.x;
   const int64_t first = shared ? blockIdx.x : (int64_t)blockIdx.x * kWarps + warp;
   const int64_t hop = shared ? gridDim.x : (int64_t)gridDim.x * kWarps;
   for (int64_t u = first; u < total; u += hop) {
-    const int r = (int)(u % (kM / 4)) * 4 + (lane >> 3), kv = (int)(u / (kM / 4) % Hkv);
-    const int4 c = __ldcg(&cuts[u / (kM / 4) / Hkv]);    // sequence, tile, first slot, pieces
+    const int part = (int)(u % kParts), r = (int)(u / kParts % (kM / 32)) * 32 + lane;
+    const int kv = (int)(u / kParts / (kM / 32) % Hkv);
+    const int4 c = __ldcg(&cuts[u / kParts / (kM / 32) / Hkv]);   // sequence, tile, slot, pieces
     const SeqSpan sp = seq_span(b, c.x);
     const int R = c.y * kM + r;
-    const bool live = R < min(sp.ql, max_q) * G;         // the same for a row's 8 lanes
-    if (!__any_sync(0xffffffffu, live)) continue;        // and for the CTA's warps, if shared
-    const int64_t p0 = ((int64_t)c.z * Hkv + kv) * kM + r, step = (int64_t)Hkv * kM;
-    const int np = live ? c.w : 0;
+    const bool live = R < min(sp.ql, max_q) * G;
+    if (!__any_sync(0xffffffffu, live)) continue;        // the same for the CTA's warps, if shared
     const int i0 = shared ? warp : 0, di = shared ? kWarps : 1;
     float4 acc[kQuads];
     float l = 0.f, m = -INFINITY;
@@ -1139,37 +1153,44 @@ paged_tc_merge(const PagedBatch b, const Header* __restrict__ hdr, const int4* _
       m = mn;
     };
 #pragma unroll 2
-    for (int i = i0; i < np; i += di) {
-      const float2 ml = __ldcg(&part_ml[p0 + i * step]);
-      const float4* p = reinterpret_cast<const float4*>(part_o + (p0 + i * step) * D) + sub;
+    for (int i = i0; i < c.w; i += di) {
+      const int64_t piece = (int64_t)(c.z + i) * Hkv + kv;
+      float2 ml = make_float2(-INFINITY, 0.f);
       float4 v[kQuads];
+      if (live) {
+        ml = __ldcg(&part_ml[piece * kM + r]);
+        const float4* p = reinterpret_cast<const float4*>(part_o) + piece * (kM * D / 4) +
+                          (int64_t)(part * kQuads) * kM + r;
 #pragma unroll
-      for (int x = 0; x < kQuads; ++x) v[x] = __ldcg(p + 8 * x);
-      add(ml.x, ml.y, v);
+        for (int x = 0; x < kQuads; ++x) v[x] = __ldcg(p + x * kM);
+        add(ml.x, ml.y, v);
+      }
     }
     if (shared) {
 #pragma unroll
-      for (int x = 0; x < kQuads; ++x) s_o[warp][lane >> 3][sub + 8 * x] = acc[x];
-      if (sub == 0) s_ml[warp][lane >> 3] = make_float2(m, l);
+      for (int x = 0; x < kQuads; ++x) s_o[warp][x][lane] = acc[x];
+      s_ml[warp][lane] = make_float2(m, l);
       __syncthreads();
       if (warp > 0) continue;                            // one unit a CTA: no trip follows
       for (int w = 1; w < kWarps; ++w) {
         float4 v[kQuads];
 #pragma unroll
-        for (int x = 0; x < kQuads; ++x) v[x] = s_o[w][lane >> 3][sub + 8 * x];
-        const float2 ml = s_ml[w][lane >> 3];
+        for (int x = 0; x < kQuads; ++x) v[x] = s_o[w][x][lane];
+        const float2 ml = s_ml[w][lane];
         add(ml.x, ml.y, v);
       }
     }
     if (!live) continue;
     const float inv = l > 0.f ? 1.f / l : 0.f;
     const int64_t row = (int64_t)(sp.q0 + R / G) * Hq + kv * G + R % G;
-    uint2* dst = reinterpret_cast<uint2*>(o + row * D) + sub;
+    uint4* dst = reinterpret_cast<uint4*>(o + row * D + part * kPart);
 #pragma unroll
-    for (int x = 0; x < kQuads; ++x)
-      dst[8 * x] = make_uint2(Pair<T>::pack(acc[x].x * inv, acc[x].y * inv),
-                              Pair<T>::pack(acc[x].z * inv, acc[x].w * inv));
-    if (lse && sub == 0) lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    for (int x = 0; x < kQuads; x += 2)
+      dst[x / 2] = make_uint4(Pair<T>::pack(acc[x].x * inv, acc[x].y * inv),
+                              Pair<T>::pack(acc[x].z * inv, acc[x].w * inv),
+                              Pair<T>::pack(acc[x + 1].x * inv, acc[x + 1].y * inv),
+                              Pair<T>::pack(acc[x + 1].z * inv, acc[x + 1].w * inv));
+    if (lse && part == 0) lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
   }
 }
 
@@ -1272,8 +1293,9 @@ TcPlan tc_plan(int n, int n_seq, int Hq, int Hkv, int d, int max_q, int64_t max_
   p.max_slots = (int)(slots * Hkv);
   p.max_entries = (int)(tiles + slots);
   p.grid = (int)imin64(kGb300Sms, (int64_t)p.max_entries * Hkv);
-  // four rows a warp, eight warps a CTA; a cut tile has at least two pieces
-  p.merge_grid = (int)imin64(8 * kGb300Sms, imax64(1, slots * Hkv * kM / 64));
+  // units of 32 rows and 16 columns, eight warps a CTA; a cut tile has at least
+  // two pieces
+  p.merge_grid = (int)imin64(8 * kGb300Sms, imax64(1, slots * Hkv * (kM / 32) * (d / 16) / 2));
   size_t at = 256;
   auto take = [&](size_t bytes) {
     const size_t r = at;
