@@ -194,7 +194,7 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int max_q, int max_tiles, 
   __syncthreads();
   // Which tiles to cut, and how far: the first `whole` of the order stay, the
   // others go into pieces of at most `per` steps.  Candidates: no cut, and
-  // whole rounds over the SMs (none, all but one, all) x 30 piece lengths.
+  // whole rounds over the SMs (none, all, all but one) x 8 to 15 piece lengths.
   // A candidate's time in key steps is at least its work spread evenly, and at
   // least what its longest chain takes.  Pieces of about one length go in
   // rounds, behind the rounds of whole tiles; others end half a piece ragged.
@@ -207,64 +207,63 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int max_q, int max_tiles, 
     const int rounds = n_tiles * Hkv / C;
     float best = INFINITY;
     int best_whole = n_tiles, best_per = longest;
-    for (int cand = warp; cand < 64; cand += 32) {
-      int w = n_tiles, p = longest;
-      if (cand > 0) {
-        // 32 piece lengths without whole tiles, 16 behind all and all but one round
-        const int kind = cand < 32 ? 0 : 1 + (cand & 1), step = cand < 32 ? cand : (cand - 32) / 2;
-        const int keep = kind == 0 ? 0 : kind == 1 ? rounds : rounds - 1;
-        if (keep < 0 || (kind > 0 && keep == 0)) continue;
-        w = min(n_tiles, keep * C / Hkv);
-        if (w == n_tiles) continue;
-        // 2 .. 12 parts, then growing by about a fifth to 384
-        const int parts = step < 11 ? step + 2 : (int)(12.f * exp2f((step - 11) * 0.25f));
+    // one candidate a warp: 16 without whole tiles (the first without a cut),
+    // 8 behind all and 8 behind all but one round
+    int w = n_tiles, p = longest;
+    const int kind = warp < 16 ? 0 : warp < 24 ? 1 : 2;
+    const int keep = kind == 0 ? 0 : rounds + 1 - kind;
+    const bool valid = warp == 0 || kind == 0 || keep > 0;
+    if (valid && warp > 0) {
+      w = min(n_tiles, keep * C / Hkv);
+      if (w < n_tiles) {
+        constexpr unsigned char kParts[16] = {1, 2, 3, 4, 5, 6, 7, 8, 10, 13, 17, 24, 36, 54, 76, 120};
+        const int parts = kParts[kind == 0 ? warp : (warp & 7) + 1];
         // no tile of the rest is longer than its first's class
         const int top = min(longest, sorted[w].z + longest / 255 + 1);
         p = (top + parts - 1) / parts;
       }
-      // pieces_of without its division (the quotient put right, as the slots are
-      // counted by it); the lengths only feed the estimate
-      const float inv = 1.f / p;
-      int n_pieces = 0, n_cut = 0;
-      float low = longest, high = 0.f;
-      for (int i = w + lane; i < n_tiles; i += 32) {
-        const int steps = sorted[i].z;
-        int np = (int)(steps * inv);
-        np += np * p < steps;
-        np -= (np - 1) * p >= steps;
-        np = max(np, 1);
-        n_pieces += np;
-        if (np > 1) n_cut += np;
-        const float len = __fdividef((float)steps, (float)np);
-        low = fminf(low, len);
-        high = fmaxf(high, len);
-      }
-      const float shortest = -warp_max(-low), widest = warp_max(high);
-      n_pieces = __reduce_add_sync(0xffffffffu, n_pieces);
-      n_cut = __reduce_add_sync(0xffffffffu, n_cut);
-      if ((long long)n_cut * Hkv > max_slots) continue;
-      const float cost = kFixed + (n_cut ? kCut : 0.f);
-      const float even = ((float)s_total * Hkv + (float)(n_pieces + w) * Hkv * kFixed +
-                          (float)n_cut * Hkv * kCut) / C;
-      // longest chain of whole tiles: k + 1 of them where the order's item
-      // k C is the k-th to follow
-      float chain = 0.f;
-      if (lane * C < w * Hkv) chain = (lane + 1) * (sorted[lane * C / Hkv].z + kFixed);
-      chain = warp_max(chain);
-      const float pieces = (float)((n_pieces * Hkv + C - 1) / C) * (widest + cost);
-      float e = fmaxf(even, chain) + (n_cut ? kCut : 0.f);
-      if (w < n_tiles) {
-        const bool equal = w == 0 || sorted[w - 1].z * 10 >= sorted[0].z * 9;
-        if (!equal || shortest * 10.f < widest * 9.f)
-          e = fmaxf(e, even + 0.5f * widest);
-        else
-          e = fmaxf(e, (w ? (float)((w * Hkv + C - 1) / C) * (sorted[0].z + kFixed) : 0.f) + pieces);
-      }
-      if (e < best) {
-        best = e;
-        best_whole = w;
-        best_per = p;
-      }
+    }
+    // pieces_of without its division (the quotient put right, as the slots are
+    // counted by it); the lengths only feed the estimate
+    const float inv = 1.f / p;
+    int n_pieces = 0, n_cut = 0;
+    float low = longest, high = 0.f;
+    for (int i = w + lane; i < n_tiles; i += 32) {
+      const int steps = sorted[i].z;
+      int np = (int)(steps * inv);
+      np += np * p < steps;
+      np -= (np - 1) * p >= steps;
+      np = max(np, 1);
+      n_pieces += np;
+      if (np > 1) n_cut += np;
+      const float len = __fdividef((float)steps, (float)np);
+      low = fminf(low, len);
+      high = fmaxf(high, len);
+    }
+    const float shortest = -warp_max(-low), widest = warp_max(high);
+    n_pieces = __reduce_add_sync(0xffffffffu, n_pieces);
+    n_cut = __reduce_add_sync(0xffffffffu, n_cut);
+    const float cost = kFixed + (n_cut ? kCut : 0.f);
+    const float even = ((float)s_total * Hkv + (float)(n_pieces + w) * Hkv * kFixed +
+                        (float)n_cut * Hkv * kCut) / C;
+    // longest chain of whole tiles: k + 1 of them where the order's item
+    // k C is the k-th to follow
+    float chain = 0.f;
+    if (lane * C < w * Hkv) chain = (lane + 1) * (sorted[lane * C / Hkv].z + kFixed);
+    chain = warp_max(chain);
+    const float pieces = (float)((n_pieces * Hkv + C - 1) / C) * (widest + cost);
+    float e = fmaxf(even, chain) + (n_cut ? kCut : 0.f);
+    if (w < n_tiles) {
+      const bool equal = w == 0 || sorted[w - 1].z * 10 >= sorted[0].z * 9;
+      if (!equal || shortest * 10.f < widest * 9.f)
+        e = fmaxf(e, even + 0.5f * widest);
+      else
+        e = fmaxf(e, (w ? (float)((w * Hkv + C - 1) / C) * (sorted[0].z + kFixed) : 0.f) + pieces);
+    }
+    if (valid && (long long)n_cut * Hkv <= max_slots) {
+      best = e;
+      best_whole = w;
+      best_per = p;
     }
     if (lane == 0) {
       est[warp] = best;
@@ -1110,7 +1109,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
 // warp's loads are contiguous.  A CTA's warps take the D / kPart column parts of
 // the rows, or where there are CTAs enough, the pieces of one part among them.
 template <typename T, int D>
-__global__ void __launch_bounds__(256, 4)
+__global__ void __launch_bounds__(256, 2)
 paged_tc_merge(const PagedBatch b, const Header* __restrict__ hdr, const int4* __restrict__ cuts,
                int Hq, int Hkv, int max_q, const float* __restrict__ part_o,
                const float2* __restrict__ part_ml, T* __restrict__ o, float* __restrict__ lse) {
@@ -1152,19 +1151,27 @@ paged_tc_merge(const PagedBatch b, const Header* __restrict__ hdr, const int4* _
       }
       m = mn;
     };
-#pragma unroll 2
-    for (int i = i0; i < c.w; i += di) {
-      const int64_t piece = (int64_t)(c.z + i) * Hkv + kv;
-      float2 ml = make_float2(-INFINITY, 0.f);
-      float4 v[kQuads];
-      if (live) {
-        ml = __ldcg(&part_ml[piece * kM + r]);
-        const float4* p = reinterpret_cast<const float4*>(part_o) + piece * (kM * D / 4) +
-                          (int64_t)(part * kQuads) * kM + r;
+    // four pieces' loads together (rows behind the tile's last are there to be
+    // read, and go nowhere)
+    constexpr int kAtOnce = 4;
+    for (int ib = i0; ib < c.w; ib += kAtOnce * di) {
+      float2 ml[kAtOnce];
+      float4 v[kAtOnce][kQuads];
 #pragma unroll
-        for (int x = 0; x < kQuads; ++x) v[x] = __ldcg(p + x * kM);
-        add(ml.x, ml.y, v);
+      for (int j = 0; j < kAtOnce; ++j) {
+        const int i = ib + j * di;
+        if (i < c.w) {
+          const int64_t piece = (int64_t)(c.z + i) * Hkv + kv;
+          ml[j] = __ldcg(&part_ml[piece * kM + r]);
+          const float4* p = reinterpret_cast<const float4*>(part_o) + piece * (kM * D / 4) +
+                            (int64_t)(part * kQuads) * kM + r;
+#pragma unroll
+          for (int x = 0; x < kQuads; ++x) v[j][x] = __ldcg(p + x * kM);
+        }
       }
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j)
+        if (ib + j * di < c.w) add(ml[j].x, ml[j].y, v[j]);
     }
     if (shared) {
 #pragma unroll
