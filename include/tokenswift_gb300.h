@@ -61,10 +61,10 @@ int ts_version(void);
 
 /* Limit of one bounded device-side wait, in SM clock cycles, for kernels
  * launched after this call (from any thread): the verification kernel of (1)
- * gives up a wait on another warp's or the copy engine's progress after
- * `cycles` clocks, writes TS_ERR_TIMEOUT into `status`, waits for its own
- * copies and tensor-core work in flight (with the default limit), releases
- * its tensor memory and returns; that call's outputs are then undefined.
+ * and the chunk kernel of (6) give up a wait on another warp's or the copy engine's progress after
+ * `cycles` clocks, write TS_ERR_TIMEOUT into `status`, wait for their own
+ * copies and tensor-core work in flight (with the default limit), release
+ * their tensor memory and return; that call's outputs are then undefined.
  * `cycles` <= 0 restores the default, 2^31 cycles (about one second).  A
  * small limit exists to exercise the expiry path; the paper has no
  * counterpart.  Returns TS_OK. */
@@ -487,7 +487,8 @@ int ts_ngram_build_tree(const int32_t* table, int V, int cap, const int32_t* roo
  *          seq_lens[s] - q_len + i.
  * Table    page_table [n_seq, max_pages] int32: row p of sequence s is row
  *          p % page_size of page page_table[s][p / page_size].  Entries
- *          behind the sequence's last row are not read.
+ *          behind the sequence's last row are not read.  max_pages *
+ *          page_size <= 2^25 rows a sequence, n_seq <= 2^20, Hq <= 1024.
  * cu_q, seq_lens and page_table are device arrays and may change between
  * replays of a captured graph.  A value out of its range (a page id, a length
  * above max_pages * page_size, a decreasing cu_q) is reported as
@@ -546,7 +547,8 @@ int ts_rope_frequencies(int rot_dim, double base, int scaling, double factor,
  *          whose first row is written now starts over; else its bounds are
  *          widened.  (A row written again leaves its old value inside the
  *          bounds: they stay bounds.)
- * No two sequences of one call may write the same page. */
+ * No two sequences of one call may write the same page.  A token whose row
+ * would be negative (seq_lens[s] < q_len) is reported and not written. */
 int ts_paged_rope_append(const void* q, const void* k, const void* v, int64_t q_stride,
                          int64_t k_stride, int64_t v_stride, int n, int Hq, int Hkv, int d,
                          const int32_t* cu_q, const int32_t* seq_lens, int n_seq,

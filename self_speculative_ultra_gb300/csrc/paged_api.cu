@@ -26,8 +26,10 @@ int paged_batch(const char* W, int n, int Hq, int Hkv, int d, const int32_t* cu_
   if (max_pages < 1 || n_pages < 1)
     return fail(TS_ERR_INVALID_ARG, "%s: max_pages=%d, n_pages=%lld", W, max_pages,
                 (long long)n_pages);
-  if ((int64_t)max_pages * page_size >= (int64_t(1) << 30))
-    return fail(TS_ERR_UNSUPPORTED, "%s: max_pages * page_size >= 2^30", W);
+  // a wait for the work before it must stay well inside the bounded waits' second
+  if ((int64_t)max_pages * page_size > (int64_t(1) << 25))
+    return fail(TS_ERR_UNSUPPORTED, "%s: max_pages * page_size > 2^25", W);
+  if (n_seq > (1 << 20)) return fail(TS_ERR_UNSUPPORTED, "%s: n_seq=%d > 2^20", W, n_seq);
   if (n_pages >= (int64_t(1) << 31) / page_size / Hkv)
     return fail(TS_ERR_UNSUPPORTED, "%s: n_pages * Hkv * page_size >= 2^31", W);
   if ((int64_t)n * Hq >= (int64_t(1) << 31))
@@ -288,8 +290,8 @@ int ts_paged_attention_selected(const void* q, const void* k_pages, const void* 
                        n_pages, flags, TS_PAGED_FP16, &b);
   if (rc) return rc;
   if (n_sel < 1) return fail(TS_ERR_INVALID_ARG, "%s: n_sel=%d", W, n_sel);
-  if ((int64_t)n_sel * page_size >= (int64_t(1) << 30))
-    return fail(TS_ERR_UNSUPPORTED, "%s: n_sel * page_size >= 2^30", W);
+  if ((int64_t)n_sel * page_size > (int64_t(1) << 25))
+    return fail(TS_ERR_UNSUPPORTED, "%s: n_sel * page_size > 2^25", W);
   if (n == 0 || n_seq == 0) return TS_OK;
   if (!q || !k_pages || !v_pages || !pages || !counts || !o)
     return fail(TS_ERR_INVALID_ARG, "%s: NULL tensor", W);

@@ -387,6 +387,55 @@ def test_pool_beyond_32_bit_offsets(ts, q):
     assert (kmax[far[3]] >= k[far[3], :, :500 - 384].amax(1)).all() or q < 116
 
 
+@pytest.mark.parametrize("q", [1, 150])
+def test_sequences_that_share_pages(ts, q):
+    """Two sequences with the same first pages (a common prefix) and their own
+    last ones."""
+    b = pu.Batch([q, q], [640, 700], 8, 2, 128, 64, BF, seed=19)
+    b.table[1, :5] = b.table[0, :5]
+    b.table_host = b.table.cpu()
+    _check_attend(ts, b)
+
+
+@pytest.mark.parametrize("q", [1, 20, 150])
+def test_two_streams_at_once(ts, q):
+    """Calls on two streams, each with its own memory, while both run."""
+    bs = [pu.Batch([q] * 4, [3000, 900, 2500, 700], 8, 2, 128, 32, BF, seed=s) for s in (42, 43)]
+    want = [_attend(ts, b) for b in bs]
+    streams = [torch.cuda.Stream() for _ in bs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(6):
+        for i, b in enumerate(bs):
+            got[i].append(ts.ts_paged_attention(b.q, b.k, b.v, b.cu_q, b.lens, b.table, q,
+                                                stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o, lse in got[i]:
+            assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_short_wait_limit_and_the_call_behind_it(ts, d):
+    """With a limit of a few clocks the chunk kernel gives up a wait that
+    outlasts one hardware attempt, reports it, ends its copies and products and
+    returns; waits that end within an attempt leave a right result."""
+    b = pu.Batch([200], [900], 4, 2, d, 32, BF, seed=44)
+    ref = b.oracle()
+    ts.ts_set_wait_limit(1)
+    try:
+        o, lse = ts.ts_paged_attention(b.q, b.k, b.v, b.cu_q, b.lens, b.table, 200,
+                                       status=b.status)
+        torch.cuda.synchronize()
+    finally:
+        ts.ts_set_wait_limit(0)
+    assert status_of(b) in (0, 4)
+    if status_of(b) == 0:
+        pu.check_attention(o, lse, ref, BF, d, p_round=P_ROUND[BF])
+    b.status.zero_()
+    _check_attend(ts, b)
+
+
 def test_batch_of_nothing(ts):
     """No new token anywhere, and no sequence at all."""
     b = pu.Batch([0, 0], [40, 0], 4, 2, 64, 16, BF, extra=3)
@@ -531,6 +580,9 @@ def _chosen(b, counts_of, seed=0):
 def test_selected(ts, dtype, d, ps):
     b = pu.Batch([1, 2, 0, 5], [1, 900, 10, 1700], 8, 2, d, ps, dtype, seed=30 + ps, extra=1)
     pages, counts = _chosen(b, [0, 1, 3, 7, 12], seed=ps)
+    for t in range(b.n):                       # the list may come in any order
+        for h in range(b.Hkv):
+            pages[t, h, :counts[t, h]] = np.random.default_rng(t).permutation(pages[t, h, :counts[t, h]])
     o = torch.full_like(b.q, 55.0)
     lse = torch.full((b.n, 8), 55.0, device="cuda")
     ts.ts_paged_attention_selected(b.q, b.k, b.v, b.cu_q, b.lens, b.table,

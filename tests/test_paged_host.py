@@ -110,7 +110,8 @@ def _selected(ts, **kw):
 @pytest.mark.parametrize("kw,rc", [
     (dict(n=-1), 1), (dict(n_seq=-1), 1), (dict(Hq=0), 1), (dict(Hkv=0), 1), (dict(Hq=31), 1),
     (dict(Hq=2048), 2), (dict(d=96), 2), (dict(ps=48), 2), (dict(ps=8), 2), (dict(ps=256), 2),
-    (dict(maxp=0), 1), (dict(n_pages=0), 1), (dict(maxp=1 << 25), 2), (dict(n_pages=1 << 24), 2),
+    (dict(maxp=0), 1), (dict(n_pages=0), 1), (dict(maxp=(1 << 19) + 1), 2),
+    (dict(n_seq=(1 << 20) + 1), 2), (dict(n_pages=1 << 24), 2),
     (dict(n=1 << 27), 2), (dict(cu=None), 1), (dict(lens=None), 1), (dict(table=None), 1),
     (dict(flags=64), 1), (dict(q=None), 1), (dict(q=ODD), 1)],
     ids=lambda x: str(x) if isinstance(x, int) else ",".join(x))
@@ -174,7 +175,7 @@ def test_select_refusals(ts, kw, rc):
 
 
 @pytest.mark.parametrize("kw,rc", [
-    (dict(n_sel=0), 1), (dict(n_sel=1 << 25), 2), (dict(pages=None), 1), (dict(counts=None), 1)],
+    (dict(n_sel=0), 1), (dict(n_sel=(1 << 19) + 1), 2), (dict(pages=None), 1), (dict(counts=None), 1)],
     ids=str)
 def test_selected_refusals(ts, kw, rc):
     assert _selected(ts, **kw) == rc
