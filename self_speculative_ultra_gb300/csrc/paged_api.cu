@@ -64,14 +64,16 @@ int64_t bound_kv(int max_pages, int page_size, int64_t max_kv) {
 
 // Which kernel takes a dense call.  The row kernel reads the keys once a block
 // of 16 packed rows of a KV head, the tensor-core tiles once for 256 rows but
-// after a plan and with a join (~20 us in all): one block always takes the row
-// kernel, up to four where they are at most 13 trips of 128 keys a SM in all.
-// Measured: 24 rows of 2 KV heads over 32K rows 22.6 us against 26.9; 32 rows of
-// 8 KV heads over 100K rows 127 against 83.
+// after a plan and with a join (~20 us in all).  One block always takes the row
+// kernel, up to four where they are at most 13 trips of 128 keys a SM in all, any
+// number at 8.  Measured: 24 rows of 2 KV heads over 32K rows (7 a SM) 22.6 us
+// against 26.9; 6 streams of 94 tokens and at most 491 rows (24 blocks, 4 a SM)
+// 7.6 against 19.1, of 154 tokens and 1000 rows (39 blocks, 12 a SM) 29.1 against
+// 27.0; 32 rows of 8 KV heads over 100K rows (84 a SM) 127 against 83.
 bool few_rows(int n_seq, int max_q, int Hq, int Hkv, int64_t kv) {
   const int64_t blocks = ((int64_t)max_q * (Hq / Hkv) + 15) / 16;
-  return blocks <= 1 ||
-         (blocks <= 4 && (int64_t)n_seq * Hkv * blocks * ((kv + 127) / 128) <= 13 * kGb300Sms);
+  const int64_t trips = (int64_t)n_seq * Hkv * blocks * ((kv + 127) / 128);
+  return blocks <= 1 || trips <= 8 * kGb300Sms || (blocks <= 4 && trips <= 13 * kGb300Sms);
 }
 
 }  // namespace

@@ -249,13 +249,18 @@ def test_tokens_without_a_key_get_zero(ts):
     b.lens = torch.tensor(b.kv_lens, dtype=torch.int32, device="cuda")
     o, lse = _check_attend(ts, b)
     assert (o[4:4 + 29] == 0).all() and torch.isneginf(lse[4:4 + 29]).all()
+    b = pu.Batch([400, 90], [400, 90], 16, 2, 128, 16, BF, extra=1)      # tiles of rows
+    b.kv_lens = [130, 0]
+    b.lens = torch.tensor(b.kv_lens, dtype=torch.int32, device="cuda")
+    o, lse = _check_attend(ts, b)
+    assert (o[:270] == 0).all() and (o[400:490] == 0).all()
     b = pu.Batch([1, 1], [1, 30], 4, 2, 64, 16, FP)
     b.kv_lens = [0, 30]
     b.lens = torch.tensor(b.kv_lens, dtype=torch.int32, device="cuda")
     _check_attend(ts, b)
 
 
-@pytest.mark.parametrize("q", [1, 50, 150])
+@pytest.mark.parametrize("q", [1, 50, 600])
 def test_large_scores(ts, q):
     """Scores of hundreds: the running maximum moves, old sums rescale."""
     b = pu.Batch([q, q], [700, 90], 4, 2, 128, 32, BF, seed=9, scale=30.0)
@@ -271,6 +276,12 @@ def test_host_bound_on_lengths_is_only_a_hint(ts, q):
     o2, lse2 = _check_attend(ts, b, max_kv=2999)
 
 
+def test_tiles_with_a_short_hint(ts):
+    """Tiles of rows where the host's bound is far below the lengths."""
+    b = pu.Batch([160] * 8, [300, 200, 160, 1000, 170, 290, 900, 161], 16, 1, 64, 16, FP, seed=45)
+    _check_attend(ts, b, max_kv=64)
+
+
 @pytest.mark.parametrize("q", [1, 33, 150])
 def test_without_lse_and_with_a_workspace(ts, q):
     b = pu.Batch([q] * 3, [900, 33, 2000], 8, 2, 64, 64, FP, seed=12)
@@ -283,13 +294,13 @@ def test_without_lse_and_with_a_workspace(ts, q):
     assert none is None and torch.equal(o, o2)
 
 
-@pytest.mark.parametrize("q", [1, 40, 150])
-def test_attention_reports_a_bad_page(ts, q):
-    b = pu.Batch([q, q], [300, 300], 4, 2, 128, 16, BF, seed=13)
+@pytest.mark.parametrize("q,Hq", [(1, 4), (40, 4), (150, 32)])
+def test_attention_reports_a_bad_page(ts, q, Hq):
+    b = pu.Batch([q, q], [300, 300], Hq, 2, 128, 16, BF, seed=13)
     ref = b.oracle()
     b.table[0, 3] = -7
     o = torch.empty_like(b.q)
-    lse = torch.empty(b.n, 4, device="cuda")
+    lse = torch.empty(b.n, Hq, device="cuda")
     ts.ts_paged_attention(b.q, b.k, b.v, b.cu_q, b.lens, b.table, q, o=o, lse=lse, status=b.status)
     assert status_of(b) == 1
     # the other sequence is as it should be
@@ -303,7 +314,7 @@ def test_more_new_tokens_than_announced_is_reported(ts):
     assert status_of(b) == 1
 
 
-@pytest.mark.parametrize("q", [1, 24, 150])
+@pytest.mark.parametrize("q", [1, 24, 300])
 def test_replay_sees_new_lengths(ts, q):
     """A captured call reads lengths, offsets and tables when it is replayed,
     and two graphs may run after one another on one workspace."""
@@ -351,10 +362,10 @@ def test_long_cache(ts, q, Hq, Hkv, d):
     _check_attend(ts, b)
 
 
-@pytest.mark.parametrize("q", [1, 30, 130])
-def test_pool_beyond_32_bit_offsets(ts, q):
+@pytest.mark.parametrize("q,Hq", [(1, 8), (30, 8), (130, 32)])
+def test_pool_beyond_32_bit_offsets(ts, q, Hq):
     """Pages whose bytes lie past 2^32: offsets are 64-bit in every kernel."""
-    b = pu.Batch([q], [500], 8, 8, 128, 128, BF, seed=18)
+    b = pu.Batch([q], [500], Hq, 8, 128, 128, BF, seed=18)
     n_pages = (1 << 32) // (8 * 128 * 128 * 2) + 40            # 4.3 GB a tensor
     k = torch.zeros(n_pages, 8, 128, 128, dtype=BF, device="cuda")
     v = torch.zeros_like(k)
@@ -387,7 +398,7 @@ def test_pool_beyond_32_bit_offsets(ts, q):
     assert (kmax[far[3]] >= k[far[3], :, :500 - 384].amax(1)).all() or q < 116
 
 
-@pytest.mark.parametrize("q", [1, 150])
+@pytest.mark.parametrize("q", [1, 300])
 def test_sequences_that_share_pages(ts, q):
     """Two sequences with the same first pages (a common prefix) and their own
     last ones."""
@@ -420,7 +431,7 @@ def test_short_wait_limit_and_the_call_behind_it(ts, d):
     """With a limit of a few clocks the chunk kernel gives up a wait that
     outlasts one hardware attempt, reports it, ends its copies and products and
     returns; waits that end within an attempt leave a right result."""
-    b = pu.Batch([200], [900], 4, 2, d, 32, BF, seed=44)
+    b = pu.Batch([200], [900], 32, 2, d, 32, BF, seed=44)
     ref = b.oracle()
     ts.ts_set_wait_limit(1)
     try:
@@ -635,7 +646,7 @@ def test_prompt_in_chunks_then_sparse_decoding(ts, dtype):
     """A prompt enters in chunks and decoding goes on over chosen pages, every
     operator fed by the one before it; each stage is checked on the values it
     was given.  With every page chosen, the sparse form gives the dense one."""
-    Hq, Hkv, d, ps = 8, 2, 128, 16
+    Hq, Hkv, d, ps = 32, 2, 128, 16
     total = 700
     b = pu.Batch([0], [total], Hq, Hkv, d, ps, dtype, seed=40)
     b.k.fill_(float("nan"))
