@@ -83,8 +83,8 @@ __device__ __forceinline__ int pieces_of(int steps, int per) {
 }
 
 __global__ void __launch_bounds__(kPlanThreads)
-paged_plan_kernel(const PagedBatch b, int Hkv, int G, int max_q, int max_tiles, int max_entries,
-                  int max_slots, Header* hdr, int4* tiles, int4* entries, int* slots, int4* cuts,
+paged_plan_kernel(const PagedBatch b, int Hkv, int G, int D, int max_q, int max_tiles,
+                  int max_entries, int max_slots, Header* hdr, int4* tiles, int4* entries, int* slots, int4* cuts,
                   int32_t* status) {
   // the tiles as found and in order: in shared memory where they fit (every
   // pass over them otherwise waits for L2, and the plan is all latency)
@@ -95,7 +95,7 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int max_q, int max_tiles, 
   __shared__ int seq_rows[kPlanThreads];
   __shared__ int scan[32];
   __shared__ int s_max;
-  __shared__ unsigned long long s_total;
+  __shared__ unsigned long long s_total, s_keys;
   __shared__ float est[32];
   __shared__ int est_per[32], est_whole[32];
   __shared__ int hist[256];
@@ -106,18 +106,20 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int max_q, int max_tiles, 
   griddep_launch_dependents();
   if (tid == 0) {
     s_max = 0;
-    s_total = 0;
+    s_total = s_keys = 0;
   }
   for (int i = tid; i < 256; i += kPlanThreads) hist[i] = 0;
   int n_tiles = 0;
   for (int base = 0; base < b.n_seq; base += kPlanThreads) {
     const int s = base + tid;
     int cnt = 0, rows = 0;
+    unsigned long long keys = 0;
     if (s < b.n_seq) {
       const SeqSpan sp = seq_span(b, s);
       if (sp.bad || sp.ql > max_q) set_status(status, TS_ERR_INVALID_ARG);
       rows = min(sp.ql, max_q) * G;
       cnt = (rows + kM - 1) / kM;
+      if (cnt) keys = sp.kl;
     }
     int inc = cnt;
 #pragma unroll
@@ -151,9 +153,13 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int max_q, int max_tiles, 
       top = max(top, steps);
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    for (int o = 16; o > 0; o >>= 1) {
+      mine += __shfl_xor_sync(0xffffffffu, mine, o);
+      keys += __shfl_xor_sync(0xffffffffu, keys, o);
+    }
     top = __reduce_max_sync(0xffffffffu, top);
     if (lane == 0) {
+      atomicAdd(&s_keys, keys);
       atomicAdd(&s_total, mine);
       atomicMax(&s_max, top);
     }
@@ -162,11 +168,8 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int max_q, int max_tiles, 
   }
   n_tiles = min(n_tiles, max_tiles);
   const int longest = max(s_max, 1);
-  // tiles by falling cost (256 classes)
-  auto bucket = [&](int steps) { return 255 - (int)((long long)steps * 255 / longest); };
-  for (int i = tid; i < n_tiles; i += kPlanThreads) atomicAdd(&hist[bucket(tiles[i].z)], 1);
-  __syncthreads();
-  if (warp == 0) {
+  // counts of the classes -> where each class starts
+  auto starts = [&]() {
     int c[8], sum = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -185,7 +188,13 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int max_q, int max_tiles, 
       hist[lane * 8 + i] = at;
       at += c[i];
     }
-  }
+    if (lane == 31) s_entries = at;
+  };
+  // tiles by falling cost (256 classes)
+  auto bucket = [&](int steps) { return 255 - (int)((long long)steps * 255 / longest); };
+  for (int i = tid; i < n_tiles; i += kPlanThreads) atomicAdd(&hist[bucket(tiles[i].z)], 1);
+  __syncthreads();
+  if (warp == 0) starts();
   __syncthreads();
   for (int i = tid; i < n_tiles; i += kPlanThreads) {
     const int4 t = tiles[i];
@@ -202,7 +211,7 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int max_q, int max_tiles, 
   // a cut one kCut for its partial rows.
   constexpr float kFixed = 3.f, kCut = 2.f;
   const int C = kGb300Sms;
-  int whole = n_tiles, per = longest;
+  int whole = n_tiles, per = longest, stretch = 0;
   if ((long long)n_tiles * Hkv < 16 * C && longest > 1 && max_slots > 0) {
     const int rounds = n_tiles * Hkv / C;
     float best = INFINITY;
@@ -285,79 +294,156 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int max_q, int max_tiles, 
     }
     whole = est_whole[from];
     per = est_per[from];
+    // Or, where pieces of about one length would leave a round half empty, cut
+    // evenly: the tiles in a line, in equal stretches, as many a KV head as it
+    // has SMs.  The stretches stand at different keys, so K and V have to stay in
+    // L2.  (2048 tokens over 32K rows, 2 KV heads: 265 us in pieces, 253 in
+    // stretches; tiles of many lengths fill the SMs better by themselves: 9 mixed
+    // streams 120 us, 127 in stretches.)
+    const int heads = C / Hkv;
+    if (heads > 0 && sorted[n_tiles - 1].z * 10 >= longest * 9 && s_keys * Hkv * D * 4 <= (64ull << 20) &&
+        (long long)(n_tiles + heads) * Hkv <= max_slots) {
+      const int even = (int)((s_total + heads - 1) / heads);
+      if (even + 3.f * kFixed + 2.f * kCut < best) stretch = even;
+    }
   }
-  // The list: whole tiles, then the others' pieces, first pieces first, so that
-  // neighbours in time read the same keys.  at[p]: where the p-th pieces go.
-  __syncthreads();
-  if (tid < kPlanParts) at[tid] = 0;
-  if (tid == 0) s_slots = s_cut = s_most = 0;
-  __syncthreads();
-  for (int i = tid; i < n_tiles; i += kPlanThreads) {
-    const int4 t = sorted[i];
-    if (i < whole) {
-      if (i < max_entries) {
-        entries[i] = make_int4(t.x, t.y, 0, t.z);
-        slots[i] = -1;
+  if (stretch > 0) {
+    // The list: the stretches' parts of tiles, the longest first (a CTA that ends
+    // a short one early takes the longest left, so two together make a stretch).
+    // sorted[i].w: where tile i starts on the line.
+    __syncthreads();
+    if (tid < 256) hist[tid] = 0;
+    if (tid == 0) s_slots = s_cut = 0;
+    int before = 0;
+    for (int base = 0; base < n_tiles; base += kPlanThreads) {
+      const int i = base + tid, z = i < n_tiles ? sorted[i].z : 0;
+      int inc = z;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
       }
-      continue;
+      if (lane == 31) scan[warp] = inc;
+      __syncthreads();
+      const int mine_w = scan[lane];
+      if (i < n_tiles) sorted[i].w = before + inc - z;
+      const int ahead = warp_sum_int(lane < warp ? mine_w : 0);
+      if (i < n_tiles) sorted[i].w += ahead;
+      before += warp_sum_int(mine_w);
+      __syncthreads();
     }
-    const int np = pieces_of(t.z, per);
-    atomicAdd(&at[np - 1], 1);          // tiles of np pieces, for now
-    atomicMax(&s_most, np);
-    int slot = -1;
-    if (np > 1) {
-      slot = atomicAdd(&s_slots, np);
-      cuts[atomicAdd(&s_cut, 1)] = make_int4(t.x, t.y, slot, np);
+    auto cls = [&](int len) { return 255 - (int)((long long)len * 255 / stretch); };
+    // part p of the tile at [at, at + z): from the p-th cut at or before it
+    auto part = [&](int at, int z, int p, int& k0, int& k1) {
+      const int cut = (at / stretch + p) * stretch;
+      k0 = max(cut, at) - at;
+      k1 = min(cut + stretch, at + z) - at;
+    };
+    auto parts = [&](int at, int z) { return z == 0 ? 1 : (at + z - 1) / stretch - at / stretch + 1; };
+    for (int i = tid; i < n_tiles; i += kPlanThreads) {
+      const int4 t = sorted[i];
+      const int np = parts(t.w, t.z);
+      for (int p = 0; p < np; ++p) {
+        int k0, k1;
+        part(t.w, t.z, p, k0, k1);
+        atomicAdd(&hist[cls(k1 - k0)], 1);
+      }
     }
-    sorted[i].w = slot;
-  }
-  __syncthreads();
-  const int most = s_most;
-  if (warp == 0) {
-    // tiles that have a p-th piece: sums from the back; then where they start
-    int n_p[kPlanParts / 32], sum = 0;
+    __syncthreads();
+    if (warp == 0) starts();
+    __syncthreads();
+    for (int i = tid; i < n_tiles; i += kPlanThreads) {
+      const int4 t = sorted[i];
+      const int np = parts(t.w, t.z);
+      int slot = -1;
+      if (np > 1) {
+        slot = atomicAdd(&s_slots, np);
+        cuts[atomicAdd(&s_cut, 1)] = make_int4(t.x, t.y, slot, np);
+      }
+      for (int p = 0; p < np; ++p) {
+        int k0, k1;
+        part(t.w, t.z, p, k0, k1);
+        const int e = atomicAdd(&hist[cls(k1 - k0)], 1);
+        if (e >= max_entries) continue;
+        entries[e] = make_int4(t.x, t.y, k0, k1);
+        slots[e] = slot < 0 ? -1 : slot + p;
+      }
+    }
+    __syncthreads();
+  } else {
+    // The list: whole tiles, then the others' pieces, first pieces first, so that
+    // neighbours in time read the same keys.  at[p]: where the p-th pieces go.
+    __syncthreads();
+    if (tid < kPlanParts) at[tid] = 0;
+    if (tid == 0) s_slots = s_cut = s_most = 0;
+    __syncthreads();
+    for (int i = tid; i < n_tiles; i += kPlanThreads) {
+      const int4 t = sorted[i];
+      if (i < whole) {
+        if (i < max_entries) {
+          entries[i] = make_int4(t.x, t.y, 0, t.z);
+          slots[i] = -1;
+        }
+        continue;
+      }
+      const int np = pieces_of(t.z, per);
+      atomicAdd(&at[np - 1], 1);          // tiles of np pieces, for now
+      atomicMax(&s_most, np);
+      int slot = -1;
+      if (np > 1) {
+        slot = atomicAdd(&s_slots, np);
+        cuts[atomicAdd(&s_cut, 1)] = make_int4(t.x, t.y, slot, np);
+      }
+      sorted[i].w = slot;
+    }
+    __syncthreads();
+    const int most = s_most;
+    if (warp == 0) {
+      // tiles that have a p-th piece: sums from the back; then where they start
+      int n_p[kPlanParts / 32], sum = 0;
 #pragma unroll
-    for (int x = kPlanParts / 32 - 1; x >= 0; --x) {
-      sum += at[lane * (kPlanParts / 32) + x];
-      n_p[x] = sum;
-    }
-    int behind = sum;
+      for (int x = kPlanParts / 32 - 1; x >= 0; --x) {
+        sum += at[lane * (kPlanParts / 32) + x];
+        n_p[x] = sum;
+      }
+      int behind = sum;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_down_sync(0xffffffffu, behind, o);
-      if (lane + o < 32) behind += x;
-    }
-    behind -= sum;                      // tiles whose last piece is a later lane's
-    sum = 0;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_down_sync(0xffffffffu, behind, o);
+        if (lane + o < 32) behind += x;
+      }
+      behind -= sum;                      // tiles whose last piece is a later lane's
+      sum = 0;
 #pragma unroll
-    for (int x = 0; x < kPlanParts / 32; ++x) {
-      n_p[x] += behind;
-      sum += n_p[x];
-    }
-    int before = sum;
+      for (int x = 0; x < kPlanParts / 32; ++x) {
+        n_p[x] += behind;
+        sum += n_p[x];
+      }
+      int before = sum;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, before, o);
-      if (lane >= o) before += x;
-    }
-    if (lane == 31) s_entries = whole + before;
-    before += whole - sum;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += x;
+      }
+      if (lane == 31) s_entries = whole + before;
+      before += whole - sum;
 #pragma unroll
-    for (int x = 0; x < kPlanParts / 32; ++x) {
-      at[lane * (kPlanParts / 32) + x] = before;
-      before += n_p[x];
+      for (int x = 0; x < kPlanParts / 32; ++x) {
+        at[lane * (kPlanParts / 32) + x] = before;
+        before += n_p[x];
+      }
     }
-  }
-  __syncthreads();
-  for (int u = tid; u < (n_tiles - whole) * most; u += kPlanThreads) {
-    const int i = whole + u / most, p = u % most;
-    const int4 t = sorted[i];
-    const int np = pieces_of(t.z, per);
-    if (p >= np) continue;
-    const int len = (t.z + np - 1) / np, e = atomicAdd(&at[p], 1);
-    if (e >= max_entries) continue;
-    entries[e] = make_int4(t.x, t.y, min(p * len, t.z), min((p + 1) * len, t.z));
-    slots[e] = t.w < 0 ? -1 : t.w + p;
+    __syncthreads();
+    for (int u = tid; u < (n_tiles - whole) * most; u += kPlanThreads) {
+      const int i = whole + u / most, p = u % most;
+      const int4 t = sorted[i];
+      const int np = pieces_of(t.z, per);
+      if (p >= np) continue;
+      const int len = (t.z + np - 1) / np, e = atomicAdd(&at[p], 1);
+      if (e >= max_entries) continue;
+      entries[e] = make_int4(t.x, t.y, min(p * len, t.z), min((p + 1) * len, t.z));
+      slots[e] = t.w < 0 ? -1 : t.w + p;
+    }
   }
   if (tid == 0) {
     hdr->n_entries = min(s_entries, max_entries);
@@ -1266,7 +1352,7 @@ int go_tc(const PagedBatch& b, const TcArgs& a, const TcPlan& p, char* ws, int32
   cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                        kPlanTiles * 2 * sizeof(int4));
   pdl_config(&cfg, attr, dim3(1), dim3(kPlanThreads), near, st);
-  cudaLaunchKernelEx(&cfg, paged_plan_kernel, b, a.Hkv, a.Hq / a.Hkv, a.max_q, p.max_tiles,
+  cudaLaunchKernelEx(&cfg, paged_plan_kernel, b, a.Hkv, a.Hq / a.Hkv, D, a.max_q, p.max_tiles,
                      p.max_entries, p.max_slots, hdr, tiles, entries, slots, cuts, status);
   rc = launch_status("paged_plan_kernel");
   if (rc) return rc;
