@@ -191,7 +191,8 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int D, int max_q, int max_
     if (lane == 31) s_entries = at;
   };
   // tiles by falling cost (256 classes)
-  auto bucket = [&](int steps) { return 255 - (int)((long long)steps * 255 / longest); };
+  const float class_of = 255.f / longest;
+  auto bucket = [&](int steps) { return 255 - min(255, (int)(steps * class_of)); };
   for (int i = tid; i < n_tiles; i += kPlanThreads) atomicAdd(&hist[bucket(tiles[i].z)], 1);
   __syncthreads();
   if (warp == 0) starts();
@@ -227,8 +228,9 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int D, int max_q, int max_
       if (w < n_tiles) {
         constexpr unsigned char kParts[16] = {1, 2, 3, 4, 5, 6, 7, 8, 10, 13, 17, 24, 36, 54, 76, 120};
         const int parts = kParts[kind == 0 ? warp : (warp & 7) + 1];
-        // no tile of the rest is longer than its first's class
-        const int top = min(longest, sorted[w].z + longest / 255 + 1);
+        // no tile of the rest is longer than its first's class (a step more for
+        // the class's rounding)
+        const int top = min(longest, sorted[w].z + longest / 255 + 2);
         p = (top + parts - 1) / parts;
       }
     }
@@ -300,10 +302,11 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int D, int max_q, int max_
     // L2.  (2048 tokens over 32K rows, 2 KV heads: 265 us in pieces, 253 in
     // stretches; tiles of many lengths fill the SMs better by themselves: 9 mixed
     // streams 120 us, 127 in stretches.)
-    const int heads = C / Hkv;
+    const unsigned heads = C / Hkv;
     if (heads > 0 && sorted[n_tiles - 1].z * 10 >= longest * 9 && s_keys * Hkv * D * 4 <= (64ull << 20) &&
         (long long)(n_tiles + heads) * Hkv <= max_slots) {
-      const int even = (int)((s_total + heads - 1) / heads);
+      // at most 16 C tiles of 2^18 steps: below 2^31
+      const int even = (int)(((unsigned)s_total + heads - 1) / heads);
       if (even + 3.f * kFixed + 2.f * kCut < best) stretch = even;
     }
   }
@@ -332,7 +335,8 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int D, int max_q, int max_
       before += warp_sum_int(mine_w);
       __syncthreads();
     }
-    auto cls = [&](int len) { return 255 - (int)((long long)len * 255 / stretch); };
+    const float part_class = 255.f / stretch;
+    auto cls = [&](int len) { return 255 - min(255, (int)(len * part_class)); };
     // part p of the tile at [at, at + z): from the p-th cut at or before it
     auto part = [&](int at, int z, int p, int& k0, int& k1) {
       const int cut = (at / stretch + p) * stretch;
