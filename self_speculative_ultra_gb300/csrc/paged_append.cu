@@ -6,7 +6,8 @@
 // two exact floats, each product with its rounding error, so only the
 // fraction of a turn is ever rounded and far positions lose nothing.
 //
-// Memory bound: every element is read and written once.  One launch; block
+// Memory bound: every element is read and written once (9.9K tokens, 32/32
+// heads, half of 128 columns rotated: 41 us, 5.95 TB/s).  One launch; block
 // roles by index:
 //   page blocks  one (touched page, chunk of KV heads): rotate the page's new
 //                key rows, copy its value rows, and fold the rows' bounds
@@ -46,8 +47,8 @@ __device__ __forceinline__ float2 sincos_turns(int pos, float2 f, float scale) {
   const float e = fmaf(hi, f.x, -p1) + fmaf(lo, f.x, -p2) + (hi + lo) * f.y;
   const float r0 = (p1 - rintf(p1)) + (p2 - rintf(p2)) + e;
   // within half a turn the hardware's sine and cosine are good to 2^-21, far
-  // below half a step of a 16-bit output; the exact ones took 10 of 54 us of a
-  // 12,000-token append
+  // below half a step of a 16-bit output (9.9K tokens, 32/32 heads of 128 rotated
+  // columns: 42.1 us, with the accurate ones 46.3)
   float s, c;
   __sincosf((r0 - rintf(r0)) * 6.283185307179586f, &s, &c);
   return make_float2(c * scale, s * scale);

