@@ -568,6 +568,8 @@ int ts_paged_rope_append(const void* q, const void* k, const void* v, int64_t q_
  * A token with no row to see (seq_lens[s] < q_len - i) gets o = 0, lse = -inf.
  * Rows [0, seq_lens[s]) must hold finite values; what the pages hold behind
  * them does not matter.
+ * A query row that makes a score NaN gets NaN in o and lse, the others what
+ * they would get without it.  The same call gives the same bits.
  *
  * q [n, Hq, d]; o [n, Hq, d] of q's type, out; lse [n, Hq] fp32 out, or NULL.
  * max_q    a bound on the sequences' new tokens, 1 .. n (a longer sequence is

@@ -190,10 +190,10 @@ __device__ __forceinline__ void write_row(const RowsArgs& a, const Unit& u, int 
                                           const float4& acc, float m, float l) {
   const int G = a.Hq / a.Hkv, R = u.r0 + r;
   const int64_t row = (int64_t)(u.tok0 + R / G) * a.Hq + u.kv * G + R % G;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   *reinterpret_cast<uint2*>(static_cast<T*>(a.o) + row * D + c4 * 4) =
       make_uint2(Pair<T>::pack(acc.x * inv, acc.y * inv), Pair<T>::pack(acc.z * inv, acc.w * inv));
-  if (a.lse && c4 == 0) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  if (a.lse && c4 == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // Clusters: the barrier, and loads from the shared memory of CTA `rank`.
@@ -648,6 +648,9 @@ paged_rows_kernel(const PagedBatch b, const RowsArgs a, int n_rb, int unit_trips
       la += __shfl_xor_sync(0xffffffffu, la, o);
       lb += __shfl_xor_sync(0xffffffffu, lb, o);
     }
+    // a sum that is NaN counts in the joins, whatever the maximum saw
+    if (la != la) ma = INFINITY;
+    if (lb != lb) mb = INFINITY;
     // -------------------------------------------------------- join the warps
 #pragma unroll
     for (int n = 0; n < D / 8; ++n) {
@@ -805,10 +808,10 @@ paged_rows_merge(const CutUnit* __restrict__ cuts, const float* __restrict__ par
   }
   const int RR = x.r0 + r;
   const int64_t row = (int64_t)(x.tok0 + RR / G) * Hq + x.kv * G + RR % G;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   *reinterpret_cast<uint2*>(o + row * D + c4 * 4) =
       make_uint2(Pair<T>::pack(acc.x * inv, acc.y * inv), Pair<T>::pack(acc.z * inv, acc.w * inv));
-  if (lse && c4 == 0) lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  if (lse && c4 == 0) lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 }  // namespace

@@ -198,9 +198,29 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int D, int max_q, int max_
   __syncthreads();
   if (warp == 0) starts();
   __syncthreads();
-  for (int i = tid; i < n_tiles; i += kPlanThreads) {
-    const int4 t = tiles[i];
-    sorted[atomicAdd(&hist[bucket(t.z)], 1)] = t;
+  // Where tiles may be cut, those of a class stay in the order of the batch: which
+  // are cut, and where, must not hang on which warp comes first, or the sums'
+  // rounding would.  One warp, 32 tiles a trip.
+  const bool may_cut = (long long)n_tiles * Hkv < 16 * kGb300Sms && longest > 1 && max_slots > 0;
+  if (!may_cut) {
+    for (int i = tid; i < n_tiles; i += kPlanThreads) {
+      const int4 t = tiles[i];
+      sorted[atomicAdd(&hist[bucket(t.z)], 1)] = t;
+    }
+  } else if (warp == 0) {
+    for (int base = 0; base < n_tiles; base += 32) {
+      const int i = base + lane;
+      const int4 t = i < n_tiles ? tiles[i] : make_int4(0, 0, 0, 0);
+      const int c = i < n_tiles ? bucket(t.z) : 256;
+      const unsigned same = __match_any_sync(0xffffffffu, c);
+      const int to = (c < 256 ? hist[c] : 0) + __popc(same & ((1u << lane) - 1u));
+      __syncwarp();
+      if (c < 256) {
+        sorted[to] = t;
+        if (lane == 31 - __clz(same)) hist[c] = to + 1;
+      }
+      __syncwarp();
+    }
   }
   __syncthreads();
   // Which tiles to cut, and how far: the first `whole` of the order stay, the
@@ -214,7 +234,7 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int D, int max_q, int max_
   constexpr float kFixed = 3.f, kCut = 2.f;
   const int C = kGb300Sms;
   int whole = n_tiles, per = longest, stretch = 0;
-  if ((long long)n_tiles * Hkv < 16 * C && longest > 1 && max_slots > 0) {
+  if (may_cut) {
     const int rounds = n_tiles * Hkv / C;
     float best = INFINITY;
     int best_whole = n_tiles, best_per = longest;
@@ -1088,6 +1108,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
             m_used = ms;
           }
           lt = exp_pack(m_used == -INFINITY ? 0.f : m_used);   // nothing seen: 2^-inf = 0
+          if (lt != lt) m_used = INFINITY;     // a join drops no NaN; the warp's others go on as they were
         }
         l += lt;
         {
@@ -1147,7 +1168,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       const int64_t row = (int64_t)(w.q0 + R / G) * Hq + w.kv * G + R % G;
       const bool cut = w.slot >= 0;
       const int64_t piece = (int64_t)w.slot * Hkv + w.kv;
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t x[32];
@@ -1178,7 +1199,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       }
       if (valid) {
         if (cut) part_ml[piece * kM + g * 128 + tr] = make_float2(m_used, l);
-        else if (lse) lse[row] = l > 0.f ? (m_used + log2f(l)) * kLn2 : -INFINITY;
+        else if (lse) lse[row] = l == 0.f ? -INFINITY : (m_used + log2f(l)) * kLn2;
       }
       // O has been read before this warp's next P is announced
       ptx::tc_fence_before();
@@ -1279,7 +1300,7 @@ paged_tc_merge(const PagedBatch b, const Header* __restrict__ hdr, const int4* _
       }
     }
     if (!live) continue;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
     const int64_t row = (int64_t)(sp.q0 + R / G) * Hq + kv * G + R % G;
     uint4* dst = reinterpret_cast<uint4*>(o + row * D + part * kPart);
 #pragma unroll
@@ -1288,7 +1309,7 @@ paged_tc_merge(const PagedBatch b, const Header* __restrict__ hdr, const int4* _
                               Pair<T>::pack(acc[x].z * inv, acc[x].w * inv),
                               Pair<T>::pack(acc[x + 1].x * inv, acc[x + 1].y * inv),
                               Pair<T>::pack(acc[x + 1].z * inv, acc[x + 1].w * inv));
-    if (lse && part == 0) lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    if (lse && part == 0) lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
   }
 }
 

@@ -355,6 +355,49 @@ def test_another_stream_and_repeatability(ts, q):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)      # same bits every time
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_same_bits_where_tiles_are_cut(ts, d):
+    """Many tiles of nearly one cost: which are cut, and where, is always the same."""
+    lens = [9000 + 37 * i % 150 for i in range(24)]
+    b = pu.Batch([320] * 24, lens, 8, 2, d, 64, BF, seed=18)
+    o, lse = _attend(ts, b)
+    for _ in range(12):
+        o2, lse2 = _attend(ts, b)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("q,kv,Hq,Hkv,d", [(1, 300, 8, 2, 64),       # a cluster a unit
+                                           (1, 60000, 8, 2, 128),    # units cut in stretches
+                                           (200, 600, 12, 2, 64),    # short tiles
+                                           (200, 600, 12, 2, 128),
+                                           (300, 30000, 12, 2, 64),  # cut tiles
+                                           (300, 30000, 12, 2, 128)])
+def test_nan_in_a_query_row(ts, q, kv, Hq, Hkv, d):
+    """It reaches that row's o and lse, however the keys are split, and no other."""
+    b = pu.Batch([q, q], [kv, kv - 1], Hq, Hkv, d, 32, BF, seed=19)
+    o, lse = _attend(ts, b)
+    t, h = q + q // 2, Hq - 2
+    b.q[t, h, 3] = float("nan")
+    o2, lse2 = _attend(ts, b)
+    assert torch.isnan(o2[t, h]).all() and torch.isnan(lse2[t, h])
+    o2[t, h], lse2[t, h] = o[t, h], lse[t, h]
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_nan_in_a_query_row_over_chosen_pages(ts):
+    b = pu.Batch([1, 1], [900, 5000], 8, 2, 128, 32, BF, seed=20)
+    pages = torch.arange(20, dtype=torch.int32, device="cuda").expand(2, 2, 20).contiguous()
+    counts = torch.full((2, 2), 20, dtype=torch.int32, device="cuda")
+    call = lambda: ts.ts_paged_attention_selected(  # noqa: E731
+        b.q, b.k, b.v, b.cu_q, b.lens, b.table, pages, counts, status=b.status)
+    o, lse = call()
+    b.q[1, 5, 9] = float("nan")
+    o2, lse2 = call()
+    assert status_of(b) == 0 and torch.isnan(o2[1, 5]).all() and torch.isnan(lse2[1, 5])
+    o2[1, 5], lse2[1, 5] = o[1, 5], lse[1, 5]
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
 @pytest.mark.parametrize("q,Hq,Hkv,d", [(1, 2, 1, 64), (40, 2, 1, 64), (1, 5, 1, 128), (33, 4, 1, 128)])
 def test_long_cache(ts, q, Hq, Hkv, d):
     """Hundreds of thousands of rows: many splits, pieces and partial sums."""
