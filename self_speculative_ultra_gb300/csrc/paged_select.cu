@@ -13,7 +13,7 @@
 // on the order of a sum: it is that of the sums formed to about 2^-45 and
 // rounded to fp32 once.  But only pages near the cut need them so well:
 //   scores  every page's sum in plain fp32 (memory bound: 4 d bytes a page and
-//           KV head; 8 lanes a page, packed fp32 pairs), and its largest bound
+//           KV head; D / 8 lanes a page, packed fp32 pairs), and its largest bound
 //           |m|: the sum is off by less than (20 + G) 2^-24 sum|u| max|m|.
 //   pick    per (token, KV head) the n_top-th largest of them, T.  With delta
 //           the largest such error, a page above T + 3 delta is kept and one
@@ -24,7 +24,8 @@
 //           kept beside the sum, Knuth's two-sum) and ranked again.  With
 //           scores that are not made to tie that is rarely a page.
 // Forming every page's sum well made the first kernel bound by fp32 arithmetic:
-// 39 us for 16 streams of up to 3200 pages (8 KV heads, d = 128).
+// 39 us for 16 streams of up to 3200 pages (8 KV heads, d = 128), which take
+// 41.5 now with both kernels.
 #include "paged.cuh"
 #include "tc_ptx.cuh"
 
@@ -93,6 +94,46 @@ paged_score_kernel(const PagedBatch b, const T* __restrict__ q, const T* __restr
   const int p0 = w.lo + (int)blockIdx.x * per_block;
   const int p1 = min(w.hi, p0 + per_block);
   if (p0 >= p1) return;
+  // lane: page lane / kL of the warp's, 8 columns of it.  (Half as many lanes a
+  // page, 16 columns each, leaves 4 blocks a SM for 7: 43.0 us for 41.5.)
+  constexpr int kL = D / 8;
+  const int sub = lane & (kL - 1);
+  const int32_t* trow = b.table + (int64_t)s * b.max_pages;
+  uint2* out = scores + ((int64_t)t * Hkv + kv) * b.max_pages;
+  // the rows of kDeep trips are on their way while a page is summed, the pool
+  // pages of the trip behind them too
+  constexpr int kDeep = 2;
+  struct Rows {
+    uint4 mx, mn;
+    bool ok;
+  };
+  auto pool_page = [&](int pg) { return pg < p1 ? trow[pg] : 0; };
+  auto ask = [&](int pg, int ph) {
+    Rows r;
+    r.ok = pg < p1;
+    if (!r.ok) return r;
+    if (ph < 0 || ph >= b.n_pages) {
+      if (sub == 0) set_status(status, TS_ERR_INVALID_ARG);
+      r.ok = false;
+    }
+    const int64_t row = ((int64_t)(r.ok ? ph : 0) * Hkv + kv) * (D / 8);
+    const uint4* mx = reinterpret_cast<const uint4*>(key_max) + row;
+    const uint4* mn = reinterpret_cast<const uint4*>(key_min) + row;
+    r.mx = __ldg(mx + sub);
+    r.mn = __ldg(mn + sub);
+    return r;
+  };
+  const int first = p0 + warp * (32 / kL) + lane / kL;
+  constexpr int kEach = kScoreThreads / kL;           // pages a trip
+  Rows next[kDeep];
+  int ph = pool_page(first);
+#pragma unroll
+  for (int x = 0; x < kDeep; ++x) {
+    const int behind = pool_page(first + (x + 1) * kEach);
+    next[x] = ask(first + x * kEach, ph);
+    ph = behind;
+  }
+  // (the query sums are formed while the first rows are on their way)
   for (int c = tid; c < D; c += kScoreThreads) {
     float up = 0.f, dn = 0.f;
     for (int g = 0; g < G; ++g) {
@@ -110,55 +151,11 @@ paged_score_kernel(const PagedBatch b, const T* __restrict__ q, const T* __restr
     sum = warp_sum(sum);
     if (lane == 0) weight[(int64_t)t * Hkv + kv] = sum;
   }
-  // lane: page lane / 8 of the warp's four, 16-byte chunks sub and sub + 8
-  constexpr int kCh = D / 64;
-  const int sub = lane & 7;
-  uint64_t up[kCh][4], dn[kCh][4];
+  uint64_t up[4], dn[4];
 #pragma unroll
-  for (int x = 0; x < kCh; ++x)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int c = (sub + 8 * x) * 8 + 2 * i;
-      up[x][i] = *reinterpret_cast<const uint64_t*>(&us[0][c]);
-      dn[x][i] = *reinterpret_cast<const uint64_t*>(&us[1][c]);
-    }
-  const int32_t* trow = b.table + (int64_t)s * b.max_pages;
-  uint2* out = scores + ((int64_t)t * Hkv + kv) * b.max_pages;
-  // the rows of kDeep trips are on their way while a page is summed, the pool
-  // pages of the trip behind them too
-  constexpr int kDeep = 2;
-  struct Rows {
-    uint4 mx[kCh], mn[kCh];
-    bool ok;
-  };
-  auto pool_page = [&](int pg) { return pg < p1 ? trow[pg] : 0; };
-  auto ask = [&](int pg, int ph) {
-    Rows r;
-    r.ok = pg < p1;
-    if (!r.ok) return r;
-    if (ph < 0 || ph >= b.n_pages) {
-      if (sub == 0) set_status(status, TS_ERR_INVALID_ARG);
-      r.ok = false;
-    }
-    const int64_t row = ((int64_t)(r.ok ? ph : 0) * Hkv + kv) * (D / 8);
-    const uint4* mx = reinterpret_cast<const uint4*>(key_max) + row;
-    const uint4* mn = reinterpret_cast<const uint4*>(key_min) + row;
-#pragma unroll
-    for (int x = 0; x < kCh; ++x) {
-      r.mx[x] = __ldg(mx + sub + 8 * x);
-      r.mn[x] = __ldg(mn + sub + 8 * x);
-    }
-    return r;
-  };
-  const int first = p0 + warp * 4 + (lane >> 3);
-  constexpr int kEach = kScoreThreads / 8;           // pages a trip
-  Rows next[kDeep];
-  int ph = pool_page(first);
-#pragma unroll
-  for (int x = 0; x < kDeep; ++x) {
-    const int behind = pool_page(first + (x + 1) * kEach);
-    next[x] = ask(first + x * kEach, ph);
-    ph = behind;
+  for (int i = 0; i < 4; ++i) {
+    up[i] = *reinterpret_cast<const uint64_t*>(&us[0][sub * 8 + 2 * i]);
+    dn[i] = *reinterpret_cast<const uint64_t*>(&us[1][sub * 8 + 2 * i]);
   }
   for (int base = p0; base < p1; base += kEach) {    // the same trips for every lane
     const int pg = base + (first - p0);
@@ -169,23 +166,20 @@ paged_score_kernel(const PagedBatch b, const T* __restrict__ q, const T* __restr
     ph = pool_page(pg + (kDeep + 1) * kEach);
     uint64_t s1 = 0, s2 = 0;
     uint32_t top = 0;                                // largest |bound| of either half, as bits
+    const uint32_t wx[4] = {r.mx.x, r.mx.y, r.mx.z, r.mx.w};
+    const uint32_t wn[4] = {r.mn.x, r.mn.y, r.mn.z, r.mn.w};
 #pragma unroll
-    for (int x = 0; x < kCh; ++x) {
-      const uint32_t wx[4] = {r.mx[x].x, r.mx[x].y, r.mx[x].z, r.mx[x].w};
-      const uint32_t wn[4] = {r.mn[x].x, r.mn[x].y, r.mn[x].z, r.mn[x].w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 fx = Pair<T>::unpack(wx[k]), fn = Pair<T>::unpack(wn[k]);
-        s1 = ptx::fma2(up[x][k], ptx::f2(fx.x, fx.y), s1);
-        s2 = ptx::fma2(dn[x][k], ptx::f2(fn.x, fn.y), s2);
-        top = __vimax3_u16x2(top, wx[k] & 0x7FFF7FFFu, wn[k] & 0x7FFF7FFFu);
-      }
+    for (int k = 0; k < 4; ++k) {
+      const float2 fx = Pair<T>::unpack(wx[k]), fn = Pair<T>::unpack(wn[k]);
+      s1 = ptx::fma2(up[k], ptx::f2(fx.x, fx.y), s1);
+      s2 = ptx::fma2(dn[k], ptx::f2(fn.x, fn.y), s2);
+      top = __vimax3_u16x2(top, wx[k] & 0x7FFF7FFFu, wn[k] & 0x7FFF7FFFu);
     }
     float a0, a1;
     ptx::f2_split(ptx::add2(s1, s2), a0, a1);
     float score = a0 + a1;
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) {
+    for (int o = 1; o < kL; o <<= 1) {
       score += __shfl_xor_sync(0xffffffffu, score, o);
       top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
     }
@@ -541,9 +535,10 @@ static int go_select(const PagedBatch& b, const void* q, const void* key_min, co
   const T* mn = static_cast<const T*>(key_min);
   const T* mx = static_cast<const T*>(key_max);
   // pages a block: enough that the query sums and the first loads' latency are
-  // spread over several trips of 16 pages, while the SMs have blocks to overlap
-  int per_block = 256;
-  while (per_block > 32 &&
+  // spread over several trips of 8 or 16 pages, while the SMs have blocks to
+  // overlap (64, 128, 256 a block: 43.0, 41.5, 42.2 us on the 16 streams above)
+  int per_block = 128;
+  while (per_block > 16 &&
          (int64_t)b.n * Hkv * ((b.max_pages + per_block - 1) / per_block) < 4 * kGb300Sms)
     per_block >>= 1;
   cudaLaunchConfig_t cfg = {};
