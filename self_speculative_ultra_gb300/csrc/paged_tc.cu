@@ -1044,10 +1044,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
               if (x >= vis) r[x] = kNegInf;
           }
         };
-        load_s();
         // P against mref, packed in place: the pair of keys 32c + 2i, 32c + 2i + 1
         // in r[32c + i]; returns the row sum of P before rounding
-        auto exp_pack = [&](float mref) -> float {
+        auto exp_pack = [&](float mref, uint32_t (&lo)[32], uint32_t (&hi)[32]) -> float {
           const uint64_t negm = ptx::f2(-mref, -mref);
           auto chunk_exp = [&](int c, float (&pe)[32]) {
             const uint32_t* x = r + 32 * c;
@@ -1067,7 +1066,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
             float (&cur)[32] = (c & 1) ? pb : pa;
             float (&nxt)[32] = (c & 1) ? pa : pb;
             if (c + 1 < kNk / 32) chunk_exp(c + 1, nxt);
-            uint32_t* x = r + 32 * c;
+            uint32_t* x = (c < 2 ? lo : hi) + 16 * (c & 1);
             uint64_t s0 = ptx::f2(cur[0], cur[1]), s1 = ptx::f2(cur[2], cur[3]);
 #pragma unroll
             for (int y = 2; y < 16; y += 2) {
@@ -1087,17 +1086,29 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
         };
         // the running maximum moves only when it has to: a row sum of at most
         // 2^15 means every P is at most 2^15, finite in either type
-        bool fast = m_used != -INFINITY;
+        auto put = [&](const uint32_t (&lo)[32], const uint32_t (&hi)[32]) {
+          ptx::tmem_st32(s_addr, lo);
+          ptx::tmem_st32(s_addr + 32, hi);
+        };
+        bool fast = m_used != -INFINITY, stored = false;
         float lt = 0.f;
         if (__all_sync(0xffffffffu, fast)) {
-          lt = exp_pack(m_used);
+          uint32_t lo[32], hi[32];
+          load_s();
+          lt = exp_pack(m_used, lo, hi);
           fast = lt <= kFastSum;
+          if (__all_sync(0xffffffffu, fast)) {
+            put(lo, hi);
+            l += lt;
+            stored = true;
+          }
         } else {
           fast = false;
         }
         bool raise = false;
         float f = 1.f;
-        if (!__all_sync(0xffffffffu, fast)) {
+        if (!stored) {
+          uint32_t lo[32], hi[32];
           load_s();
           const float ms = fmaxf(fmaxf(fmax32(&r[0]), fmax32(&r[32])),
                                  fmaxf(fmax32(&r[64]), fmax32(&r[96]))) * sl2;
@@ -1107,21 +1118,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
             l *= f;
             m_used = ms;
           }
-          lt = exp_pack(m_used == -INFINITY ? 0.f : m_used);   // nothing seen: 2^-inf = 0
+          lt = exp_pack(m_used == -INFINITY ? 0.f : m_used, lo, hi);   // nothing seen: 2^-inf = 0
           if (lt != lt) m_used = INFINITY;     // a join drops no NaN; the warp's others go on as they were
-        }
-        l += lt;
-        {
-          uint32_t lo[32], hi[32];
-#pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            lo[x] = r[x];
-            lo[16 + x] = r[32 + x];
-            hi[x] = r[64 + x];
-            hi[16 + x] = r[96 + x];
-          }
-          ptx::tmem_st32(s_addr, lo);
-          ptx::tmem_st32(s_addr + 32, hi);
+          put(lo, hi);
+          l += lt;
         }
         ptx::tmem_st_wait();
         if (k > 0 && __any_sync(0xffffffffu, raise)) {
