@@ -22,7 +22,8 @@
 //   warps 0, 2   copy K (2 stages) and V (3 stages), one box a page and
 //                64-column panel, each lane one box; 128-byte swizzle
 //   warp 1       S_g = Q_g K^T (M = N = 128, fp32 in TMEM); when the softmax
-//                has written P_g over S_g, O_g += P_g V with P read from TMEM
+//                has written P_g over S_g, O_g += P_g V with P read from TMEM (at
+//                d = 64 that is warp 3's)
 //   warps 4..7   the item's query rows into shared memory; rows of V behind
 //                the sequence's last are cleared (0 * NaN would reach O)
 //   warps 8..15  softmax, one thread a row: all 128 scores in registers,
@@ -494,14 +495,14 @@ constexpr int kNext = 4;
 constexpr int kMostStages = 4;
 
 struct Aux {
-  uint64_t k_full[kMostStages], k_empty[kMostStages], v_full[kMostStages], v_empty[kMostStages];
+  uint64_t k_full[kMostStages], v_full[kMostStages], v_empty[kMostStages];
   // a V tile that reaches behind the sequence's rows lands on v_tail, and
   // v_clear follows when the rows behind are cleared (v_full only counts it)
   uint64_t v_tail[kMostStages], v_clear[kMostStages];
   // a group's tiles take these in turn: a tile's turn comes again only when
   // every waiter has seen its last
   uint64_t s_full[2][kRing], p_ready[2][kRing], o_done[2][kRing];
-  uint64_t q_full, q_empty, drain;
+  uint64_t q_full, q_empty, drain[2];
   uint64_t next_full[kNext], next_empty[kNext];   // items handed to the other warps
   uint32_t tmem_base;
   volatile int32_t abort_flag;
@@ -560,6 +561,12 @@ __device__ __forceinline__ Item load_item(const PagedBatch& b, const Work& w, in
   return it;
 }
 
+// A group's turn as the place of its barrier in [2][kRing] and the parity of its round.
+__device__ __forceinline__ uint32_t use_of(uint32_t g, uint32_t turn) {
+  static_assert(kRing == 4, "three bits for the place");
+  return g * kRing + turn % kRing + (turn / kRing % 2) * 8;
+}
+
 __device__ __forceinline__ void give_up(Aux* aux, int32_t* status) {
   aux->abort_flag = 1;
   set_status(status, TS_ERR_TIMEOUT);
@@ -612,7 +619,6 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
   if (tid == 0) {
     for (int i = 0; i < kSK; ++i) {
       ptx::mbar_init(&aux->k_full[i], 1);
-      ptx::mbar_init(&aux->k_empty[i], 1);
     }
     for (int i = 0; i < kSV; ++i) {
       ptx::mbar_init(&aux->v_full[i], 1);
@@ -629,10 +635,12 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
         ptx::mbar_init(&aux->o_done[g][i], 1);
       }
     }
-    ptx::mbar_init(&aux->drain, 1);
+    ptx::mbar_init(&aux->drain[0], 1);
+    ptx::mbar_init(&aux->drain[1], 1);
     for (int i = 0; i < kNext; ++i) {
       ptx::mbar_init(&aux->next_full[i], 1);
-      ptx::mbar_init(&aux->next_empty[i], 2 + 4 + 8);   // warps 1, 2, 4..7, 8..15
+      // warps 1, 2, 4..7, 8..15, and 3 where it has work
+      ptx::mbar_init(&aux->next_empty[i], (kScores == 2 ? 2 : 3) + 4 + 8);
     }
     aux->abort_flag = 0;
     ptx::fence_mbar_init();
@@ -661,11 +669,17 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       const uint32_t depth = is_k ? kSK : kSV;
       const CUtensorMap* map = is_k ? &tmap_k : &tmap_v;
       uint64_t* full = is_k ? aux->k_full : aux->v_full;
-      uint64_t* empty = is_k ? aux->k_empty : aux->v_empty;
       const uint32_t ring = ptx::smem_u32(is_k ? sk : sv);
       const int boxes = kNk >> b.page_shift;
       const uint64_t pol = ptx::l2_evict_first_policy();
       uint32_t it = 0, done = 0;          // key tiles so far; copies issued
+      uint32_t base_g[2] = {0, 0};        // tiles of each group before this item
+      // A stage is free when its tile's last product is complete, which that
+      // product's own barrier says: its group and turn, 4 bits a stage.  (A barrier
+      // of the stage's own would be one more commit between products.)  The barrier
+      // cannot pass its next round unseen, since that needs a later tile of this
+      // ring; and its last round is over, since products end in order.
+      uint32_t uses = 0;
       uint32_t tail_on = 0, tail_par = 0; // a stage's v_tail was used; parity of its last use
       bool ok = true;
       auto ids = [&](const Item& w, int step) -> int64_t {
@@ -712,7 +726,17 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
           const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, ph >= 0)) *
                                  (uint32_t)(ps * D * 2);
           const uint32_t st = it % depth;
-          if (it >= depth) ok = ptx::mbar_wait(&empty[st], (it / depth - 1) & 1u, wait_limit);
+          if (it >= depth) {
+            if (kScores == 2 && !is_k) {
+              ok = ptx::mbar_wait(&aux->v_empty[st], (it / depth - 1) & 1u, wait_limit);
+            } else {
+              const uint32_t x = uses >> (4 * st);
+              uint64_t* last = is_k ? &aux->s_full[0][0] : &aux->o_done[0][0];
+              ok = ptx::mbar_wait(last + (x & 7u), (x >> 3) & 1u, wait_limit);
+            }
+          }
+          const uint32_t g = k < w.n_g[1] ? 1u : 0u, turn = (g ? base_g[1] : base_g[0]) + k;
+          uses = (uses & ~(15u << (4 * st))) | use_of(g, turn) << (4 * st);
           ok = __all_sync(0xffffffffu, ok && aux->abort_flag == 0);
           if (!ok) break;
           const bool tail = !is_k && (w.k0 + k + 1) * kNk > w.kl;
@@ -732,6 +756,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
                                   land, p * 64, row, pol);
           ++done;
         }
+        base_g[0] += w.n_g[0];
+        base_g[1] += w.n_g[1];
       }
       if (!ok) give_up(aux, status);
       // every copy issued must land before the CTA exits
@@ -742,7 +768,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
           if ((tail_on >> t) & 1u)
             ptx::mbar_wait(&aux->v_tail[t], (tail_par >> t) & 1u, kDrainCycles);
       }
-    } else if (warp == 1) {
+    } else if (warp == 1 || (kScores > 2 && warp == 3)) {
       // ------------------------------------------------------------ products
       // The whole warp walks the loop, and one lane issues under a predicate.
       // Everything an instruction's operands come from is the same in all lanes,
@@ -766,8 +792,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       const uint64_t vd0 = ptx::sdesc_sw128(base + Ly::kV, Ly::kPanel, 1024);
       constexpr uint32_t kTile16 = Ly::kTile >> 4;
       uint32_t it = 0, items = 0, clear_par = 0, count = 0;
-      uint32_t scores_g[2] = {0, 0}, tiles_g[2] = {0, 0};   // S and P V products issued
-      uint32_t outs_g[2] = {0, 0};                          // items ended
+      uint32_t base0 = 0, base1 = 0;      // tiles of each group before this item
+      uint32_t outs_g[2] = {0, 0};        // items ended
+      uint32_t ops = 0, at = 0, uses = 0; // ops so far; S tile of the next; who used each last
       bool ok = true;
       auto commit = [&](uint32_t off) { ptx::mma_commit_if(lead, bars + off); };
       auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -783,11 +810,11 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
         const bool tail = same((w.k0 + w.n) * kNk > w.kl) != 0;   // of the item's last tile
         if (n < 0) break;
         if (n == 0) continue;
-        ok = wait(&aux->q_full, items);
+        if (warp == 1) ok = wait(&aux->q_full, items);
         if constexpr (kScores == 2) {
-          // S tile g is group g's: its next scores go behind its P V.  (The loop
-          // of three S tiles below costs more between the products than it gives
-          // here: 2079 us for 1974 on 2048 tokens over 100K rows.)
+          // S tile g is group g's: its next scores go behind its P V, in the order
+          // of one warp's products.  (S tiles in turn, as below, took 2079 us for
+          // 1974 on 2048 tokens over 100K rows.)
           auto scores = [&](int g, uint32_t t) {
             const uint64_t a0 = qd0 + (uint64_t)(g * kTile16);
             const uint64_t b0 = kd0 + (uint64_t)((t % kSK) * kTile16);
@@ -796,13 +823,12 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
               const uint32_t off = (ks >> 2) * (Ly::kPanel >> 4) + (ks & 3) * 2;
               ptx::mma_ss_if(lead, tm + Ly::sbase(g), a0 + off, b0 + off, idesc_qk, ks > 0 ? 1u : 0u);
             }
-            commit(offsetof(Aux, s_full) + (g * kRing + scores_g[g]++ % kRing) * 8);
+            commit(offsetof(Aux, s_full) + (g * kRing + ((g ? base1 : base0) + (t - it)) % kRing) * 8);
           };
           ok = ok && wait(&aux->k_full[it % kSK], it / kSK);
           if (!ok) break;
           if (n0 > 0) scores(0, it);
           if (n1 > 0) scores(1, it);
-          commit(offsetof(Aux, k_empty) + it % kSK * 8);
           if (n == 1) commit(offsetof(Aux, q_empty));
           for (int k = 0; k < n; ++k) {
             const uint32_t t = it + k, stV = t % kSV;
@@ -816,7 +842,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
             for (int g = 0; g < 2; ++g) {
               const int ng = g == 0 ? n0 : n1;
               if (ok && k < ng) {
-                const uint32_t turn = tiles_g[g]++;
+                const uint32_t turn = (g ? base1 : base0) + k;
                 ok = wait(&aux->p_ready[g][turn % kRing], turn / kRing);
                 if (ok) {
                   const uint64_t b0 = vd0 + (uint64_t)(stV * kTile16);
@@ -834,81 +860,75 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
             }
             if (!ok) break;
             commit(offsetof(Aux, v_empty) + stV * 8);
-            if (k + 1 < n) {
-              commit(offsetof(Aux, k_empty) + (t + 1) % kSK * 8);
-              if (k + 2 == n) commit(offsetof(Aux, q_empty));
-            }
+            if (k + 2 == n) commit(offsetof(Aux, q_empty));
           }
         } else {
           // The item's products in pairs, by tile and group: op i writes its scores
           // to S tile i % kScores and, once they are P, multiplies them by V.  The
           // scores of op i + kScores go behind the P V of op i, so every group has
           // its next scores while it works on these.
-          struct Op {
-            int g, k;
-          };
-          auto step = [&](Op& x) {
-            do {
-              x.k += x.g;
-              x.g ^= 1;
-            } while (x.k < n && x.k >= (x.g == 0 ? n0 : n1));
-          };
-          const int total = n0 + n1;
-          Op a{n0 > 0 ? 0 : 1, 0}, p = a;
-          int ka = -1, kp = -1, sa = 0, sp_ = 0;     // tiles waited for; S tiles of the next ops
-          auto scores = [&]() {
-            const uint32_t t = it + a.k;
-            if (a.k != ka) {
-              ka = a.k;
-              ok = wait(&aux->k_full[t % kSK], t / kSK);
-              if (!ok) return;
-            }
-            const uint64_t a0 = qd0 + (uint64_t)(a.g * kTile16);
-            const uint64_t b0 = kd0 + (uint64_t)((t % kSK) * kTile16);
-            const uint32_t d0 = tm + Ly::sbase(sa);
-            const uint32_t turn = (a.g == 0 ? scores_g[0]++ : scores_g[1]++) % kRing;
-            const Op at = a;
-            step(a);
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-              const uint32_t off = (ks >> 2) * (Ly::kPanel >> 4) + (ks & 3) * 2;
-              ptx::mma_ss_if(lead, d0, a0 + off, b0 + off, idesc_qk, ks > 0 ? 1u : 0u);
-            }
-            commit(offsetof(Aux, s_full) + (at.g * kRing + turn) * 8);
-            if (a.k != at.k) commit(offsetof(Aux, k_empty) + t % kSK * 8);
-            if (a.k >= n) commit(offsetof(Aux, q_empty));
-            sa = sa + 1 == kScores ? 0 : sa + 1;
-          };
-          for (int i = 0; ok && i < min(kScores, total); ++i) scores();
-          for (int i = 0; ok && i < total; ++i) {
-            const uint32_t t = it + p.k, stV = t % kSV;
-            if (p.k != kp) {
-              kp = p.k;
-              ok = wait(&aux->v_full[stV], t / kSV);
-              if (ok && tail && p.k + 1 == n) {
-                ok = wait(&aux->v_clear[stV], clear_par >> stV);
-                clear_par ^= 1u << stV;
+          // Warp 1 forms the scores, warp 3 the products with V: what a warp does
+          // between two products is longer than a product at d = 64 (one warp for
+          // both: 195 us for 179 on 2048 tokens over 32K rows, 12/2 heads).  Op i of
+          // the item: while both groups have tiles, theirs in turn; then the rest of
+          // one's.  The ops of all items take the S tiles in turn, and scores go
+          // where the P V of three ops before is complete.
+          const int both = 2 * min(n0, n1), total = n0 + n1, rest = n1 > n0 ? 1 : 0;
+          if (warp == 1) {
+            for (int i = 0; ok && i < total; ++i) {
+              const bool two = i < both;
+              const uint32_t g = two ? i & 1 : rest, k = two ? i >> 1 : i - (both >> 1), t = it + k;
+              const uint32_t turn = (g ? base1 : base0) + k;
+              if (!two || g == 0) ok = wait(&aux->k_full[t % kSK], t / kSK);
+              if (ops >= kScores) {
+                const uint32_t x = uses >> (4 * at);
+                ok = ok && wait(&aux->o_done[0][0] + (x & 7u), (x >> 3) & 1u);
               }
-            }
-            const uint32_t turn = p.g == 0 ? tiles_g[0]++ : tiles_g[1]++;
-            ok = ok && wait(&aux->p_ready[p.g][turn % kRing], turn / kRing);
-            if (!ok) break;
-            const uint64_t b0 = vd0 + (uint64_t)(stV * kTile16);
-            const uint32_t s0 = tm + Ly::sbase(sp_), d0 = tm + Ly::obase(p.g);
-            const uint32_t acc = p.k > 0 ? 1u : 0u;
-            const Op at = p;
-            step(p);
+              if (!ok) break;
+              uses = (uses & ~(15u << (4 * at))) | use_of(g, turn) << (4 * at);
+              const uint64_t a0 = qd0 + (uint64_t)(g * kTile16);
+              const uint64_t b0 = kd0 + (uint64_t)((t % kSK) * kTile16);
+              const uint32_t d0 = tm + 2 * D + at * kNk;
 #pragma unroll
-            for (int ks = 0; ks < kNk / 16; ++ks)
-              ptx::mma_ts_if(lead, d0, s0 + 8 * ks, b0 + (uint64_t)(ks * 128), idesc_pv,
-                             ks > 0 ? 1u : acc);
-            commit(offsetof(Aux, o_done) + (at.g * kRing + turn % kRing) * 8);
-            if (p.k != at.k) commit(offsetof(Aux, v_empty) + stV * 8);
-            sp_ = sp_ + 1 == kScores ? 0 : sp_ + 1;
-            if (i + kScores < total) scores();
+              for (int ks = 0; ks < D / 16; ++ks) {
+                const uint32_t off = (ks >> 2) * (Ly::kPanel >> 4) + (ks & 3) * 2;
+                ptx::mma_ss_if(lead, d0, a0 + off, b0 + off, idesc_qk, ks > 0 ? 1u : 0u);
+              }
+              commit(offsetof(Aux, s_full) + (g * kRing + turn % kRing) * 8);
+              if (i + 1 == total) commit(offsetof(Aux, q_empty));
+              ++ops;
+              at = at + 1 == kScores ? 0 : at + 1;
+            }
+          } else {
+            for (int i = 0; ok && i < total; ++i) {
+              const bool two = i < both;
+              const uint32_t g = two ? i & 1 : rest, k = two ? i >> 1 : i - (both >> 1), t = it + k;
+              const uint32_t turn = (g ? base1 : base0) + k, bar = g * kRing + turn % kRing;
+              const uint32_t stV = t % kSV;
+              if (!two || g == 0) {
+                ok = wait(&aux->v_full[stV], t / kSV);
+                if (ok && tail && (int)k + 1 == n) {
+                  ok = wait(&aux->v_clear[stV], clear_par >> stV);
+                  clear_par ^= 1u << stV;
+                }
+              }
+              ok = ok && wait(&aux->p_ready[0][0] + bar, turn / kRing);
+              if (!ok) break;
+              const uint64_t b0 = vd0 + (uint64_t)(stV * kTile16);
+              const uint32_t s0 = tm + 2 * D + at * kNk, d0 = tm + g * D;
+              const uint32_t acc = k > 0 ? 1u : 0u;
+#pragma unroll
+              for (int ks = 0; ks < kNk / 16; ++ks)
+                ptx::mma_ts_if(lead, d0, s0 + 8 * ks, b0 + (uint64_t)(ks * 128), idesc_pv,
+                               ks > 0 ? 1u : acc);
+              commit(offsetof(Aux, o_done) + bar * 8);
+              at = at + 1 == kScores ? 0 : at + 1;
+            }
           }
         }
         it += n;
+        base0 += n0;
+        base1 += n1;
         ++items;
       }
       if (!ok) give_up(aux, status);
@@ -920,10 +940,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       if constexpr (kScores == 2) {
         commit(offsetof(Aux, drain));
       } else {
-        if (ptx::elect_one()) ptx::mma_commit(&aux->drain);
+        if (ptx::elect_one()) ptx::mma_commit(&aux->drain[warp >> 1]);
         __syncwarp();
       }
-      ptx::mbar_wait(&aux->drain, 0, kDrainCycles);
+      ptx::mbar_wait(&aux->drain[warp >> 1], 0, kDrainCycles);
     } else if (warp >= 4) {
       // ------------------------------------------------------------ query rows, V tails
       const int t = tid - 128;
@@ -998,7 +1018,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
     const uint32_t o_addr = tmem + lane_off + Ly::obase(g);
     const float sl2 = kLog2e / sqrtf((float)D);
     const uint64_t sl2x2 = ptx::f2(sl2, sl2);
-    uint32_t tiles = 0, outs = 0, count = 0;
+    uint32_t tiles = 0, outs = 0, count = 0, ops = 0;
     bool ok = true;
     while (ok) {
       Item w;
@@ -1024,9 +1044,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
           continue;
         }
         // this tile's place among the item's products
-        const int op = kScores == 2 ? g
-                                    : min(k, w.n_g[0]) + min(k, w.n_g[1]) +
-                                          (g == 1 && k < w.n_g[0] ? 1 : 0);
+        const uint32_t op = kScores == 2 ? g
+                                         : ops + min(k, w.n_g[0]) + min(k, w.n_g[1]) +
+                                               (g == 1 && k < w.n_g[0] ? 1 : 0);
         const uint32_t s_addr = tmem + lane_off + Ly::sbase(op % kScores);
         const int key0 = (w.k0 + k) * kNk;
         const bool edge = key0 + kNk > lim0 + 1;    // warp-uniform
@@ -1152,6 +1172,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
         if (lane == 0) ptx::mbar_arrive(&aux->p_ready[g][tiles % kRing]);
       }
       if (!ok) break;
+      ops = (ops + w.n_g[0] + w.n_g[1]) % kScores;
       // ------------------------------------------------------------ the item's output
       if (n_mine > 0) {
         // with an S tile a group, o_done counts items, not tiles
