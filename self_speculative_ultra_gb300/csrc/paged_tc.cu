@@ -932,17 +932,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
         ++items;
       }
       if (!ok) give_up(aux, status);
-      // This warp's products end before TMEM is freed.  (How this last commit is
-      // written decides how the compiler arranges the loops above: by measurement
-      // under the predicate for two S tiles, 1990 us against 2125 for 2048 tokens
-      // over 100K rows, and in a branch for three, 124 against 137 for 9 mixed
-      // streams at d = 64.)
-      if constexpr (kScores == 2) {
-        commit(offsetof(Aux, drain));
-      } else {
-        if (ptx::elect_one()) ptx::mma_commit(&aux->drain[warp >> 1]);
-        __syncwarp();
-      }
+      // this warp's products end before TMEM is freed
+      commit(offsetof(Aux, drain) + (warp >> 1) * 8);
       ptx::mbar_wait(&aux->drain[warp >> 1], 0, kDrainCycles);
     } else if (warp >= 4) {
       // ------------------------------------------------------------ query rows, V tails
