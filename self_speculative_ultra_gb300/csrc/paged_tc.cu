@@ -9,7 +9,8 @@
 // bound by the tensor cores (4 d flops a row and key); the softmax stands between
 // the two products, so the groups alternate: while one group's scores are
 // exponentiated the tensor core works for the other.  2048 tokens over 100K rows,
-// 32/8 heads, d = 128: 1.97 ms, 1725 TFLOP/s; over 32K rows, 12/2 heads: 250 us.
+// 32/8 heads, d = 128: 1.91 ms, 1780 TFLOP/s; over 32K rows, 12/2 heads: 243 us,
+// at d = 64 177 us.
 //
 // Three launches.  The plan (one CTA) lists the work from the device-side
 // lengths in order of falling cost: the tiles of whole rounds over the SMs as
@@ -321,9 +322,9 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int D, int max_q, int max_
     // Or, where pieces of about one length would leave a round half empty, cut
     // evenly: the tiles in a line, in equal stretches, as many a KV head as it
     // has SMs.  The stretches stand at different keys, so K and V have to stay in
-    // L2.  (2048 tokens over 32K rows, 2 KV heads: 265 us in pieces, 253 in
+    // L2.  (2048 tokens over 32K rows, 2 KV heads: 257 us in pieces, 244 in
     // stretches; tiles of many lengths fill the SMs better by themselves: 9 mixed
-    // streams 120 us, 127 in stretches.)
+    // streams take 6 % longer in stretches.)
     const unsigned heads = C / Hkv;
     if (heads > 0 && sorted[n_tiles - 1].z * 10 >= longest * 9 && s_keys * Hkv * D * 4 <= (64ull << 20) &&
         (long long)(n_tiles + heads) * Hkv <= max_slots) {
@@ -776,8 +777,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       // them in uniform registers.  The queue in front of the tensor core is
       // short, so what this warp spends between products leaves it idle: issued
       // by one lane of a divergent warp a step took 3.6 K cycles, in a branch of
-      // the elected lane 2.9 K (2182 us for 2048 tokens over 100K rows, 8B
-      // shape), under a predicate 2.6 K (1974 us).
+      // the elected lane 2.9 K, under a predicate 2.6 K (2182 and 1974 us for 2048
+      // tokens over 100K rows, 8B shape, with the softmax as it was then).
       constexpr uint32_t idesc_qk = Pair<T>::kFp16 ? ptx::idesc_f16_f32(128, kNk, false)
                                                    : ptx::idesc_bf16_f32(128, kNk, false);
       constexpr uint32_t idesc_pv = Pair<T>::kFp16 ? ptx::idesc_f16_f32(128, D, true)
@@ -813,8 +814,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
         if (warp == 1) ok = wait(&aux->q_full, items);
         if constexpr (kScores == 2) {
           // S tile g is group g's: its next scores go behind its P V, in the order
-          // of one warp's products.  (S tiles in turn, as below, took 2079 us for
-          // 1974 on 2048 tokens over 100K rows.)
+          // of one warp's products.  (S tiles in turn, as below, took 5 % longer
+          // on 2048 tokens over 100K rows.)
           auto scores = [&](int g, uint32_t t) {
             const uint64_t a0 = qd0 + (uint64_t)(g * kTile16);
             const uint64_t b0 = kd0 + (uint64_t)((t % kSK) * kTile16);
