@@ -595,7 +595,7 @@ int ts_paged_attention(const void* q, const void* k_pages, const void* v_pages, 
  * are the first n_sink of them, the last n_recent, and the n_top best of those
  * between by (score desc, page asc), or all when they are no more than
  * N = n_sink + n_top + n_recent.  Pages with a bound that is not finite, or a
- * score or partial sum beyond the range of fp32, rank last.
+ * score or the sum of its terms' magnitudes beyond the range of fp32, rank last.
  *
  * q        [n, Hq, d] rotated; key_min, key_max [n_pages, Hkv, d].
  * n_recent >= 1 (the last page is the token's own); n_sink, n_top >= 0;

@@ -12,20 +12,23 @@
 // The scores decide which whole numbers come out, so the choice must not hang
 // on the order of a sum: it is that of the sums formed to about 2^-45 and
 // rounded to fp32 once.  But only pages near the cut need them so well:
-//   scores  every page's sum in plain fp32 (memory bound: 4 d bytes a page and
-//           KV head; D / 8 lanes a page, packed fp32 pairs), and its largest bound
-//           |m|: the sum is off by less than (20 + G) 2^-24 sum|u| max|m|.
-//   pick    per (token, KV head) the n_top-th largest of them, T.  With delta
-//           the largest such error, a page above T + 3 delta is kept and one
-//           below T - 3 delta is not, whatever the errors; when more are left
+//   scores  every page's sum and its size S = sum |u| |m|, on the tensor cores
+//           (memory bound: 4 d bytes a page and KV head).  The sum is off by less
+//           than e = (76 + G) 2^-24 S: products are exact, a chain of two products
+//           has 32 additions, off by at most 2^-23 of what is summed, behind it
+//           come 7 roundings to fp32, the query sums' G and the score's own.
+//   pick    per (token, KV head) the n_top-th largest of them, T.  With e the
+//           largest such error, a page above T + 2 e is kept and one below
+//           T - 2 e is not, whatever the errors; when more are left
 //           than places, the pages between are formed well (query sums split
 //           into a part of 12 bits, whose product with a 16-bit element is
 //           exact in fp32, and the rest; the rounding error of every addition
 //           kept beside the sum, Knuth's two-sum) and ranked again.  With
 //           scores that are not made to tie that is rarely a page.
 // Forming every page's sum well made the first kernel bound by fp32 arithmetic:
-// 39 us for 16 streams of up to 3200 pages (8 KV heads, d = 128), which take
-// 41.5 now with both kernels.
+// 39 us for 16 streams of up to 3200 pages (8 KV heads, d = 128), which take 38
+// now with both kernels.  (Plain sums on the fp32 pipes took ~90 instructions a
+// page: 41.5 us, at d = 64 27.6 for 23.0.)
 #include "paged.cuh"
 #include "tc_ptx.cuh"
 
@@ -73,17 +76,51 @@ __device__ __forceinline__ Span span_of(const SeqSpan& sp, int t, int shift, int
   return r;
 }
 
-// Per page: .x the score's key, .y the largest |bound| (fp32 bits).  Per
-// (token, KV head): weight = sum |u|.
+// C += A B for 16 pages (rows of A) and 16 columns of their bounds.
+template <typename T>
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, uint2 b) {
+  if (Pair<T>::kFp16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
+                 "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, "
+                 "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
+}
+
+// The first 8 (bf16) or 11 (fp16) bits of x as a T; x becomes the rest.
+template <typename T>
+__device__ __forceinline__ T lead_bits(float& x) {
+  T h;
+  if constexpr (Pair<T>::kFp16) h = __float2half_rn(x);
+  else h = __ushort_as_bfloat16((unsigned short)(__float_as_uint(x) >> 16));
+  x -= Pair<T>::one(h);
+  return h;
+}
+
+// Per page: .x the score's key, .y its size S (fp32 bits).
+//
+// A warp takes 16 pages a trip.  Their bounds are the rows of A, read as 16-byte
+// words: lane (g, c) = (lane / 4, lane % 4) reads columns 8 (c + 4 x) .. + 7 of
+// pages g and g + 8, and as a product does not mind the order of its columns,
+// these words are the operand as they lie.  B's columns 0, 1, 2 hold the query
+// sums in three parts of T's bits, which together are exact to fp32 (fp16: but
+// for 2^-38 of the largest, which is brought to 2^13 .. 2^14).
 template <typename T, int D>
-__global__ void __launch_bounds__(kScoreThreads)
+__global__ void __launch_bounds__(kScoreThreads, 3)
 paged_score_kernel(const PagedBatch b, const T* __restrict__ q, const T* __restrict__ key_min,
                    const T* __restrict__ key_max, int Hq, int Hkv, int n_top, int n_sink,
-                   int n_recent, int per_block, uint2* __restrict__ scores,
-                   float* __restrict__ weight, int32_t* status) {
-  __shared__ __align__(16) float us[2][D];      // query sums: positive, negative parts
+                   int n_recent, int per_block, uint2* __restrict__ scores, int32_t* status) {
+  constexpr int kX = D / 32, kWarps = kScoreThreads / 32;
+  __shared__ __align__(16) T parts[2][4][D];    // query sums' positive, negative parts; [3] is 0
+  __shared__ float s_top[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int t = blockIdx.y, kv = blockIdx.z, G = Hq / Hkv;
+  const int g = lane >> 2, c = lane & 3;
   griddep_wait();
   griddep_launch_dependents();
   const int s = warp_find_seq(b, t, lane);
@@ -94,100 +131,118 @@ paged_score_kernel(const PagedBatch b, const T* __restrict__ q, const T* __restr
   const int p0 = w.lo + (int)blockIdx.x * per_block;
   const int p1 = min(w.hi, p0 + per_block);
   if (p0 >= p1) return;
-  // lane: page lane / kL of the warp's, 8 columns of it.  (Half as many lanes a
-  // page, 16 columns each, leaves 4 blocks a SM for 7: 43.0 us for 41.5.)
-  constexpr int kL = D / 8;
-  const int sub = lane & (kL - 1);
   const int32_t* trow = b.table + (int64_t)s * b.max_pages;
   uint2* out = scores + ((int64_t)t * Hkv + kv) * b.max_pages;
-  // the rows of kDeep trips are on their way while a page is summed, the pool
-  // pages of the trip behind them too
-  constexpr int kDeep = 2;
-  struct Rows {
-    uint4 mx, mn;
-    bool ok;
-  };
   auto pool_page = [&](int pg) { return pg < p1 ? trow[pg] : 0; };
-  auto ask = [&](int pg, int ph) {
-    Rows r;
-    r.ok = pg < p1;
-    if (!r.ok) return r;
-    if (ph < 0 || ph >= b.n_pages) {
-      if (sub == 0) set_status(status, TS_ERR_INVALID_ARG);
-      r.ok = false;
+  int first = p0 + warp * 16;
+  int ph[2] = {pool_page(first + g), pool_page(first + g + 8)};
+  uint4 mx[2][kX], mn[2][kX];
+  bool ok[2];
+  // ask for a trip's rows; then for the pool pages of the next
+  auto ask = [&]() {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int pg = first + g + 8 * i;
+      ok[i] = pg < p1;
+      if (ok[i] && (ph[i] < 0 || ph[i] >= b.n_pages)) {
+        if (c == 0) set_status(status, TS_ERR_INVALID_ARG);
+        ok[i] = false;
+      }
+      const int64_t row = ((int64_t)(ok[i] ? ph[i] : 0) * Hkv + kv) * (D / 8) + c;
+#pragma unroll
+      for (int x = 0; x < kX; ++x) {
+        mx[i][x] = __ldg(reinterpret_cast<const uint4*>(key_max) + row + 4 * x);
+        mn[i][x] = __ldg(reinterpret_cast<const uint4*>(key_min) + row + 4 * x);
+      }
+      ph[i] = pool_page(pg + kWarps * 16);
     }
-    const int64_t row = ((int64_t)(r.ok ? ph : 0) * Hkv + kv) * (D / 8);
-    const uint4* mx = reinterpret_cast<const uint4*>(key_max) + row;
-    const uint4* mn = reinterpret_cast<const uint4*>(key_min) + row;
-    r.mx = __ldg(mx + sub);
-    r.mn = __ldg(mn + sub);
-    return r;
   };
-  const int first = p0 + warp * (32 / kL) + lane / kL;
-  constexpr int kEach = kScoreThreads / kL;           // pages a trip
-  Rows next[kDeep];
-  int ph = pool_page(first);
-#pragma unroll
-  for (int x = 0; x < kDeep; ++x) {
-    const int behind = pool_page(first + (x + 1) * kEach);
-    next[x] = ask(first + x * kEach, ph);
-    ph = behind;
-  }
-  // (the query sums are formed while the first rows are on their way)
-  for (int c = tid; c < D; c += kScoreThreads) {
+  if (first < p1) ask();
+  float unscale = 1.f;
+  {
+    // the query sums, while the first rows are on their way
     float up = 0.f, dn = 0.f;
-    for (int g = 0; g < G; ++g) {
-      const float x = Pair<T>::one(q[((int64_t)t * Hq + kv * G + g) * D + c]);
-      up += fmaxf(x, 0.f);
-      dn += fminf(x, 0.f);
+    if (tid < D) {
+      const T* x = q + ((int64_t)t * Hq + kv * G) * D + tid;
+#pragma unroll 4
+      for (int h = 0; h < G; ++h) {
+        const float v = Pair<T>::one(x[h * D]);
+        up += fmaxf(v, 0.f);
+        dn += fminf(v, 0.f);
+      }
     }
-    us[0][c] = up;
-    us[1][c] = dn;
-  }
-  __syncthreads();
-  if (blockIdx.x == 0 && warp == 0) {
-    float sum = 0.f;
-    for (int c = lane; c < D; c += 32) sum += us[0][c] - us[1][c];
-    sum = warp_sum(sum);
-    if (lane == 0) weight[(int64_t)t * Hkv + kv] = sum;
-  }
-  uint64_t up[4], dn[4];
+    float scale = 1.f;
+    if constexpr (Pair<T>::kFp16) {
+      const float top = warp_max(fmaxf(up, -dn));
+      if (lane == 0) s_top[warp] = top;
+      __syncthreads();
+      float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    up[i] = *reinterpret_cast<const uint64_t*>(&us[0][sub * 8 + 2 * i]);
-    dn[i] = *reinterpret_cast<const uint64_t*>(&us[1][sub * 8 + 2 * i]);
-  }
-  for (int base = p0; base < p1; base += kEach) {    // the same trips for every lane
-    const int pg = base + (first - p0);
-    const Rows r = next[0];
-#pragma unroll
-    for (int x = 0; x + 1 < kDeep; ++x) next[x] = next[x + 1];
-    next[kDeep - 1] = ask(pg + kDeep * kEach, ph);
-    ph = pool_page(pg + (kDeep + 1) * kEach);
-    uint64_t s1 = 0, s2 = 0;
-    uint32_t top = 0;                                // largest |bound| of either half, as bits
-    const uint32_t wx[4] = {r.mx.x, r.mx.y, r.mx.z, r.mx.w};
-    const uint32_t wn[4] = {r.mn.x, r.mn.y, r.mn.z, r.mn.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 fx = Pair<T>::unpack(wx[k]), fn = Pair<T>::unpack(wn[k]);
-      s1 = ptx::fma2(up[k], ptx::f2(fx.x, fx.y), s1);
-      s2 = ptx::fma2(dn[k], ptx::f2(fn.x, fn.y), s2);
-      top = __vimax3_u16x2(top, wx[k] & 0x7FFF7FFFu, wn[k] & 0x7FFF7FFFu);
+      for (int i = 0; i < kWarps; ++i) m = fmaxf(m, s_top[i]);
+      const int e = (int)(__float_as_uint(m) >> 23) - 127;
+      if (m > 0.f) scale = __uint_as_float((uint32_t)(127 + 13 - e) << 23);
+      unscale = 1.f / scale;
     }
-    float a0, a1;
-    ptx::f2_split(ptx::add2(s1, s2), a0, a1);
-    float score = a0 + a1;
+    if (tid < D) {
+      float u = up * scale, d = dn * scale;
 #pragma unroll
-    for (int o = 1; o < kL; o <<= 1) {
-      score += __shfl_xor_sync(0xffffffffu, score, o);
-      top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+      for (int i = 0; i < 3; ++i) {
+        parts[0][i][tid] = lead_bits<T>(u);
+        parts[1][i][tid] = lead_bits<T>(d);
+      }
+      parts[0][3][tid] = parts[1][3][tid] = T(0.f);
     }
-    if (sub == 0 && pg < p1) {
-      const uint32_t m16 = max(top & 0xFFFFu, top >> 16);
-      const float m = Pair<T>::unpack(m16).x;
-      const bool good = r.ok && isfinite(score) && isfinite(m);     // the others rank last
-      out[pg] = make_uint2(good ? float_key(score) : kLowest, good ? __float_as_uint(m) : 0u);
+    __syncthreads();
+  }
+  uint2 uf[2][kX][2];
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+#pragma unroll
+    for (int x = 0; x < kX; ++x) {
+      const uint4 v = *reinterpret_cast<const uint4*>(&parts[p][min(g, 3)][(c + 4 * x) * 8]);
+      uf[p][x][0] = make_uint2(v.x, v.y);
+      uf[p][x][1] = make_uint2(v.z, v.w);
+    }
+  while (first < p1) {
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    float size[4] = {0.f, 0.f, 0.f, 0.f};            // sums of |u| |bound|
+#pragma unroll
+    for (int x = 0; x < kX; ++x) {
+      // (few additions in a row: the error's bound decides how many pages near the
+      // cut are formed well)
+      float z[2][4] = {};
+      mma<T>(z[0], mx[0][x].x, mx[1][x].x, mx[0][x].y, mx[1][x].y, uf[0][x][0]);
+      mma<T>(z[1], mn[0][x].x, mn[1][x].x, mn[0][x].y, mn[1][x].y, uf[1][x][0]);
+      mma<T>(z[0], mx[0][x].z, mx[1][x].z, mx[0][x].w, mx[1][x].w, uf[0][x][1]);
+      mma<T>(z[1], mn[0][x].z, mn[1][x].z, mn[0][x].w, mn[1][x].w, uf[1][x][1]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] += z[0][i] + z[1][i];
+      auto abs4 = [](const uint4& v) {
+        return make_uint4(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu, v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu);
+      };
+      const uint4 ax0 = abs4(mx[0][x]), ax1 = abs4(mx[1][x]), an0 = abs4(mn[0][x]), an1 = abs4(mn[1][x]);
+      auto mag = [](uint2 v) { return make_uint2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu); };
+      mma<T>(size, ax0.x, ax1.x, ax0.y, ax1.y, uf[0][x][0]);
+      mma<T>(size, an0.x, an1.x, an0.y, an1.y, mag(uf[1][x][0]));
+      mma<T>(size, ax0.z, ax1.z, ax0.w, ax1.w, uf[0][x][1]);
+      mma<T>(size, an0.z, an1.z, an0.w, an1.w, mag(uf[1][x][1]));
+    }
+    const int done = first;
+    const bool read[2] = {ok[0], ok[1]};
+    first += kWarps * 16;
+    if (first < p1) ask();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      // columns 2 c, 2 c + 1 of the products: lane c = 0 has parts 0, 1, lane 1 part 2
+      const float a = acc[2 * i];
+      const float score = ((a + acc[2 * i + 1]) + __shfl_xor_sync(0xffffffffu, a, 1)) * unscale;
+      const int pg = done + g + 8 * i;
+      if (c == 0 && pg < p1) {
+        // |u|'s leading part is at most 2^-7 of it short
+        const float m = size[2 * i] * unscale * 1.01f;
+        const bool good = read[i] && isfinite(score) && isfinite(m);     // the others rank last
+        out[pg] = make_uint2(good ? float_key(score) : kLowest, good ? __float_as_uint(m) : 0u);
+      }
     }
   }
 }
@@ -308,7 +363,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kPickThreads)
 paged_pick_kernel(const PagedBatch b, const T* __restrict__ q, const T* __restrict__ key_min,
                   const T* __restrict__ key_max, uint2* __restrict__ scores,
-                  const float* __restrict__ weight, int Hq, int Hkv, int n_top, int n_sink,
+                  int Hq, int Hkv, int n_top, int n_sink,
                   int n_recent, int smem_keys, int32_t* __restrict__ pages,
                   int32_t* __restrict__ counts) {
   extern __shared__ uint32_t held[];
@@ -383,12 +438,11 @@ paged_pick_kernel(const PagedBatch b, const T* __restrict__ q, const T* __restri
     high = max(high, x.x);
     widest = max(widest, x.y);                     // magnitudes order as their bits
   }
-  const float u = weight[unit];
   if (tid == 0) sm.listed = 0;
   bounds(low, high, widest);
   Cut cut = find_cut(sm, keys, m, n_top, sm.low, sm.high);
   // pages that may be on either side of the cut
-  const float delta = 3.f * (20.f + G) * 5.9604645e-8f * u * __uint_as_float(sm.widest);
+  const float delta = 2.125f * (76.f + G) * 5.9604645e-8f * __uint_as_float(sm.widest);
   const uint32_t bin0 = cut.low + cut.at;
   const uint32_t bin1 = cut.shift == 32 ? 0xFFFFFFFFu : bin0 + ((1u << cut.shift) - 1u);
   const float from = key_float(bin0) - delta, to = key_float(min(bin1, sm.high)) + delta;
@@ -514,14 +568,10 @@ paged_pick_kernel(const PagedBatch b, const T* __restrict__ q, const T* __restri
   }
 }
 
-size_t scores_bytes(int n, int Hkv, int max_pages) {
-  return align_up((size_t)n * Hkv * max_pages * sizeof(uint2), 256);
-}
-
 }  // namespace
 
 size_t paged_select_ws_bytes(int n, int Hkv, int max_pages) {
-  return scores_bytes(n, Hkv, max_pages) + align_up((size_t)n * Hkv * sizeof(float), 256);
+  return align_up((size_t)n * Hkv * max_pages * sizeof(uint2), 256);
 }
 
 template <typename T, int D>
@@ -529,16 +579,14 @@ static int go_select(const PagedBatch& b, const void* q, const void* key_min, co
                      int Hq, int Hkv, int n_top, int n_sink, int n_recent, int32_t* pages,
                      int32_t* counts, void* ws, int32_t* status, cudaStream_t st) {
   uint2* scores = static_cast<uint2*>(ws);
-  float* weight =
-      reinterpret_cast<float*>(static_cast<char*>(ws) + scores_bytes(b.n, Hkv, b.max_pages));
   const T* qt = static_cast<const T*>(q);
   const T* mn = static_cast<const T*>(key_min);
   const T* mx = static_cast<const T*>(key_max);
   // pages a block: enough that the query sums and the first loads' latency are
-  // spread over several trips of 8 or 16 pages, while the SMs have blocks to
-  // overlap (64, 128, 256 a block: 43.0, 41.5, 42.2 us on the 16 streams above)
-  int per_block = 128;
-  while (per_block > 16 &&
+  // spread over several trips of 64 pages, while the SMs have blocks to overlap
+  // (128, 256, 512 a block: 39.0, 38.6, 42.2 us on the 16 streams above)
+  int per_block = 256;
+  while (per_block > 64 &&
          (int64_t)b.n * Hkv * ((b.max_pages + per_block - 1) / per_block) < 4 * kGb300Sms)
     per_block >>= 1;
   cudaLaunchConfig_t cfg = {};
@@ -546,14 +594,14 @@ static int go_select(const PagedBatch& b, const void* q, const void* key_min, co
   pdl_config(&cfg, attr, dim3((b.max_pages + per_block - 1) / per_block, b.n, Hkv),
              dim3(kScoreThreads), 0, st);
   cudaLaunchKernelEx(&cfg, paged_score_kernel<T, D>, b, qt, mn, mx, Hq, Hkv, n_top, n_sink,
-                     n_recent, per_block, scores, weight, status);
+                     n_recent, per_block, scores, status);
   int rc = launch_status("paged_score_kernel");
   if (rc) return rc;
   const int smem_keys = b.max_pages < kPickSmemKeys ? b.max_pages : kPickSmemKeys;
   cudaFuncSetAttribute(paged_pick_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                        kPickSmemKeys * 4);
   pdl_config(&cfg, attr, dim3(b.n, Hkv), dim3(kPickThreads), (size_t)smem_keys * 4, st);
-  cudaLaunchKernelEx(&cfg, paged_pick_kernel<T, D>, b, qt, mn, mx, scores, (const float*)weight, Hq,
+  cudaLaunchKernelEx(&cfg, paged_pick_kernel<T, D>, b, qt, mn, mx, scores, Hq,
                      Hkv, n_top, n_sink, n_recent, smem_keys, pages, counts);
   return launch_status("paged_pick_kernel");
 }
