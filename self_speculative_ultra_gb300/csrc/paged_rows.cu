@@ -19,8 +19,9 @@
 // unit's end in shared memory.
 // Q.K^T and P.V use 16x8x16 matrix instructions: 16 rows never fill a tensor
 // core tile, so the copy engine's 128-row tiles would only pad.  P is split
-// into a 16-bit value and its 16-bit remainder (two products), so P.V sees P
-// to 16 bits or more and the only rounding to 16 bits is the output's.
+// into a 16-bit value and its 16-bit remainder (two products), so P.V sees a
+// weight to 16 bits (bf16), or to 22 (fp16) but for 2^-33 of the largest weight
+// of its 32 keys (see moved()).
 #include "paged.cuh"
 
 namespace ts {
@@ -86,6 +87,26 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Where the reference m of P = 2^(x - m) stands for 32 keys whose largest
+// exponent is y.  In bf16 it is the running maximum.  fp16 has nothing below
+// 2^-24: against a maximum far above (a first key that draws most of the
+// attention) the tail's weights would round to 0 while their sum counts them.
+// So there the reference goes with the keys, up and down: it stays while their
+// largest P is 2^8 .. 2^15 and is set for 2^12 else, and a weight is off by at
+// most 2^-25 in these units.  O and l are held in the same units; `least` keeps
+// them below 2^120 (2^64 for a reference that falls, 2^15 a weight, 2^25 keys,
+// |v| < 2^16), and what lies below it is 2^-64 of what was seen before.
+constexpr float kTop = 15.f, kAt = 12.f, kLow = 8.f, kFall = 64.f;
+template <bool kFp16>
+__device__ __forceinline__ float moved(float m, float& least, float y) {
+  if (!kFp16) return fmaxf(m, y);
+  if (y > m + kTop || (y < m + kLow && y != -INFINITY)) {
+    m = fmaxf(y - kAt, least);
+    least = fmaxf(least, m - kFall);
+  }
+  return m;
 }
 
 // 16-byte chunk c of tile row r, swizzled so that the eight rows of an 8x8
@@ -519,6 +540,7 @@ paged_rows_kernel(const PagedBatch b, const RowsArgs a, int n_rb, int unit_trips
 #pragma unroll
       for (int x = 0; x < 4; ++x) oacc[i][x] = 0.f;
     float ma = -INFINITY, mb = -INFINITY, la = 0.f, lb = 0.f;
+    float least_a = -INFINITY, least_b = -INFINITY;
     // query fragments (16 x 16 blocks), straight from global memory
     uint32_t qf[D / 16][4];
     {
@@ -593,7 +615,8 @@ paged_rows_kernel(const PagedBatch b, const RowsArgs a, int n_rb, int unit_trips
         xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, o));
         xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, o));
       }
-      const float na = fmaxf(ma, xa * sl2), nb_ = fmaxf(mb, xb * sl2);
+      const float na = moved<Pair<T>::kFp16>(ma, least_a, xa * sl2);
+      const float nb_ = moved<Pair<T>::kFp16>(mb, least_b, xb * sl2);
       // nothing seen so far: reference 0 keeps 2^(-inf) = 0
       const float refa = na == -INFINITY ? 0.f : na, refb = nb_ == -INFINITY ? 0.f : nb_;
       const float fa = ex2(ma - refa), fb = ex2(mb - refb);

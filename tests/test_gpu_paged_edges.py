@@ -1,0 +1,163 @@
+"""GPU: the paged calls where their numbers and their paths go to the edge:
+attention sinks, weights of few keys."""
+import numpy as np
+import pytest
+import torch
+
+import paged_util as pu
+
+pytestmark = pytest.mark.gpu
+BF, FP = torch.bfloat16, torch.float16
+
+
+@pytest.fixture(scope="module")
+def ts():
+    import self_speculative_ultra_gb300 as ts
+    ts.build()
+    return ts
+
+
+# ------------------------------------------------------------------ attention sinks
+class Stream:
+    """One stream whose rows lie in shuffled pages; k, v [Hkv, kv, d]."""
+
+    def __init__(self, q, k, v, ps):
+        Hkv, kv, d = k.shape
+        self.q, self.n, self.Hq, self.Hkv, self.d, self.kv, self.ps = \
+            q, q.shape[0], q.shape[1], Hkv, d, kv, ps
+        m = (kv + ps - 1) // ps
+        perm = torch.randperm(m, generator=torch.Generator().manual_seed(1)).cuda()
+        self.table = perm.int()[None].contiguous()
+        self.rows = (k, v)
+
+        def pool(x):
+            pages = torch.zeros(m, Hkv, ps, d, dtype=x.dtype, device="cuda")
+            pad = torch.cat([x, x.new_zeros(Hkv, m * ps - kv, d)], 1)
+            pages[perm] = pad.view(Hkv, m, ps, d).permute(1, 0, 2, 3)
+            return pages
+        self.k, self.v = pool(k), pool(v)
+        self.cu_q = torch.tensor([0, self.n], dtype=torch.int32, device="cuda")
+        self.lens = torch.tensor([kv], dtype=torch.int32, device="cuda")
+        self.status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def reference(self):
+        """(o, lse, sum p |v|, largest sum |q k| / sqrt d) in 64 bits."""
+        G, n = self.Hq // self.Hkv, self.n
+        last = torch.arange(self.kv - n, self.kv, device="cuda")
+        hide = torch.arange(self.kv, device="cuda")[None, None] > last[:, None, None]
+        out = []
+        for h in range(self.Hkv):
+            q = self.q[:, h * G:(h + 1) * G].double()
+            k, v = (x[h].double() for x in self.rows)
+            x = (q @ k.t() / self.d ** 0.5).masked_fill(hide, -float("inf"))
+            lse = x.logsumexp(2)
+            p = (x - lse[..., None]).exp()
+            aq = (q.abs() @ k.abs().t()).masked_fill(hide, 0.0).amax(2) / self.d ** 0.5
+            out.append((p @ v, lse, p @ v.abs(), aq))
+        return tuple(torch.cat(x, 1).cpu().numpy() for x in zip(*out))
+
+
+def _sink_stream(q, kv, Hq, Hkv, d, ps, dtype, nats, at, seed):
+    """Row `at` stands `nats` above all others and has a value of zero, so the
+    outputs are the tail's alone.  The others' scores spread by a quarter nat."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    qs, k, v = rnd(q, Hq, d) * 0.5, rnd(Hkv, kv, d) * 0.5, 1.0 + 0.25 * rnd(Hkv, kv, d)
+    qs[..., 0] = 8.0
+    k[..., 0] = 0.0
+    k[:, at] = 0.0
+    k[:, at, 0] = nats * d ** 0.5 / 8.0
+    v[:, at] = 0.0
+    return Stream(qs.to(dtype), k.to(dtype), v.to(dtype), ps)
+
+
+def _check_sink(o, lse, ref, dtype, d, p_round):
+    """check_attention's bound, and what a 16-bit weight may lose beside a key far
+    above it in the same 128 keys: for fp16 at most 2^-32 of the largest there a
+    weight, 2^-25 a tile, times the largest |v| (below 4 here)."""
+    O, L, av, aq = ref
+    e_w = 3 * d * 2.0 ** -23 * aq + 2.0 ** -20
+    delta = (2 * e_w + p_round + 2.0 ** -18)[..., None] * av
+    if dtype == FP:
+        delta = delta + 4 * 2.0 ** -25
+    err = np.abs(pu.f64(o) - O) - (pu.U[dtype] * (np.abs(O) + delta) + delta + pu.TINY[dtype])
+    assert err.max() <= 0, f"o off by {err.max():.3e} beyond its bound, |o| {np.abs(O).mean():.3e}"
+    el = np.abs(pu.f64(lse) - L) - (2 * e_w + 2.0 ** -22 * np.abs(L))
+    assert el.max() <= 0
+
+
+SINKS = [(FP, 16.0), (FP, 17.0), (FP, 18.0), (FP, 20.0), (FP, 24.0), (FP, 60.0), (BF, 18.0)]
+SINK_IDS = [f"{'fp16' if t is FP else 'bf16'}-{x:g}" for t, x in SINKS]
+
+
+@pytest.mark.parametrize("dtype,nats", SINKS, ids=SINK_IDS)
+@pytest.mark.parametrize("at", [0, 20001])
+@pytest.mark.parametrize("q,kv,Hq,Hkv,d", [(1, 102400, 8, 2, 128),   # units cut in stretches
+                                           (1, 30000, 4, 1, 64),     # a cluster a unit
+                                           (3, 60000, 12, 2, 64)])
+def test_tail_behind_a_sink_few_rows(ts, q, kv, Hq, Hkv, d, at, dtype, nats):
+    s = _sink_stream(q, kv, Hq, Hkv, d, 64, dtype, nats, at, 3)
+    o, lse = ts.ts_paged_attention(s.q, s.k, s.v, s.cu_q, s.lens, s.table, q, status=s.status)
+    assert int(s.status.item()) == 0
+    # a weight is a 16-bit value and its remainder: off by 2^-16 (bf16); fp16: 2^-22,
+    # and where it is small 2^-25 of a step in which its 32 keys' largest is 2^8 or more
+    _check_sink(o, lse, s.reference(), dtype, d, 2.0 ** -16)
+
+
+@pytest.mark.parametrize("dtype,nats", SINKS, ids=SINK_IDS)
+@pytest.mark.parametrize("at", [0, 20001])
+def test_tail_behind_a_sink_chosen_pages(ts, at, dtype, nats):
+    s = _sink_stream(1, 40000, 8, 2, 128, 32, dtype, nats, at, 4)
+    m = s.table.shape[1]
+    pages = torch.arange(m, dtype=torch.int32, device="cuda").expand(1, 2, m).contiguous()
+    counts = torch.full((1, 2), m, dtype=torch.int32, device="cuda")
+    o, lse = ts.ts_paged_attention_selected(s.q, s.k, s.v, s.cu_q, s.lens, s.table, pages, counts,
+                                            status=s.status)
+    assert int(s.status.item()) == 0
+    _check_sink(o, lse, s.reference(), dtype, 128, 2.0 ** -16)
+
+
+@pytest.mark.parametrize("q,Hq", [(1, 4)])
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
+def test_scores_that_swing_from_tile_to_tile(ts, q, Hq, dtype):
+    """Stretches of keys up and down by tens of nats, both ways: the reference of
+    the weights follows within its bounds."""
+    g = torch.Generator(device="cuda").manual_seed(6)
+    kv, d = 40000, 64
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    qs, k, v = rnd(q, Hq, d) * 0.5, rnd(1, kv, d) * 0.5, rnd(1, kv, d)
+    qs[..., 0] = 8.0
+    level = torch.randint(-60, 61, ((kv + 99) // 100,), generator=g, device="cuda").float()
+    k[0, :, 0] = level.repeat_interleave(100)[:kv]
+    s = Stream(qs.to(dtype), k.to(dtype), v.to(dtype), 64)
+    o, lse = ts.ts_paged_attention(s.q, s.k, s.v, s.cu_q, s.lens, s.table, q, status=s.status)
+    assert int(s.status.item()) == 0
+    _check_sink(o, lse, s.reference(), dtype, d, 2.0 ** -8 if dtype == BF else 2.0 ** -10)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("Hq", [1, 16])
+def test_few_rows_keep_the_remainder_of_a_weight(ts, dtype, Hq):
+    """Eight keys whose values cancel in pairs: the outputs are far below sum p|v|,
+    so a weight of one 16-bit value (2^-9, 2^-12 on average) would show."""
+    g = torch.Generator(device="cuda").manual_seed(7)
+    d = 128
+    k = torch.randn(1, 8, d, generator=g, device="cuda")
+    k[:, 1::2] = k[:, 0::2]
+    k[:, 1::2] += 0.03 * torch.randn(1, 4, d, generator=g, device="cuda")
+    v = torch.randn(1, 8, d, generator=g, device="cuda")
+    v[:, 1::2] = -v[:, 0::2]
+    q = torch.randn(1, Hq, d, generator=g, device="cuda") * 0.02
+    s = Stream(q.to(dtype), k.to(dtype), v.to(dtype), 16)
+    o, lse = ts.ts_paged_attention(s.q, s.k, s.v, s.cu_q, s.lens, s.table, 1, status=s.status)
+    assert int(s.status.item()) == 0
+    ref = s.reference()
+    # half a step of either part's rounding, relative: bf16 2^-16, fp16 2^-22
+    pu.check_attention(o, lse, ref, dtype, d, p_round=2.0 ** -16 if dtype == BF else 2.0 ** -22)
+    # the case shows it: with the weights rounded once the bound is broken
+    x = s.q[0].double() @ s.rows[0][0].double().t() / d ** 0.5
+    p = (x - x.amax(1, keepdim=True)).exp()
+    once = (p.to(dtype).double() @ s.rows[1][0].double() / p.sum(1, keepdim=True)).to(dtype)
+    with pytest.raises(AssertionError):
+        pu.check_attention(once[None], lse, ref, dtype, d,
+                           p_round=2.0 ** -16 if dtype == BF else 2.0 ** -22)
