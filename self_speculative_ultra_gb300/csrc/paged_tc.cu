@@ -28,12 +28,12 @@
 //   warps 4..7   the item's query rows into shared memory; rows of V behind
 //                the sequence's last are cleared (0 * NaN would reach O)
 //   warps 8..15  softmax, one thread a row: all 128 scores in registers,
-//                P = 2^(s log2e / sqrt(d) - m) against a running maximum m that
-//                moves only when a tile's row sum of P exceeds 2^15; sums in
-//                fp32.  P is rounded once, to the type of V, since the tensor
-//                core takes both operands of a product in one 16-bit type: off
-//                by half a step a weight, as the output's own rounding is, and
-//                averaged over the keys.
+//                P = 2^(s log2e / sqrt(d) - m) against a reference m that moves
+//                only when a tile's row sum of P exceeds 2^15 (or in fp16 falls
+//                below 2^-7, see kHead); sums in fp32.  P is rounded once, to
+//                the type of V, since the tensor core takes both operands of a
+//                product in one 16-bit type: off by half a step a weight, as the
+//                output's own rounding is, and averaged over the keys.
 // At the end of an item the softmax warps write O / l (or the piece's O, m, l
 // in fp32); the next item's first scores are formed meanwhile.
 //
@@ -60,6 +60,17 @@ static_assert(2 * 128 * kRegsLow + 2 * 128 * kRegsSoftmax == kThreads * 128,
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kFastSum = 32768.0f;
+// Where the reference m of P = 2^(x - m) stands.  In bf16 it is the largest
+// exponent x at its last move, and only rises.  fp16 has nothing below 2^-24:
+// against a maximum far above (a first key that draws most of the attention) the
+// tail's weights would round to 0 while their sum counts them.  So there it is
+// set kHead below the largest (128 weights of 2^7 sum to 2^14), and falls too,
+// where a row's 128 weights sum to less than kLeastSum: above that they lose at
+// most 128 * 2^-25 = 2^-11 of their sum beside their own half steps.  It falls by
+// kFall at most and only while l is below kFallSum, which keeps O and l in fp32's
+// range (2^40 * 2^64, |v| < 2^16); 128 keys that it does not follow are less
+// than 2^-47 of what was seen.
+constexpr float kHead = 7.f, kLeastSum = 1.f / 128.f, kFall = 64.f, kFallSum = 1.1e12f;
 constexpr long long kDrainCycles = 1ll << 31;
 constexpr uint32_t kNegInf = 0xFF800000u;
 
@@ -1096,19 +1107,21 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
           ptx::f2_split(s, x, y);
           return x + y;
         };
-        // the running maximum moves only when it has to: a row sum of at most
-        // 2^15 means every P is at most 2^15, finite in either type
+        // the reference moves only when it has to: a row sum of at most 2^15
+        // means every P is at most 2^15, finite in either type
         auto put = [&](const uint32_t (&lo)[32], const uint32_t (&hi)[32]) {
           ptx::tmem_st32(s_addr, lo);
           ptx::tmem_st32(s_addr + 32, hi);
         };
         bool fast = m_used != -INFINITY, stored = false;
-        float lt = 0.f;
+        float lt = 1.f;
         if (__all_sync(0xffffffffu, fast)) {
           uint32_t lo[32], hi[32];
           load_s();
           lt = exp_pack(m_used, lo, hi);
           fast = lt <= kFastSum;
+          // (a row that sees none of the tile's keys stays)
+          if (Pair<T>::kFp16 && lt < kLeastSum) fast = l >= kFallSum || (edge && lim < key0);
           if (__all_sync(0xffffffffu, fast)) {
             put(lo, hi);
             l += lt;
@@ -1117,18 +1130,19 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
         } else {
           fast = false;
         }
-        bool raise = false;
+        bool move = false;
         float f = 1.f;
         if (!stored) {
           uint32_t lo[32], hi[32];
           load_s();
           const float ms = fmaxf(fmaxf(fmax32(&r[0]), fmax32(&r[32])),
                                  fmaxf(fmax32(&r[64]), fmax32(&r[96]))) * sl2;
-          raise = !fast && ms > m_used;
-          f = raise ? ptx::ex2(m_used - ms) : 1.f;
-          if (raise) {
+          const float to = Pair<T>::kFp16 ? fmaxf(ms - kHead, m_used - kFall) : ms;
+          move = !fast && (to > m_used || lt < 1.f);
+          f = move ? ptx::ex2(m_used - to) : 1.f;
+          if (move) {
             l *= f;
-            m_used = ms;
+            m_used = to;
           }
           lt = exp_pack(m_used == -INFINITY ? 0.f : m_used, lo, hi);   // nothing seen: 2^-inf = 0
           if (lt != lt) m_used = INFINITY;     // a join drops no NaN; the warp's others go on as they were
@@ -1136,7 +1150,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
           l += lt;
         }
         ptx::tmem_st_wait();
-        if (k > 0 && __any_sync(0xffffffffu, raise)) {
+        if (k > 0 && __any_sync(0xffffffffu, move)) {
           // O may be rescaled once the P V of the tile before is complete.  With
           // an S tile a group this tile's scores went behind it; else it is asked
           if constexpr (kScores > 2) {

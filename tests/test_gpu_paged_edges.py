@@ -117,7 +117,19 @@ def test_tail_behind_a_sink_chosen_pages(ts, at, dtype, nats):
     _check_sink(o, lse, s.reference(), dtype, 128, 2.0 ** -16)
 
 
-@pytest.mark.parametrize("q,Hq", [(1, 4)])
+@pytest.mark.parametrize("dtype,nats", SINKS, ids=SINK_IDS)
+@pytest.mark.parametrize("at", [0, 20001])
+@pytest.mark.parametrize("d", [64, 128])
+def test_tail_behind_a_sink_tiles(ts, d, at, dtype, nats):
+    s = _sink_stream(90, 40000, 4, 1, d, 64, dtype, nats, at, 5)
+    o, lse = ts.ts_paged_attention(s.q, s.k, s.v, s.cu_q, s.lens, s.table, 90, status=s.status)
+    assert int(s.status.item()) == 0
+    # one 16-bit value: half a step a weight; fp16: a row whose weights sum to 2^-7
+    # or more over 128 keys has lost at most 128 * 2^-25 = 2^-11 of the sum besides
+    _check_sink(o, lse, s.reference(), dtype, d, 2.0 ** -8 if dtype == BF else 2.0 ** -10)
+
+
+@pytest.mark.parametrize("q,Hq", [(1, 4), (90, 4)])
 @pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
 def test_scores_that_swing_from_tile_to_tile(ts, q, Hq, dtype):
     """Stretches of keys up and down by tens of nats, both ways: the reference of
