@@ -1137,8 +1137,12 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
           load_s();
           const float ms = fmaxf(fmaxf(fmax32(&r[0]), fmax32(&r[32])),
                                  fmaxf(fmax32(&r[64]), fmax32(&r[96]))) * sl2;
-          const float to = Pair<T>::kFp16 ? fmaxf(ms - kHead, m_used - kFall) : ms;
-          move = !fast && (to > m_used || lt < 1.f);
+          float to = ms;
+          move = !fast && ms > m_used;
+          if constexpr (Pair<T>::kFp16) {
+            to = fmaxf(ms - kHead, m_used - kFall);
+            move = !fast && (to > m_used || lt < 1.f);
+          }
           f = move ? ptx::ex2(m_used - to) : 1.f;
           if (move) {
             l *= f;
