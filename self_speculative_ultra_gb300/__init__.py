@@ -677,18 +677,29 @@ def _paged_batch(cu_q, seq_lens, page_table, dev):
             _need(page_table, i32, shape, dev, "page_table"))
 
 
-def _paged_call(fn, dev, stream, taken, args):
-    """One library call with the tensors' device current.  `taken`: memory that
-    the binding allocated for it, tied to `stream` where that is not the current
-    one."""
+def _alloc(shape, dtype, device, stream):
+    """Memory of a call on `stream` (None: the current one), from that stream's own
+    blocks: what was freed on the current stream may still be read by kernels that
+    are queued there, and nothing holds `stream` back until they are done."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _paged_call(fn, dev, stream, outputs, args):
+    """One library call with the tensors' device current.  `outputs`: what the binding
+    allocated for the caller, who may read it on the current stream (after waiting for
+    `stream`): once freed, it is not used again before those readers are done."""
     if _raw_device() == dev:
         rc = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
     else:
         with torch.cuda.device(dev):
             rc = fn(*args, _raw_stream(dev) if stream is None else stream.cuda_stream)
-    if stream is not None:
-        for t in taken:
-            t.record_stream(stream)
+    if stream is not None and outputs:
+        here = torch.cuda.current_stream(dev)
+        for t in outputs:
+            t.record_stream(here)
     if rc:
         _check(rc)
 
@@ -753,13 +764,13 @@ def ts_paged_rope_append(q, k, v, cu_q, seq_lens, page_table, k_pages, v_pages, 
         mx = _need(key_max, dt, (n_pages, Hkv, d), dev, "key_max")
     if status is not None:
         st = _need(status, torch.int32, status.shape, dev, "status")
-    taken = ()
+    outputs = ()
     if q_out is None:
-        q_out = torch.empty((n, Hq, d), dtype=dt, device=q.device)
-        out, taken = q_out.data_ptr(), (q_out,)
+        q_out = _alloc((n, Hq, d), dt, q.device, stream)
+        out, outputs = q_out.data_ptr(), (q_out,)
     else:
         out = _need(q_out, dt, (n, Hq, d), dev, "q_out")
-    _paged_call(lib().ts_paged_rope_append, dev, stream, taken, (
+    _paged_call(lib().ts_paged_rope_append, dev, stream, outputs, (
         qp, kr, vr, q_stride, k_stride, v_stride, n, Hq, Hkv, d, cu, lens, n_seq, table, max_pages,
         ps, n_pages, pos, fr, 2 * freqs.numel(), rope_scale, out, kp, vp, mn, mx, flags, st))
     return q_out
@@ -776,29 +787,28 @@ def _attend(fn, q, pools, o, lse, want_lse, nbytes, workspace, status, stream, h
     """Outputs, workspace and launch that the two attention calls share; head: the
     arguments in front of (o, lse, workspace, bytes, flags, status, stream)."""
     n, Hq, d, dt, dev, flags = pools
-    taken = []
+    outputs = []
     if o is None:
-        o = torch.empty((n, Hq, d), dtype=dt, device=q.device)
+        o = _alloc((n, Hq, d), dt, q.device, stream)
         out = o.data_ptr()
-        taken.append(o)
+        outputs.append(o)
     else:
         out = _need(o, dt, (n, Hq, d), dev, "o")
     ls = None
     if lse is not None:
         ls = _need(lse, torch.float32, (n, Hq), dev, "lse")
     elif want_lse:
-        lse = torch.empty((n, Hq), dtype=torch.float32, device=q.device)
+        lse = _alloc((n, Hq), torch.float32, q.device, stream)
         ls = lse.data_ptr()
-        taken.append(lse)
+        outputs.append(lse)
     ws, nb = None, nbytes
     if workspace is not None:
         ws, nb = _given_workspace(workspace, nbytes, dev)
     elif nbytes:
-        scratch = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        scratch = _alloc(nbytes, torch.uint8, q.device, stream)
         ws = scratch.data_ptr()
-        taken.append(scratch)
     st = None if status is None else _need(status, torch.int32, status.shape, dev, "status")
-    _paged_call(fn, dev, stream, taken, head + (out, ls, ws, nb, flags, st))
+    _paged_call(fn, dev, stream, outputs, head + (out, ls, ws, nb, flags, st))
     return o, lse
 
 
@@ -843,17 +853,17 @@ def ts_paged_select_pages(q, key_min, key_max, cu_q, seq_lens, page_table, page_
     mn = _need(key_min, dt, bounds, dev, "key_min")
     mx = _need(key_max, dt, bounds, dev, "key_max")
     n_sel = max(n_sink + n_top + n_recent, 0)
-    taken = []
+    outputs = []
     if pages is None:
-        pages = torch.empty((n, Hkv, n_sel), dtype=torch.int32, device=q.device)
+        pages = _alloc((n, Hkv, n_sel), torch.int32, q.device, stream)
         pg = pages.data_ptr()
-        taken.append(pages)
+        outputs.append(pages)
     else:
         pg = _need(pages, torch.int32, (n, Hkv, n_sel), dev, "pages")
     if counts is None:
-        counts = torch.empty((n, Hkv), dtype=torch.int32, device=q.device)
+        counts = _alloc((n, Hkv), torch.int32, q.device, stream)
         ct = counts.data_ptr()
-        taken.append(counts)
+        outputs.append(counts)
     else:
         ct = _need(counts, torch.int32, (n, Hkv), dev, "counts")
     nb = ts_paged_select_workspace_bytes(n, Hkv, max_pages)
@@ -861,11 +871,10 @@ def ts_paged_select_pages(q, key_min, key_max, cu_q, seq_lens, page_table, page_
     if workspace is not None:
         ws, nb = _given_workspace(workspace, nb, dev)
     elif nb:
-        scratch = torch.empty(nb, dtype=torch.uint8, device=q.device)
+        scratch = _alloc(nb, torch.uint8, q.device, stream)
         ws = scratch.data_ptr()
-        taken.append(scratch)
     st = None if status is None else _need(status, torch.int32, status.shape, dev, "status")
-    _paged_call(lib().ts_paged_select_pages, dev, stream, taken, (
+    _paged_call(lib().ts_paged_select_pages, dev, stream, outputs, (
         qp, mn, mx, n, Hq, Hkv, d, cu, lens, n_seq, table, max_pages, page_size, n_pages, n_top,
         n_sink, n_recent, pg, ct, ws, nb, flags, st))
     return pages, counts

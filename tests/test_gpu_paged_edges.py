@@ -1,5 +1,7 @@
 """GPU: the paged calls where their numbers and their paths go to the edge:
-attention sinks, weights of few keys."""
+attention sinks, weights of few keys, queries that are not finite, channels far
+apart in size, tables that are wrong where no token looks, long candidate lists,
+plans of many short tiles, and calls on a stream of their own."""
 import numpy as np
 import pytest
 import torch
@@ -173,3 +175,68 @@ def test_few_rows_keep_the_remainder_of_a_weight(ts, dtype, Hq):
     with pytest.raises(AssertionError):
         pu.check_attention(once[None], lse, ref, dtype, d,
                            p_round=2.0 ** -16 if dtype == BF else 2.0 ** -22)
+
+
+@pytest.mark.parametrize("which", ["append", "attend", "tiles", "select", "selected"])
+def test_a_call_on_its_own_stream_leaves_freed_memory_to_its_readers(ts, which):
+    """Memory freed on the current stream while kernels queued there still read it
+    must not become an output or the workspace of a call on another stream."""
+    q = 200 if which == "tiles" else 2
+    b = pu.Batch([q] * 3, [3000, 2100, 800], 32, 2, 128, 32, BF, seed=14)
+    x = torch.randn(b.n, 2, 128, device="cuda").to(BF)
+    freqs, _ = ts.ts_rope_frequencies(128)
+    mn, mx = b.k.nan_to_num().amin(2), b.k.nan_to_num().amax(2)
+    pages = torch.zeros(b.n, 2, 4, dtype=torch.int32, device="cuda")
+    pages[:] = torch.arange(4, dtype=torch.int32, device="cuda")
+    counts = torch.full((b.n, 2), 4, dtype=torch.int32, device="cuda")
+
+    def call(stream):
+        if which == "append":
+            return [ts.ts_paged_rope_append(b.q, x, x, b.cu_q, b.lens, b.table, b.k, b.v, freqs,
+                                            stream=stream)]
+        if which == "select":
+            return list(ts.ts_paged_select_pages(b.q, mn, mx, b.cu_q, b.lens, b.table, 32, 8, 1, 1,
+                                                 stream=stream))
+        if which == "selected":
+            return list(ts.ts_paged_attention_selected(b.q, b.k, b.v, b.cu_q, b.lens, b.table,
+                                                       pages, counts, stream=stream))
+        return list(ts.ts_paged_attention(b.q, b.k, b.v, b.cu_q, b.lens, b.table, q, stream=stream))
+    want = call(None)
+    sizes = sorted({t.untyped_storage().nbytes() for t in want} |
+                   {ts.ts_paged_attention_workspace_bytes(b.n, 3, 32, 2, 128, b.table.shape[1], 32, q),
+                    ts.ts_paged_select_workspace_bytes(b.n, 2, b.table.shape[1])})
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    busy = [torch.full((s,), 91, dtype=torch.uint8, device="cuda") for s in sizes if s for _ in range(40)]
+    kept = [torch.zeros_like(t) for t in busy]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)              # a tenth of a second
+    for k, t in zip(kept, busy):
+        k.copy_(t)                              # queued readers
+    del busy, t
+    got = call(st)
+    torch.cuda.synchronize()
+    for k in kept:
+        assert (k == 91).all()
+    for a, c in zip(got, want):
+        assert torch.equal(a, c)
+
+
+def test_outputs_of_a_call_on_its_own_stream_outlive_their_readers(ts):
+    """An output that a queued kernel of the current stream still reads is not
+    handed out again on the call's stream once it is freed."""
+    b = pu.Batch([2] * 3, [3000, 2100, 800], 32, 2, 128, 32, BF, seed=15)
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    o = ts.ts_paged_attention(b.q, b.k, b.v, b.cu_q, b.lens, b.table, 2, stream=st)[0]
+    st.synchronize()
+    want, kept = o.clone(), torch.zeros_like(o)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)
+    kept.copy_(o)
+    del o
+    with torch.cuda.stream(st):
+        others = [torch.full_like(want, 5.0) for _ in range(8)]
+    torch.cuda.synchronize()
+    assert torch.equal(kept, want) and len(others) == 8
