@@ -54,6 +54,9 @@ __device__ __forceinline__ void two_sum(float& s, float& e, float p) {
   s = t;
 }
 
+// x where it is above 0; a NaN stays one (its pages' scores are not finite)
+__device__ __forceinline__ float positive(float x) { return x <= 0.f ? 0.f : x; }
+
 __device__ __forceinline__ float key_float(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
@@ -167,8 +170,8 @@ paged_score_kernel(const PagedBatch b, const T* __restrict__ q, const T* __restr
 #pragma unroll 4
       for (int h = 0; h < G; ++h) {
         const float v = Pair<T>::one(x[h * D]);
-        up += fmaxf(v, 0.f);
-        dn += fminf(v, 0.f);
+        up += positive(v);
+        dn -= positive(-v);
       }
     }
     float scale = 1.f;
@@ -383,8 +386,8 @@ paged_pick_kernel(const PagedBatch b, const T* __restrict__ q, const T* __restri
 #pragma unroll 4
     for (int g = 0; g < G; ++g) {
       const float x = Pair<T>::one(q[((int64_t)t * Hq + kv * G + g) * D + c]);
-      two_sum(up, upe, fmaxf(x, 0.f));
-      two_sum(dn, dne, fminf(x, 0.f));
+      two_sum(up, upe, positive(x));
+      two_sum(dn, dne, -positive(-x));
     }
     // 12 leading bits: the product with an 11-bit element is exact
     const float uh = __uint_as_float(__float_as_uint(up) & 0xFFFFF000u);

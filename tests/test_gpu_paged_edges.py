@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import paged_oracle as po
 import paged_util as pu
 
 pytestmark = pytest.mark.gpu
@@ -175,6 +176,58 @@ def test_few_rows_keep_the_remainder_of_a_weight(ts, dtype, Hq):
     with pytest.raises(AssertionError):
         pu.check_attention(once[None], lse, ref, dtype, d,
                            p_round=2.0 ** -16 if dtype == BF else 2.0 ** -22)
+
+
+# ------------------------------------------------------------------ choice of pages
+class Bounds:
+    """A batch for the choice alone: tables and bounds, no rows."""
+
+    def __init__(self, q_lens, kv_lens, Hq, Hkv, d, ps, dtype, seed=0):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        self.rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")
+        self.cu = [0]
+        for x in q_lens:
+            self.cu.append(self.cu[-1] + x)
+        self.kv_lens, self.n, self.Hkv, self.d, self.ps = kv_lens, self.cu[-1], Hkv, d, ps
+        need = [(x + ps - 1) // ps for x in kv_lens]
+        self.n_pages = sum(need)
+        perm = torch.randperm(self.n_pages, generator=torch.Generator().manual_seed(seed)).int()
+        table = torch.zeros(len(need), max(need), dtype=torch.int32)
+        at = 0
+        for s, m in enumerate(need):
+            table[s, :m] = perm[at:at + m]
+            at += m
+        self.table_host, self.table = table, table.cuda()
+        self.q = self.rnd(self.n, Hq, d).to(dtype)
+        mid, half = self.rnd(self.n_pages, Hkv, d), self.rnd(self.n_pages, Hkv, d).abs()
+        self.mn, self.mx = (mid - half).to(dtype), (mid + half).to(dtype)
+        self.cu_q = torch.tensor(self.cu, dtype=torch.int32, device="cuda")
+        self.lens = torch.tensor(kv_lens, dtype=torch.int32, device="cuda")
+        self.status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def check(self, ts, n_top, n_sink, n_recent):
+        pages, counts = ts.ts_paged_select_pages(self.q, self.mn, self.mx, self.cu_q, self.lens,
+                                                 self.table, self.ps, n_top, n_sink, n_recent,
+                                                 status=self.status)
+        assert int(self.status.item()) == 0
+        P, C = po.select_pages(pu.f64(self.q), pu.f64(self.mn), pu.f64(self.mx), self.cu,
+                               self.kv_lens, self.table_host.numpy(), self.ps, n_top, n_sink,
+                               n_recent)
+        np.testing.assert_array_equal(counts.cpu().numpy(), C)
+        np.testing.assert_array_equal(pages.cpu().numpy(), P)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("Hq", [1, 4])
+@pytest.mark.parametrize("what", [float("nan"), float("inf"), -float("inf")])
+def test_choice_with_a_query_that_is_not_finite(ts, dtype, Hq, what):
+    """No score of that token and KV head is finite: all pages rank last, the
+    lowest are taken.  The other tokens choose as ever."""
+    b = Bounds([1, 2], [3000, 5000], 2 * Hq, 2, 64, 16, dtype, seed=8)
+    b.q[1, Hq, 9] = what
+    with np.errstate(invalid="ignore"):
+        b.check(ts, 20, 1, 2)
+        b.check(ts, 100, 0, 1)
 
 
 @pytest.mark.parametrize("which", ["append", "attend", "tiles", "select", "selected"])
