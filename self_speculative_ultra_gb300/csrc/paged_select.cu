@@ -126,10 +126,12 @@ paged_score_kernel(const PagedBatch b, const T* __restrict__ q, const T* __restr
   const int g = lane >> 2, c = lane & 3;
   griddep_wait();
   griddep_launch_dependents();
+  if (blockIdx.x == 0 && t == 0 && kv == 0)     // every sequence's tables, once
+    for (int i = tid; i < b.n_seq; i += kScoreThreads)
+      if (seq_span(b, i).bad) set_status(status, TS_ERR_INVALID_ARG);
   const int s = warp_find_seq(b, t, lane);
   if (s < 0) return;
   const SeqSpan sp = seq_span(b, s);
-  if (blockIdx.x == 0 && kv == 0 && tid == 0 && sp.bad) set_status(status, TS_ERR_INVALID_ARG);
   const Span w = span_of(sp, t, b.page_shift, n_top, n_sink, n_recent);
   const int p0 = w.lo + (int)blockIdx.x * per_block;
   const int p1 = min(w.hi, p0 + per_block);

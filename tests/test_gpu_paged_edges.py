@@ -230,6 +230,30 @@ def test_choice_with_a_query_that_is_not_finite(ts, dtype, Hq, what):
         b.check(ts, 100, 0, 1)
 
 
+@pytest.mark.parametrize("cu,lens", [([0, 1, 1, 2], [900, 10 ** 9, 700]),   # no token of its own
+                                     ([0, 1, 1, 2], [900, -1, 700]),
+                                     ([0, 2, 1, 2], [900, 500, 700]),      # falls behind a token
+                                     ([0, 1, 2, 9], [900, 500, 700])])
+def test_every_call_reports_a_bad_batch(ts, cu, lens):
+    b = Bounds([1, 1, 0], [900, 500, 700], 4, 2, 64, 16, BF, seed=11)
+    cu_q = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    ln = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    kp = torch.zeros(b.n_pages, 2, 16, 64, dtype=BF, device="cuda")
+    vp, x = torch.zeros_like(kp), torch.zeros(2, 2, 64, dtype=BF, device="cuda")
+    freqs, _ = ts.ts_rope_frequencies(64)
+    pages = torch.zeros(2, 2, 1, dtype=torch.int32, device="cuda")
+    counts = torch.ones(2, 2, dtype=torch.int32, device="cuda")
+    calls = [lambda st: ts.ts_paged_select_pages(b.q, b.mn, b.mx, cu_q, ln, b.table, 16, 8, 1, 1, status=st),
+             lambda st: ts.ts_paged_select_pages(b.q, b.mn, b.mx, cu_q, ln, b.table, 16, 900, 1, 1, status=st),
+             lambda st: ts.ts_paged_attention(b.q, kp, vp, cu_q, ln, b.table, 2, status=st),
+             lambda st: ts.ts_paged_attention_selected(b.q, kp, vp, cu_q, ln, b.table, pages, counts, status=st),
+             lambda st: ts.ts_paged_rope_append(b.q, x, x, cu_q, ln, b.table, kp, vp, freqs, status=st)]
+    for i, call in enumerate(calls):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        call(status)
+        assert int(status.item()) == 1, i
+
+
 @pytest.mark.parametrize("which", ["append", "attend", "tiles", "select", "selected"])
 def test_a_call_on_its_own_stream_leaves_freed_memory_to_its_readers(ts, which):
     """Memory freed on the current stream while kernels queued there still read it
