@@ -112,14 +112,16 @@ __device__ __forceinline__ T lead_bits(float& x) {
 // pages g and g + 8, and as a product does not mind the order of its columns,
 // these words are the operand as they lie.  B's columns 0, 1, 2 hold the query
 // sums in three parts of T's bits, which together are exact to fp32 (fp16: but
-// for 2^-38 of the largest, which is brought to 2^13 .. 2^14).
+// for 2^-25, where the largest is brought to 2^13 .. 2^14).  Column 3 holds the
+// size's |u|: its leading part, and in fp16 2^-7 more, so that e covers what the
+// parts lose (76 * 2^-24 * 2^-7 > 2^-25).
 template <typename T, int D>
 __global__ void __launch_bounds__(kScoreThreads, 3)
 paged_score_kernel(const PagedBatch b, const T* __restrict__ q, const T* __restrict__ key_min,
                    const T* __restrict__ key_max, int Hq, int Hkv, int n_top, int n_sink,
                    int n_recent, int per_block, uint2* __restrict__ scores, int32_t* status) {
   constexpr int kX = D / 32, kWarps = kScoreThreads / 32;
-  __shared__ __align__(16) T parts[2][4][D];    // query sums' positive, negative parts; [3] is 0
+  __shared__ __align__(16) T parts[2][4][D];    // query sums' positive, negative parts
   __shared__ float s_top[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int t = blockIdx.y, kv = blockIdx.z, G = Hq / Hkv;
@@ -195,7 +197,9 @@ paged_score_kernel(const PagedBatch b, const T* __restrict__ q, const T* __restr
         parts[0][i][tid] = lead_bits<T>(u);
         parts[1][i][tid] = lead_bits<T>(d);
       }
-      parts[0][3][tid] = parts[1][3][tid] = T(0.f);
+      constexpr float kMore = Pair<T>::kFp16 ? 0.0078125f : 0.f;
+      parts[0][3][tid] = T(Pair<T>::one(parts[0][0][tid]) + kMore);
+      parts[1][3][tid] = T(kMore - Pair<T>::one(parts[1][0][tid]));
     }
     __syncthreads();
   }
@@ -226,11 +230,10 @@ paged_score_kernel(const PagedBatch b, const T* __restrict__ q, const T* __restr
         return make_uint4(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu, v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu);
       };
       const uint4 ax0 = abs4(mx[0][x]), ax1 = abs4(mx[1][x]), an0 = abs4(mn[0][x]), an1 = abs4(mn[1][x]);
-      auto mag = [](uint2 v) { return make_uint2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu); };
       mma<T>(size, ax0.x, ax1.x, ax0.y, ax1.y, uf[0][x][0]);
-      mma<T>(size, an0.x, an1.x, an0.y, an1.y, mag(uf[1][x][0]));
+      mma<T>(size, an0.x, an1.x, an0.y, an1.y, uf[1][x][0]);
       mma<T>(size, ax0.z, ax1.z, ax0.w, ax1.w, uf[0][x][1]);
-      mma<T>(size, an0.z, an1.z, an0.w, an1.w, mag(uf[1][x][1]));
+      mma<T>(size, an0.z, an1.z, an0.w, an1.w, uf[1][x][1]);
     }
     const int done = first;
     const bool read[2] = {ok[0], ok[1]};
@@ -239,12 +242,14 @@ paged_score_kernel(const PagedBatch b, const T* __restrict__ q, const T* __restr
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       // columns 2 c, 2 c + 1 of the products: lane c = 0 has parts 0, 1, lane 1 part 2
+      // and the size
       const float a = acc[2 * i];
       const float score = ((a + acc[2 * i + 1]) + __shfl_xor_sync(0xffffffffu, a, 1)) * unscale;
+      const float mag = __shfl_xor_sync(0xffffffffu, size[2 * i + 1], 1);
       const int pg = done + g + 8 * i;
       if (c == 0 && pg < p1) {
         // |u|'s leading part is at most 2^-7 of it short
-        const float m = size[2 * i] * unscale * 1.01f;
+        const float m = mag * unscale * 1.01f;
         const bool good = read[i] && isfinite(score) && isfinite(m);     // the others rank last
         out[pg] = make_uint2(good ? float_key(score) : kLowest, good ? __float_as_uint(m) : 0u);
       }

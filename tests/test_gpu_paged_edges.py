@@ -230,6 +230,19 @@ def test_choice_with_a_query_that_is_not_finite(ts, dtype, Hq, what):
         b.check(ts, 100, 0, 1)
 
 
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("big", [1.0, 2048.0, 32768.0])
+def test_choice_beside_a_large_query_channel_without_keys(ts, dtype, big):
+    """A channel of large queries and zero keys: the scores are the small channels'
+    alone, to their last bits."""
+    b = Bounds([1, 1], [90000, 40000], 2, 1, 64, 16, dtype, seed=9)
+    b.q = (b.rnd(2, 2, 64) * 2.0 ** -13).to(dtype)
+    b.q[..., 5] = big
+    b.mn[..., 5] = b.mx[..., 5] = 0.0
+    for top in (50, 700, 2000):
+        b.check(ts, top, 1, 1)
+
+
 @pytest.mark.parametrize("cu,lens", [([0, 1, 1, 2], [900, 10 ** 9, 700]),   # no token of its own
                                      ([0, 1, 1, 2], [900, -1, 700]),
                                      ([0, 2, 1, 2], [900, 500, 700]),      # falls behind a token
