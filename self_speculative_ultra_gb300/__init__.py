@@ -708,6 +708,8 @@ def _given_workspace(workspace, nbytes, dev):
     """(address, bytes) of a caller's workspace."""
     if workspace.get_device() != dev:
         raise ValueError(f"workspace is on {workspace.device}, q is on cuda:{dev}")
+    if not workspace.is_contiguous():      # an expanded one has fewer bytes than its shape says
+        raise ValueError("workspace must be contiguous")
     have = workspace.numel() * workspace.element_size()
     if have < nbytes:
         raise ValueError(f"workspace too small: {nbytes} bytes needed")
