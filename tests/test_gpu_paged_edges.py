@@ -243,6 +243,27 @@ def test_choice_beside_a_large_query_channel_without_keys(ts, dtype, big):
         b.check(ts, top, 1, 1)
 
 
+@pytest.mark.parametrize("coarse", [None, 1.0, 0.0])
+def test_choice_among_more_pages_than_shared_memory_holds(ts, coarse):
+    """50,000 candidates: scores apart (all near the cut fit, or few are ranked) and
+    scores that tie in their thousands (all are ranked again)."""
+    b = Bounds([1, 2], [16 * 50100, 16 * 49160], 2, 1, 64, 16, BF, seed=10)
+    if coarse is not None:
+        b.q = (b.q * 2).round()
+        b.mn, b.mx = (x.float().mul(coarse).round().to(BF) for x in (b.mn, b.mx))
+    for top in (1, 700, 49000):
+        b.check(ts, top, 1, 1)
+    if coarse is None:
+        # neighbours at the cut that only well formed scores rank
+        b.mx = b.mx[:1].expand_as(b.mx).clone()
+        b.mn = b.mn[:1].expand_as(b.mn).clone()
+        pick = torch.arange(0, b.n_pages, 997, device="cuda")
+        bits = b.mx.view(torch.int16)
+        bits[pick, 0, (pick // 997) % 64] = bits[pick, 0, (pick // 997) % 64] + 1
+        for top in (20, 80):
+            b.check(ts, top, 1, 1)
+
+
 @pytest.mark.parametrize("cu,lens", [([0, 1, 1, 2], [900, 10 ** 9, 700]),   # no token of its own
                                      ([0, 1, 1, 2], [900, -1, 700]),
                                      ([0, 2, 1, 2], [900, 500, 700]),      # falls behind a token
@@ -265,6 +286,48 @@ def test_every_call_reports_a_bad_batch(ts, cu, lens):
         status = torch.zeros(1, dtype=torch.int32, device="cuda")
         call(status)
         assert int(status.item()) == 1, i
+
+
+# ------------------------------------------------------------------ plans, waits, streams
+@pytest.mark.parametrize("Hkv,long", [(1, 0), (1, 3000), (2, 3000)])
+def test_thousands_of_short_tiles(ts, Hkv, long):
+    """More sequences than the plan's threads and more tiles than its shared memory
+    holds; with few KV heads some may be cut."""
+    rng = np.random.default_rng(12)
+    n_seq, Hq, d, ps = 2300, 8 * Hkv, 64, 16
+    ql = rng.integers(0, 10, n_seq)
+    kl = np.maximum(ql, rng.integers(0, 60, n_seq))
+    ql[5], kl[5] = 9, 57
+    if long:
+        kl[7] = kl[1500] = kl[2200] = long
+    b = pu.Batch([int(x) for x in ql], [int(x) for x in kl], Hq, Hkv, d, ps, BF, seed=13, extra=2)
+    o = torch.full((b.n, Hq, d), 55.0, dtype=BF, device="cuda")
+    lse = torch.full((b.n, Hq), 55.0, device="cuda")
+    ts.ts_paged_attention(b.q, b.k, b.v, b.cu_q, b.lens, b.table, 9, o=o, lse=lse, status=b.status)
+    assert int(b.status.item()) == 0
+    assert (o[b.cu[-1]:] == 55.0).all() and (lse[b.cu[-1]:] == 55.0).all()
+    pu.check_attention(o, lse, b.oracle(), BF, d, p_round=2.0 ** -8)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_expired_wait_of_the_chunk_kernel_is_reported(ts, d):
+    """With a limit of one clock a wait that outlasts one hardware attempt is given
+    up, reported, and the kernel returns; items of tens of thousands of rows have such
+    waits (a next item, its queries' place).  The call behind it is right."""
+    g = torch.Generator(device="cuda").manual_seed(16)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").to(BF)  # noqa: E731
+    s = Stream(rnd(64, 8, d), rnd(2, 30000, d), rnd(2, 30000, d), 32)
+    ts.ts_set_wait_limit(1)
+    try:
+        ts.ts_paged_attention(s.q, s.k, s.v, s.cu_q, s.lens, s.table, 64, status=s.status)
+        torch.cuda.synchronize()
+    finally:
+        ts.ts_set_wait_limit(0)
+    assert int(s.status.item()) == 4
+    s.status.zero_()
+    o, lse = ts.ts_paged_attention(s.q, s.k, s.v, s.cu_q, s.lens, s.table, 64, status=s.status)
+    assert int(s.status.item()) == 0
+    pu.check_attention(o, lse, s.reference(), BF, d, p_round=2.0 ** -8)
 
 
 @pytest.mark.parametrize("which", ["append", "attend", "tiles", "select", "selected"])
