@@ -312,20 +312,21 @@ def test_thousands_of_short_tiles(ts, Hkv, long):
 @pytest.mark.parametrize("d", [64, 128])
 def test_expired_wait_of_the_chunk_kernel_is_reported(ts, d):
     """With a limit of one clock a wait that outlasts one hardware attempt is given
-    up, reported, and the kernel returns; items of tens of thousands of rows have such
-    waits (a next item, its queries' place).  The call behind it is right."""
+    up, reported, and the kernel returns.  Items of a hundred microseconds have such
+    waits (for the next item, for the place of its queries); the call behind it is
+    right."""
     g = torch.Generator(device="cuda").manual_seed(16)
     rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").to(BF)  # noqa: E731
-    s = Stream(rnd(64, 8, d), rnd(2, 30000, d), rnd(2, 30000, d), 32)
+    s = Stream(rnd(200, 32, d), rnd(2, 60000, d), rnd(2, 60000, d), 32)
     ts.ts_set_wait_limit(1)
     try:
-        ts.ts_paged_attention(s.q, s.k, s.v, s.cu_q, s.lens, s.table, 64, status=s.status)
+        ts.ts_paged_attention(s.q, s.k, s.v, s.cu_q, s.lens, s.table, 200, status=s.status)
         torch.cuda.synchronize()
     finally:
         ts.ts_set_wait_limit(0)
     assert int(s.status.item()) == 4
     s.status.zero_()
-    o, lse = ts.ts_paged_attention(s.q, s.k, s.v, s.cu_q, s.lens, s.table, 64, status=s.status)
+    o, lse = ts.ts_paged_attention(s.q, s.k, s.v, s.cu_q, s.lens, s.table, 200, status=s.status)
     assert int(s.status.item()) == 0
     pu.check_attention(o, lse, s.reference(), BF, d, p_round=2.0 ** -8)
 
