@@ -546,7 +546,9 @@ int ts_rope_frequencies(int rot_dim, double base, int scaling, double factor,
  *          bounds of each page's key rows, for ts_paged_select_pages.  A page
  *          whose first row is written now starts over; else its bounds are
  *          widened.  (A row written again leaves its old value inside the
- *          bounds: they stay bounds.)
+ *          bounds: they stay bounds, but wider ones, so where draft rows are
+ *          often rejected and overwritten the pages' scores grow looser until
+ *          a page starts over.)
  * No two sequences of one call may write the same page.  A token whose row
  * would be negative (seq_lens[s] < q_len) is reported and not written. */
 int ts_paged_rope_append(const void* q, const void* k, const void* v, int64_t q_stride,
@@ -570,6 +572,13 @@ int ts_paged_rope_append(const void* q, const void* k, const void* v, int64_t q_
  * them does not matter.
  * A query row that makes a score NaN gets NaN in o and lse, the others what
  * they would get without it.  The same call gives the same bits.
+ * Scores, sums and o before its last rounding are fp32.  The weights p meet V
+ * in 16 bits: where a call's rows are few, as a value and its remainder (off by
+ * 2^-16 of a weight, fp16 2^-22), else as one value of V's type (half a step:
+ * 2^-8, fp16 2^-11).  Which, n_seq, max_q, max_kv, Hq and Hkv decide, so a row
+ * may differ by that much from one call to another.  An fp16 weight is besides
+ * off by up to 2^-33 of the largest among its 32 keys (few rows), or 2^-18 of
+ * the sum over its 128 (else).
  *
  * q [n, Hq, d]; o [n, Hq, d] of q's type, out; lse [n, Hq] fp32 out, or NULL.
  * max_q    a bound on the sequences' new tokens, 1 .. n (a longer sequence is
@@ -591,11 +600,14 @@ int ts_paged_attention(const void* q, const void* k_pages, const void* v_pages, 
  * the largest sum of scores its key bounds allow the head's group:
  *   score = sum over the group's heads h and columns c of
  *           max(q[t,h,c] * key_min[c], q[t,h,c] * key_max[c]),
- * rounded to fp32 once.  A token at row p sees pages 0 .. p / page_size; kept
+ * formed to 2^-45 of the sum of its terms' magnitudes and rounded to fp32 once.
+ * A token at row p sees pages 0 .. p / page_size; kept
  * are the first n_sink of them, the last n_recent, and the n_top best of those
  * between by (score desc, page asc), or all when they are no more than
  * N = n_sink + n_top + n_recent.  Pages with a bound that is not finite, or a
- * score or the sum of its terms' magnitudes beyond the range of fp32, rank last.
+ * score or the sum of its terms' magnitudes beyond the range of fp32, rank last:
+ * all of them where a query of the group is not finite, or a column's queries
+ * sum beyond that range.
  *
  * q        [n, Hq, d] rotated; key_min, key_max [n_pages, Hkv, d].
  * n_recent >= 1 (the last page is the token's own); n_sink, n_top >= 0;

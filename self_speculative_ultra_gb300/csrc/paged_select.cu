@@ -15,8 +15,11 @@
 //   scores  every page's sum and its size S = sum |u| |m|, on the tensor cores
 //           (memory bound: 4 d bytes a page and KV head).  The sum is off by less
 //           than e = (76 + G) 2^-24 S: products are exact, a chain of two products
-//           has 32 additions, off by at most 2^-23 of what is summed, behind it
-//           come 7 roundings to fp32, the query sums' G and the score's own.
+//           has 32 additions, each taken to be off by at most 2^-23 of what is summed
+//           (an assumption: a truncating fp32 adder; nothing documents what the matrix
+//           instruction adds in, and choices among scores that differ by its rounding
+//           are tested), behind it come 7 roundings to fp32, the query sums' G and the
+//           score's own.
 //   pick    per (token, KV head) the n_top-th largest of them, T.  With e the
 //           largest such error, a page above T + 2 e is kept and one below
 //           T - 2 e is not, whatever the errors; when more are left
@@ -24,7 +27,8 @@
 //           into a part of 12 bits, whose product with a 16-bit element is
 //           exact in fp32, and the rest; the rounding error of every addition
 //           kept beside the sum, Knuth's two-sum) and ranked again.  With
-//           scores that are not made to tie that is rarely a page.
+//           scores that are not made to tie that is rarely a page.  (One page of very
+//           large bounds widens e for all, and many may have to be formed.)
 // Forming every page's sum well made the first kernel bound by fp32 arithmetic:
 // 39 us for 16 streams of up to 3200 pages (8 KV heads, d = 128), which take 38
 // now with both kernels.  (Plain sums on the fp32 pipes took ~90 instructions a

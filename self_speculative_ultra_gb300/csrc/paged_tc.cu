@@ -9,8 +9,9 @@
 // bound by the tensor cores (4 d flops a row and key); the softmax stands between
 // the two products, so the groups alternate: while one group's scores are
 // exponentiated the tensor core works for the other.  2048 tokens over 100K rows,
-// 32/8 heads, d = 128: 1.91 ms, 1780 TFLOP/s; over 32K rows, 12/2 heads: 243 us,
-// at d = 64 177 us.
+// 32/8 heads, d = 128: 1.93 ms, 1760 TFLOP/s; over 32K rows, 12/2 heads: 245 us, in
+// fp16 250, at d = 64 177 and 180 us (the best of a few calls in a row; called for
+// seconds on end, at the power cap, the first two take 2.15 ms and 266 us).
 //
 // Three launches.  The plan (one CTA) lists the work from the device-side
 // lengths in order of falling cost: the tiles of whole rounds over the SMs as
@@ -69,7 +70,9 @@ constexpr float kFastSum = 32768.0f;
 // most 128 * 2^-25 = 2^-11 of their sum beside their own half steps.  It falls by
 // kFall at most and only while l is below kFallSum, which keeps O and l in fp32's
 // range (2^40 * 2^64, |v| < 2^16); 128 keys that it does not follow are less
-// than 2^-47 of what was seen.
+// than 2^-47 of what was seen.  A tile that moves it is loaded and exponentiated
+// twice: one sink moves it once (2048 tokens over 32K rows: 260 us with and without),
+// scores that swing by tens of nats every 128 keys at every tile (387 us).
 constexpr float kHead = 7.f, kLeastSum = 1.f / 128.f, kFall = 64.f, kFallSum = 1.1e12f;
 constexpr long long kDrainCycles = 1ll << 31;
 constexpr uint32_t kNegInf = 0xFF800000u;
