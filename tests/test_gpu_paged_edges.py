@@ -394,3 +394,83 @@ def test_outputs_of_a_call_on_its_own_stream_outlive_their_readers(ts):
         others = [torch.full_like(want, 5.0) for _ in range(8)]
     torch.cuda.synchronize()
     assert torch.equal(kept, want) and len(others) == 8
+
+
+@pytest.mark.parametrize("own", [False, True], ids=["current", "own-stream"])
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
+def test_a_captured_step_replayed_on_new_tokens(ts, dtype, own):
+    """Append, choice, and both attentions in one graph, on the capture's stream or
+    forked to another: replays on new queries, lengths and tables give what eager calls
+    give, and two replays of a step end in the same bits."""
+    b = pu.Batch([3, 1, 0, 2], [2100, 900, 40, 1700], 8, 2, 128, 16, dtype, seed=17, extra=2)
+    b.k.nan_to_num_(nan=0.0)
+    b.v.nan_to_num_(nan=0.0)
+    mn, mx = b.k.amin(2).contiguous(), b.k.amax(2).contiguous()
+    pools = (b.k, b.v, mn, mx)
+    freqs, _ = ts.ts_rope_frequencies(128)
+    g = torch.Generator(device="cuda").manual_seed(18)
+    fresh = lambda h: torch.randn(b.n, h, 128, generator=g, device="cuda").to(dtype)  # noqa: E731
+    q, k, v = fresh(8), fresh(2), fresh(2)
+
+    def step(stream=None):
+        kw = dict(status=b.status, stream=stream)
+        r = ts.ts_paged_rope_append(q, k, v, b.cu_q, b.lens, b.table, b.k, b.v, freqs,
+                                    key_min=mn, key_max=mx, **kw)
+        pages, counts = ts.ts_paged_select_pages(r, mn, mx, b.cu_q, b.lens, b.table, 16, 9, 1, 2, **kw)
+        sparse = ts.ts_paged_attention_selected(r, b.k, b.v, b.cu_q, b.lens, b.table, pages, counts, **kw)
+        dense = ts.ts_paged_attention(r, b.k, b.v, b.cu_q, b.lens, b.table, 3, **kw)
+        return (r, pages, counts) + sparse + dense
+    side = torch.cuda.Stream()
+    warm = torch.cuda.Stream()
+    with torch.cuda.stream(warm):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        if own:
+            side.wait_stream(torch.cuda.current_stream())
+        outs = step(side if own else None)
+        if own:
+            torch.cuda.current_stream().wait_stream(side)
+    live = b.cu[-1]
+    for lens in ([2100, 900, 40, 1700], [2050, 17, 40, 3], [3, 1, 0, 2]):
+        b.lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        for x, h in ((q, 8), (k, 2), (v, 2)):
+            x.copy_(fresh(h))
+        start = [x.clone() for x in pools]
+        want = [x[:live].clone() for x in step()]
+        pool_want = [x.clone() for x in pools]
+        for _ in range(2):
+            for x, y in zip(pools, start):
+                x.copy_(y)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert int(b.status.item()) == 0
+            for x, y in zip(outs, want):
+                assert torch.equal(x[:live], y)
+            for x, y in zip(pools, pool_want):
+                assert torch.equal(x, y)
+
+
+def test_choices_and_reads_on_two_streams_at_once(ts):
+    """The sparse step on two streams, each with its own memory, while both run."""
+    bs = [pu.Batch([1, 2, 1], [9000, 5000, 7000], 8, 2, 128, 16, FP, seed=s) for s in (51, 52)]
+    bounds = [tuple(f(b.k.nan_to_num(nan=0.0), 2).contiguous() for f in (torch.amin, torch.amax)) for b in bs]
+
+    def step(b, mm, stream=None):
+        pages, counts = ts.ts_paged_select_pages(b.q, *mm, b.cu_q, b.lens, b.table, 16, 50, 1, 2,
+                                                 stream=stream)
+        return (pages, counts) + ts.ts_paged_attention_selected(b.q, b.k, b.v, b.cu_q, b.lens, b.table,
+                                                                pages, counts, stream=stream)
+    want = [step(b, mm) for b, mm in zip(bs, bounds)]
+    streams = [torch.cuda.Stream() for _ in bs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(8):
+        for i in range(2):
+            got[i].append(step(bs[i], bounds[i], streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for out in got[i]:
+            for x, y in zip(out, want[i]):
+                assert torch.equal(x, y)
