@@ -638,6 +638,137 @@ int ts_paged_attention_selected(const void* q, const void* k_pages, const void* 
                                 float* lse, void* workspace, size_t workspace_bytes, int flags,
                                 int32_t* status, void* stream);
 
+/* ------------------------------------------------------------------------
+ * (7) Draft trees of several streams over the paged cache.
+ *
+ * §E Tree-Based Attention: each tree token attends to its predecessors alone;
+ * (1) verifies one stream's tree over a contiguous cache, this call the trees
+ * of a batch over pages.  The new tokens of sequence s are the nodes of its
+ * tree, rows L .. seq_lens[s] - 1 with L = seq_lens[s] - q_len, written by
+ * ts_paged_rope_append at positions L + depth.  Node i, head h, KV head kv:
+ *   s_j = q[t,h,:] . k_j / sqrt(d) over the rows j < L and the rows L + a of
+ *   every node a on the root path of i (i itself included),
+ *   o[t,h,:] = softmax_j(s) . v_j,  lse[t,h] = ln sum_j exp(s_j).
+ *
+ * Batch, table, precision, NaN and errors as in ts_paged_attention (6): a
+ * chain of nodes is a causal chunk.  A node none of whose rows is there
+ * (seq_lens[s] < q_len) gets o = 0, lse = -inf.
+ * parents  [n] int32, device, packed as the tokens are: the node's parent
+ *          within its own tree, 0 <= parents[i] < i, and -1 of each tree's
+ *          first node.  Another value is reported as TS_ERR_INVALID_ARG in
+ *          `status`; its node then counts as a root.
+ * max_q    a bound on the trees' nodes, 1 .. min(n, 64) (a longer sequence is
+ *          reported in `status`, its tokens behind max_q are not written).
+ * workspace >= ts_paged_tree_attention_workspace_bytes of the same arguments. */
+size_t ts_paged_tree_attention_workspace_bytes(int n, int n_seq, int Hq, int Hkv, int d,
+                                               int max_pages, int page_size, int max_q,
+                                               int64_t max_kv);
+int ts_paged_tree_attention(const void* q, const void* k_pages, const void* v_pages, int n, int Hq,
+                            int Hkv, int d, const int32_t* cu_q, const int32_t* seq_lens,
+                            int n_seq, const int32_t* page_table, int max_pages, int page_size,
+                            int64_t n_pages, const int32_t* parents, int max_q, int64_t max_kv,
+                            void* o, float* lse, void* workspace, size_t workspace_bytes,
+                            int flags, int32_t* status, void* stream);
+
+/* KV commit of the accepted paths over pages, every layer in one launch (§3.1:
+ * after verification the KV cache is updated with the accepted draft).  For
+ * t = 1 .. n_path[s] - 1: row L + path[s][t] of every KV head is copied to row
+ * L + t, in K and V, in place (the root's row is at L already), as
+ * ts_kv_commit does it over a contiguous cache.
+ *
+ * k_pages, v_pages  DEVICE arrays of n_layers pointers, each layer's pool
+ *          [n_pages, Hkv, page_size, d] 16-byte aligned; one batch and one page
+ *          table for all layers, as in (6).  A sequence without new tokens
+ *          keeps its rows.
+ * path     [n_seq, path_stride] int32, path_stride 1 .. 64; n_path [n_seq]
+ *          int32, as the acceptance calls write them: node indices, root first,
+ *          t <= path[s][t] < q_len (path[s][0] is not read), 1 <= n_path[s] <=
+ *          min(q_len, path_stride).
+ * key_min, key_max  DEVICE arrays of n_layers pointers to the pages' key bounds
+ *          [n_pages, Hkv, d], or both NULL.  A page that starts at or behind row
+ *          L and holds a committed row gets the bounds of its committed rows;
+ *          the page in front is widened by its own.  (Rejected rows so leave
+ *          no trace but in the page that holds row L - 1.)
+ * new_lens [n_seq] int32 out, or NULL: L + n_path[s], or seq_lens[s] where the
+ *          sequence has no new token; not seq_lens itself.
+ * A path, page or length out of its range is reported as TS_ERR_INVALID_ARG in
+ * `status`; that sequence's rows, bounds and length then stay as they were.
+ * No two sequences of one call may hold the same page among their trees'. */
+int ts_paged_kv_commit(int n_layers, void* const* k_pages, void* const* v_pages, int Hkv, int d,
+                       const int32_t* cu_q, const int32_t* seq_lens, int n_seq,
+                       const int32_t* page_table, int max_pages, int page_size, int64_t n_pages,
+                       const int32_t* path, int path_stride, const int32_t* n_path,
+                       void* const* key_min, void* const* key_max, int32_t* new_lens, int flags,
+                       int32_t* status, void* stream);
+
+/* ------------------------------------------------------------------------
+ * (8) Logits of a batch's rows under penalties, biases and masks.
+ *
+ * §3.4 Contextual Penalty penalises the tokens of a window inside the sampling
+ * calls (3); these two calls hold what a server adds per request: penalties
+ * over everything a stream has met, biases of single tokens and the masks of a
+ * grammar, for the next token of several streams or every node of their draft
+ * trees.  The result is what the calls of (3) take (of a token without mass
+ * they keep none: -inf is fine there, except that the entropy of eta-sampling
+ * needs finite logits, for which masked_value may be finite).
+ *
+ * State of n_seq sequences, kept from step to step by the caller:
+ *   seen    [n_seq, ceil(V/32)] int32: bit v % 32 of word v / 32 says that token
+ *           v has been met (prompt or generated);
+ *   counts  [n_seq, V] int32: how often it was generated.
+ *
+ * Add tokens to the state: sequence s's are tokens[s, 0 : lens[s]].
+ * tokens   [n_seq, stride] int32, lens [n_seq] int32, both device: a step's
+ *          accepted tokens fit as they are (lens = n_path).
+ * counts   in/out, or NULL: only the bits are kept.
+ * flags    TS_COUNTS_RESET: the state starts over with these tokens.
+ *          TS_COUNTS_PROMPT: they are met but not counted.
+ * A length or token id out of its range is reported as TS_ERR_INVALID_ARG in
+ * `status` (a token is then skipped, a length clamped to 0 .. stride).
+ * V <= 262144.
+ * ------------------------------------------------------------------------ */
+#define TS_COUNTS_RESET 1
+#define TS_COUNTS_PROMPT 2
+int ts_token_counts(const int32_t* tokens, int stride, const int32_t* lens, int n_seq, int V,
+                    int32_t* counts, int32_t* seen, int flags, int32_t* status, void* stream);
+
+/* Row t of sequence s, token v, all in fp32, each operation rounded once:
+ *   x = logits[t, v] + bias of v
+ *   met = seen bit of v, or v among the drafted tokens on the node's path
+ *   c = counts[s, v] (0 where its bit is clear) + how often the path holds v
+ *   where met: x = x > 0 ? x / repetition[s] : x * repetition[s],
+ *              x = x - frequency[s] * c, and x = x - presence[s] if c > 0
+ *   x = masked_value where row t's mask has v's bit clear.
+ *
+ * logits   n rows of V values, row_stride elements apart: fp32, or bf16, fp16
+ *          with a flag.  out: n rows of V fp32 values, out_stride apart; may be
+ *          logits itself where both are fp32 of one stride, else they must not
+ *          overlap.
+ * cu_q     [n_seq + 1] int32: sequence s owns rows [cu_q[s], cu_q[s+1]), as in
+ *          (6); rows behind the last are left as they were.
+ * tree_tokens, parents  [n] int32, or both NULL: the rows are the nodes of draft
+ *          trees (at most 64 a sequence, parents as in (7)), and the path of a
+ *          node is its ancestors and itself without the root, whose token is
+ *          in the state already.
+ * counts, seen  the state, either NULL: 0 (counts need seen).
+ * repetition (> 0), frequency, presence  [n_seq] fp32, each or NULL: 1, 0, 0.
+ * bias_ids, bias  [n_seq, n_bias] int32 and fp32 (n_bias <= 65535): the bias of
+ *          single tokens; -1 is none, and of equal ids the last counts.
+ * mask     [n_masks, ceil(V/32)] int32, or NULL; mask_rows [n] int32: the mask
+ *          of each row, -1 for none; NULL: row t has mask t.  A mask without a
+ *          set bit leaves masked_value everywhere.
+ * Ids, offsets, mask rows or a repetition penalty out of their range are
+ * reported as TS_ERR_INVALID_ARG in `status` and count as absent. */
+#define TS_LOGITS_BF16 1
+#define TS_LOGITS_FP16 2
+int ts_logits_process(const void* logits, int64_t row_stride, int n, int V, const int32_t* cu_q,
+                      int n_seq, const int32_t* tree_tokens, const int32_t* parents,
+                      const int32_t* counts, const int32_t* seen, const float* repetition,
+                      const float* frequency, const float* presence, const int32_t* bias_ids,
+                      const float* bias, int n_bias, const int32_t* mask, int n_masks,
+                      const int32_t* mask_rows, float masked_value, float* out, int64_t out_stride,
+                      int flags, int32_t* status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -139,3 +139,83 @@ def select_pages(q, key_min, key_max, cu_q, seq_lens, table, ps, n_top, n_sink, 
             counts[t, kv] = len(kept)
             pages[t, kv] = kept + [-1] * (N - len(kept))
     return pages, counts
+
+
+def root_paths(parents):
+    """Each node's ancestors and itself, root first; the first node is the root."""
+    paths = []
+    for i, p in enumerate(parents):
+        paths.append((paths[p] if i else []) + [i])
+    return paths
+
+
+def tree_attention(q, k_pages, v_pages, cu_q, seq_lens, table, parents):
+    """attention() with each sequence's tokens as the nodes of a tree: a node sees
+    the rows in front of the tree, its ancestors' and its own."""
+    n, Hq, d = q.shape
+    Hkv = k_pages.shape[1]
+    G = Hq // Hkv
+    o, av = np.full((n, Hq, d), np.nan), np.full((n, Hq, d), np.nan)
+    lse, aq = np.full((n, Hq), np.nan), np.full((n, Hq), np.nan)
+    for s, kl in enumerate(seq_lens):
+        t0, ql = cu_q[s], cu_q[s + 1] - cu_q[s]
+        if ql == 0:
+            continue
+        paths = root_paths([int(p) for p in parents[t0:t0 + ql]])
+        see = np.tile(np.arange(kl) < kl - ql, (ql, 1))
+        for i in range(ql):
+            see[i, [kl - ql + a for a in paths[i] if kl - ql + a >= 0]] = True
+        see = np.repeat(see, G, axis=0)                     # rows (node, head of the group)
+        none = ~see.any(1)
+        for kv in range(Hkv):
+            k = sequence_rows(k_pages, table[s], kl, kv)
+            v = sequence_rows(v_pages, table[s], kl, kv)
+            hs = slice(kv * G, kv * G + G)
+            x = q[t0:t0 + ql, hs].reshape(-1, d)
+            at = np.where(see, x @ k.T / np.sqrt(d), -np.inf)
+            top = np.where(none, 0.0, at.max(1, initial=-np.inf))
+            p = np.exp(at - top[:, None])
+            z = p.sum(1)
+            p /= np.where(none, 1.0, z)[:, None]
+            size = np.where(see, np.abs(x) @ np.abs(k).T, 0.0).max(1, initial=0.0) / np.sqrt(d)
+            with np.errstate(divide="ignore"):
+                total = np.where(none, -np.inf, top + np.log(z))
+            o[t0:t0 + ql, hs] = (p @ v).reshape(ql, G, d)
+            av[t0:t0 + ql, hs] = (p @ np.abs(v)).reshape(ql, G, d)
+            lse[t0:t0 + ql, hs] = total.reshape(ql, G)
+            aq[t0:t0 + ql, hs] = size.reshape(ql, G)
+    return o, lse, av, aq
+
+
+def kv_commit(k_pages, v_pages, key_min, key_max, cu_q, seq_lens, table, path, n_path):
+    """One layer's (k, v, key_min, key_max, new lengths) after the accepted rows'
+    move; key_min, key_max None: no bounds.  Arrays are copied."""
+    k, v = k_pages.copy(), v_pages.copy()
+    mn, mx = (None, None) if key_min is None else (key_min.copy(), key_max.copy())
+    ps = k.shape[2]
+    new = []
+    for s, kl in enumerate(seq_lens):
+        ql = cu_q[s + 1] - cu_q[s]
+        if ql == 0:
+            new.append(kl)
+            continue
+        L, m = kl - ql, n_path[s]
+
+        def at(r):
+            return table[s][r // ps], r % ps
+
+        src = [at(L + path[s][t]) for t in range(1, m)]
+        rows = [(k_pages[p, :, r], v_pages[p, :, r]) for p, r in src]
+        for t in range(1, m):
+            p, r = at(L + t)
+            k[p, :, r], v[p, :, r] = rows[t - 1]
+        new.append(L + m)
+        if mn is None:
+            continue
+        for pg in range(L // ps, (L + m - 1) // ps + 1):
+            held = [k[table[s][pg], :, r - pg * ps] for r in range(max(L, pg * ps), min(L + m, (pg + 1) * ps))]
+            if pg * ps < L:
+                held += [mn[table[s][pg]], mx[table[s][pg]]]
+            mn[table[s][pg]] = np.min(held, axis=0)
+            mx[table[s][pg]] = np.max(held, axis=0)
+    return k, v, mn, mx, new

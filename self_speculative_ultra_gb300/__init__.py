@@ -31,6 +31,8 @@ __all__ = [
     "ts_paged_attention_workspace_bytes", "ts_paged_attention",
     "ts_paged_select_workspace_bytes", "ts_paged_select_pages",
     "ts_paged_selected_workspace_bytes", "ts_paged_attention_selected",
+    "ts_paged_tree_attention_workspace_bytes", "ts_paged_tree_attention", "ts_paged_kv_commit",
+    "ts_token_counts", "ts_logits_process",
 ]
 
 TS_OK, TS_ERR_INVALID_ARG, TS_ERR_UNSUPPORTED, TS_ERR_CUDA, TS_ERR_TIMEOUT, TS_ERR_WORKSPACE = range(6)
@@ -133,6 +135,21 @@ _SIGNATURES = {
                                            _c_void_p, _c_void_p, _i32, _c_void_p, _i32, _i32, _i64,
                                            _c_void_p, _c_void_p, _i32, _c_void_p, _c_void_p,
                                            _c_void_p, _sz, _i32, _c_void_p, _c_void_p]),
+    "ts_paged_tree_attention_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32, _i32,
+                                                      _i32, _i64]),
+    "ts_paged_tree_attention": (_i32, [_c_void_p, _c_void_p, _c_void_p, _i32, _i32, _i32, _i32,
+                                       _c_void_p, _c_void_p, _i32, _c_void_p, _i32, _i32, _i64,
+                                       _c_void_p, _i32, _i64, _c_void_p, _c_void_p, _c_void_p, _sz,
+                                       _i32, _c_void_p, _c_void_p]),
+    "ts_paged_kv_commit": (_i32, [_i32, _c_void_p, _c_void_p, _i32, _i32, _c_void_p, _c_void_p,
+                                  _i32, _c_void_p, _i32, _i32, _i64, _c_void_p, _i32, _c_void_p,
+                                  _c_void_p, _c_void_p, _c_void_p, _i32, _c_void_p, _c_void_p]),
+    "ts_token_counts": (_i32, [_c_void_p, _i32, _c_void_p, _i32, _i32, _c_void_p, _c_void_p, _i32,
+                               _c_void_p, _c_void_p]),
+    "ts_logits_process": (_i32, [_c_void_p, _i64, _i32, _i32, _c_void_p, _i32, _c_void_p,
+                                 _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+                                 _c_void_p, _c_void_p, _i32, _c_void_p, _i32, _c_void_p, _f32,
+                                 _c_void_p, _i64, _i32, _c_void_p, _c_void_p]),
 }
 
 _LIB = None
@@ -650,7 +667,7 @@ def _need(t, dtype, shape, dev, name):
     except AttributeError:
         pass
     _dev(t, dtype, name, shape)
-    raise ValueError(f"{name} is on {t.device}, q is on cuda:{dev}")
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
 
 
 def _paged_q(q):
@@ -905,3 +922,194 @@ def ts_paged_attention_selected(q, k_pages, v_pages, cu_q, seq_lens, page_table,
          _need(v_pages, dt, pool, dev, "v_pages"), n, Hq, Hkv, d, cu, lens, n_seq, table,
          max_pages, ps, n_pages, _need(pages, torch.int32, (n, Hkv, n_sel), dev, "pages"),
          _need(counts, torch.int32, (n, Hkv), dev, "counts"), n_sel))
+
+
+@functools.lru_cache(maxsize=4096)
+def ts_paged_tree_attention_workspace_bytes(n, n_seq, Hq, Hkv, d, max_pages, page_size, max_q,
+                                            max_kv=0) -> int:
+    return lib().ts_paged_tree_attention_workspace_bytes(n, n_seq, Hq, Hkv, d, max_pages,
+                                                         page_size, max_q, max_kv)
+
+
+def ts_paged_tree_attention(q, k_pages, v_pages, cu_q, seq_lens, page_table, parents, max_q,
+                            max_kv=0, o=None, lse=None, want_lse=True, workspace=None, status=None,
+                            stream=None):
+    """Attention of the nodes of several streams' draft trees over a paged
+    cache that holds their rows already: each node sees the rows in front of
+    its tree, its ancestors' and its own.  q [n, Hq, d] bf16 or fp16, parents
+    [n] int32 (within each tree, -1 of its first node), max_q (at most 64)
+    bounds the trees' nodes; the rest as in ts_paged_attention.  Returns
+    (o [n, Hq, d], lse [n, Hq] fp32)."""
+    n, Hq, d, dt, dev, _ = what = _paged_q(q)
+    n_pages, Hkv, ps, _ = k_pages.shape
+    pool = (n_pages, Hkv, ps, d)
+    n_seq, max_pages, cu, lens, table = _paged_batch(cu_q, seq_lens, page_table, dev)
+    return _attend(
+        lib().ts_paged_tree_attention, q, what, o, lse, want_lse,
+        ts_paged_tree_attention_workspace_bytes(n, n_seq, Hq, Hkv, d, max_pages, ps, max_q,
+                                                max_kv),
+        workspace, status, stream,
+        (_need(q, dt, (n, Hq, d), dev, "q"), _need(k_pages, dt, pool, dev, "k_pages"),
+         _need(v_pages, dt, pool, dev, "v_pages"), n, Hq, Hkv, d, cu, lens, n_seq, table,
+         max_pages, ps, n_pages, _need(parents, torch.int32, (n,), dev, "parents"), max_q, max_kv))
+
+
+def _layers(x, name, dt, shape, dev):
+    """The number of layers of per-layer tensors of one shape: a list of them, or
+    one tensor with the layers in front."""
+    if isinstance(x, torch.Tensor):
+        _need(x, dt, (x.shape[0], *shape), dev, name)
+        return x.shape[0]
+    for t in x:
+        _need(t, dt, shape, dev, name)
+    return len(x)
+
+
+def ts_paged_kv_commit(k_pages, v_pages, cu_q, seq_lens, page_table, path, n_path, key_min=None,
+                       key_max=None, new_lens=None, table=None, bounds_table=None, status=None,
+                       stream=None):
+    """Move the accepted rows of several streams' draft trees to the end of
+    their sequences, in every layer's pages and in place.  k_pages, v_pages: a
+    list of the layers' pools [n_pages, Hkv, page_size, d], or one tensor
+    [n_layers, n_pages, Hkv, page_size, d]; path [n_seq, T], n_path [n_seq]
+    int32 (node indices, root first); key_min, key_max: the layers' key bounds
+    likewise.  table = commit_pointer_table(k_pages, v_pages), bounds_table =
+    commit_pointer_table(key_min, key_max): make them once and reuse them while
+    the pools live.  Returns the new lengths [n_seq] int32."""
+    if len(k_pages) == 0:
+        raise ValueError("at least one layer is needed")
+    first = k_pages[0] if not isinstance(k_pages, torch.Tensor) else k_pages
+    if not isinstance(first, torch.Tensor) or not first.is_cuda:
+        raise TypeError("k_pages must be CUDA tensors")
+    dt, dev, pool = first.dtype, first.get_device(), tuple(first.shape[-4:])
+    if dt not in _PAGED_DTYPES:
+        raise TypeError(f"k_pages must be {_PAGED_DTYPES}, got {dt}")
+    if len(pool) != 4:
+        raise ValueError("a layer's pool has shape [n_pages, Hkv, page_size, d]")
+    n_pages, Hkv, ps, d = pool
+    n_layers = _layers(k_pages, "k_pages", dt, pool, dev)
+    if _layers(v_pages, "v_pages", dt, pool, dev) != n_layers:
+        raise ValueError("k_pages and v_pages must have one entry per layer")
+    n_seq, max_pages, cu, lens, pt = _paged_batch(cu_q, seq_lens, page_table, dev)
+    i32 = torch.int32
+    if path.dim() != 2:
+        raise ValueError(f"path has shape {tuple(path.shape)}, expected (n_seq, T)")
+    T = path.shape[1]
+    if (key_min is None) != (key_max is None):
+        raise ValueError("key_min and key_max go together")
+    mn = mx = None
+    if table is None:
+        table = commit_pointer_table(k_pages, v_pages)
+    at = _need(table, torch.int64, (2, n_layers), dev, "table")
+    if key_min is not None:
+        bounds = (n_pages, Hkv, d)
+        if _layers(key_min, "key_min", dt, bounds, dev) != n_layers or \
+                _layers(key_max, "key_max", dt, bounds, dev) != n_layers:
+            raise ValueError("key_min and key_max must have one entry per layer")
+        if bounds_table is None:
+            bounds_table = commit_pointer_table(key_min, key_max)
+        mn = _need(bounds_table, torch.int64, (2, n_layers), dev, "bounds_table")
+        mx = mn + 8 * n_layers
+    outputs = ()
+    if new_lens is None:
+        new_lens = _alloc((n_seq,), i32, first.device, stream)
+        new, outputs = new_lens.data_ptr(), (new_lens,)
+    else:
+        new = _need(new_lens, i32, (n_seq,), dev, "new_lens")
+    st = None if status is None else _need(status, i32, status.shape, dev, "status")
+    _paged_call(lib().ts_paged_kv_commit, dev, stream, outputs, (
+        n_layers, at, at + 8 * n_layers, Hkv, d, cu, lens, n_seq, pt, max_pages, ps, n_pages,
+        _need(path, i32, (n_seq, T), dev, "path"), T, _need(n_path, i32, (n_seq,), dev, "n_path"),
+        mn, mx, new, TS_PAGED_FP16 if dt is torch.float16 else 0, st))
+    return new_lens
+
+
+# ---------------------------------------------------------------------------
+# logits of a batch's rows
+# ---------------------------------------------------------------------------
+TS_COUNTS_RESET, TS_COUNTS_PROMPT = 1, 2
+_LOGITS_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def ts_token_counts(tokens, lens, V, seen, counts=None, reset=False, prompt=False, status=None,
+                    stream=None):
+    """Add tokens[s, :lens[s]] to what the sequences have met: their bits in
+    seen [n_seq, ceil(V / 32)] and, except with prompt=True, counts [n_seq, V]
+    (None: only the bits are kept), all int32.  reset=True starts over with
+    these tokens."""
+    if not isinstance(tokens, torch.Tensor) or not tokens.is_cuda:
+        raise TypeError("tokens must be a CUDA tensor")
+    if tokens.dim() != 2:
+        raise ValueError(f"tokens has shape {tuple(tokens.shape)}, expected (n_seq, m)")
+    dev, i32 = tokens.get_device(), torch.int32
+    n_seq, m = shape = tokens.shape
+    st = None if status is None else _need(status, i32, status.shape, dev, "status")
+    _paged_call(lib().ts_token_counts, dev, stream, (), (
+        _need(tokens, i32, shape, dev, "tokens"), m, _need(lens, i32, (n_seq,), dev, "lens"), n_seq,
+        V, _need(counts, i32, (n_seq, V), dev, "counts"),
+        _need(seen, i32, (n_seq, (V + 31) // 32), dev, "seen"),
+        (TS_COUNTS_RESET if reset else 0) | (TS_COUNTS_PROMPT if prompt else 0), st))
+
+
+def ts_logits_process(logits, cu_q, seen=None, counts=None, repetition=None, frequency=None,
+                      presence=None, tree_tokens=None, parents=None, bias_ids=None, bias=None,
+                      mask=None, mask_rows=None, masked_value=float("-inf"), out=None, status=None,
+                      stream=None):
+    """Logits [n, V] (fp32, bf16 or fp16; any row stride) of the sequences' rows
+    (cu_q [n_seq + 1]) under biases, penalties for the tokens met and masks:
+    fp32 [n, V].  seen, counts: the state of ts_token_counts; repetition,
+    frequency, presence [n_seq] fp32; tree_tokens, parents [n]: the rows are
+    nodes of draft trees, whose paths are met too; bias_ids, bias [n_seq, m];
+    mask [n_masks, ceil(V / 32)] int32 bits of the tokens allowed, mask_rows [n]
+    (None: row t has mask t; -1: none).  out may be logits itself if fp32."""
+    if not isinstance(logits, torch.Tensor) or not logits.is_cuda:
+        raise TypeError("logits must be a CUDA tensor")
+    kind = _LOGITS_TYPES.get(logits.dtype)
+    if kind is None:
+        raise TypeError(f"logits must be {tuple(_LOGITS_TYPES)}, got {logits.dtype}")
+    if logits.dim() != 2:
+        raise ValueError(f"logits has shape {tuple(logits.shape)}, expected (n, V)")
+    n, V = shape = logits.shape
+    dev, i32, f32 = logits.get_device(), torch.int32, torch.float32
+
+    def rows(t, name):
+        row, one = t.stride()
+        if (one != 1 and V > 1) or (row < V and n > 1):
+            raise ValueError(f"{name}: a row's values must be dense")
+        return row if n > 1 else V
+
+    stride = rows(logits, "logits")
+    if not isinstance(cu_q, torch.Tensor) or cu_q.dim() != 1 or cu_q.shape[0] < 1:
+        raise ValueError("cu_q must be a tensor [n_seq + 1]")
+    n_seq, words = cu_q.shape[0] - 1, (V + 31) // 32
+    if (bias_ids is None) != (bias is None):
+        raise ValueError("bias_ids and bias go together")
+    n_bias = 0
+    if bias_ids is not None:
+        n_bias = bias_ids.shape[-1]
+    n_masks = 0
+    if mask is not None:
+        n_masks = mask.shape[0]
+    outputs = ()
+    if out is None:
+        out = _alloc(shape, f32, logits.device, stream)
+        outputs, out_stride = (out,), V
+    else:
+        if not isinstance(out, torch.Tensor) or out.dtype is not f32 or out.shape != shape or \
+                out.get_device() != dev:
+            raise ValueError(f"out must be a float32 tensor {tuple(shape)} on cuda:{dev}")
+        out_stride = rows(out, "out")
+    st = None if status is None else _need(status, i32, status.shape, dev, "status")
+    _paged_call(lib().ts_logits_process, dev, stream, outputs, (
+        logits.data_ptr(), stride, n, V, _need(cu_q, i32, (n_seq + 1,), dev, "cu_q"), n_seq,
+        _need(tree_tokens, i32, (n,), dev, "tree_tokens"), _need(parents, i32, (n,), dev, "parents"),
+        _need(counts, i32, (n_seq, V), dev, "counts"), _need(seen, i32, (n_seq, words), dev, "seen"),
+        _need(repetition, f32, (n_seq,), dev, "repetition"),
+        _need(frequency, f32, (n_seq,), dev, "frequency"),
+        _need(presence, f32, (n_seq,), dev, "presence"),
+        _need(bias_ids, i32, (n_seq, n_bias), dev, "bias_ids"),
+        _need(bias, f32, (n_seq, n_bias), dev, "bias"), n_bias,
+        _need(mask, i32, (n_masks, words), dev, "mask"), n_masks,
+        _need(mask_rows, i32, (n,), dev, "mask_rows"), masked_value, out.data_ptr(), out_stride,
+        kind, st))
+    return out

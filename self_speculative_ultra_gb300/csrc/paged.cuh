@@ -60,6 +60,65 @@ __device__ __forceinline__ int warp_find_seq(const PagedBatch& b, int t, int lan
   return -1;
 }
 
+// The draft tree of one sequence: which nodes are ancestors of which.  Lane i
+// holds node i's ancestor-or-self bits (below 32: nodes only look back) and node
+// 32 + i's.  Built by a warp by pointer jumping, a round for every doubling of
+// the depth (a [1, 3, 3, 3] tree takes two), instead of a chain of loads.
+constexpr int kTreeNodes = 64;
+struct TreeBits {
+  uint32_t low;           // node lane
+  uint32_t up_lo, up_hi;  // node 32 + lane
+
+  // parents: of the sequence's first `nodes` tokens.  A parent that is not an
+  // earlier node (-1 of the first) is reported, and its node becomes a root.
+  __device__ __forceinline__ void build(const int32_t* parents, int nodes, int lane,
+                                        int32_t* status) {
+    int p0 = lane < nodes ? parents[lane] : -1;
+    int p1 = 32 + lane < nodes ? parents[32 + lane] : -1;
+    bool bad = false;
+    if (lane < nodes && (lane == 0 ? p0 != -1 : p0 < 0 || p0 >= lane)) {
+      bad = true;
+      p0 = -1;
+    }
+    if (32 + lane < nodes && (p1 < 0 || p1 >= 32 + lane)) {
+      bad = true;
+      p1 = -1;
+    }
+    if (bad) set_status(status, TS_ERR_INVALID_ARG);
+    low = 1u << lane;
+    up_lo = 0u;
+    up_hi = 1u << lane;
+    while (__any_sync(0xffffffffu, p0 >= 0 || p1 >= 0)) {
+      const uint32_t a = __shfl_sync(0xffffffffu, low, p0 & 31);
+      const int pa = __shfl_sync(0xffffffffu, p0, p0 & 31);
+      const uint32_t b = __shfl_sync(0xffffffffu, low, p1 & 31);
+      const int pb = __shfl_sync(0xffffffffu, p0, p1 & 31);
+      const uint32_t c = __shfl_sync(0xffffffffu, up_lo, p1 & 31);
+      const uint32_t d = __shfl_sync(0xffffffffu, up_hi, p1 & 31);
+      const int pc = __shfl_sync(0xffffffffu, p1, p1 & 31);
+      if (p0 >= 0) {
+        low |= a;
+        p0 = pa;
+      }
+      if (p1 >= 32) {
+        up_lo |= c;
+        up_hi |= d;
+        p1 = pc;
+      } else if (p1 >= 0) {
+        up_lo |= b;
+        p1 = pb;
+      }
+    }
+  }
+  // node i's bits, a node a lane; called by the whole warp
+  __device__ __forceinline__ unsigned long long of(int i) const {
+    const uint32_t a = __shfl_sync(0xffffffffu, low, i & 31);
+    const uint32_t b = __shfl_sync(0xffffffffu, up_lo, i & 31);
+    const uint32_t c = __shfl_sync(0xffffffffu, up_hi, i & 31);
+    return i < 32 ? a : ((unsigned long long)c << 32 | b);
+  }
+};
+
 // 16-bit element types.
 template <typename T>
 struct Pair;
@@ -107,7 +166,7 @@ int launch_paged_append(const PagedBatch& b, const AppendArgs& a, int d, bool fp
                         int32_t* status, cudaStream_t st);
 
 // Attention of few query rows a KV head (new tokens x group), keys split over
-// CTAs, and its sparse form over per-token page lists.
+// CTAs, its sparse form over per-token page lists, and its form for draft trees.
 struct RowsPlan {
   int n_rb;            // blocks of 16 query rows
   int unit_trips;      // trips of 128 keys a unit, by the host's bound
@@ -120,12 +179,23 @@ struct RowsArgs {
   const void *q, *k_pages, *v_pages;
   const int32_t *pages, *counts;   // sparse form: [n, Hkv, n_sel], [n, Hkv]; else NULL
   int n_sel;
+  const int32_t* parents;          // draft trees: [n], else NULL
   int Hq, Hkv, max_q;
   void* o;
   float* lse;
 };
 int launch_paged_rows(const PagedBatch& b, const RowsArgs& a, const RowsPlan& p, int d, bool fp16,
                       void* ws, int32_t* status, cudaStream_t st);
+
+struct CommitArgs {
+  void *const *k_pages, *const *v_pages;       // [n_layers] on the device
+  void *const *key_min, *const *key_max;       // [n_layers] on the device, or NULL
+  const int32_t *path, *n_path;                // [n_seq, path_stride], [n_seq]
+  int path_stride, Hkv;
+  int32_t* new_lens;                           // [n_seq] or NULL
+};
+int launch_paged_commit(const PagedBatch& b, const CommitArgs& a, int n_layers, int d, bool fp16,
+                        int32_t* status, cudaStream_t st);
 
 size_t paged_select_ws_bytes(int n, int Hkv, int max_pages);
 int launch_paged_select(const PagedBatch& b, const void* q, const void* key_min,

@@ -1,5 +1,6 @@
 // C-ABI entry points of the paged-cache operators: host-side argument checks,
 // then the launchers.
+#include <climits>
 #include <cmath>
 
 #include "paged.cuh"
@@ -74,6 +75,49 @@ bool few_rows(int n_seq, int max_q, int Hq, int Hkv, int64_t kv) {
   const int64_t blocks = ((int64_t)max_q * (Hq / Hkv) + 15) / 16;
   const int64_t trips = (int64_t)n_seq * Hkv * blocks * ((kv + 127) / 128);
   return blocks <= 1 || trips <= 8 * kGb300Sms || (blocks <= 4 && trips <= 13 * kGb300Sms);
+}
+
+// The dense call and its form for draft trees (parents not NULL).
+int dense_attention(const char* W, const void* q, const void* k_pages, const void* v_pages, int n,
+                    int Hq, int Hkv, int d, const int32_t* cu_q, const int32_t* seq_lens,
+                    int n_seq, const int32_t* page_table, int max_pages, int page_size,
+                    int64_t n_pages, const int32_t* parents, int max_q, int64_t max_kv, void* o,
+                    float* lse, void* workspace, size_t workspace_bytes, int flags,
+                    int32_t* status, void* stream) {
+  PagedBatch b;
+  int rc = paged_batch(W, n, Hq, Hkv, d, cu_q, seq_lens, n_seq, page_table, max_pages, page_size,
+                       n_pages, flags, TS_PAGED_FP16, &b);
+  if (rc) return rc;
+  if (n == 0 || n_seq == 0) return TS_OK;
+  if (max_q < 1 || max_q > n)
+    return fail(TS_ERR_INVALID_ARG, "%s: max_q=%d not in 1 .. n=%d", W, max_q, n);
+  if (!q || !k_pages || !v_pages || !o) return fail(TS_ERR_INVALID_ARG, "%s: NULL tensor", W);
+  for (const void* p : {q, k_pages, v_pages, (const void*)o})
+    if (!aligned16(p)) return fail(TS_ERR_INVALID_ARG, "%s: a tensor is not 16-byte aligned", W);
+  const int64_t kv = bound_kv(max_pages, page_size, max_kv);
+  if (!parents && !few_rows(n_seq, max_q, Hq, Hkv, kv)) {
+    const TcPlan p = tc_plan(n, n_seq, Hq, Hkv, d, max_q, kv);
+    rc = check_paged_ws(workspace, workspace_bytes, p.ws_bytes, W);
+    if (rc) return rc;
+    const TcArgs a{q, k_pages, v_pages, Hq, Hkv, max_q, o, lse};
+    return launch_paged_tc(b, a, p, d, (flags & TS_PAGED_FP16) != 0, workspace, status,
+                           static_cast<cudaStream_t>(stream));
+  }
+  const RowsPlan p = rows_plan((int64_t)n_seq * Hkv, max_q * (Hq / Hkv), d, kv);
+  rc = check_paged_ws(workspace, workspace_bytes, p.ws_bytes, W);
+  if (rc) return rc;
+  RowsArgs a{};
+  a.q = q;
+  a.k_pages = k_pages;
+  a.v_pages = v_pages;
+  a.parents = parents;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.max_q = max_q;
+  a.o = o;
+  a.lse = lse;
+  return launch_paged_rows(b, a, p, d, (flags & TS_PAGED_FP16) != 0, workspace, status,
+                           static_cast<cudaStream_t>(stream));
 }
 
 }  // namespace
@@ -203,40 +247,71 @@ int ts_paged_attention(const void* q, const void* k_pages, const void* v_pages, 
                        int max_q, int64_t max_kv, void* o, float* lse, void* workspace,
                        size_t workspace_bytes, int flags, int32_t* status, void* stream) {
   clear_error();
-  const char* W = "ts_paged_attention";
+  return dense_attention("ts_paged_attention", q, k_pages, v_pages, n, Hq, Hkv, d, cu_q, seq_lens,
+                         n_seq, page_table, max_pages, page_size, n_pages, nullptr, max_q, max_kv,
+                         o, lse, workspace, workspace_bytes, flags, status, stream);
+}
+
+size_t ts_paged_tree_attention_workspace_bytes(int n, int n_seq, int Hq, int Hkv, int d,
+                                               int max_pages, int page_size, int max_q,
+                                               int64_t max_kv) {
+  if (n < 1 || n_seq < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || max_pages < 1 || page_size < 1 ||
+      max_q < 1 || max_q > kTreeNodes)
+    return 0;
+  const int64_t kv = bound_kv(max_pages, page_size, max_kv);
+  return rows_plan((int64_t)n_seq * Hkv, max_q * (Hq / Hkv), d, kv).ws_bytes;
+}
+
+int ts_paged_tree_attention(const void* q, const void* k_pages, const void* v_pages, int n, int Hq,
+                            int Hkv, int d, const int32_t* cu_q, const int32_t* seq_lens,
+                            int n_seq, const int32_t* page_table, int max_pages, int page_size,
+                            int64_t n_pages, const int32_t* parents, int max_q, int64_t max_kv,
+                            void* o, float* lse, void* workspace, size_t workspace_bytes,
+                            int flags, int32_t* status, void* stream) {
+  clear_error();
+  const char* W = "ts_paged_tree_attention";
+  if (max_q > kTreeNodes)
+    return fail(TS_ERR_UNSUPPORTED, "%s: max_q=%d > %d nodes a tree", W, max_q, kTreeNodes);
+  if (n > 0 && n_seq > 0 && !parents) return fail(TS_ERR_INVALID_ARG, "%s: NULL parents", W);
+  return dense_attention(W, q, k_pages, v_pages, n, Hq, Hkv, d, cu_q, seq_lens, n_seq, page_table,
+                         max_pages, page_size, n_pages, parents, max_q, max_kv, o, lse, workspace,
+                         workspace_bytes, flags, status, stream);
+}
+
+int ts_paged_kv_commit(int n_layers, void* const* k_pages, void* const* v_pages, int Hkv, int d,
+                       const int32_t* cu_q, const int32_t* seq_lens, int n_seq,
+                       const int32_t* page_table, int max_pages, int page_size, int64_t n_pages,
+                       const int32_t* path, int path_stride, const int32_t* n_path,
+                       void* const* key_min, void* const* key_max, int32_t* new_lens, int flags,
+                       int32_t* status, void* stream) {
+  clear_error();
+  const char* W = "ts_paged_kv_commit";
   PagedBatch b;
-  int rc = paged_batch(W, n, Hq, Hkv, d, cu_q, seq_lens, n_seq, page_table, max_pages, page_size,
+  // the tokens' own tensors are not touched: any offset of theirs is in range
+  int rc = paged_batch(W, INT_MAX, 1, 1, d, cu_q, seq_lens, n_seq, page_table, max_pages, page_size,
                        n_pages, flags, TS_PAGED_FP16, &b);
   if (rc) return rc;
-  if (n == 0 || n_seq == 0) return TS_OK;
-  if (max_q < 1 || max_q > n)
-    return fail(TS_ERR_INVALID_ARG, "%s: max_q=%d not in 1 .. n=%d", W, max_q, n);
-  if (!q || !k_pages || !v_pages || !o) return fail(TS_ERR_INVALID_ARG, "%s: NULL tensor", W);
-  for (const void* p : {q, k_pages, v_pages, (const void*)o})
-    if (!aligned16(p)) return fail(TS_ERR_INVALID_ARG, "%s: a tensor is not 16-byte aligned", W);
-  const int64_t kv = bound_kv(max_pages, page_size, max_kv);
-  if (!few_rows(n_seq, max_q, Hq, Hkv, kv)) {
-    const TcPlan p = tc_plan(n, n_seq, Hq, Hkv, d, max_q, kv);
-    rc = check_paged_ws(workspace, workspace_bytes, p.ws_bytes, W);
-    if (rc) return rc;
-    const TcArgs a{q, k_pages, v_pages, Hq, Hkv, max_q, o, lse};
-    return launch_paged_tc(b, a, p, d, (flags & TS_PAGED_FP16) != 0, workspace, status,
-                           static_cast<cudaStream_t>(stream));
-  }
-  const RowsPlan p = rows_plan((int64_t)n_seq * Hkv, max_q * (Hq / Hkv), d, kv);
-  rc = check_paged_ws(workspace, workspace_bytes, p.ws_bytes, W);
-  if (rc) return rc;
-  RowsArgs a{};
-  a.q = q;
-  a.k_pages = k_pages;
-  a.v_pages = v_pages;
-  a.Hq = Hq;
-  a.Hkv = Hkv;
-  a.max_q = max_q;
-  a.o = o;
-  a.lse = lse;
-  return launch_paged_rows(b, a, p, d, (flags & TS_PAGED_FP16) != 0, workspace, status,
-                           static_cast<cudaStream_t>(stream));
+  if (n_layers < 0 || Hkv < 1)
+    return fail(TS_ERR_INVALID_ARG, "%s: n_layers=%d, Hkv=%d", W, n_layers, Hkv);
+  if (n_pages >= (int64_t(1) << 31) / page_size / Hkv)
+    return fail(TS_ERR_UNSUPPORTED, "%s: n_pages * Hkv * page_size >= 2^31", W);
+  if (path_stride < 1) return fail(TS_ERR_INVALID_ARG, "%s: path_stride=%d", W, path_stride);
+  if (path_stride > kTreeNodes)
+    return fail(TS_ERR_UNSUPPORTED, "%s: path_stride=%d > %d nodes a tree", W, path_stride,
+                kTreeNodes);
+  if (!key_min != !key_max)
+    return fail(TS_ERR_INVALID_ARG, "%s: key_min and key_max go together", W);
+  if ((int64_t)n_layers * n_seq * Hkv >= (int64_t(1) << 31))
+    return fail(TS_ERR_UNSUPPORTED, "%s: n_layers * n_seq * Hkv >= 2^31", W);
+  if (n_layers == 0 || n_seq == 0) return TS_OK;
+  if (!k_pages || !v_pages || !path || !n_path)
+    return fail(TS_ERR_INVALID_ARG, "%s: NULL tensor", W);
+  // lengths that change under the blocks that read them
+  if (new_lens && new_lens < seq_lens + n_seq && seq_lens < new_lens + n_seq)
+    return fail(TS_ERR_INVALID_ARG, "%s: new_lens must not overlap seq_lens", W);
+  const CommitArgs a{k_pages, v_pages, key_min, key_max, path, n_path, path_stride, Hkv, new_lens};
+  return launch_paged_commit(b, a, n_layers, d, (flags & TS_PAGED_FP16) != 0, status,
+                             static_cast<cudaStream_t>(stream));
 }
 
 size_t ts_paged_select_workspace_bytes(int n, int Hkv, int max_pages) {

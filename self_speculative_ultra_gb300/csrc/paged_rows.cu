@@ -4,8 +4,9 @@
 //
 //   s_ij = q_i . k_j / sqrt(d),  o_i = softmax_j(s) . v,  lse_i = ln sum exp(s)
 //
-// over the rows j <= seq_len - q_len + i of the sequence (dense), or those of
-// them in the token's listed pages (sparse).
+// over the rows j <= seq_len - q_len + i of the sequence (dense), those of them
+// in the token's listed pages (sparse), or the rows below seq_len - q_len and
+// those of the node's ancestors and itself (a draft tree).
 //
 // Memory bound: K and V are read once, 4 d bytes a key and KV head.  The
 // query rows of a KV head (new tokens x group) are packed into blocks of 16,
@@ -244,7 +245,7 @@ __device__ __forceinline__ float2 far_float2(const void* p, int rank) {
   return v;
 }
 
-template <typename T, int D, bool kSparse>
+template <typename T, int D, bool kSparse, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_rows_kernel(const PagedBatch b, const RowsArgs a, int n_rb, int unit_trips, int cluster,
                   float* __restrict__ part_o, float2* __restrict__ part_ml,
@@ -533,7 +534,16 @@ paged_rows_kernel(const PagedBatch b, const RowsArgs a, int n_rb, int unit_trips
     const int lim_b = rb8 < u.nr ? u.see0 + (u.r0 + rb8) / G : -1;
     // below this key every live row sees everything (rows without a query only
     // ever feed accumulators that are not written)
-    const int free_to = u.see0 + u.r0 / G + 1;
+    const int free_to = kTree ? u.see0 : u.see0 + u.r0 / G + 1;
+    // a tree's rows see the keys below see0, and behind it their nodes' bits
+    unsigned long long tree_a = 0, tree_b = 0;
+    if constexpr (kTree) {
+      TreeBits tree;
+      const SeqSpan sp = seq_span(b, u.s);
+      tree.build(a.parents + sp.q0, min(sp.ql, a.max_q), lane, status);
+      tree_a = tree.of((u.r0 + min(ra, max(u.nr - 1, 0))) / G);
+      tree_b = tree.of((u.r0 + min(rb8, max(u.nr - 1, 0))) / G);
+    }
     float oacc[D / 8][4];
 #pragma unroll
     for (int i = 0; i < D / 8; ++i)
@@ -599,8 +609,14 @@ paged_rows_kernel(const PagedBatch b, const RowsArgs a, int n_rb, int unit_trips
             int key = j + r;
             const bool none = key >= u.n_keys || (nb < 2 ? cur.lp0 : cur.lp1) < 0;
             if (kSparse) key = ((nb < 2 ? cur.lp0 : cur.lp1) << b.page_shift) + (key & (ps - 1));
-            if (none || key > lim_a) c[nb][x] = -INFINITY;
-            if (none || key > lim_b) c[nb][2 + x] = -INFINITY;
+            if constexpr (kTree) {
+              const int node = key - u.see0;             // below 64: n_keys ends there
+              if (none || (node >= 0 && !(tree_a >> (node & 63) & 1))) c[nb][x] = -INFINITY;
+              if (none || (node >= 0 && !(tree_b >> (node & 63) & 1))) c[nb][2 + x] = -INFINITY;
+            } else {
+              if (none || key > lim_a) c[nb][x] = -INFINITY;
+              if (none || key > lim_b) c[nb][2 + x] = -INFINITY;
+            }
           }
       }
       // online softmax over the rows ra (c[.][0..1]) and rb8 (c[.][2..3])
@@ -873,7 +889,9 @@ static int go_rows(const PagedBatch& b, const RowsArgs& a, const RowsPlan& p, vo
   float* part_o = reinterpret_cast<float*>(w + p.cuts_bytes);
   float2* part_ml = reinterpret_cast<float2*>(w + p.cuts_bytes + p.part_bytes);
   const bool sparse = a.pages != nullptr;
-  auto kern = sparse ? paged_rows_kernel<T, D, true> : paged_rows_kernel<T, D, false>;
+  auto kern = sparse ? paged_rows_kernel<T, D, true, false>
+              : a.parents ? paged_rows_kernel<T, D, false, true>
+                          : paged_rows_kernel<T, D, false, false>;
   cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<D>::kBytes);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];

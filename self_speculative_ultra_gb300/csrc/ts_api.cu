@@ -5,6 +5,7 @@
 #include <cstring>
 
 #include "importance.cuh"
+#include "logits.cuh"
 #include "refresh.cuh"
 #include "ts_common.cuh"
 
@@ -385,6 +386,78 @@ int ts_penalized_sample_accept_eta(const float* logits, const int32_t* tree_toke
                               temperature, 1.f, 0.f, 1, eta_epsilon, eta_alpha, uniforms, sampled,
                               path, n_path, bonus, workspace, nullptr, nullptr, status,
                               static_cast<cudaStream_t>(stream));
+}
+
+int ts_token_counts(const int32_t* tokens, int stride, const int32_t* lens, int n_seq, int V,
+                    int32_t* counts, int32_t* seen, int flags, int32_t* status, void* stream) {
+  clear_error();
+  const char* F = "ts_token_counts";
+  if (flags & ~(TS_COUNTS_RESET | TS_COUNTS_PROMPT))
+    return fail(TS_ERR_INVALID_ARG, "%s: unknown flags 0x%x", F, flags);
+  if (n_seq < 0 || stride < 0)
+    return fail(TS_ERR_INVALID_ARG, "%s: n_seq=%d, stride=%d", F, n_seq, stride);
+  if (V < 1) return fail(TS_ERR_INVALID_ARG, "%s: V=%d", F, V);
+  if (V > 262144) return fail(TS_ERR_UNSUPPORTED, "%s: V=%d > 262144", F, V);
+  if (n_seq > (1 << 20)) return fail(TS_ERR_UNSUPPORTED, "%s: n_seq=%d > 2^20", F, n_seq);
+  if (stride > (1 << 25)) return fail(TS_ERR_UNSUPPORTED, "%s: stride=%d > 2^25", F, stride);
+  if ((int64_t)n_seq * stride >= (int64_t(1) << 38))
+    return fail(TS_ERR_UNSUPPORTED, "%s: n_seq * stride >= 2^38", F);
+  const bool reset = (flags & TS_COUNTS_RESET) != 0;
+  if (n_seq == 0 || (stride == 0 && !reset)) return TS_OK;
+  if (!seen || !lens || (stride > 0 && !tokens))
+    return fail(TS_ERR_INVALID_ARG, "%s: NULL tensor", F);
+  return launch_token_counts(tokens, lens, n_seq, stride, V, counts, seen, reset,
+                             (flags & TS_COUNTS_PROMPT) != 0, status,
+                             static_cast<cudaStream_t>(stream));
+}
+
+int ts_logits_process(const void* logits, int64_t row_stride, int n, int V, const int32_t* cu_q,
+                      int n_seq, const int32_t* tree_tokens, const int32_t* parents,
+                      const int32_t* counts, const int32_t* seen, const float* repetition,
+                      const float* frequency, const float* presence, const int32_t* bias_ids,
+                      const float* bias, int n_bias, const int32_t* mask, int n_masks,
+                      const int32_t* mask_rows, float masked_value, float* out, int64_t out_stride,
+                      int flags, int32_t* status, void* stream) {
+  clear_error();
+  const char* F = "ts_logits_process";
+  const int type = flags & (TS_LOGITS_BF16 | TS_LOGITS_FP16);
+  if ((flags & ~(TS_LOGITS_BF16 | TS_LOGITS_FP16)) || type == (TS_LOGITS_BF16 | TS_LOGITS_FP16))
+    return fail(TS_ERR_INVALID_ARG, "%s: unknown flags 0x%x", F, flags);
+  if (n < 0 || n_seq < 0) return fail(TS_ERR_INVALID_ARG, "%s: n=%d, n_seq=%d", F, n, n_seq);
+  if (V < 1) return fail(TS_ERR_INVALID_ARG, "%s: V=%d", F, V);
+  if (V > 262144) return fail(TS_ERR_UNSUPPORTED, "%s: V=%d > 262144", F, V);
+  if (n > (1 << 20) || n_seq > (1 << 20))
+    return fail(TS_ERR_UNSUPPORTED, "%s: more than 2^20 rows or sequences", F);
+  if (n_bias < 0 || n_masks < 0)
+    return fail(TS_ERR_INVALID_ARG, "%s: n_bias=%d, n_masks=%d", F, n_bias, n_masks);
+  if (n_bias > 65535) return fail(TS_ERR_UNSUPPORTED, "%s: n_bias=%d > 65535", F, n_bias);
+  if (!tree_tokens != !parents)
+    return fail(TS_ERR_INVALID_ARG, "%s: tree_tokens and parents go together", F);
+  if (n == 0 || n_seq == 0) return TS_OK;
+  if (row_stride < V || out_stride < V)
+    return fail(TS_ERR_INVALID_ARG, "%s: a row stride is shorter than V=%d", F, V);
+  if (!logits || !out || !cu_q || (n_bias > 0 && (!bias_ids || !bias)))
+    return fail(TS_ERR_INVALID_ARG, "%s: NULL tensor", F);
+  if (counts && !seen)
+    return fail(TS_ERR_INVALID_ARG, "%s: counts are read where seen bits say so", F);
+  if (mask && !mask_rows && n_masks < n)
+    return fail(TS_ERR_INVALID_ARG, "%s: %d masks for %d rows", F, n_masks, n);
+  if (mask_rows && !mask) return fail(TS_ERR_INVALID_ARG, "%s: mask_rows without masks", F);
+  const size_t size = type ? 2 : 4;
+  if (reinterpret_cast<uintptr_t>(logits) % size || reinterpret_cast<uintptr_t>(out) % 4)
+    return fail(TS_ERR_INVALID_ARG, "%s: a tensor is not aligned to its type", F);
+  // rows of another type or stride would be overwritten before they are read
+  const char* a = static_cast<const char*>(logits);
+  const char* o = reinterpret_cast<const char*>(out);
+  const int64_t a_bytes = ((n - 1) * row_stride + V) * (int64_t)size;
+  const int64_t o_bytes = ((n - 1) * out_stride + V) * 4;
+  const bool in_place = a == o && !type && row_stride == out_stride;
+  if (!in_place && a < o + o_bytes && o < a + a_bytes)
+    return fail(TS_ERR_INVALID_ARG, "%s: out overlaps logits", F);
+  const LogitsArgs x{logits, row_stride, out_stride, n, V, n_seq, cu_q, tree_tokens, parents,
+                     counts, seen, repetition, frequency, presence, bias_ids, bias, n_bias, mask,
+                     mask_rows, n_masks, masked_value, out};
+  return launch_logits(x, type, status, static_cast<cudaStream_t>(stream));
 }
 
 int ts_kv_commit(void* k, void* v, int64_t L, int64_t L_cap, int Hkv, int d, int T,
