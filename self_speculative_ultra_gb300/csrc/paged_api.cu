@@ -95,11 +95,11 @@ int dense_attention(const char* W, const void* q, const void* k_pages, const voi
   for (const void* p : {q, k_pages, v_pages, (const void*)o})
     if (!aligned16(p)) return fail(TS_ERR_INVALID_ARG, "%s: a tensor is not 16-byte aligned", W);
   const int64_t kv = bound_kv(max_pages, page_size, max_kv);
-  if (!parents && !few_rows(n_seq, max_q, Hq, Hkv, kv)) {
+  if (!few_rows(n_seq, max_q, Hq, Hkv, kv)) {
     const TcPlan p = tc_plan(n, n_seq, Hq, Hkv, d, max_q, kv);
     rc = check_paged_ws(workspace, workspace_bytes, p.ws_bytes, W);
     if (rc) return rc;
-    const TcArgs a{q, k_pages, v_pages, Hq, Hkv, max_q, o, lse};
+    const TcArgs a{q, k_pages, v_pages, Hq, Hkv, max_q, o, lse, parents};
     return launch_paged_tc(b, a, p, d, (flags & TS_PAGED_FP16) != 0, workspace, status,
                            static_cast<cudaStream_t>(stream));
   }
@@ -255,11 +255,9 @@ int ts_paged_attention(const void* q, const void* k_pages, const void* v_pages, 
 size_t ts_paged_tree_attention_workspace_bytes(int n, int n_seq, int Hq, int Hkv, int d,
                                                int max_pages, int page_size, int max_q,
                                                int64_t max_kv) {
-  if (n < 1 || n_seq < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || max_pages < 1 || page_size < 1 ||
-      max_q < 1 || max_q > kTreeNodes)
-    return 0;
-  const int64_t kv = bound_kv(max_pages, page_size, max_kv);
-  return rows_plan((int64_t)n_seq * Hkv, max_q * (Hq / Hkv), d, kv).ws_bytes;
+  if (max_q > kTreeNodes) return 0;
+  return ts_paged_attention_workspace_bytes(n, n_seq, Hq, Hkv, d, max_pages, page_size, max_q,
+                                            max_kv);
 }
 
 int ts_paged_tree_attention(const void* q, const void* k_pages, const void* v_pages, int n, int Hq,

@@ -4,6 +4,8 @@
 //   s_ij = q_i . k_j / sqrt(d), j <= seq_len - q_len + i
 //   o_i = softmax_j(s) . v,  lse_i = ln sum_j exp(s_ij)
 //
+// or, where the new tokens are the nodes of a draft tree, over the rows in front
+// of the tree and those of the node's ancestors and itself.
 // The query rows of a KV head (row R = new token R / G, head kv * G + R % G)
 // are cut into tiles of 256, two groups of 128.  A chunk over a long cache is
 // bound by the tensor cores (4 d flops a row and key); the softmax stands between
@@ -611,10 +613,22 @@ __device__ __forceinline__ float fmax32(const uint32_t* r) {
   return ptx::max3(a, c, fmaxf(__uint_as_float(r[30]), __uint_as_float(r[31])));
 }
 
-template <typename T, int D>
+// Keys 32 c .. 32 c + 31 of a tile as bits, for a row that sees all keys before
+// the tile's key `base` (which may lie in front of the tile or behind it) and
+// behind it the tree's nodes `nodes`.
+__device__ __forceinline__ uint32_t tree_word(unsigned long long nodes, int base, int c) {
+  const int first = 32 * c - base;             // the word's first key as a node
+  if (first >= 64) return 0u;
+  if (first >= 0) return (uint32_t)(nodes >> first);
+  if (first <= -32) return 0xFFFFFFFFu;
+  return (uint32_t)(nodes << -first) | ((1u << -first) - 1u);
+}
+
+template <typename T, int D, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                 const PagedBatch b, const T* __restrict__ q, int Hq, int Hkv, int max_q,
+                const int32_t* __restrict__ parents,
                 const Work work, T* __restrict__ o, float* __restrict__ lse,
                 float* __restrict__ part_o, float2* __restrict__ part_ml, long long wait_limit,
                 int32_t* status) {
@@ -1036,6 +1050,12 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       const bool valid = R < w.rows;
       const int lim = w.see0 + (valid ? R : w.rows - 1) / G;   // last key this row sees
       const int lim0 = w.see0 + min(wr0, w.rows - 1) / G;      // least of the warp
+      unsigned long long nodes = 0;                            // a tree's: those this row sees
+      if constexpr (kTree) {
+        TreeBits tree;
+        tree.build(parents + w.q0, (w.rows + G - 1) / G, lane, status);
+        nodes = tree.of((valid ? R : w.rows - 1) / G);
+      }
       const int n_mine = g == 0 ? w.n_g[0] : w.n_g[1];
       float m_used = -INFINITY, l = 0.f;
       for (int k = 0; k < n_mine; ++k, ++tiles) {
@@ -1055,7 +1075,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
                                                (g == 1 && k < w.n_g[0] ? 1 : 0);
         const uint32_t s_addr = tmem + lane_off + Ly::sbase(op % kScores);
         const int key0 = (w.k0 + k) * kNk;
-        const bool edge = key0 + kNk > lim0 + 1;    // warp-uniform
+        // warp-uniform
+        const bool edge = kTree ? key0 + kNk > w.see0 : key0 + kNk > lim0 + 1;
         uint32_t r[kNk];
         auto load_s = [&]() {
           ptx::tc_fence_after();
@@ -1064,10 +1085,20 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
             ptx::tmem_ld32(s_addr + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(r + 32 * c));
           ptx::tmem_ld_wait();
           if (edge) {
-            const int vis = lim + 1 - key0;
+            if constexpr (kTree) {
 #pragma unroll
-            for (int x = 0; x < kNk; ++x)
-              if (x >= vis) r[x] = kNegInf;
+              for (int c = 0; c < kNk / 32; ++c) {
+                const uint32_t see = tree_word(nodes, w.see0 - key0, c);
+#pragma unroll
+                for (int x = 0; x < 32; ++x)
+                  if (!(see >> x & 1u)) r[32 * c + x] = kNegInf;
+              }
+            } else {
+              const int vis = lim + 1 - key0;
+#pragma unroll
+              for (int x = 0; x < kNk; ++x)
+                if (x >= vis) r[x] = kNegInf;
+            }
           }
         };
         // P against mref, packed in place: the pair of keys 32c + 2i, 32c + 2i + 1
@@ -1124,7 +1155,12 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
           lt = exp_pack(m_used, lo, hi);
           fast = lt <= kFastSum;
           // (a row that sees none of the tile's keys stays)
-          if (Pair<T>::kFp16 && lt < kLeastSum) fast = l >= kFallSum || (edge && lim < key0);
+          if (Pair<T>::kFp16 && lt < kLeastSum) {
+            bool none = lim < key0;
+            if constexpr (kTree)
+              none = key0 >= w.see0 && (key0 - w.see0 >= 64 || nodes >> (key0 - w.see0) == 0);
+            fast = l >= kFallSum || (edge && none);
+          }
           if (__all_sync(0xffffffffu, fast)) {
             put(lo, hi);
             l += lt;
@@ -1391,7 +1427,7 @@ int go_tc(const PagedBatch& b, const TcArgs& a, const TcPlan& p, char* ws, int32
   int rc = pool_map(&mk, a.k_pages, b, a.Hkv, D, Pair<T>::kFp16);
   if (!rc) rc = pool_map(&mv, a.v_pages, b, a.Hkv, D, Pair<T>::kFp16);
   if (rc) return rc;
-  auto kern = paged_tc_kernel<T, D>;
+  auto kern = a.parents ? paged_tc_kernel<T, D, true> : paged_tc_kernel<T, D, false>;
   // the warps' register split adds up to 128 registers a thread at launch; any
   // other count would leave the softmax warps waiting for registers
   cudaFuncAttributes fa{};
@@ -1418,8 +1454,8 @@ int go_tc(const PagedBatch& b, const TcArgs& a, const TcPlan& p, char* ws, int32
   if (rc) return rc;
   const Work work{hdr, entries, slots};
   pdl_config(&cfg, attr, dim3(p.grid), dim3(kThreads), Layout<D>::kBytes, st);
-  cudaLaunchKernelEx(&cfg, kern, mk, mv, b, static_cast<const T*>(a.q), a.Hq, a.Hkv, a.max_q, work,
-                     static_cast<T*>(a.o), a.lse, part_o, part_ml, wait_limit_cycles(), status);
+  cudaLaunchKernelEx(&cfg, kern, mk, mv, b, static_cast<const T*>(a.q), a.Hq, a.Hkv, a.max_q,
+                     a.parents, work, static_cast<T*>(a.o), a.lse, part_o, part_ml, wait_limit_cycles(), status);
   rc = launch_status("paged_tc_kernel");
   if (rc || p.max_slots == 0) return rc;
   pdl_config(&cfg, attr, dim3(p.merge_grid), dim3(256), 0, st);

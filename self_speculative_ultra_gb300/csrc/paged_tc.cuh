@@ -21,6 +21,7 @@ struct TcArgs {
   int Hq, Hkv, max_q;
   void* o;
   float* lse;
+  const int32_t* parents;      // draft trees: [n], else NULL
 };
 int launch_paged_tc(const PagedBatch& b, const TcArgs& a, const TcPlan& p, int d, bool fp16,
                     void* ws, int32_t* status, cudaStream_t st);

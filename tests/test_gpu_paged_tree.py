@@ -123,9 +123,7 @@ def test_chain_is_a_causal_chunk(ts, Hq, kv):
     b = pu.Batch([64, 20], [kv, kv], Hq, 2, 128, 32, BF, seed=6)
     o, lse = attend(ts, b, parents_of(b.q_lens, "chain"))
     o2, lse2 = ts.ts_paged_attention(b.q, b.k, b.v, b.cu_q, b.lens, b.table, 64)
-    ref = b.oracle() if kv < 1000 else oracle(b, parents_of(b.q_lens, "chain"))
-    for x, y in ((o, lse), (o2, lse2)):
-        pu.check_attention(x, y, ref, BF, 128, p_round=P_ROUND[BF])
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
 @pytest.mark.parametrize("Hq", [4, 64])
