@@ -736,8 +736,8 @@ int ts_token_counts(const int32_t* tokens, int stride, const int32_t* lens, int 
  *   x = logits[t, v] + bias of v
  *   met = seen bit of v, or v among the drafted tokens on the node's path
  *   c = counts[s, v] (0 where its bit is clear) + how often the path holds v
- *   where met: x = x > 0 ? x / repetition[s] : x * repetition[s],
- *              x = x - frequency[s] * c, and x = x - presence[s] if c > 0
+ *   p = frequency[s] * c, and p = p + presence[s] if c > 0
+ *   where met: x = (x > 0 ? x * (1 / repetition[s]) : x * repetition[s]) - p
  *   x = masked_value where row t's mask has v's bit clear.
  *
  * logits   n rows of V values, row_stride elements apart: fp32, or bf16, fp16
@@ -751,7 +751,8 @@ int ts_token_counts(const int32_t* tokens, int stride, const int32_t* lens, int 
  *          node is its ancestors and itself without the root, whose token is
  *          in the state already.
  * counts, seen  the state, either NULL: 0 (counts need seen).
- * repetition (> 0), frequency, presence  [n_seq] fp32, each or NULL: 1, 0, 0.
+ * repetition (2^-64 .. 2^64), frequency, presence  [n_seq] fp32, each or NULL:
+ *          1, 0, 0.
  * bias_ids, bias  [n_seq, n_bias] int32 and fp32 (n_bias <= 65535): the bias of
  *          single tokens; -1 is none, and of equal ids the last counts.
  * mask     [n_masks, ceil(V/32)] int32, or NULL; mask_rows [n] int32: the mask

@@ -54,12 +54,14 @@ def process_row(x, bias, seen, counts, path_tokens, repetition, frequency, prese
     i = np.nonzero(met)[0]
     y, e = x[i], err[i]
     pos = y > 0
-    y = np.where(pos, y / r, y * r).astype(f)
-    e = np.where(pos, e / float(r), e * float(r)) + U * np.abs(y)
+    y = np.where(pos, y * (f(1) / r) if literal32 else y / r, y * r).astype(f)
+    # the reciprocal's rounding and the product's
+    e = np.where(pos, e / float(r) + U * np.abs(y), e * float(r)) + U * np.abs(y)
     p = (fr * c[i].astype(f)).astype(f)
+    e = e + U * np.abs(p)
+    p = np.where(c[i] > 0, p + pr, p).astype(f)
+    e = e + U * np.abs(p)
     y = (y - p).astype(f)
-    e = e + U * np.abs(p) + U * np.abs(y)
-    y = np.where(c[i] > 0, y - pr, y).astype(f)
     e = e + U * np.abs(y)
     x[i], err[i] = y, e
     if allowed is not None:

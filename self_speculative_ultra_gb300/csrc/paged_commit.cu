@@ -4,9 +4,12 @@
 //   row L + path[t] -> row L + t, t = 1 .. n_path - 1, L = seq_len - q_len
 //
 // A tree's rows are a few hundred bytes each: one launch, bound by its chain of
-// loads (lengths and path, page table, rows).  A block takes one (layer,
-// sequence, KV head): it holds all of the head's rows that move, so every source
-// is read before a destination is written, whatever their order.
+// loads (lengths and path, page table, rows).  A small block takes one (layer,
+// sequence, KV head), so that thousands stand on the SMs at once.  Nothing is
+// written before the whole path and its pages are known to be good; then the rows
+// go a few at a time in rising order: the source of a row lies at or behind it, so
+// what a later one reads has not been written yet, and within a turn all are read
+// before any is written.
 // Key bounds: a page that starts inside the tree starts over with the committed
 // rows, which drops what rejected rows had left there; the page in front, whose
 // older rows are not read here, is widened.
@@ -16,7 +19,8 @@ namespace ts {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 64;
+static_assert(kThreads >= kTreeNodes, "a thread looks up one row of the path");
 
 template <typename T>
 __device__ __forceinline__ void fold(uint4& lo, uint4& hi, const uint4& v) {
@@ -34,9 +38,9 @@ __device__ __forceinline__ void fold(uint4& lo, uint4& hi, const uint4& v) {
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
 paged_commit_kernel(const PagedBatch b, const CommitArgs a, int32_t* status) {
-  constexpr int V16 = D / 8;
-  constexpr int kEach = ((kTreeNodes - 1) * V16 + kThreads - 1) / kThreads;
-  __shared__ uint4 rows[kTreeNodes][V16];        // committed keys, for the bounds
+  constexpr int V16 = D / 8, kRows = kThreads / V16;     // rows a turn
+  // where row L + path[t] lies and where row L + t does, in 16-byte chunks
+  __shared__ int64_t from[kTreeNodes], to[kTreeNodes];
   const int tid = threadIdx.x;
   griddep_wait();
   griddep_launch_dependents();
@@ -44,69 +48,56 @@ paged_commit_kernel(const PagedBatch b, const CommitArgs a, int32_t* status) {
   const int layer = blockIdx.x / a.Hkv / b.n_seq;
   const SeqSpan sp = seq_span(b, s);
   const int n = a.n_path[s];
+  const int step = tid < a.path_stride ? a.path[(int64_t)s * a.path_stride + tid] : 0;
+  uint4* k = static_cast<uint4*>(a.k_pages[layer]);
+  uint4* v = static_cast<uint4*>(a.v_pages[layer]);
   const int L = sp.kl - sp.ql;
   const bool owns = sp.ql > 0 && !sp.bad;
   bool bad = sp.bad || (owns && (n < 1 || n > min(sp.ql, a.path_stride) || L < 0));
-  // a row's place in the pool, in 16-byte chunks; -1: its page is not there
-  auto place = [&](int r) -> int64_t {
-    const int64_t ph = b.table[(int64_t)s * b.max_pages + (r >> b.page_shift)];
-    if (ph < 0 || ph >= b.n_pages) return -1;
-    return ((((ph * a.Hkv + h) << b.page_shift)) + (r & ((1 << b.page_shift) - 1))) * V16;
-  };
-  const int moved = owns && !bad ? (n - 1) * V16 : 0;
-  uint4* k = static_cast<uint4*>(a.k_pages[layer]);
-  uint4* v = static_cast<uint4*>(a.v_pages[layer]);
-  uint4 kr[kEach], vr[kEach];
-  int64_t to[kEach];
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int e = tid + i * kThreads, t = e / V16 + 1, x = e % V16;
-    to[i] = -1;
-    if (e < moved) {
-      const int from = a.path[(int64_t)s * a.path_stride + t];
-      if (from < t || from >= sp.ql) {
-        bad = true;
-      } else {
-        const int64_t src = place(L + from), dst = place(L + t);
-        if (src < 0 || dst < 0) {
-          bad = true;
-        } else {
-          kr[i] = k[src + x];
-          vr[i] = v[src + x];
-          to[i] = dst + x;
-        }
-      }
+  if (owns && !bad && tid < n) {
+    // the root stays (its path entry is not looked at)
+    const int src = tid == 0 ? 0 : step;
+    if (src < tid || src >= sp.ql) {
+      bad = true;
+    } else {
+      const int in = (1 << b.page_shift) - 1;
+      const int32_t* table = b.table + (int64_t)s * b.max_pages;
+      const int64_t p = table[(L + src) >> b.page_shift], q = table[(L + tid) >> b.page_shift];
+      bad = p < 0 || p >= b.n_pages || q < 0 || q >= b.n_pages;
+      from[tid] = (((p * a.Hkv + h) << b.page_shift) + ((L + src) & in)) * V16;
+      to[tid] = (((q * a.Hkv + h) << b.page_shift) + ((L + tid) & in)) * V16;
     }
   }
-  const bool bounds = a.key_min != nullptr;
-  if (bounds && owns && !bad && tid < V16) {
-    const int64_t root = place(L);
-    if (root < 0) bad = true;
-    else rows[0][tid] = k[root + tid];
-  }
-  bad = __syncthreads_or(bad);               // every source is read
+  bad = __syncthreads_or(bad);
   if (bad && tid == 0) set_status(status, TS_ERR_INVALID_ARG);
-  if (blockIdx.x == (int64_t)s * a.Hkv && tid == 0 && a.new_lens)
+  if (blockIdx.x == s * a.Hkv && tid == 0 && a.new_lens)
     a.new_lens[s] = owns && !bad ? L + n : b.seq_lens[s];
   if (bad || !owns) return;
-#pragma unroll
-  for (int i = 0; i < kEach; ++i)
-    if (to[i] >= 0) {
-      k[to[i]] = kr[i];
-      v[to[i]] = vr[i];
-      const int e = tid + i * kThreads;
-      if (bounds) rows[e / V16 + 1][e % V16] = kr[i];
+  const int x = tid % V16;
+  for (int t0 = 1; t0 < n; t0 += kRows) {
+    const int t = t0 + tid / V16;
+    uint4 kr, vr;
+    if (t < n) {
+      kr = k[from[t] + x];
+      vr = v[from[t] + x];
     }
-  if (!bounds) return;
+    __syncthreads();
+    if (t < n) {
+      k[to[t] + x] = kr;
+      v[to[t] + x] = vr;
+    }
+  }
+  if (!a.key_min) return;
   __syncthreads();
   const int first = L >> b.page_shift, pages = ((L + n - 1) >> b.page_shift) - first + 1;
   for (int e = tid; e < pages * V16; e += kThreads) {
-    const int pg = first + e / V16, x = e % V16, start = pg << b.page_shift;
-    const int64_t ph = b.table[(int64_t)s * b.max_pages + pg];    // seen above
+    const int start = (first + e / V16) << b.page_shift;
     const int t0 = max(start - L, 0), t1 = min(start + (1 << b.page_shift) - L, n);
-    uint4 lo = rows[t0][x], hi = lo;
-    for (int t = t0 + 1; t < t1; ++t) fold<T>(lo, hi, rows[t][x]);
-    const int64_t at = (ph * a.Hkv + h) * V16 + x;
+    uint4 lo = k[to[t0] + x], hi = lo;
+#pragma unroll 4
+    for (int t = t0 + 1; t < t1; ++t) fold<T>(lo, hi, k[to[t] + x]);
+    // the page's bounds, from the place of its row t0
+    const int64_t at = (to[t0] / V16 >> b.page_shift) * V16 + x;
     uint4* mn = static_cast<uint4*>(a.key_min[layer]) + at;
     uint4* mx = static_cast<uint4*>(a.key_max[layer]) + at;
     if (start < L) {
