@@ -15,6 +15,16 @@
 // fp16 250, at d = 64 177 and 180 us (the best of a few calls in a row; called for
 // seconds on end, at the power cap, the first two take 2.15 ms and 266 us).
 //
+// A draft tree has at most 64 nodes, so its rows are one tile of 256 (or a few), and
+// the call stands between HBM and the tensor cores: a step reads 64 KB at d = 128,
+// 1.47 us at an even share of the copy bandwidth, and takes 1.5 us of products.  A
+// node's ancestors are 64 bits a row, laid over the one or two key tiles that hold
+// the tree; all other tiles are as in a chunk.  A tile of at most 128 rows is one
+// group, which takes both S tiles in turn (0.9 us a step for 1.5).  64 nodes over
+// 100K rows, 32/8 heads: 91 us, 4.6 TB/s with plan, start and join; 12 trees of 25
+// nodes over 24K rows, 40/8 heads: 192 us (6.3 TB/s), of 51 nodes 234, of 64 (a tile
+// of 256 rows and one of 64, which read the keys twice) 363.
+//
 // Three launches.  The plan (one CTA) lists the work from the device-side
 // lengths in order of falling cost: the tiles of whole rounds over the SMs as
 // they are, the rest cut along the keys into pieces where it pays.  The
@@ -96,13 +106,18 @@ __device__ __forceinline__ int tile_steps(const SeqSpan& sp, int rows, int tile,
   return vis <= 0 ? 0 : (vis + kNk - 1) / kNk;
 }
 
+// A tile of one group (at most 128 rows) carries this bit beside its number.  Where
+// one group takes both S tiles (draft trees at d = 128) a step of it costs less
+// than one of two groups: 1720 cycles for 2870 with K and V in L2.
+constexpr int kSoloBit = 1 << 30, kSoloEighths = 5;
+
 // Pieces of a tile of `steps` key tiles when a piece takes at most `per`.
 __device__ __forceinline__ int pieces_of(int steps, int per) {
   return steps <= per ? 1 : (steps + per - 1) / per;
 }
 
 __global__ void __launch_bounds__(kPlanThreads)
-paged_plan_kernel(const PagedBatch b, int Hkv, int G, int D, int max_q, int max_tiles,
+paged_plan_kernel(const PagedBatch b, int Hkv, int G, int D, int max_q, int solo, int max_tiles,
                   int max_entries, int max_slots, Header* hdr, int4* tiles, int4* entries, int* slots, int4* cuts,
                   int32_t* status) {
   // the tiles as found and in order: in shared memory where they fit (every
@@ -128,6 +143,8 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int D, int max_q, int max_
     s_total = s_keys = 0;
   }
   for (int i = tid; i < 256; i += kPlanThreads) hist[i] = 0;
+  // a tile (sequence, number and bit, steps): what it costs, in steps of two groups
+  auto price = [&](const int4& t) { return t.y & kSoloBit ? (t.z * solo + 7) >> 3 : t.z; };
   int n_tiles = 0;
   for (int base = 0; base < b.n_seq; base += kPlanThreads) {
     const int s = base + tid;
@@ -167,9 +184,10 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int D, int max_q, int max_
       }
       const int sq = base + lo, t = i - first[lo];
       const int steps = tile_steps(seq_span(b, sq), seq_rows[lo], t, G);
-      if (n_tiles + i < max_tiles) tiles[n_tiles + i] = make_int4(sq, t, steps, 0);
-      mine += steps;
-      top = max(top, steps);
+      const int4 tile = make_int4(sq, seq_rows[lo] - t * kM <= 128 ? t | kSoloBit : t, steps, 0);
+      if (n_tiles + i < max_tiles) tiles[n_tiles + i] = tile;
+      mine += price(tile);
+      top = max(top, price(tile));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
@@ -212,7 +230,7 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int D, int max_q, int max_
   // tiles by falling cost (256 classes)
   const float class_of = 255.f / longest;
   auto bucket = [&](int steps) { return 255 - min(255, (int)(steps * class_of)); };
-  for (int i = tid; i < n_tiles; i += kPlanThreads) atomicAdd(&hist[bucket(tiles[i].z)], 1);
+  for (int i = tid; i < n_tiles; i += kPlanThreads) atomicAdd(&hist[bucket(price(tiles[i]))], 1);
   __syncthreads();
   if (warp == 0) starts();
   __syncthreads();
@@ -223,13 +241,13 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int D, int max_q, int max_
   if (!may_cut) {
     for (int i = tid; i < n_tiles; i += kPlanThreads) {
       const int4 t = tiles[i];
-      sorted[atomicAdd(&hist[bucket(t.z)], 1)] = t;
+      sorted[atomicAdd(&hist[bucket(price(t))], 1)] = t;
     }
   } else if (warp == 0) {
     for (int base = 0; base < n_tiles; base += 32) {
       const int i = base + lane;
       const int4 t = i < n_tiles ? tiles[i] : make_int4(0, 0, 0, 0);
-      const int c = i < n_tiles ? bucket(t.z) : 256;
+      const int c = i < n_tiles ? bucket(price(t)) : 256;
       const unsigned same = __match_any_sync(0xffffffffu, c);
       const int to = (c < 256 ? hist[c] : 0) + __popc(same & ((1u << lane) - 1u));
       __syncwarp();
@@ -269,7 +287,7 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int D, int max_q, int max_
         const int parts = kParts[kind == 0 ? warp : (warp & 7) + 1];
         // no tile of the rest is longer than its first's class (a step more for
         // the class's rounding)
-        const int top = min(longest, sorted[w].z + longest / 255 + 2);
+        const int top = min(longest, price(sorted[w]) + longest / 255 + 2);
         p = (top + parts - 1) / parts;
       }
     }
@@ -279,7 +297,7 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int D, int max_q, int max_
     int n_pieces = 0, n_cut = 0;
     float low = longest, high = 0.f;
     for (int i = w + lane; i < n_tiles; i += 32) {
-      const int steps = sorted[i].z;
+      const int steps = price(sorted[i]);
       int np = (int)(steps * inv);
       np += np * p < steps;
       np -= (np - 1) * p >= steps;
@@ -299,16 +317,16 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int D, int max_q, int max_
     // longest chain of whole tiles: k + 1 of them where the order's item
     // k C is the k-th to follow
     float chain = 0.f;
-    if (lane * C < w * Hkv) chain = (lane + 1) * (sorted[lane * C / Hkv].z + kFixed);
+    if (lane * C < w * Hkv) chain = (lane + 1) * (price(sorted[lane * C / Hkv]) + kFixed);
     chain = warp_max(chain);
     const float pieces = (float)((n_pieces * Hkv + C - 1) / C) * (widest + cost);
     float e = fmaxf(even, chain) + (n_cut ? kCut : 0.f);
     if (w < n_tiles) {
-      const bool equal = w == 0 || sorted[w - 1].z * 10 >= sorted[0].z * 9;
+      const bool equal = w == 0 || price(sorted[w - 1]) * 10 >= price(sorted[0]) * 9;
       if (!equal || shortest * 10.f < widest * 9.f)
         e = fmaxf(e, even + 0.5f * widest);
       else
-        e = fmaxf(e, (w ? (float)((w * Hkv + C - 1) / C) * (sorted[0].z + kFixed) : 0.f) + pieces);
+        e = fmaxf(e, (w ? (float)((w * Hkv + C - 1) / C) * (price(sorted[0]) + kFixed) : 0.f) + pieces);
     }
     if (valid && (long long)n_cut * Hkv <= max_slots) {
       best = e;
@@ -340,9 +358,9 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int D, int max_q, int max_
     // has SMs.  The stretches stand at different keys, so K and V have to stay in
     // L2.  (2048 tokens over 32K rows, 2 KV heads: 257 us in pieces, 244 in
     // stretches; tiles of many lengths fill the SMs better by themselves: 9 mixed
-    // streams take 6 % longer in stretches.)
+    // streams take 6 % longer in stretches, 10 draft trees over 3K to 24K rows too.)
     const unsigned heads = C / Hkv;
-    if (heads > 0 && sorted[n_tiles - 1].z * 10 >= longest * 9 && s_keys * Hkv * D * 4 <= (64ull << 20) &&
+    if (heads > 0 && price(sorted[n_tiles - 1]) * 10 >= longest * 9 && s_keys * Hkv * D * 4 <= (64ull << 20) &&
         (long long)(n_tiles + heads) * Hkv <= max_slots) {
       // at most 16 C tiles of 2^18 steps: below 2^31
       const int even = (int)(((unsigned)s_total + heads - 1) / heads);
@@ -352,13 +370,13 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int D, int max_q, int max_
   if (stretch > 0) {
     // The list: the stretches' parts of tiles, the longest first (a CTA that ends
     // a short one early takes the longest left, so two together make a stretch).
-    // sorted[i].w: where tile i starts on the line.
+    // sorted[i].w: where tile i starts on the line, which is measured in cost.
     __syncthreads();
     if (tid < 256) hist[tid] = 0;
     if (tid == 0) s_slots = s_cut = 0;
     int before = 0;
     for (int base = 0; base < n_tiles; base += kPlanThreads) {
-      const int i = base + tid, z = i < n_tiles ? sorted[i].z : 0;
+      const int i = base + tid, z = i < n_tiles ? price(sorted[i]) : 0;
       int inc = z;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -376,20 +394,25 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int D, int max_q, int max_
     }
     const float part_class = 255.f / stretch;
     auto cls = [&](int len) { return 255 - min(255, (int)(len * part_class)); };
-    // part p of the tile at [at, at + z): from the p-th cut at or before it
-    auto part = [&](int at, int z, int p, int& k0, int& k1) {
-      const int cut = (at / stretch + p) * stretch;
-      k0 = max(cut, at) - at;
-      k1 = min(cut + stretch, at + z) - at;
+    // part p of tile t at [w, w + price): from the p-th cut at or before it, in steps;
+    // returns its cost
+    auto part = [&](const int4& t, int p, int& k0, int& k1) {
+      const int at = t.w, z = price(t), cut = (at / stretch + p) * stretch;
+      const int c0 = max(cut, at) - at, c1 = min(cut + stretch, at + z) - at;
+      const int eighths = t.y & kSoloBit ? solo : 8;
+      k0 = min(c0 * 8 / eighths, t.z);
+      k1 = c1 == z ? t.z : min(c1 * 8 / eighths, t.z);
+      return c1 - c0;
     };
-    auto parts = [&](int at, int z) { return z == 0 ? 1 : (at + z - 1) / stretch - at / stretch + 1; };
+    auto parts = [&](const int4& t) {
+      return t.z == 0 ? 1 : (t.w + price(t) - 1) / stretch - t.w / stretch + 1;
+    };
     for (int i = tid; i < n_tiles; i += kPlanThreads) {
       const int4 t = sorted[i];
-      const int np = parts(t.w, t.z);
+      const int np = parts(t);
       for (int p = 0; p < np; ++p) {
         int k0, k1;
-        part(t.w, t.z, p, k0, k1);
-        atomicAdd(&hist[cls(k1 - k0)], 1);
+        atomicAdd(&hist[cls(part(t, p, k0, k1))], 1);
       }
     }
     __syncthreads();
@@ -397,18 +420,17 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int D, int max_q, int max_
     __syncthreads();
     for (int i = tid; i < n_tiles; i += kPlanThreads) {
       const int4 t = sorted[i];
-      const int np = parts(t.w, t.z);
+      const int np = parts(t);
       int slot = -1;
       if (np > 1) {
         slot = atomicAdd(&s_slots, np);
-        cuts[atomicAdd(&s_cut, 1)] = make_int4(t.x, t.y, slot, np);
+        cuts[atomicAdd(&s_cut, 1)] = make_int4(t.x, t.y & ~kSoloBit, slot, np);
       }
       for (int p = 0; p < np; ++p) {
         int k0, k1;
-        part(t.w, t.z, p, k0, k1);
-        const int e = atomicAdd(&hist[cls(k1 - k0)], 1);
+        const int e = atomicAdd(&hist[cls(part(t, p, k0, k1))], 1);
         if (e >= max_entries) continue;
-        entries[e] = make_int4(t.x, t.y, k0, k1);
+        entries[e] = make_int4(t.x, t.y & ~kSoloBit, k0, k1);
         slots[e] = slot < 0 ? -1 : slot + p;
       }
     }
@@ -424,18 +446,18 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int D, int max_q, int max_
       const int4 t = sorted[i];
       if (i < whole) {
         if (i < max_entries) {
-          entries[i] = make_int4(t.x, t.y, 0, t.z);
+          entries[i] = make_int4(t.x, t.y & ~kSoloBit, 0, t.z);
           slots[i] = -1;
         }
         continue;
       }
-      const int np = pieces_of(t.z, per);
+      const int np = pieces_of(price(t), per);
       atomicAdd(&at[np - 1], 1);          // tiles of np pieces, for now
       atomicMax(&s_most, np);
       int slot = -1;
       if (np > 1) {
         slot = atomicAdd(&s_slots, np);
-        cuts[atomicAdd(&s_cut, 1)] = make_int4(t.x, t.y, slot, np);
+        cuts[atomicAdd(&s_cut, 1)] = make_int4(t.x, t.y & ~kSoloBit, slot, np);
       }
       sorted[i].w = slot;
     }
@@ -480,11 +502,11 @@ paged_plan_kernel(const PagedBatch b, int Hkv, int G, int D, int max_q, int max_
     for (int u = tid; u < (n_tiles - whole) * most; u += kPlanThreads) {
       const int i = whole + u / most, p = u % most;
       const int4 t = sorted[i];
-      const int np = pieces_of(t.z, per);
+      const int np = pieces_of(price(t), per);
       if (p >= np) continue;
       const int len = (t.z + np - 1) / np, e = atomicAdd(&at[p], 1);
       if (e >= max_entries) continue;
-      entries[e] = make_int4(t.x, t.y, min(p * len, t.z), min((p + 1) * len, t.z));
+      entries[e] = make_int4(t.x, t.y & ~kSoloBit, min(p * len, t.z), min((p + 1) * len, t.z));
       slots[e] = t.w < 0 ? -1 : t.w + p;
     }
   }
@@ -519,6 +541,7 @@ struct Aux {
   // a group's tiles take these in turn: a tile's turn comes again only when
   // every waiter has seen its last
   uint64_t s_full[2][kRing], p_ready[2][kRing], o_done[2][kRing];
+  uint64_t solo_done[kRing];                      // P V of the tiles of one-group items
   uint64_t q_full, q_empty, drain[2];
   uint64_t next_full[kNext], next_empty[kNext];   // items handed to the other warps
   uint32_t tmem_base;
@@ -664,6 +687,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
         ptx::mbar_init(&aux->o_done[g][i], 1);
       }
     }
+    for (int i = 0; i < kRing; ++i) ptx::mbar_init(&aux->solo_done[i], 1);
     ptx::mbar_init(&aux->drain[0], 1);
     ptx::mbar_init(&aux->drain[1], 1);
     for (int i = 0; i < kNext; ++i) {
@@ -824,6 +848,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       uint32_t base0 = 0, base1 = 0;      // tiles of each group before this item
       uint32_t outs_g[2] = {0, 0};        // items ended
       uint32_t ops = 0, at = 0, uses = 0; // ops so far; S tile of the next; who used each last
+      uint32_t solo = 0;                  // tiles of one-group items so far
       bool ok = true;
       auto commit = [&](uint32_t off) { ptx::mma_commit_if(lead, bars + off); };
       auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -844,18 +869,62 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
           // S tile g is group g's: its next scores go behind its P V, in the order
           // of one warp's products.  (S tiles in turn took 5 % longer on 2048
           // tokens over 100K rows, in turn and two warps, as below, 11 %.)
-          auto scores = [&](int g, uint32_t t) {
+          auto scores_to = [&](int g, uint32_t t, uint32_t to) {
             const uint64_t a0 = qd0 + (uint64_t)(g * kTile16);
             const uint64_t b0 = kd0 + (uint64_t)((t % kSK) * kTile16);
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
               const uint32_t off = (ks >> 2) * (Ly::kPanel >> 4) + (ks & 3) * 2;
-              ptx::mma_ss_if(lead, tm + Ly::sbase(g), a0 + off, b0 + off, idesc_qk, ks > 0 ? 1u : 0u);
+              ptx::mma_ss_if(lead, to, a0 + off, b0 + off, idesc_qk, ks > 0 ? 1u : 0u);
             }
             commit(offsetof(Aux, s_full) + (g * kRing + ((g ? base1 : base0) + (t - it)) % kRing) * 8);
           };
+          auto scores = [&](int g, uint32_t t) { scores_to(g, t, tm + Ly::sbase(g)); };
           ok = ok && wait(&aux->k_full[it % kSK], it / kSK);
           if (!ok) break;
+          if (kTree && n1 == 0) {
+            // One group alone takes both S tiles in turn: its next scores are formed
+            // while it works on these.  (P V of the tile before is then not implied by
+            // a tile's scores: solo_done tells it.)
+            scores(0, it);
+            if (n > 1) {
+              ok = wait(&aux->k_full[(it + 1) % kSK], (it + 1) / kSK);
+              if (!ok) break;
+              scores_to(0, it + 1, tm + Ly::sbase(1));
+            }
+            if (n <= 2) commit(offsetof(Aux, q_empty));
+            for (int k = 0; k < n; ++k, ++solo) {
+              const uint32_t t = it + k, stV = t % kSV, turn = base0 + k;
+              const uint32_t s0 = tm + 2 * D + (k & 1) * kNk;
+              ok = wait(&aux->v_full[stV], t / kSV);
+              if (ok && tail && k + 1 == n) {
+                ok = wait(&aux->v_clear[stV], clear_par >> stV);
+                clear_par ^= 1u << stV;
+              }
+              ok = ok && wait(&aux->p_ready[0][turn % kRing], turn / kRing);
+              if (!ok) break;
+              const uint64_t b0 = vd0 + (uint64_t)(stV * kTile16);
+              const uint32_t acc = k > 0 ? 1u : 0u;
+#pragma unroll
+              for (int ks = 0; ks < kNk / 16; ++ks)
+                ptx::mma_ts_if(lead, tm + Ly::obase(0), s0 + 8 * ks, b0 + (uint64_t)(ks * 128),
+                               idesc_pv, ks > 0 ? 1u : acc);
+              commit(offsetof(Aux, solo_done) + (solo % kRing) * 8);
+              commit(offsetof(Aux, v_empty) + stV * 8);
+              if (k + 1 == n) commit(offsetof(Aux, o_done) + (outs_g[0]++ % kRing) * 8);
+              if (k + 2 < n) {
+                ok = wait(&aux->k_full[(t + 2) % kSK], (t + 2) / kSK);
+                if (!ok) break;
+                scores_to(0, t + 2, s0);
+                if (k + 3 == n) commit(offsetof(Aux, q_empty));
+              }
+            }
+            if (!ok) break;
+            it += n;
+            base0 += n0;
+            ++items;
+            continue;
+          }
           if (n0 > 0) scores(0, it);
           if (n1 > 0) scores(1, it);
           if (n == 1) commit(offsetof(Aux, q_empty));
@@ -1038,7 +1107,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
     const uint32_t o_addr = tmem + lane_off + Ly::obase(g);
     const float sl2 = kLog2e / sqrtf((float)D);
     const uint64_t sl2x2 = ptx::f2(sl2, sl2);
-    uint32_t tiles = 0, outs = 0, count = 0, ops = 0;
+    uint32_t tiles = 0, outs = 0, count = 0, ops = 0, solos = 0;
     bool ok = true;
     while (ok) {
       Item w;
@@ -1057,8 +1126,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
         nodes = tree.of((valid ? R : w.rows - 1) / G);
       }
       const int n_mine = g == 0 ? w.n_g[0] : w.n_g[1];
+      const bool solo = kTree && kScores == 2 && w.n_g[1] == 0;   // one group, both S tiles
       float m_used = -INFINITY, l = 0.f;
-      for (int k = 0; k < n_mine; ++k, ++tiles) {
+      for (int k = 0; k < n_mine; ++k, ++tiles, solos += solo) {
         bool got = !aux->abort_flag && ptx::mbar_wait(&aux->s_full[g][tiles % kRing], (tiles / kRing) & 1u, wait_limit);
         if (!__all_sync(0xffffffffu, got)) {
           ok = false;
@@ -1070,7 +1140,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
           continue;
         }
         // this tile's place among the item's products
-        const uint32_t op = kScores == 2 ? g
+        const uint32_t op = kScores == 2 ? (solo ? k & 1 : g)
                                          : ops + min(k, w.n_g[0]) + min(k, w.n_g[1]) +
                                                (g == 1 && k < w.n_g[0] ? 1 : 0);
         const uint32_t s_addr = tmem + lane_off + Ly::sbase(op % kScores);
@@ -1199,6 +1269,14 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
           if constexpr (kScores > 2) {
             const uint32_t last = tiles - 1;
             bool done = ptx::mbar_wait(&aux->o_done[g][last % kRing], (last / kRing) & 1u, wait_limit);
+            if (!__all_sync(0xffffffffu, done)) {
+              ok = false;
+              break;
+            }
+            ptx::tc_fence_after();
+          } else if (solo) {
+            const uint32_t last = solos - 1;
+            bool done = ptx::mbar_wait(&aux->solo_done[last % kRing], (last / kRing) & 1u, wait_limit);
             if (!__all_sync(0xffffffffu, done)) {
               ok = false;
               break;
@@ -1448,7 +1526,8 @@ int go_tc(const PagedBatch& b, const TcArgs& a, const TcPlan& p, char* ws, int32
   cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                        kPlanTiles * 2 * sizeof(int4));
   pdl_config(&cfg, attr, dim3(1), dim3(kPlanThreads), near, st);
-  cudaLaunchKernelEx(&cfg, paged_plan_kernel, b, a.Hkv, a.Hq / a.Hkv, D, a.max_q, p.max_tiles,
+  cudaLaunchKernelEx(&cfg, paged_plan_kernel, b, a.Hkv, a.Hq / a.Hkv, D, a.max_q,
+                     a.parents && D == 128 ? kSoloEighths : 8, p.max_tiles,
                      p.max_entries, p.max_slots, hdr, tiles, entries, slots, cuts, status);
   rc = launch_status("paged_plan_kernel");
   if (rc) return rc;

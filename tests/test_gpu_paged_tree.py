@@ -123,7 +123,9 @@ def test_chain_is_a_causal_chunk(ts, Hq, kv):
     b = pu.Batch([64, 20], [kv, kv], Hq, 2, 128, 32, BF, seed=6)
     o, lse = attend(ts, b, parents_of(b.q_lens, "chain"))
     o2, lse2 = ts.ts_paged_attention(b.q, b.k, b.v, b.cu_q, b.lens, b.table, 64)
-    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    ref = oracle(b, parents_of(b.q_lens, "chain"))     # (the two may cut the keys elsewhere)
+    pu.check_attention(o, lse, ref, BF, 128, p_round=P_ROUND[BF])
+    pu.check_attention(o2, lse2, ref, BF, 128, p_round=P_ROUND[BF])
 
 
 @pytest.mark.parametrize("Hq", [4, 64])
