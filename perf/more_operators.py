@@ -286,7 +286,7 @@ def _run_own(st):
     if c["op"] == "tree":
         return ts.ts_paged_tree_attention(st["q"], st["k_pages"], st["v_pages"], st["cu_q"],
                                           st["seq_lens"], st["table"], st["parents"],
-                                          max_q=c["q"])
+                                          max_q=max(st["ql"]))
     if c["op"] == "commit":
         more = {}
         if st["bounds"]:
