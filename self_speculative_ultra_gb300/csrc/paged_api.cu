@@ -77,6 +77,17 @@ bool few_rows(int n_seq, int max_q, int Hq, int Hkv, int64_t kv) {
   return blocks <= 1 || trips <= 8 * kGb300Sms || (blocks <= 4 && trips <= 13 * kGb300Sms);
 }
 
+size_t dense_ws_bytes(int n, int n_seq, int Hq, int Hkv, int d, int max_pages, int page_size,
+                      int max_q, int64_t max_kv, bool tree) {
+  if (n < 1 || n_seq < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || max_pages < 1 || page_size < 1 ||
+      max_q < 1)
+    return 0;
+  const int64_t kv = bound_kv(max_pages, page_size, max_kv);
+  if (few_rows(n_seq, max_q, Hq, Hkv, kv))
+    return rows_plan((int64_t)n_seq * Hkv, max_q * (Hq / Hkv), d, kv).ws_bytes;
+  return tc_plan(n, n_seq, Hq, Hkv, d, max_q, kv, tree).ws_bytes;
+}
+
 // The dense call and its form for draft trees (parents not NULL).
 int dense_attention(const char* W, const void* q, const void* k_pages, const void* v_pages, int n,
                     int Hq, int Hkv, int d, const int32_t* cu_q, const int32_t* seq_lens,
@@ -96,7 +107,7 @@ int dense_attention(const char* W, const void* q, const void* k_pages, const voi
     if (!aligned16(p)) return fail(TS_ERR_INVALID_ARG, "%s: a tensor is not 16-byte aligned", W);
   const int64_t kv = bound_kv(max_pages, page_size, max_kv);
   if (!few_rows(n_seq, max_q, Hq, Hkv, kv)) {
-    const TcPlan p = tc_plan(n, n_seq, Hq, Hkv, d, max_q, kv);
+    const TcPlan p = tc_plan(n, n_seq, Hq, Hkv, d, max_q, kv, parents != nullptr);
     rc = check_paged_ws(workspace, workspace_bytes, p.ws_bytes, W);
     if (rc) return rc;
     const TcArgs a{q, k_pages, v_pages, Hq, Hkv, max_q, o, lse, parents};
@@ -232,13 +243,7 @@ int ts_paged_rope_append(const void* q, const void* k, const void* v, int64_t q_
 
 size_t ts_paged_attention_workspace_bytes(int n, int n_seq, int Hq, int Hkv, int d, int max_pages,
                                           int page_size, int max_q, int64_t max_kv) {
-  if (n < 1 || n_seq < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || max_pages < 1 || page_size < 1 ||
-      max_q < 1)
-    return 0;
-  const int64_t kv = bound_kv(max_pages, page_size, max_kv);
-  if (few_rows(n_seq, max_q, Hq, Hkv, kv))
-    return rows_plan((int64_t)n_seq * Hkv, max_q * (Hq / Hkv), d, kv).ws_bytes;
-  return tc_plan(n, n_seq, Hq, Hkv, d, max_q, kv).ws_bytes;
+  return dense_ws_bytes(n, n_seq, Hq, Hkv, d, max_pages, page_size, max_q, max_kv, false);
 }
 
 int ts_paged_attention(const void* q, const void* k_pages, const void* v_pages, int n, int Hq,
@@ -256,8 +261,7 @@ size_t ts_paged_tree_attention_workspace_bytes(int n, int n_seq, int Hq, int Hkv
                                                int max_pages, int page_size, int max_q,
                                                int64_t max_kv) {
   if (max_q > kTreeNodes) return 0;
-  return ts_paged_attention_workspace_bytes(n, n_seq, Hq, Hkv, d, max_pages, page_size, max_q,
-                                            max_kv);
+  return dense_ws_bytes(n, n_seq, Hq, Hkv, d, max_pages, page_size, max_q, max_kv, true);
 }
 
 int ts_paged_tree_attention(const void* q, const void* k_pages, const void* v_pages, int n, int Hq,

@@ -570,6 +570,186 @@ struct Work {
   Header* hdr;
   const int4* entries;
   const int* slots;
+  int4* line_cuts;      // trees of one tile (see Line), else NULL
+  bool by_tile;         // line_cuts by tile, else by the CTA that starts one
+};
+
+// -------------------------------------------------------------------- a line of trees
+// Where every tree is one tile, nothing is gained from a list: a tile's keys are
+// read by nobody else, so pieces need no order in time.  The tiles (sequence, KV
+// head) stand on a line, each as long as it costs, and CTA c takes the c-th of C
+// equal stretches of it, which it finds from the lengths by itself; a tile that
+// cuts fall into is joined as in the plan's list.  That saves the plan's launch.
+constexpr int kLineFixed = 3;   // what a tile costs beside its steps, in steps
+constexpr int kLineLeast = 8;   // a stretch is at least as long
+
+struct Line {
+  long long total, w0, w1;      // the line, and this CTA's stretch
+  int C;
+  int s;                        // the sequence that holds w0, and where it starts
+  long long at;
+};
+
+// The tile of a tree's rows: its steps, and its length without kLineFixed, in
+// eighths of a step each.
+struct TreeTile {
+  int rows, steps, eighths;
+  __device__ __forceinline__ int price() const { return (steps * eighths + 7) >> 3; }
+  __device__ __forceinline__ int length() const { return rows > 0 ? price() + kLineFixed : 0; }
+  // steps in front of the tile's place c
+  __device__ __forceinline__ int steps_at(int c) const {
+    return c >= length() ? steps : c <= kLineFixed ? 0 : min((c - kLineFixed) * 8 / eighths, steps);
+  }
+};
+template <int D>
+__device__ __forceinline__ TreeTile tree_tile(const SeqSpan& sp, int max_q, int G) {
+  TreeTile t;
+  t.rows = min(sp.ql, max_q) * G;
+  t.steps = t.rows > 0 ? tile_steps(sp, t.rows, 0, G) : 0;
+  t.eighths = D == 128 && t.rows <= 128 ? kSoloEighths : 8;
+  return t;
+}
+
+template <int D>
+__device__ __forceinline__ Line find_line(const PagedBatch& b, int Hkv, int G, int max_q,
+                                          int32_t* status) {
+  __shared__ long long sums[kThreads / 32];
+  __shared__ long long s_at;
+  __shared__ int s_seq;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
+  auto length = [&](int s, bool report) -> long long {
+    if (s >= b.n_seq) return 0;
+    const SeqSpan sp = seq_span(b, s);
+    if (report && (sp.bad || sp.ql > max_q)) set_status(status, TS_ERR_INVALID_ARG);
+    return (long long)Hkv * tree_tile<D>(sp, max_q, G).length();
+  };
+  const long long first = length(tid, c == 0);
+  long long mine = first;
+  for (int s = tid + kThreads; s < b.n_seq; s += kThreads) mine += length(s, c == 0);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) sums[warp] = mine;
+  if (tid == 0) {
+    s_seq = 0;
+    s_at = 0;
+  }
+  __syncthreads();
+  Line r;
+  r.total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) r.total += sums[w];
+  r.C = (int)imax64(1, imin64(r.total / kLineLeast, gridDim.x));
+  r.w0 = c < r.C ? r.total * c / r.C : r.total;
+  r.w1 = c < r.C ? r.total * (c + 1) / r.C : r.total;
+  long long before = 0;
+  for (int base = 0; base < b.n_seq && before <= r.w0; base += kThreads) {
+    const long long x = base == 0 ? first : length(base + tid, false);
+    long long inc = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    __syncthreads();
+    if (lane == 31) sums[warp] = inc;
+    __syncthreads();
+    long long at = before + inc - x;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) at += sums[w];
+      before += sums[w];
+    }
+    if (x > 0 && r.w0 >= at && r.w0 < at + x) {
+      s_seq = base + tid;
+      s_at = at;
+    }
+  }
+  __syncthreads();
+  r.s = s_seq;
+  r.at = s_at;
+  return r;
+}
+
+// The stretch's items in turn: part of a tile each.
+template <int D>
+struct LineWalk {
+  int s, kv;                    // the tile ahead
+  long long at;                 // where it starts
+  SeqSpan sp;
+  __device__ __forceinline__ void begin(const PagedBatch& b, const Line& l, int Hkv, int G,
+                                        int max_q) {
+    s = l.s;
+    kv = 0;
+    at = l.at;
+    if (l.w0 >= l.w1) return;
+    sp = seq_span(b, s);
+    const int length = tree_tile<D>(sp, max_q, G).length();
+    kv = (int)((l.w0 - at) / length);          // w0 lies in this sequence: length > 0
+    at += (long long)kv * length;
+  }
+  // n < 0: the stretch is at its end
+  __device__ __forceinline__ Item next(const PagedBatch& b, const Line& l, const Work& work,
+                                       int Hkv, int G, int max_q, int lane) {
+    Item w;
+    w.n = -1;
+    while (at < l.w1) {
+      const TreeTile t = tree_tile<D>(sp, max_q, G);
+      const int length = t.length(), head = kv, seq = s;
+      const SeqSpan own = sp;
+      const long long from = at;
+      at += length;
+      if (++kv == Hkv) {
+        kv = 0;
+        // (a sequence without tokens has no length; behind one that ends before w1
+        // there is another)
+        while (at < l.w1) {
+          sp = seq_span(b, ++s);
+          if (sp.ql > 0) break;
+        }
+      }
+      const int c0 = (int)imax64(l.w0 - from, 0), c1 = (int)imin64(l.w1 - from, length);
+      const int k0 = t.steps_at(c0), k1 = t.steps_at(c1);
+      const bool starts = t.steps > 0 ? k0 == 0 : c0 == 0, ends = k1 == t.steps;
+      if (k0 == k1 && (t.steps > 0 || !starts)) continue;      // between two tiles' steps
+      w.kv = head;
+      w.s = seq;
+      w.q0 = own.q0;
+      w.r0 = 0;
+      w.rows = t.rows;
+      w.see0 = own.kl - own.ql;
+      w.kl = own.kl;
+      w.k0 = k0;
+      w.n = k1 - k0;
+      w.slot = starts && ends ? -1 : 2 * blockIdx.x + (starts ? 1 : 0);
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int a = g * 128;
+        int steps = 0;
+        if (a < t.rows) {
+          const int vis = w.see0 + (min(a + 128, t.rows) - 1) / G + 1;
+          steps = vis <= 0 ? 0 : (vis + kNk - 1) / kNk;
+        }
+        w.n_g[g] = max(0, min(steps, k1) - k0);
+      }
+      if (starts && lane == 0) {
+        // the CTA with the tile's last step: the last whose stretch starts at or
+        // before the tile's last place
+        int parts = 0;
+        if (!ends) {
+          const long long z = from + length - 1;
+          int q = (int)(z * l.C / l.total);
+          while (q + 1 < l.C && l.total * (q + 1) / l.C <= z) ++q;
+          while (l.total * q / l.C > z) --q;
+          parts = q - (int)blockIdx.x + 1;
+        }
+        if (work.by_tile || parts > 0)
+          work.line_cuts[work.by_tile ? seq * Hkv + head : (int)blockIdx.x] =
+              make_int4(seq, head, (int)blockIdx.x, parts);
+      }
+      break;
+    }
+    return w;
+  }
 };
 
 __device__ __forceinline__ Item load_item(const PagedBatch& b, const Work& w, int i, int Hkv, int G,
@@ -708,7 +888,16 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
   const uint32_t tmem = aux->tmem_base;
   griddep_wait();
   griddep_launch_dependents();
-  const int n_items = __ldcg(&work.hdr->n_entries) * Hkv;
+  const bool on_line = kTree && work.line_cuts != nullptr;
+  Line line{};
+  if constexpr (kTree) {
+    if (on_line) {
+      line = find_line<D>(b, Hkv, G, max_q, status);
+      if (!work.by_tile && tid == 0) work.line_cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
+      __syncthreads();
+    }
+  }
+  const int n_items = on_line ? 0 : __ldcg(&work.hdr->n_entries) * Hkv;
   const int ps = 1 << b.page_shift;
 
   if (warp < 8) {
@@ -747,6 +936,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
         return ph;
       };
       int taken = blockIdx.x;             // warp 0: the next item; the first is the CTA's own
+      LineWalk<D> walk;
+      if constexpr (kTree) {
+        if (on_line && is_k) walk.begin(b, line, Hkv, G, max_q);
+      }
       for (uint32_t count = 0; ok;) {
         Item w;
         if (is_k) {
@@ -758,6 +951,9 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
           if (!ok) break;
           w.n = -1;
           if (i < n_items) w = load_item(b, work, i, Hkv, G, max_q);
+          if constexpr (kTree) {
+            if (on_line) w = walk.next(b, line, work, Hkv, G, max_q, lane);
+          }
           if (lane == 0) {
             aux->next[at] = w;
             ptx::mbar_arrive(&aux->next_full[at]);
@@ -768,10 +964,10 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
         }
         if (!ok || w.n < 0) break;
         int64_t next = ids(w, 0);
-        if (w.n == 0 && lane == 0 && is_k) taken = gridDim.x + atomicAdd(&work.hdr->taken, 1);
+        if (w.n == 0 && lane == 0 && is_k && !on_line) taken = gridDim.x + atomicAdd(&work.hdr->taken, 1);
         for (int k = 0; ok && k < w.n; ++k, ++it) {
           // the next item is taken as late as its latency allows
-          if (is_k && k == max(0, w.n - 2) && lane == 0)
+          if (is_k && k == max(0, w.n - 2) && lane == 0 && !on_line)
             taken = gridDim.x + atomicAdd(&work.hdr->taken, 1);
           const int64_t ph = next;
           next = ids(w, k + 1);
@@ -1315,7 +1511,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       if (!warp_rows) continue;
       const int64_t row = (int64_t)(w.q0 + R / G) * Hq + w.kv * G + R % G;
       const bool cut = w.slot >= 0;
-      const int64_t piece = (int64_t)w.slot * Hkv + w.kv;
+      const int64_t piece = on_line ? w.slot : (int64_t)w.slot * Hkv + w.kv;
       const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
@@ -1364,14 +1560,16 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
 }
 
 // -------------------------------------------------------------------- join
+// (kLine: n_line cut tiles of trees, by tile or by the CTA that starts one, whose
+// parts lie with the CTAs behind it.)
 // The rows of cut tiles, 32 neighbouring rows at a time, a row a lane and
 // kPart columns a thread: a piece's O lies by column quads, rows inside, so a
 // warp's loads are contiguous.  A CTA's warps take the D / kPart column parts of
 // the rows, or where there are CTAs enough, the pieces of one part among them.
-template <typename T, int D>
+template <typename T, int D, bool kLine>
 __global__ void __launch_bounds__(256, 2)
 paged_tc_merge(const PagedBatch b, const Header* __restrict__ hdr, const int4* __restrict__ cuts,
-               int Hq, int Hkv, int max_q, const float* __restrict__ part_o,
+               int n_line, bool by_tile, int Hq, int Hkv, int max_q, const float* __restrict__ part_o,
                const float2* __restrict__ part_ml, T* __restrict__ o, float* __restrict__ lse) {
   constexpr int kWarps = 8, kPart = 16, kQuads = kPart / 4, kParts = D / kPart;
   __shared__ float4 s_o[kWarps][kQuads][32];
@@ -1380,17 +1578,28 @@ paged_tc_merge(const PagedBatch b, const Header* __restrict__ hdr, const int4* _
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = Hq / Hkv;
   // units: (cut tile, KV head, 32 rows, part)
-  const int64_t total = (int64_t)__ldcg(&hdr->n_cut) * Hkv * (kM / 32) * kParts;
+  const int64_t total = (kLine ? n_line : (int64_t)__ldcg(&hdr->n_cut) * Hkv) * (kM / 32) * kParts;
   const bool shared = total <= gridDim.x;
   const int64_t first = shared ? blockIdx.x : (int64_t)blockIdx.x * kWarps + warp;
   const int64_t hop = shared ? gridDim.x : (int64_t)gridDim.x * kWarps;
   for (int64_t u = first; u < total; u += hop) {
     const int part = (int)(u % kParts), r = (int)(u / kParts % (kM / 32)) * 32 + lane;
-    const int kv = (int)(u / kParts / (kM / 32) % Hkv);
-    const int4 c = __ldcg(&cuts[u / kParts / (kM / 32) / Hkv]);   // sequence, tile, slot, pieces
-    const SeqSpan sp = seq_span(b, c.x);
+    const int64_t at = u / kParts / (kM / 32);
+    int kv = (int)(at % Hkv);
+    int4 c = __ldcg(&cuts[kLine ? at : at / Hkv]);       // sequence, tile, slot, pieces
+    SeqSpan sp;
+    if constexpr (kLine) {
+      // sequence, KV head, CTA, pieces; a sequence without tokens wrote none
+      if (by_tile) c.x = (int)(at / Hkv);
+      else kv = c.y;
+      sp = seq_span(b, c.x);
+      if (sp.ql == 0) c.w = 0;
+      c.y = 0;
+    } else {
+      sp = seq_span(b, c.x);
+    }
     const int R = c.y * kM + r;
-    const bool live = R < min(sp.ql, max_q) * G;
+    const bool live = c.w > 0 && R < min(sp.ql, max_q) * G;
     if (!__any_sync(0xffffffffu, live)) continue;        // the same for the CTA's warps, if shared
     const int i0 = shared ? warp : 0, di = shared ? kWarps : 1;
     float4 acc[kQuads];
@@ -1421,7 +1630,8 @@ paged_tc_merge(const PagedBatch b, const Header* __restrict__ hdr, const int4* _
       for (int j = 0; j < kAtOnce; ++j) {
         const int i = ib + j * di;
         if (i < c.w) {
-          const int64_t piece = (int64_t)(c.z + i) * Hkv + kv;
+          const int64_t piece = kLine ? (i == 0 ? 2 * (int64_t)c.z + 1 : 2 * (int64_t)(c.z + i))
+                                      : (int64_t)(c.z + i) * Hkv + kv;
           ml[j] = __ldcg(&part_ml[piece * kM + r]);
           const float4* p = reinterpret_cast<const float4*>(part_o) + piece * (kM * D / 4) +
                             (int64_t)(part * kQuads) * kM + r;
@@ -1522,31 +1732,34 @@ int go_tc(const PagedBatch& b, const TcArgs& a, const TcPlan& p, char* ws, int32
   float2* part_ml = reinterpret_cast<float2*>(ws + p.ml_at);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  const size_t near = p.max_tiles <= kPlanTiles ? (size_t)p.max_tiles * 2 * sizeof(int4) : 0;
-  cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                       kPlanTiles * 2 * sizeof(int4));
-  pdl_config(&cfg, attr, dim3(1), dim3(kPlanThreads), near, st);
-  cudaLaunchKernelEx(&cfg, paged_plan_kernel, b, a.Hkv, a.Hq / a.Hkv, D, a.max_q,
-                     a.parents && D == 128 ? kSoloEighths : 8, p.max_tiles,
-                     p.max_entries, p.max_slots, hdr, tiles, entries, slots, cuts, status);
-  rc = launch_status("paged_plan_kernel");
-  if (rc) return rc;
-  const Work work{hdr, entries, slots};
+  const Work work{hdr, entries, slots, p.line ? cuts : nullptr, p.line && p.line_cuts < p.grid};
+  if (!p.line) {
+    const size_t near = p.max_tiles <= kPlanTiles ? (size_t)p.max_tiles * 2 * sizeof(int4) : 0;
+    cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                         kPlanTiles * 2 * sizeof(int4));
+    pdl_config(&cfg, attr, dim3(1), dim3(kPlanThreads), near, st);
+    cudaLaunchKernelEx(&cfg, paged_plan_kernel, b, a.Hkv, a.Hq / a.Hkv, D, a.max_q,
+                       a.parents && D == 128 ? kSoloEighths : 8, p.max_tiles,
+                       p.max_entries, p.max_slots, hdr, tiles, entries, slots, cuts, status);
+    rc = launch_status("paged_plan_kernel");
+    if (rc) return rc;
+  }
   pdl_config(&cfg, attr, dim3(p.grid), dim3(kThreads), Layout<D>::kBytes, st);
   cudaLaunchKernelEx(&cfg, kern, mk, mv, b, static_cast<const T*>(a.q), a.Hq, a.Hkv, a.max_q,
                      a.parents, work, static_cast<T*>(a.o), a.lse, part_o, part_ml, wait_limit_cycles(), status);
   rc = launch_status("paged_tc_kernel");
   if (rc || p.max_slots == 0) return rc;
   pdl_config(&cfg, attr, dim3(p.merge_grid), dim3(256), 0, st);
-  cudaLaunchKernelEx(&cfg, paged_tc_merge<T, D>, b, (const Header*)hdr, (const int4*)cuts, a.Hq,
-                     a.Hkv, a.max_q, (const float*)part_o, (const float2*)part_ml,
-                     static_cast<T*>(a.o), a.lse);
+  cudaLaunchKernelEx(&cfg, p.line ? paged_tc_merge<T, D, true> : paged_tc_merge<T, D, false>, b,
+                     (const Header*)hdr, (const int4*)cuts, p.line_cuts, work.by_tile, a.Hq, a.Hkv,
+                     a.max_q, (const float*)part_o, (const float2*)part_ml, static_cast<T*>(a.o),
+                     a.lse);
   return launch_status("paged_tc_merge");
 }
 
 }  // namespace
 
-TcPlan tc_plan(int n, int n_seq, int Hq, int Hkv, int d, int max_q, int64_t max_kv) {
+TcPlan tc_plan(int n, int n_seq, int Hq, int Hkv, int d, int max_q, int64_t max_kv, bool tree) {
   TcPlan p{};
   const int64_t G = Hq / Hkv;
   // tiles: a sequence's rows rounded up to whole tiles
@@ -1570,6 +1783,19 @@ TcPlan tc_plan(int n, int n_seq, int Hq, int Hkv, int d, int max_q, int64_t max_
     at += align_up(bytes, 256);
     return r;
   };
+  if (tree && max_q * G <= kM) {
+    p.line = true;
+    const int64_t units = (int64_t)n_seq * Hkv;
+    p.grid = (int)imax64(1, imin64(kGb300Sms, units * (steps + kLineFixed) / kLineLeast));
+    p.line_cuts = (int)imin64(units, p.grid);
+    p.max_slots = p.grid > 1 ? 2 * p.grid : 0;
+    p.merge_grid = (int)imin64(8 * kGb300Sms, (int64_t)p.line_cuts * (kM / 32) * (d / 16));
+    p.cuts_at = take((size_t)p.grid * sizeof(int4));
+    p.part_at = take((size_t)p.max_slots * kM * d * sizeof(float));
+    p.ml_at = take((size_t)p.max_slots * kM * sizeof(float2));
+    p.ws_bytes = at;
+    return p;
+  }
   p.tiles_at = take((size_t)tiles * 2 * sizeof(int4));
   p.entries_at = take((size_t)p.max_entries * sizeof(int4));
   p.slots_at = take((size_t)p.max_entries * sizeof(int));

@@ -12,9 +12,11 @@ struct TcPlan {
   int max_tiles, max_entries;
   int max_slots;               // partial tiles, KV heads included (0: nothing is cut)
   int grid, merge_grid;
+  bool line;                   // trees of one tile: no plan kernel, stretches of a line
+  int line_cuts;               // tiles that may be cut, as the join counts them
   size_t tiles_at, entries_at, slots_at, cuts_at, part_at, ml_at, ws_bytes;
 };
-TcPlan tc_plan(int n, int n_seq, int Hq, int Hkv, int d, int max_q, int64_t max_kv);
+TcPlan tc_plan(int n, int n_seq, int Hq, int Hkv, int d, int max_q, int64_t max_kv, bool tree);
 
 struct TcArgs {
   const void *q, *k_pages, *v_pages;

@@ -95,6 +95,44 @@ def test_tiles_of_rows(ts, dtype, d, kind):
     check(ts, b, parents_of(b.q_lens, kind, seed=2))
 
 
+def _streams(n, seed, top, kv):
+    """Nodes and lengths of n streams, some without nodes, some without a cache."""
+    rng = np.random.default_rng(seed)
+    q = [0 if x < 0.2 else int(rng.integers(1, top + 1)) for x in rng.random(n)]
+    q[n // 2] = top
+    k = [a if x < 0.1 else a + int(rng.integers(0, kv)) for a, x in zip(q, rng.random(n))]
+    return q, k
+
+
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,top,kv,Hq,Hkv", [
+    (1, 64, 60000, 8, 2),          # one tile a KV head, cut many times
+    (1, 64, 30000, 2, 1),          # of one group
+    (5, 64, 9000, 12, 3),
+    (100, 64, 1500, 4, 2),         # more tiles than SMs
+    (40, 32, 4000, 8, 4),
+    (700, 33, 300, 4, 1),          # more streams than threads
+    (90, 64, 700, 4, 4),
+])
+def test_lines_of_tiles(ts, dtype, d, n, top, kv, Hq, Hkv):
+    """Trees of one tile: stretches over many streams, cut tiles, streams without nodes."""
+    q, k = _streams(n, n + top, top, kv)
+    if n == 1:
+        k = [kv]
+    b = pu.Batch(q, k, Hq, Hkv, d, 32, dtype, seed=n, extra=2)
+    par = parents_of(q, "mixed", seed=n, extra=2)
+    o, lse = check(ts, b, par)
+    o2, lse2 = attend(ts, b, par)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    check(ts, b, par, max_kv=64)                   # the host's hint is far too short
+    need = ts.ts_paged_tree_attention_workspace_bytes(b.n, n, Hq, Hkv, d, b.table.shape[1], 32, top)
+    ws = torch.full((max(need, 1) + 256,), 255, dtype=torch.uint8, device="cuda")
+    ws = ws[(-ws.data_ptr()) % 256:][:max(need, 1)]
+    o2, lse2 = attend(ts, b, par, workspace=ws)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
 @pytest.mark.parametrize("kv", [64 + x for x in (0, 1, 31, 32, 33, 63, 64, 65, 96, 127, 128, 129)])
 def test_every_place_in_a_tile(ts, kv):
     for dtype, Hq in ((BF, 4), (FP, 64)):
@@ -102,7 +140,7 @@ def test_every_place_in_a_tile(ts, kv):
         check(ts, b, parents_of(b.q_lens, "any", seed=kv))
 
 
-@pytest.mark.parametrize("Hq,kv", [(4, 300), (32, 40000)])
+@pytest.mark.parametrize("Hq,kv", [(4, 300), (2, 40000), (8, 40000), (32, 40000)])
 def test_other_branches_do_not_count(ts, Hq, kv):
     """Rows of other branches point along every query, far above the seen scores."""
     for dtype in (BF, FP):
@@ -128,7 +166,7 @@ def test_chain_is_a_causal_chunk(ts, Hq, kv):
     pu.check_attention(o2, lse2, ref, BF, 128, p_round=P_ROUND[BF])
 
 
-@pytest.mark.parametrize("Hq", [4, 64])
+@pytest.mark.parametrize("Hq", [4, 8, 64])
 def test_nodes_without_a_row(ts, Hq):
     """Lengths shorter than the trees: nodes whose rows and ancestors' are not there."""
     b = pu.Batch([40, 64, 5, 3], [40, 64, 5, 3], Hq, 2, 128, 16, BF, extra=1)
@@ -140,14 +178,14 @@ def test_nodes_without_a_row(ts, Hq):
     assert (o[104:109] == 0).all()
 
 
-@pytest.mark.parametrize("Hq,kv", [(4, 700), (64, 20000)])
+@pytest.mark.parametrize("Hq,kv", [(4, 700), (2, 40000), (8, 20000), (64, 20000)])
 @pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
 def test_large_scores(ts, Hq, kv, dtype):
     b = pu.Batch([64, 9], [kv, 90], Hq, 2, 128, 32, dtype, seed=9, scale=30.0)
     check(ts, b, parents_of(b.q_lens, "ternary"))
 
 
-@pytest.mark.parametrize("Hq,kv", [(4, 300), (64, 20000)])
+@pytest.mark.parametrize("Hq,kv", [(4, 300), (8, 20000), (64, 20000)])
 @pytest.mark.parametrize("bad", [-1, -5, 30, 31, 10 ** 9])
 def test_a_bad_parent_is_reported(ts, Hq, kv, bad):
     """Its node counts as a root; the other trees are as they should be."""
@@ -168,7 +206,7 @@ def test_a_bad_parent_is_reported(ts, Hq, kv, bad):
     assert status_of(b) == 1
 
 
-@pytest.mark.parametrize("Hq,kv", [(4, 300), (64, 20000)])
+@pytest.mark.parametrize("Hq,kv", [(4, 300), (8, 20000), (64, 20000)])
 def test_bad_pages_lengths_and_trees_are_reported(ts, Hq, kv):
     def call(b, max_q=64, **kw):
         b.status.zero_()
@@ -194,7 +232,8 @@ def test_bad_pages_lengths_and_trees_are_reported(ts, Hq, kv):
         assert call(b, cu=torch.tensor(cu, **i32)) == 1
 
 
-@pytest.mark.parametrize("Hq,kv,q", [(4, 300, 64), (64, 20000, 64), (8, 60000, 5)])
+@pytest.mark.parametrize("Hq,kv,q", [(4, 300, 64), (64, 20000, 64), (8, 20000, 64), (2, 90000, 64),
+                                     (8, 60000, 5)])
 def test_nan_in_a_query_row(ts, Hq, kv, q):
     b = pu.Batch([q, q], [kv, kv - 1], Hq, 2, 128, 32, FP, seed=19)
     par = parents_of(b.q_lens, "ternary")
@@ -207,7 +246,7 @@ def test_nan_in_a_query_row(ts, Hq, kv, q):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
-@pytest.mark.parametrize("Hq,q", [(4, 5), (4, 64), (32, 64)])
+@pytest.mark.parametrize("Hq,q", [(4, 5), (4, 64), (8, 64), (32, 64)])
 def test_replay_sees_new_trees_and_lengths(ts, Hq, q):
     """Two graphs on one workspace, replayed on other lengths and parents."""
     b = pu.Batch([q, q], [15000, 7000], Hq, 2, 128, 16, BF, seed=15)
