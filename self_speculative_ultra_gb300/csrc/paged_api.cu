@@ -71,9 +71,14 @@ int64_t bound_kv(int max_pages, int page_size, int64_t max_kv) {
 // against 26.9; 6 streams of 94 tokens and at most 491 rows (24 blocks, 4 a SM)
 // 7.6 against 19.1, of 154 tokens and 1000 rows (39 blocks, 12 a SM) 29.1 against
 // 27.0; 32 rows of 8 KV heads over 100K rows (84 a SM) 127 against 83.
-bool few_rows(int n_seq, int max_q, int Hq, int Hkv, int64_t kv) {
+// Draft trees of one tile need no plan (~11 us in all): there any number of blocks
+// but one at 5 trips a SM.  4 streams of 8 nodes over 1500 rows, 32/8 heads (5.1 a
+// SM) 14.1 against 16.2, 12 streams of 40 nodes over 300, 8/8 heads (5.7) 21.6
+// against 16.7, one of 40 nodes over 1500, 32/8 heads (6.3) 19.7 against 15.3.
+bool few_rows(int n_seq, int max_q, int Hq, int Hkv, int64_t kv, bool tree) {
   const int64_t blocks = ((int64_t)max_q * (Hq / Hkv) + 15) / 16;
   const int64_t trips = (int64_t)n_seq * Hkv * blocks * ((kv + 127) / 128);
+  if (tree && max_q * (Hq / Hkv) <= kTcRows) return blocks <= 1 || trips <= 5 * kGb300Sms;
   return blocks <= 1 || trips <= 8 * kGb300Sms || (blocks <= 4 && trips <= 13 * kGb300Sms);
 }
 
@@ -83,9 +88,9 @@ size_t dense_ws_bytes(int n, int n_seq, int Hq, int Hkv, int d, int max_pages, i
       max_q < 1)
     return 0;
   const int64_t kv = bound_kv(max_pages, page_size, max_kv);
-  if (few_rows(n_seq, max_q, Hq, Hkv, kv))
+  if (few_rows(n_seq, max_q, Hq, Hkv, kv, tree))
     return rows_plan((int64_t)n_seq * Hkv, max_q * (Hq / Hkv), d, kv).ws_bytes;
-  return tc_plan(n, n_seq, Hq, Hkv, d, max_q, kv, tree).ws_bytes;
+  return tc_plan(n, n_seq, Hq, Hkv, d, max_q, kv, (int64_t)max_pages * page_size, tree).ws_bytes;
 }
 
 // The dense call and its form for draft trees (parents not NULL).
@@ -106,8 +111,9 @@ int dense_attention(const char* W, const void* q, const void* k_pages, const voi
   for (const void* p : {q, k_pages, v_pages, (const void*)o})
     if (!aligned16(p)) return fail(TS_ERR_INVALID_ARG, "%s: a tensor is not 16-byte aligned", W);
   const int64_t kv = bound_kv(max_pages, page_size, max_kv);
-  if (!few_rows(n_seq, max_q, Hq, Hkv, kv)) {
-    const TcPlan p = tc_plan(n, n_seq, Hq, Hkv, d, max_q, kv, parents != nullptr);
+  if (!few_rows(n_seq, max_q, Hq, Hkv, kv, parents != nullptr)) {
+    const TcPlan p = tc_plan(n, n_seq, Hq, Hkv, d, max_q, kv, (int64_t)max_pages * page_size,
+                             parents != nullptr);
     rc = check_paged_ws(workspace, workspace_bytes, p.ws_bytes, W);
     if (rc) return rc;
     const TcArgs a{q, k_pages, v_pages, Hq, Hkv, max_q, o, lse, parents};

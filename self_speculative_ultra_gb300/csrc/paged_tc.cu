@@ -20,10 +20,11 @@
 // 1.47 us at an even share of the copy bandwidth, and takes 1.5 us of products.  A
 // node's ancestors are 64 bits a row, laid over the one or two key tiles that hold
 // the tree; all other tiles are as in a chunk.  A tile of at most 128 rows is one
-// group, which takes both S tiles in turn (0.9 us a step for 1.5).  64 nodes over
-// 100K rows, 32/8 heads: 91 us, 4.6 TB/s with plan, start and join; 12 trees of 25
-// nodes over 24K rows, 40/8 heads: 192 us (6.3 TB/s), of 51 nodes 234, of 64 (a tile
-// of 256 rows and one of 64, which read the keys twice) 363.
+// group, which takes both S tiles in turn (0.9 us a step for 1.5).  Where every tree
+// is one tile there is no plan (see Line).  64 nodes over 100K rows, 32/8 heads: 81
+// us, 5.2 TB/s with start and join; 12 trees of 25 nodes over 24K rows, 40/8 heads:
+// 189 us (6.4 TB/s), of 51 nodes 229, of 64 (a tile of 256 rows and one of 64, which
+// read the keys twice) 365.
 //
 // Three launches.  The plan (one CTA) lists the work from the device-side
 // lengths in order of falling cost: the tiles of whole rounds over the SMs as
@@ -570,7 +571,7 @@ struct Work {
   Header* hdr;
   const int4* entries;
   const int* slots;
-  int4* line_cuts;      // trees of one tile (see Line), else NULL
+  int4* line_cuts;      // of trees of one tile (see Line)
   bool by_tile;         // line_cuts by tile, else by the CTA that starts one
 };
 
@@ -579,87 +580,103 @@ struct Work {
 // read by nobody else, so pieces need no order in time.  The tiles (sequence, KV
 // head) stand on a line, each as long as it costs, and CTA c takes the c-th of C
 // equal stretches of it, which it finds from the lengths by itself; a tile that
-// cuts fall into is joined as in the plan's list.  That saves the plan's launch.
+// cuts fall into is joined as in the plan's list.  That saves the plan's launch (64
+// nodes over 100K rows 91 -> 81 us, nine short streams 33 -> 22).  The host sees to
+// it that the line is shorter than 2^31.
+// The first copy waits for all of this, and for its instructions too, which a new
+// kernel fetches from afar: a warp does it alone, in few of them.
 constexpr int kLineFixed = 3;   // what a tile costs beside its steps, in steps
-constexpr int kLineLeast = 8;   // a stretch is at least as long
+constexpr int kLineLeast = 3;   // a stretch is at least as long
 
-struct Line {
-  long long total, w0, w1;      // the line, and this CTA's stretch
-  int C;
-  int s;                        // the sequence that holds w0, and where it starts
-  long long at;
-};
-
-// The tile of a tree's rows: its steps, and its length without kLineFixed, in
-// eighths of a step each.
+// The tile of a tree's rows: its steps, and its length on the line.
+template <int D>
 struct TreeTile {
-  int rows, steps, eighths;
+  int q0, nodes, see0, kl, steps;
+  bool bad;
+  int eighths;                  // what a step costs
   __device__ __forceinline__ int price() const { return (steps * eighths + 7) >> 3; }
-  __device__ __forceinline__ int length() const { return rows > 0 ? price() + kLineFixed : 0; }
+  __device__ __forceinline__ int length() const { return nodes > 0 ? price() + kLineFixed : 0; }
   // steps in front of the tile's place c
   __device__ __forceinline__ int steps_at(int c) const {
     return c >= length() ? steps : c <= kLineFixed ? 0 : min((c - kLineFixed) * 8 / eighths, steps);
   }
+  __device__ __forceinline__ void set(const PagedBatch& b, int s, int max_q, int G) {
+    nodes = 0;
+    bad = false;
+    if (s >= b.n_seq) return;
+    const SeqSpan sp = seq_span(b, s);
+    bad = sp.bad || sp.ql > max_q;
+    q0 = sp.q0;
+    nodes = min(sp.ql, max_q);
+    see0 = sp.kl - sp.ql;
+    kl = sp.kl;
+    finish(G);
+  }
+  __device__ __forceinline__ void finish(int G) {
+    steps = (max(see0 + nodes, 0) + kNk - 1) / kNk;        // the last node sees up to its own row
+    eighths = D == 128 && nodes * G <= 128 ? kSoloEighths : 8;
+  }
 };
-template <int D>
-__device__ __forceinline__ TreeTile tree_tile(const SeqSpan& sp, int max_q, int G) {
-  TreeTile t;
-  t.rows = min(sp.ql, max_q) * G;
-  t.steps = t.rows > 0 ? tile_steps(sp, t.rows, 0, G) : 0;
-  t.eighths = D == 128 && t.rows <= 128 ? kSoloEighths : 8;
-  return t;
-}
 
+struct Line {
+  uint32_t each, more;          // the first `more` stretches are each + 1 long, the others each
+  uint32_t w0, len;             // this CTA's stretch
+  int s;                        // the sequence that holds w0, and where it starts
+  uint32_t at;
+  __device__ __forceinline__ void cut(uint32_t total) {
+    const uint32_t C = max(1u, min(total / kLineLeast, gridDim.x)), c = blockIdx.x;
+    each = total / C;
+    more = total - each * C;
+    w0 = each * c + min(c, more);
+    len = c < C ? each + (c < more) : 0;
+  }
+};
+
+// The line, found by the whole CTA.
 template <int D>
 __device__ __forceinline__ Line find_line(const PagedBatch& b, int Hkv, int G, int max_q,
                                           int32_t* status) {
-  __shared__ long long sums[kThreads / 32];
-  __shared__ long long s_at;
+  __shared__ uint32_t sums[kThreads / 32], s_at;
   __shared__ int s_seq;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x;
-  auto length = [&](int s, bool report) -> long long {
-    if (s >= b.n_seq) return 0;
-    const SeqSpan sp = seq_span(b, s);
-    if (report && (sp.bad || sp.ql > max_q)) set_status(status, TS_ERR_INVALID_ARG);
-    return (long long)Hkv * tree_tile<D>(sp, max_q, G).length();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto length = [&](int s, bool report) -> uint32_t {
+    TreeTile<D> t;
+    t.set(b, s, max_q, G);
+    if (report && t.bad) set_status(status, TS_ERR_INVALID_ARG);
+    return (uint32_t)Hkv * t.length();
   };
-  const long long first = length(tid, c == 0);
-  long long mine = first;
-  for (int s = tid + kThreads; s < b.n_seq; s += kThreads) mine += length(s, c == 0);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  const uint32_t first = length(tid, blockIdx.x == 0);
+  uint32_t mine = first;
+  for (int s = tid + kThreads; s < b.n_seq; s += kThreads) mine += length(s, blockIdx.x == 0);
+  mine = __reduce_add_sync(0xffffffffu, mine);
   if (lane == 0) sums[warp] = mine;
   if (tid == 0) {
     s_seq = 0;
     s_at = 0;
   }
   __syncthreads();
+  uint32_t total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) total += sums[w];
   Line r;
-  r.total = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) r.total += sums[w];
-  r.C = (int)imax64(1, imin64(r.total / kLineLeast, gridDim.x));
-  r.w0 = c < r.C ? r.total * c / r.C : r.total;
-  r.w1 = c < r.C ? r.total * (c + 1) / r.C : r.total;
-  long long before = 0;
+  r.cut(total);
+  uint32_t before = 0;
   for (int base = 0; base < b.n_seq && before <= r.w0; base += kThreads) {
-    const long long x = base == 0 ? first : length(base + tid, false);
-    long long inc = x;
+    const uint32_t x = base == 0 ? first : length(base + tid, false);
+    uint32_t inc = x;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+      const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += y;
     }
     __syncthreads();
     if (lane == 31) sums[warp] = inc;
     __syncthreads();
-    long long at = before + inc - x;
-#pragma unroll
+    uint32_t at = before + inc - x;
     for (int w = 0; w < kThreads / 32; ++w) {
       if (w < warp) at += sums[w];
       before += sums[w];
     }
-    if (x > 0 && r.w0 >= at && r.w0 < at + x) {
+    if (x > 0 && r.w0 >= at && r.w0 - at < x) {
       s_seq = base + tid;
       s_at = at;
     }
@@ -670,85 +687,109 @@ __device__ __forceinline__ Line find_line(const PagedBatch& b, int Hkv, int G, i
   return r;
 }
 
-// The stretch's items in turn: part of a tile each.
+// The stretch's items in turn: part of a tile each.  A warp walks; the tiles of 32
+// sequences are its lanes'.  Up to 32 sequences' line is its own work, without a
+// barrier.
 template <int D>
 struct LineWalk {
-  int s, kv;                    // the tile ahead
-  long long at;                 // where it starts
-  SeqSpan sp;
-  __device__ __forceinline__ void begin(const PagedBatch& b, const Line& l, int Hkv, int G,
-                                        int max_q) {
+  TreeTile<D> mine, t;          // of sequence base + lane; the tile ahead
+  int base, s, kv, c0;          // c0: where the stretch enters it
+  int left;                     // what is left of the stretch
+  int each, more;               // of the stretches behind this one
+  int rest;                     // of the item's tile behind the stretch; -1: none that it starts
+  __device__ __forceinline__ void take(const PagedBatch& b, int max_q, int G, int lane) {
+    if (s - base >= 32) {
+      base = s;
+      mine.set(b, base + lane, max_q, G);
+    }
+    t.q0 = __shfl_sync(0xffffffffu, mine.q0, s - base);
+    t.nodes = __shfl_sync(0xffffffffu, mine.nodes, s - base);
+    t.see0 = __shfl_sync(0xffffffffu, mine.see0, s - base);
+    t.kl = __shfl_sync(0xffffffffu, mine.kl, s - base);
+    t.finish(G);
+  }
+  __device__ __forceinline__ void begin(const PagedBatch& b, Line l, int Hkv, int G, int max_q,
+                                        int lane, int32_t* status) {
+    base = b.n_seq > 32 ? l.s : 0;
+    mine.set(b, base + lane, max_q, G);
+    if (b.n_seq <= 32) {
+      if (blockIdx.x == 0 && mine.bad) set_status(status, TS_ERR_INVALID_ARG);
+      const uint32_t x = mine.length();
+      uint32_t inc = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      l.cut(__shfl_sync(0xffffffffu, inc, 31) * (uint32_t)Hkv);
+      // the last that starts at or before w0 and has tokens
+      const unsigned in = __ballot_sync(0xffffffffu, x > 0 && (inc - x) * Hkv <= l.w0);
+      l.s = in ? 31 - __clz(in) : 0;
+      l.at = __shfl_sync(0xffffffffu, inc - x, l.s) * (uint32_t)Hkv;
+    }
+    left = l.len;
+    each = (int)l.each;
+    more = max((int)l.more - (int)blockIdx.x - 1, 0);
     s = l.s;
-    kv = 0;
-    at = l.at;
-    if (l.w0 >= l.w1) return;
-    sp = seq_span(b, s);
-    const int length = tree_tile<D>(sp, max_q, G).length();
-    kv = (int)((l.w0 - at) / length);          // w0 lies in this sequence: length > 0
-    at += (long long)kv * length;
+    kv = c0 = 0;
+    if (left == 0) return;
+    take(b, max_q, G, lane);
+    const uint32_t length = t.length(), in = l.w0 - l.at;
+    kv = in / length;                          // w0 lies in this sequence
+    c0 = in - kv * length;
   }
   // n < 0: the stretch is at its end
-  __device__ __forceinline__ Item next(const PagedBatch& b, const Line& l, const Work& work,
-                                       int Hkv, int G, int max_q, int lane) {
+  __device__ __forceinline__ Item next(const PagedBatch& b, int Hkv, int G, int max_q, int lane) {
     Item w;
     w.n = -1;
-    while (at < l.w1) {
-      const TreeTile t = tree_tile<D>(sp, max_q, G);
-      const int length = t.length(), head = kv, seq = s;
-      const SeqSpan own = sp;
-      const long long from = at;
-      at += length;
-      if (++kv == Hkv) {
-        kv = 0;
-        // (a sequence without tokens has no length; behind one that ends before w1
-        // there is another)
-        while (at < l.w1) {
-          sp = seq_span(b, ++s);
-          if (sp.ql > 0) break;
-        }
-      }
-      const int c0 = (int)imax64(l.w0 - from, 0), c1 = (int)imin64(l.w1 - from, length);
+    bool some = false;
+    while (!some && left > 0) {
+      const int length = t.length(), c1 = min(c0 + left, length);
       const int k0 = t.steps_at(c0), k1 = t.steps_at(c1);
       const bool starts = t.steps > 0 ? k0 == 0 : c0 == 0, ends = k1 == t.steps;
-      if (k0 == k1 && (t.steps > 0 || !starts)) continue;      // between two tiles' steps
-      w.kv = head;
-      w.s = seq;
-      w.q0 = own.q0;
+      some = k0 < k1 || (t.steps == 0 && starts);              // else between two tiles' steps
+      left -= c1 - c0;
+      c0 = 0;
+      rest = !starts ? -1 : ends ? 0 : length - c1;
+      w.kv = kv;
+      w.s = s;
+      w.q0 = t.q0;
       w.r0 = 0;
-      w.rows = t.rows;
-      w.see0 = own.kl - own.ql;
-      w.kl = own.kl;
+      w.rows = t.nodes * G;
+      w.see0 = t.see0;
+      w.kl = t.kl;
       w.k0 = k0;
-      w.n = k1 - k0;
-      w.slot = starts && ends ? -1 : 2 * blockIdx.x + (starts ? 1 : 0);
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const int a = g * 128;
-        int steps = 0;
-        if (a < t.rows) {
-          const int vis = w.see0 + (min(a + 128, t.rows) - 1) / G + 1;
-          steps = vis <= 0 ? 0 : (vis + kNk - 1) / kNk;
+      w.n = some ? k1 - k0 : -1;
+      w.slot = starts && ends ? -1 : 2 * (int)blockIdx.x + (starts ? 1 : 0);
+      // group 0 ends with the node of its last row
+      const int vis = t.see0 + min(127 / G, t.nodes - 1) + 1;
+      w.n_g[0] = max(min(vis <= 0 ? 0 : (vis + kNk - 1) / kNk, k1) - k0, 0);
+      w.n_g[1] = w.rows > 128 ? k1 - k0 : 0;
+      if (++kv == Hkv) {
+        kv = 0;
+        // (a sequence without tokens has no length; while the stretch goes on there
+        // is one with)
+        while (left > 0) {
+          ++s;
+          take(b, max_q, G, lane);
+          if (t.nodes > 0) break;
         }
-        w.n_g[g] = max(0, min(steps, k1) - k0);
       }
-      if (starts && lane == 0) {
-        // the CTA with the tile's last step: the last whose stretch starts at or
-        // before the tile's last place
-        int parts = 0;
-        if (!ends) {
-          const long long z = from + length - 1;
-          int q = (int)(z * l.C / l.total);
-          while (q + 1 < l.C && l.total * (q + 1) / l.C <= z) ++q;
-          while (l.total * q / l.C > z) --q;
-          parts = q - (int)blockIdx.x + 1;
-        }
-        if (work.by_tile || parts > 0)
-          work.line_cuts[work.by_tile ? seq * Hkv + head : (int)blockIdx.x] =
-              make_int4(seq, head, (int)blockIdx.x, parts);
-      }
-      break;
     }
     return w;
+  }
+  // Where the item's pieces lie, if the tile starts with it: with the CTAs up to the
+  // one where it ends (0: it is whole).
+  __device__ __forceinline__ void note(const Work& work, const Item& w, int Hkv) const {
+    if (rest < 0) return;
+    int parts = 0;
+    if (rest > 0)
+      parts = 1 + (rest <= (int64_t)more * (each + 1)
+                       ? (rest + each) / (each + 1)
+                       : more + (rest - more * (each + 1) + each - 1) / each);
+    if (work.by_tile || parts > 0)
+      work.line_cuts[work.by_tile ? w.s * Hkv + w.kv : (int)blockIdx.x] =
+          make_int4(w.q0, w.rows | w.kv << 16, (int)blockIdx.x, parts);
   }
 };
 
@@ -827,7 +868,11 @@ __device__ __forceinline__ uint32_t tree_word(unsigned long long nodes, int base
   return (uint32_t)(nodes << -first) | ((1u << -first) - 1u);
 }
 
-template <typename T, int D, bool kTree>
+// What the new tokens are: a chunk, the nodes of trees whose tiles the plan lists, or
+// of trees of one tile on a line.
+enum Kind { kChunk, kTreeList, kTreeLine };
+
+template <typename T, int D, Kind kKind>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v,
                 const PagedBatch b, const T* __restrict__ q, int Hq, int Hkv, int max_q,
@@ -836,6 +881,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
                 float* __restrict__ part_o, float2* __restrict__ part_ml, long long wait_limit,
                 int32_t* status) {
   using Ly = Layout<D>;
+  constexpr bool kTree = kKind != kChunk, kOnLine = kKind == kTreeLine;
   constexpr int kSK = Ly::kSK, kSV = Ly::kSV, kScores = Ly::kScores;
   extern __shared__ __align__(1024) uint8_t sm[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -882,22 +928,24 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
     ptx::tmem_alloc(&aux->tmem_base, Ly::kTmemCols);
     ptx::tmem_relinquish();
   }
+  if (kOnLine && tid == 0) {
+    ptx::prefetch_map(&tmap_k);
+    ptx::prefetch_map(&tmap_v);
+  }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = aux->tmem_base;
   griddep_wait();
   griddep_launch_dependents();
-  const bool on_line = kTree && work.line_cuts != nullptr;
   Line line{};
-  if constexpr (kTree) {
-    if (on_line) {
-      line = find_line<D>(b, Hkv, G, max_q, status);
-      if (!work.by_tile && tid == 0) work.line_cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
-      __syncthreads();
-    }
+  int n_items = 0;
+  if constexpr (kOnLine) {
+    if (!work.by_tile && tid == 0) work.line_cuts[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (b.n_seq > 32) line = find_line<D>(b, Hkv, G, max_q, status);
+  } else {
+    n_items = __ldcg(&work.hdr->n_entries) * Hkv;
   }
-  const int n_items = on_line ? 0 : __ldcg(&work.hdr->n_entries) * Hkv;
   const int ps = 1 << b.page_shift;
 
   if (warp < 8) {
@@ -937,8 +985,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       };
       int taken = blockIdx.x;             // warp 0: the next item; the first is the CTA's own
       LineWalk<D> walk;
-      if constexpr (kTree) {
-        if (on_line && is_k) walk.begin(b, line, Hkv, G, max_q);
+      if constexpr (kOnLine) {
+        if (is_k) walk.begin(b, line, Hkv, G, max_q, lane, status);
       }
       for (uint32_t count = 0; ok;) {
         Item w;
@@ -950,10 +998,8 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           w.n = -1;
-          if (i < n_items) w = load_item(b, work, i, Hkv, G, max_q);
-          if constexpr (kTree) {
-            if (on_line) w = walk.next(b, line, work, Hkv, G, max_q, lane);
-          }
+          if constexpr (kOnLine) w = walk.next(b, Hkv, G, max_q, lane);
+          else if (i < n_items) w = load_item(b, work, i, Hkv, G, max_q);
           if (lane == 0) {
             aux->next[at] = w;
             ptx::mbar_arrive(&aux->next_full[at]);
@@ -964,10 +1010,11 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
         }
         if (!ok || w.n < 0) break;
         int64_t next = ids(w, 0);
-        if (w.n == 0 && lane == 0 && is_k && !on_line) taken = gridDim.x + atomicAdd(&work.hdr->taken, 1);
+        if (kOnLine && is_k && lane == 0 && w.n == 0) walk.note(work, w, Hkv);
+        if (!kOnLine && w.n == 0 && lane == 0 && is_k) taken = gridDim.x + atomicAdd(&work.hdr->taken, 1);
         for (int k = 0; ok && k < w.n; ++k, ++it) {
           // the next item is taken as late as its latency allows
-          if (is_k && k == max(0, w.n - 2) && lane == 0 && !on_line)
+          if (!kOnLine && is_k && k == max(0, w.n - 2) && lane == 0)
             taken = gridDim.x + atomicAdd(&work.hdr->taken, 1);
           const int64_t ph = next;
           next = ids(w, k + 1);
@@ -1003,6 +1050,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
             for (int p = 0; p < D / 64; ++p)
               ptx::tma_load_2d_at(ring + st * Ly::kTile + p * Ly::kPanel + lane * ps * 128, map,
                                   land, p * 64, row, pol);
+          if (kOnLine && is_k && lane == 0 && k == 0) walk.note(work, w, Hkv);
           ++done;
         }
         base_g[0] += w.n_g[0];
@@ -1511,7 +1559,7 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
       if (!warp_rows) continue;
       const int64_t row = (int64_t)(w.q0 + R / G) * Hq + w.kv * G + R % G;
       const bool cut = w.slot >= 0;
-      const int64_t piece = on_line ? w.slot : (int64_t)w.slot * Hkv + w.kv;
+      const int64_t piece = kOnLine ? w.slot : (int64_t)w.slot * Hkv + w.kv;
       const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
@@ -1566,12 +1614,14 @@ paged_tc_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constan
 // kPart columns a thread: a piece's O lies by column quads, rows inside, so a
 // warp's loads are contiguous.  A CTA's warps take the D / kPart column parts of
 // the rows, or where there are CTAs enough, the pieces of one part among them.
+// (Few rows are many pieces of few tiles: smaller CTAs, so that all are there at once.)
+constexpr int merge_warps(bool line) { return line ? 4 : 8; }
 template <typename T, int D, bool kLine>
-__global__ void __launch_bounds__(256, 2)
+__global__ void __launch_bounds__(merge_warps(kLine) * 32, kLine ? 4 : 2)
 paged_tc_merge(const PagedBatch b, const Header* __restrict__ hdr, const int4* __restrict__ cuts,
-               int n_line, bool by_tile, int Hq, int Hkv, int max_q, const float* __restrict__ part_o,
+               int n_line, bool by_tile, int n_ctas, int Hq, int Hkv, int max_q, const float* __restrict__ part_o,
                const float2* __restrict__ part_ml, T* __restrict__ o, float* __restrict__ lse) {
-  constexpr int kWarps = 8, kPart = 16, kQuads = kPart / 4, kParts = D / kPart;
+  constexpr int kWarps = merge_warps(kLine), kPart = 16, kQuads = kPart / 4, kParts = D / kPart;
   __shared__ float4 s_o[kWarps][kQuads][32];
   __shared__ float2 s_ml[kWarps][32];
   griddep_wait();
@@ -1585,21 +1635,32 @@ paged_tc_merge(const PagedBatch b, const Header* __restrict__ hdr, const int4* _
   for (int64_t u = first; u < total; u += hop) {
     const int part = (int)(u % kParts), r = (int)(u / kParts % (kM / 32)) * 32 + lane;
     const int64_t at = u / kParts / (kM / 32);
-    int kv = (int)(at % Hkv);
-    int4 c = __ldcg(&cuts[kLine ? at : at / Hkv]);       // sequence, tile, slot, pieces
-    SeqSpan sp;
+    const int4 c = __ldcg(&cuts[kLine ? at : at / Hkv]);
+    int kv, q0, R;
+    bool live;
     if constexpr (kLine) {
-      // sequence, KV head, CTA, pieces; a sequence without tokens wrote none
-      if (by_tile) c.x = (int)(at / Hkv);
-      else kv = c.y;
-      sp = seq_span(b, c.x);
-      if (sp.ql == 0) c.w = 0;
-      c.y = 0;
+      // first token, rows and KV head, CTA, pieces.  By tile, a sequence without tokens
+      // wrote none, and one whose CTA gave up may not have: the entry only says where
+      // the pieces lie, if it says so within the workspace.
+      kv = c.y >> 16;
+      q0 = c.x;
+      int rows = c.y & 0xFFFF;
+      if (by_tile) {
+        const SeqSpan sp = seq_span(b, (int)(at / Hkv));
+        kv = (int)(at % Hkv);
+        q0 = sp.q0;
+        rows = min(sp.ql, max_q) * G;
+      }
+      R = r;
+      live = r < rows && c.w > 0 && c.z >= 0 && c.z < n_ctas && c.w <= n_ctas - c.z;
     } else {
-      sp = seq_span(b, c.x);
+      // sequence, tile, slot, pieces
+      const SeqSpan sp = seq_span(b, c.x);
+      kv = (int)(at % Hkv);
+      q0 = sp.q0;
+      R = c.y * kM + r;
+      live = R < min(sp.ql, max_q) * G;
     }
-    const int R = c.y * kM + r;
-    const bool live = c.w > 0 && R < min(sp.ql, max_q) * G;
     if (!__any_sync(0xffffffffu, live)) continue;        // the same for the CTA's warps, if shared
     const int i0 = shared ? warp : 0, di = shared ? kWarps : 1;
     float4 acc[kQuads];
@@ -1659,7 +1720,7 @@ paged_tc_merge(const PagedBatch b, const Header* __restrict__ hdr, const int4* _
     }
     if (!live) continue;
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int64_t row = (int64_t)(sp.q0 + R / G) * Hq + kv * G + R % G;
+    const int64_t row = (int64_t)(q0 + R / G) * Hq + kv * G + R % G;
     uint4* dst = reinterpret_cast<uint4*>(o + row * D + part * kPart);
 #pragma unroll
     for (int x = 0; x < kQuads; x += 2)
@@ -1715,7 +1776,9 @@ int go_tc(const PagedBatch& b, const TcArgs& a, const TcPlan& p, char* ws, int32
   int rc = pool_map(&mk, a.k_pages, b, a.Hkv, D, Pair<T>::kFp16);
   if (!rc) rc = pool_map(&mv, a.v_pages, b, a.Hkv, D, Pair<T>::kFp16);
   if (rc) return rc;
-  auto kern = a.parents ? paged_tc_kernel<T, D, true> : paged_tc_kernel<T, D, false>;
+  auto kern = p.line      ? paged_tc_kernel<T, D, kTreeLine>
+              : a.parents ? paged_tc_kernel<T, D, kTreeList>
+                          : paged_tc_kernel<T, D, kChunk>;
   // the warps' register split adds up to 128 registers a thread at launch; any
   // other count would leave the softmax warps waiting for registers
   cudaFuncAttributes fa{};
@@ -1732,7 +1795,7 @@ int go_tc(const PagedBatch& b, const TcArgs& a, const TcPlan& p, char* ws, int32
   float2* part_ml = reinterpret_cast<float2*>(ws + p.ml_at);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
-  const Work work{hdr, entries, slots, p.line ? cuts : nullptr, p.line && p.line_cuts < p.grid};
+  const Work work{hdr, entries, slots, cuts, p.line && p.line_cuts < p.grid};
   if (!p.line) {
     const size_t near = p.max_tiles <= kPlanTiles ? (size_t)p.max_tiles * 2 * sizeof(int4) : 0;
     cudaFuncSetAttribute(paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -1749,17 +1812,18 @@ int go_tc(const PagedBatch& b, const TcArgs& a, const TcPlan& p, char* ws, int32
                      a.parents, work, static_cast<T*>(a.o), a.lse, part_o, part_ml, wait_limit_cycles(), status);
   rc = launch_status("paged_tc_kernel");
   if (rc || p.max_slots == 0) return rc;
-  pdl_config(&cfg, attr, dim3(p.merge_grid), dim3(256), 0, st);
+  pdl_config(&cfg, attr, dim3(p.merge_grid), dim3(merge_warps(p.line) * 32), 0, st);
   cudaLaunchKernelEx(&cfg, p.line ? paged_tc_merge<T, D, true> : paged_tc_merge<T, D, false>, b,
-                     (const Header*)hdr, (const int4*)cuts, p.line_cuts, work.by_tile, a.Hq, a.Hkv,
-                     a.max_q, (const float*)part_o, (const float2*)part_ml, static_cast<T*>(a.o),
+                     (const Header*)hdr, (const int4*)cuts, p.line_cuts, work.by_tile, p.grid, a.Hq,
+                     a.Hkv, a.max_q, (const float*)part_o, (const float2*)part_ml, static_cast<T*>(a.o),
                      a.lse);
   return launch_status("paged_tc_merge");
 }
 
 }  // namespace
 
-TcPlan tc_plan(int n, int n_seq, int Hq, int Hkv, int d, int max_q, int64_t max_kv, bool tree) {
+TcPlan tc_plan(int n, int n_seq, int Hq, int Hkv, int d, int max_q, int64_t max_kv, int64_t cap,
+               bool tree) {
   TcPlan p{};
   const int64_t G = Hq / Hkv;
   // tiles: a sequence's rows rounded up to whole tiles
@@ -1783,9 +1847,9 @@ TcPlan tc_plan(int n, int n_seq, int Hq, int Hkv, int d, int max_q, int64_t max_
     at += align_up(bytes, 256);
     return r;
   };
-  if (tree && max_q * G <= kM) {
+  const int64_t units = (int64_t)n_seq * Hkv;
+  if (tree && max_q * G <= kM && units < (int64_t(1) << 31) / (cap / kNk + 1 + kLineFixed)) {
     p.line = true;
-    const int64_t units = (int64_t)n_seq * Hkv;
     p.grid = (int)imax64(1, imin64(kGb300Sms, units * (steps + kLineFixed) / kLineLeast));
     p.line_cuts = (int)imin64(units, p.grid);
     p.max_slots = p.grid > 1 ? 2 * p.grid : 0;

@@ -16,7 +16,9 @@ struct TcPlan {
   int line_cuts;               // tiles that may be cut, as the join counts them
   size_t tiles_at, entries_at, slots_at, cuts_at, part_at, ml_at, ws_bytes;
 };
-TcPlan tc_plan(int n, int n_seq, int Hq, int Hkv, int d, int max_q, int64_t max_kv, bool tree);
+// cap: the rows a sequence may have at most (max_kv is only what the host expects)
+TcPlan tc_plan(int n, int n_seq, int Hq, int Hkv, int d, int max_q, int64_t max_kv, int64_t cap,
+               bool tree);
 
 struct TcArgs {
   const void *q, *k_pages, *v_pages;
