@@ -756,8 +756,8 @@ int ts_token_counts(const int32_t* tokens, int stride, const int32_t* lens, int 
  * bias_ids, bias  [n_seq, n_bias] int32 and fp32 (n_bias <= 65535): the bias of
  *          single tokens; -1 is none, and of equal ids the last counts.
  * mask     [n_masks, ceil(V/32)] int32, or NULL; mask_rows [n] int32: the mask
- *          of each row, -1 for none; NULL: row t has mask t.  A mask without a
- *          set bit leaves masked_value everywhere.
+ *          of each row, -1 for none (with n_masks = 0 all are); NULL: row t has
+ *          mask t.  A mask without a set bit leaves masked_value everywhere.
  * Ids, offsets, mask rows or a repetition penalty out of their range are
  * reported as TS_ERR_INVALID_ARG in `status` and count as absent. */
 #define TS_LOGITS_BF16 1

@@ -142,7 +142,7 @@ logits_kernel(const LogitsArgs a, int n_slices, int run, int32_t* status) {
     }
   };
   auto mask_row = [&](int row) -> int {
-    if (!a.mask || row >= row1) return -1;
+    if ((!a.mask && !a.mask_rows) || row >= row1) return -1;
     const int mr = a.mask_rows ? a.mask_rows[row] : row;
     if (mr >= -1 && mr < a.n_masks) return mr;
     if (v0 == 0 && tid == 0) set_status(status, TS_ERR_INVALID_ARG);

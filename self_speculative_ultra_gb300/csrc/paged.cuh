@@ -174,7 +174,7 @@ struct RowsPlan {
   int cluster;         // CTAs a unit, joined on chip (0: stretches of the line)
   size_t cuts_bytes, part_bytes, ws_bytes;
 };
-RowsPlan rows_plan(int64_t units, int rows, int d, int64_t max_keys);
+RowsPlan rows_plan(int64_t units, int rows, int d, int64_t max_keys, bool tree = false);
 struct RowsArgs {
   const void *q, *k_pages, *v_pages;
   const int32_t *pages, *counts;   // sparse form: [n, Hkv, n_sel], [n, Hkv]; else NULL

@@ -89,7 +89,7 @@ size_t dense_ws_bytes(int n, int n_seq, int Hq, int Hkv, int d, int max_pages, i
     return 0;
   const int64_t kv = bound_kv(max_pages, page_size, max_kv);
   if (few_rows(n_seq, max_q, Hq, Hkv, kv, tree))
-    return rows_plan((int64_t)n_seq * Hkv, max_q * (Hq / Hkv), d, kv).ws_bytes;
+    return rows_plan((int64_t)n_seq * Hkv, max_q * (Hq / Hkv), d, kv, tree).ws_bytes;
   return tc_plan(n, n_seq, Hq, Hkv, d, max_q, kv, (int64_t)max_pages * page_size, tree).ws_bytes;
 }
 
@@ -120,7 +120,8 @@ int dense_attention(const char* W, const void* q, const void* k_pages, const voi
     return launch_paged_tc(b, a, p, d, (flags & TS_PAGED_FP16) != 0, workspace, status,
                            static_cast<cudaStream_t>(stream));
   }
-  const RowsPlan p = rows_plan((int64_t)n_seq * Hkv, max_q * (Hq / Hkv), d, kv);
+  const RowsPlan p =
+      rows_plan((int64_t)n_seq * Hkv, max_q * (Hq / Hkv), d, kv, parents != nullptr);
   rc = check_paged_ws(workspace, workspace_bytes, p.ws_bytes, W);
   if (rc) return rc;
   RowsArgs a{};

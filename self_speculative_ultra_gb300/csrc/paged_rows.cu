@@ -859,7 +859,7 @@ paged_rows_merge(const CutUnit* __restrict__ cuts, const float* __restrict__ par
 // a cluster of CTAs each, which join in shared memory: no second kernel and no
 // workspace, worth ~4 trips (3 streams of up to 4096 rows: 9.0 -> 7.4 us).  Else
 // the line of all units is cut into stretches of at least kMinTrips.
-RowsPlan rows_plan(int64_t units, int rows, int d, int64_t max_keys) {
+RowsPlan rows_plan(int64_t units, int rows, int d, int64_t max_keys, bool tree) {
   constexpr int64_t kJoinTrips = 4;
   RowsPlan p{};
   p.n_rb = (rows + 15) / 16;
@@ -867,7 +867,14 @@ RowsPlan rows_plan(int64_t units, int rows, int d, int64_t max_keys) {
   units *= p.n_rb;
   const int64_t trips = units * p.unit_trips;
   int64_t size = kMostCluster;
-  while (size > 1 && (units * size > kGb300Sms || size > p.unit_trips)) size >>= 1;
+  // Clusters that are there at once: at d = 128 a CTA fills its SM, and the SMs of a
+  // group hold 15 clusters of 8 in all or 36 of 4; one more waits for the others (8
+  // nodes over 6000 rows, 32/8 heads, 16 units: 26.5 us in clusters of 8, 17.8 of 4).
+  // (Trees only: the other calls' cuts, and so their last bits, stay as they are.)
+  auto fits = [&](int64_t n, int64_t c) {
+    return n * c <= kGb300Sms && !(tree && d == 128 && ((c == 8 && n > 15) || (c == 4 && n > 36)));
+  };
+  while (size > 1 && (!fits(units, size) || size > p.unit_trips)) size >>= 1;
   if (units * size <= kGb300Sms &&
       (p.unit_trips + size - 1) / size <= imax64(trips / kGb300Sms, kMinTrips) + kJoinTrips) {
     p.cluster = (int)size;

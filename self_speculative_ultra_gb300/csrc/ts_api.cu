@@ -442,7 +442,7 @@ int ts_logits_process(const void* logits, int64_t row_stride, int n, int V, cons
     return fail(TS_ERR_INVALID_ARG, "%s: counts are read where seen bits say so", F);
   if (mask && !mask_rows && n_masks < n)
     return fail(TS_ERR_INVALID_ARG, "%s: %d masks for %d rows", F, n_masks, n);
-  if (mask_rows && !mask) return fail(TS_ERR_INVALID_ARG, "%s: mask_rows without masks", F);
+  if (!mask && n_masks > 0) return fail(TS_ERR_INVALID_ARG, "%s: NULL mask", F);
   const size_t size = type ? 2 : 4;
   if (reinterpret_cast<uintptr_t>(logits) % size || reinterpret_cast<uintptr_t>(out) % 4)
     return fail(TS_ERR_INVALID_ARG, "%s: a tensor is not aligned to its type", F);

@@ -209,6 +209,12 @@ def test_equal_ids_and_special_values(ts):
     words = cuda(lo.pack(np.zeros((1, 4500), dtype=bool)))
     hidden = ts.ts_logits_process(x, i32(c.cu), mask=words, mask_rows=i32([0, -1]), masked_value=-7.0)
     assert (hidden[0] == -7.0).all() and torch.equal(hidden[1], x[1])
+    # no grammar at all: a table without masks
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    free = ts.ts_logits_process(x, i32(c.cu), mask=words[:0], mask_rows=i32([-1, -1]), status=status)
+    assert torch.equal(free[1], x[1]) and int(status.item()) == 0
+    ts.ts_logits_process(x, i32(c.cu), mask=words[:0], mask_rows=i32([-1, 0]), status=status)
+    assert int(status.item()) == 1
 
 
 def test_large_vocabulary_and_many_rows(ts):
@@ -279,6 +285,31 @@ def test_logits_replay_and_streams(ts):
         torch.cuda.synchronize()
         assert int(c.status.item()) == 0
         c.check(out)
+
+
+def test_calls_on_two_streams_at_once(ts):
+    """Two batches' logits and counts on two streams, back and forth, without waits."""
+    cases = [Case([5, 20], 50000, dtype, seed=20 + i, n_bias=30, masks="each")
+             for i, dtype in enumerate((BF, F32))]
+    args = [(c.logits, i32(c.cu), c.args()) for c in cases]
+    tokens = [cuda(c.rng.integers(0, c.V, (2, 4000)).astype(np.int32)) for c in cases]
+    lens = i32([4000, 17])
+    states = [(torch.zeros((2, (c.V + 31) // 32), dtype=torch.int32, device="cuda"),
+               torch.zeros((2, c.V), dtype=torch.int32, device="cuda")) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for i in range(6):
+        for k, st in enumerate(streams):
+            outs[k].append(ts.ts_logits_process(args[k][0], args[k][1], stream=st, **args[k][2]))
+            ts.ts_token_counts(tokens[k], lens, cases[k].V, *states[k], reset=i % 3 == 0, stream=st)
+    torch.cuda.synchronize()
+    for k, c in enumerate(cases):
+        c.check(outs[k][0])
+        assert all(torch.equal(outs[k][0], x) for x in outs[k][1:])
+        C = np.stack([np.bincount(t[:m], minlength=c.V) for t, m in
+                      zip(tokens[k].cpu().numpy(), (4000, 17))])
+        np.testing.assert_array_equal(states[k][1].cpu().numpy(), 3 * C)
 
 
 def test_an_empty_batch_of_rows(ts):

@@ -323,6 +323,43 @@ def test_pool_beyond_32_bit_offsets(ts, q, Hq):
     assert torch.equal(k[far[(L + 1) // 128], :, (L + 1) % 128], want)
 
 
+@pytest.mark.parametrize("Hq,kv", [(8, 30000), (2, 30000), (16, 30000)])
+def test_an_expired_wait_is_reported(ts, Hq, kv):
+    """A limit of a few clocks: a status, and the next call is as it should be."""
+    b = pu.Batch([64, 64], [kv, kv - 77], Hq, 2, 128, 32, BF, seed=21)
+    par = parents_of(b.q_lens, "any")
+    o, lse = attend(ts, b, par)
+    try:
+        ts.ts_set_wait_limit(1)
+        ts.ts_paged_tree_attention(b.q, b.k, b.v, b.cu_q, b.lens, b.table, par, 64, status=b.status)
+        assert status_of(b) == 4
+    finally:
+        ts.ts_set_wait_limit(0)
+    b.status.zero_()
+    o2, lse2 = attend(ts, b, par)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_trees_on_two_streams_at_once(ts):
+    batches = [pu.Batch([64] * 6, [9000 + 50 * i + k for i in range(6)], 8, 2, 128, 32, dt, seed=22 + k)
+               for k, dt in enumerate((BF, FP))]
+    pars = [parents_of(b.q_lens, "any", seed=k) for k, b in enumerate(batches)]
+    refs = [attend(ts, b, p) for b, p in zip(batches, pars)]
+    streams = [torch.cuda.Stream() for _ in batches]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(8):
+        for k, st in enumerate(streams):
+            b = batches[k]
+            outs[k].append(ts.ts_paged_tree_attention(b.q, b.k, b.v, b.cu_q, b.lens, b.table, pars[k],
+                                                      64, status=b.status, stream=st))
+    torch.cuda.synchronize()
+    for k, (o, lse) in enumerate(refs):
+        assert status_of(batches[k]) == 0
+        for x, y in outs[k]:
+            assert torch.equal(o, x) and torch.equal(lse, y)
+
+
 def test_an_empty_batch(ts):
     b = pu.Batch([3], [3], 4, 2, 64, 16, BF)
     none = torch.empty(0, 4, 64, dtype=BF, device="cuda")

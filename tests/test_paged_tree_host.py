@@ -176,7 +176,7 @@ def test_logits_refusals(ts):
     assert _logits(ts, n_seq=0, cu=None) == 0
     for kw in (dict(x=None), dict(out=None), dict(cu=None), dict(tokens=None), dict(par=None),
                dict(seen=None), dict(ids=None), dict(bias=None), dict(n_bias=-1), dict(n_masks=-1),
-               dict(mask=None), dict(rows=None, n_masks=3), dict(V=0), dict(n=-1), dict(n_seq=-1),
+               dict(mask=None), dict(mask=None, rows=None), dict(rows=None, n_masks=3), dict(V=0), dict(n=-1), dict(n_seq=-1),
                dict(row=999), dict(out_row=999), dict(flags=3), dict(flags=4),
                dict(x=ctypes.c_void_p(257)), dict(out=ctypes.c_void_p((1 << 40) + 2)),
                dict(x=ctypes.c_void_p(257), flags=1)):
