@@ -61,7 +61,7 @@ int ts_version(void);
 
 /* Limit of one bounded device-side wait, in SM clock cycles, for kernels
  * launched after this call (from any thread): the verification kernel of (1)
- * and the chunk kernel of (6) give up a wait on another warp's or the copy engine's progress after
+ * and the chunk kernel of (6) and (7) give up a wait on another warp's or the copy engine's progress after
  * `cycles` clocks, write TS_ERR_TIMEOUT into `status`, wait for their own
  * copies and tensor-core work in flight (with the default limit), release
  * their tensor memory and return; that call's outputs are then undefined.

@@ -704,6 +704,14 @@ def _alloc(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _alloc_like(t, dtype, stream):
+    """_alloc of t's shape, dense (half of torch.empty's host time)."""
+    if stream is None:
+        return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
+
+
 def _paged_call(fn, dev, stream, outputs, args):
     """One library call with the tensors' device current.  `outputs`: what the binding
     allocated for the caller, who may read it on the current stream (after waiting for
@@ -808,7 +816,7 @@ def _attend(fn, q, pools, o, lse, want_lse, nbytes, workspace, status, stream, h
     n, Hq, d, dt, dev, flags = pools
     outputs = []
     if o is None:
-        o = _alloc((n, Hq, d), dt, q.device, stream)
+        o = _alloc_like(q, dt, stream)
         out = o.data_ptr()
         outputs.append(o)
     else:
@@ -976,12 +984,12 @@ def ts_paged_kv_commit(k_pages, v_pages, cu_q, seq_lens, page_table, path, n_pat
     likewise.  table = commit_pointer_table(k_pages, v_pages), bounds_table =
     commit_pointer_table(key_min, key_max): make them once and reuse them while
     the pools live.  Returns the new lengths [n_seq] int32."""
-    if len(k_pages) == 0:
+    first = k_pages if isinstance(k_pages, torch.Tensor) else k_pages[0] if len(k_pages) else None
+    if first is None or first.shape[0] == 0:
         raise ValueError("at least one layer is needed")
-    first = k_pages[0] if not isinstance(k_pages, torch.Tensor) else k_pages
     if not isinstance(first, torch.Tensor) or not first.is_cuda:
         raise TypeError("k_pages must be CUDA tensors")
-    dt, dev, pool = first.dtype, first.get_device(), tuple(first.shape[-4:])
+    dt, dev, pool = first.dtype, first.get_device(), first.shape[-4:]
     if dt not in _PAGED_DTYPES:
         raise TypeError(f"k_pages must be {_PAGED_DTYPES}, got {dt}")
     if len(pool) != 4:
@@ -992,16 +1000,14 @@ def ts_paged_kv_commit(k_pages, v_pages, cu_q, seq_lens, page_table, path, n_pat
         raise ValueError("k_pages and v_pages must have one entry per layer")
     n_seq, max_pages, cu, lens, pt = _paged_batch(cu_q, seq_lens, page_table, dev)
     i32 = torch.int32
-    if path.dim() != 2:
-        raise ValueError(f"path has shape {tuple(path.shape)}, expected (n_seq, T)")
-    T = path.shape[1]
-    if (key_min is None) != (key_max is None):
-        raise ValueError("key_min and key_max go together")
-    mn = mx = None
+    T = path.shape[-1]
     if table is None:
         table = commit_pointer_table(k_pages, v_pages)
     at = _need(table, torch.int64, (2, n_layers), dev, "table")
-    if key_min is not None:
+    mn = mx = st = None
+    if key_min is not None or key_max is not None:
+        if key_min is None or key_max is None:
+            raise ValueError("key_min and key_max go together")
         bounds = (n_pages, Hkv, d)
         if _layers(key_min, "key_min", dt, bounds, dev) != n_layers or \
                 _layers(key_max, "key_max", dt, bounds, dev) != n_layers:
@@ -1012,11 +1018,12 @@ def ts_paged_kv_commit(k_pages, v_pages, cu_q, seq_lens, page_table, path, n_pat
         mx = mn + 8 * n_layers
     outputs = ()
     if new_lens is None:
-        new_lens = _alloc((n_seq,), i32, first.device, stream)
+        new_lens = _alloc_like(seq_lens, i32, stream)
         new, outputs = new_lens.data_ptr(), (new_lens,)
     else:
         new = _need(new_lens, i32, (n_seq,), dev, "new_lens")
-    st = None if status is None else _need(status, i32, status.shape, dev, "status")
+    if status is not None:
+        st = _need(status, i32, status.shape, dev, "status")
     _paged_call(lib().ts_paged_kv_commit, dev, stream, outputs, (
         n_layers, at, at + 8 * n_layers, Hkv, d, cu, lens, n_seq, pt, max_pages, ps, n_pages,
         _need(path, i32, (n_seq, T), dev, "path"), T, _need(n_path, i32, (n_seq,), dev, "n_path"),
@@ -1051,6 +1058,14 @@ def ts_token_counts(tokens, lens, V, seen, counts=None, reset=False, prompt=Fals
         (TS_COUNTS_RESET if reset else 0) | (TS_COUNTS_PROMPT if prompt else 0), st))
 
 
+def _row_stride(t, n, V, name):
+    """Elements between the rows of a [n, V] tensor whose rows are dense."""
+    row, one = t.stride()
+    if (one != 1 and V > 1) or (row < V and n > 1):
+        raise ValueError(f"{name}: a row's values must be dense")
+    return row if n > 1 else V
+
+
 def ts_logits_process(logits, cu_q, seen=None, counts=None, repetition=None, frequency=None,
                       presence=None, tree_tokens=None, parents=None, bias_ids=None, bias=None,
                       mask=None, mask_rows=None, masked_value=float("-inf"), out=None, status=None,
@@ -1071,45 +1086,51 @@ def ts_logits_process(logits, cu_q, seen=None, counts=None, repetition=None, fre
         raise ValueError(f"logits has shape {tuple(logits.shape)}, expected (n, V)")
     n, V = shape = logits.shape
     dev, i32, f32 = logits.get_device(), torch.int32, torch.float32
-
-    def rows(t, name):
-        row, one = t.stride()
-        if (one != 1 and V > 1) or (row < V and n > 1):
-            raise ValueError(f"{name}: a row's values must be dense")
-        return row if n > 1 else V
-
-    stride = rows(logits, "logits")
+    stride = _row_stride(logits, n, V, "logits")
     if not isinstance(cu_q, torch.Tensor) or cu_q.dim() != 1 or cu_q.shape[0] < 1:
         raise ValueError("cu_q must be a tensor [n_seq + 1]")
     n_seq, words = cu_q.shape[0] - 1, (V + 31) // 32
-    if (bias_ids is None) != (bias is None):
-        raise ValueError("bias_ids and bias go together")
-    n_bias = 0
-    if bias_ids is not None:
+    per_row, per_seq = (n,), (n_seq,)
+    tok = par = cnt = sn = rep = frq = prs = ids = bv = mk = rows = st = None
+    n_bias = n_masks = 0
+    if tree_tokens is not None:
+        tok = _need(tree_tokens, i32, per_row, dev, "tree_tokens")
+    if parents is not None:
+        par = _need(parents, i32, per_row, dev, "parents")
+    if counts is not None:
+        cnt = _need(counts, i32, (n_seq, V), dev, "counts")
+    if seen is not None:
+        sn = _need(seen, i32, (n_seq, words), dev, "seen")
+    if repetition is not None:
+        rep = _need(repetition, f32, per_seq, dev, "repetition")
+    if frequency is not None:
+        frq = _need(frequency, f32, per_seq, dev, "frequency")
+    if presence is not None:
+        prs = _need(presence, f32, per_seq, dev, "presence")
+    if bias_ids is not None or bias is not None:
+        if bias_ids is None or bias is None:
+            raise ValueError("bias_ids and bias go together")
         n_bias = bias_ids.shape[-1]
-    n_masks = 0
+        ids = _need(bias_ids, i32, (n_seq, n_bias), dev, "bias_ids")
+        bv = _need(bias, f32, (n_seq, n_bias), dev, "bias")
     if mask is not None:
         n_masks = mask.shape[0]
+        mk = _need(mask, i32, (n_masks, words), dev, "mask")
+    if mask_rows is not None:
+        rows = _need(mask_rows, i32, per_row, dev, "mask_rows")
+    if status is not None:
+        st = _need(status, i32, status.shape, dev, "status")
     outputs = ()
     if out is None:
-        out = _alloc(shape, f32, logits.device, stream)
+        out = _alloc_like(logits, f32, stream)
         outputs, out_stride = (out,), V
     else:
         if not isinstance(out, torch.Tensor) or out.dtype is not f32 or out.shape != shape or \
                 out.get_device() != dev:
             raise ValueError(f"out must be a float32 tensor {tuple(shape)} on cuda:{dev}")
-        out_stride = rows(out, "out")
-    st = None if status is None else _need(status, i32, status.shape, dev, "status")
+        out_stride = _row_stride(out, n, V, "out")
     _paged_call(lib().ts_logits_process, dev, stream, outputs, (
-        logits.data_ptr(), stride, n, V, _need(cu_q, i32, (n_seq + 1,), dev, "cu_q"), n_seq,
-        _need(tree_tokens, i32, (n,), dev, "tree_tokens"), _need(parents, i32, (n,), dev, "parents"),
-        _need(counts, i32, (n_seq, V), dev, "counts"), _need(seen, i32, (n_seq, words), dev, "seen"),
-        _need(repetition, f32, (n_seq,), dev, "repetition"),
-        _need(frequency, f32, (n_seq,), dev, "frequency"),
-        _need(presence, f32, (n_seq,), dev, "presence"),
-        _need(bias_ids, i32, (n_seq, n_bias), dev, "bias_ids"),
-        _need(bias, f32, (n_seq, n_bias), dev, "bias"), n_bias,
-        _need(mask, i32, (n_masks, words), dev, "mask"), n_masks,
-        _need(mask_rows, i32, (n,), dev, "mask_rows"), masked_value, out.data_ptr(), out_stride,
-        kind, st))
+        logits.data_ptr(), stride, n, V, _need(cu_q, i32, (n_seq + 1,), dev, "cu_q"), n_seq, tok,
+        par, cnt, sn, rep, frq, prs, ids, bv, n_bias, mk, n_masks, rows, masked_value,
+        out.data_ptr(), out_stride, kind, st))
     return out
