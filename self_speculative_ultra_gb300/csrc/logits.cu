@@ -22,21 +22,44 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kEach = 16;              // values of a thread
 constexpr int kSlice = kThreads * kEach;   // values of a block
-constexpr int kGroup = 4;              // neighbouring values of a thread, in the vector form
 constexpr int kMostRun = 16, kBlocksPerSm = 6;
 constexpr int kAddThreads = 256;
 
-// Values of one or four neighbours in fp32.
-__device__ __forceinline__ float widen(float x) { return x; }
-__device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float widen(__half x) { return __half2float(x); }
-template <typename T>
-__device__ __forceinline__ float4 widen4(const float4& x) { return x; }
-template <typename T>
-__device__ __forceinline__ float4 widen4(const uint2& x) {
-  const float2 a = Pair<T>::unpack(x.x), b = Pair<T>::unpack(x.y);
-  return make_float4(a.x, a.y, b.x, b.y);
+// kG neighbouring values as they lie in memory, and in fp32.
+template <int kBytes>
+struct RawOf;
+template <>
+struct RawOf<2> { using type = unsigned short; };
+template <>
+struct RawOf<4> { using type = uint32_t; };
+template <>
+struct RawOf<8> { using type = uint2; };
+template <>
+struct RawOf<16> { using type = uint4; };
+template <typename T, int kG, typename Raw>
+__device__ __forceinline__ void widen(const Raw& raw, float* x) {
+  if constexpr (sizeof(T) == 4) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw);
+#pragma unroll
+    for (int i = 0; i < kG; ++i) x[i] = __uint_as_float(w[i]);
+  } else if constexpr (kG == 1) {
+    x[0] = Pair<T>::unpack(raw).x;
+  } else {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw);
+#pragma unroll
+    for (int i = 0; i < kG / 2; ++i) {
+      const float2 y = Pair<T>::unpack(w[i]);
+      x[2 * i] = y.x;
+      x[2 * i + 1] = y.y;
+    }
+  }
 }
+template <int kG>
+struct FloatsOf { using type = float4; };
+template <>
+struct FloatsOf<2> { using type = float2; };
+template <>
+struct FloatsOf<1> { using type = float; };
 
 // The sequence whose rows hold `row` (-1: none), searched by a whole warp in 32
 // steps at once: one round of loads up to 32 sequences, two up to a thousand.
@@ -77,8 +100,8 @@ __device__ __forceinline__ float penalised(float x, float inv, float rep, float 
 // value goes through the penalties' arithmetic and is selected by its bit: the
 // tokens met lie anywhere, so branches around single ones only diverge.
 // Memory bound: a value is read and written once, and a mask's bit a row.  1024
-// rows of 128256 bf16 values under masks, biases and drafted paths: 141 us, 5.7
-// TB/s (0.84 of a copy); 64 fp32 rows of 151936: 18 us; four rows of 32000: 2.7.
+// rows of 128256 bf16 values under masks, biases and drafted paths: 143 us, 5.6
+// TB/s (0.83 of a copy); 64 fp32 rows of 151936: 17 us; four rows of 32000: 2.7.
 // What a row costs besides its values (addresses, masks, the path) is shared by a
 // thread's 16, what a sequence costs by up to 16 rows: with 8 values a thread 163
 // us, with 32 152, in blocks of 256 threads (three a SM) 153, with 8 rows 157.
@@ -86,12 +109,18 @@ struct State {
   float less[kSlice];                      // what a token's count takes off
   uint32_t bias[kSlice];                   // a token's bias; its place in the list + 1 before
   unsigned long long path[kTreeNodes];     // nodes on each node's path
+  unsigned long long same[kTreeNodes];     // nodes with the same token
   unsigned long long here;                 // nodes whose token is in the slice
   int token[kTreeNodes];                   // drafted tokens, from the slice's first
+  int before[kTreeNodes];                  // how often they were generated before
+  float saved[kTreeNodes];                 // `less` of a drafted token while a row counts it
 };
 
-template <typename T, bool kVec>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+// kG: neighbouring values of a thread that its rows allow to go together (4, 2 or 1;
+// single values want 91 registers, and in the 80 of six blocks a SM take 434 us for
+// 166).
+template <typename T, int kG>
+__global__ void __launch_bounds__(kThreads, kG == 1 ? 5 : kBlocksPerSm)
 logits_kernel(const LogitsArgs a, int n_slices, int run, int32_t* status) {
   extern __shared__ __align__(16) uint8_t smem[];
   State& st = *reinterpret_cast<State*>(smem);
@@ -103,43 +132,36 @@ logits_kernel(const LogitsArgs a, int n_slices, int run, int32_t* status) {
   griddep_launch_dependents();
   // value e of this thread: its token, from the slice's first
   auto slot = [&](int e) {
-    return kVec ? (e / kGroup * kThreads + tid) * kGroup + e % kGroup : e * kThreads + tid;
+    return (e / kG * kThreads + tid) * kG + e % kG;
   };
   uint32_t valid = 0;                      // values inside the slice
 #pragma unroll
   for (int e = 0; e < kEach; ++e) valid |= (uint32_t)(v0 + slot(e) < v1) << e;
   // A row of bits: a warp's tokens take kEach words, one a lane; then each thread
   // picks the bits of its own.
-  const int my_word = kVec ? (lane >> 2) * (kThreads / 8) + warp * 4 + (lane & 3)
-                           : lane * (kThreads / 32) + warp;
+  const int my_word = lane / kG * (kThreads * kG / 32) + warp * kG + lane % kG;
   const bool has_word = lane < kEach && (v0 >> 5) + my_word < words;
   auto ask_bits = [&](const int32_t* w) -> uint32_t {
     return has_word ? (uint32_t)w[(v0 >> 5) + my_word] : 0u;
   };
+  constexpr uint32_t kBits = (1u << kG) - 1u;
   auto own_bits = [&](uint32_t w) -> uint32_t {
     uint32_t r = 0;
 #pragma unroll
-    for (int e = 0; e < kEach; e += kVec ? kGroup : 1) {
-      const uint32_t x = __shfl_sync(0xffffffffu, w, kVec ? e + (lane >> 3) : e);
-      r |= (kVec ? x >> (lane & 7) * 4 & 15u : x >> lane & 1u) << e;
+    for (int e = 0; e < kEach; e += kG) {
+      const uint32_t x = __shfl_sync(0xffffffffu, w, e + lane * kG / 32);
+      r |= (x >> lane * kG % 32 & kBits) << e;
     }
     return r;
   };
-  using Raw = std::conditional_t<sizeof(T) == 4, float4, uint2>;
-  Raw raw[kEach / kGroup];                 // the next row's values; the scalar form holds them in order
-  float next[kVec ? 1 : kEach];
+  using Raw = typename RawOf<kG * sizeof(T)>::type;
+  using Floats = typename FloatsOf<kG>::type;
+  Raw raw[kEach / kG];                     // the next row's values
   auto ask = [&](int row) {
     const T* in = static_cast<const T*>(a.logits) + row * a.row_stride + v0;
-    if constexpr (kVec) {
 #pragma unroll
-      for (int g = 0; g < kEach / kGroup; ++g)
-        if (valid >> g * kGroup & 1u)
-          raw[g] = __ldcs(reinterpret_cast<const Raw*>(in + slot(g * kGroup)));
-    } else {
-#pragma unroll
-      for (int e = 0; e < kEach; ++e)
-        if (valid >> e & 1u) next[e] = widen(in[slot(e)]);
-    }
+    for (int e = 0; e < kEach; e += kG)
+      if (valid >> e & 1u) raw[e / kG] = __ldcs(reinterpret_cast<const Raw*>(in + slot(e)));
   };
   auto mask_row = [&](int row) -> int {
     if ((!a.mask && !a.mask_rows) || row >= row1) return -1;
@@ -160,7 +182,6 @@ logits_kernel(const LogitsArgs a, int n_slices, int run, int32_t* status) {
       if (a0 < 0 || a1 < a0 || a1 > a.n) set_status(status, TS_ERR_INVALID_ARG);
     }
   int q0 = 0, q1 = row0;                   // the rows of the sequence at hand
-  const int32_t* counts = nullptr;         // its counts in the slice
   uint32_t met = 0, biased = 0;            // its bits of this thread's tokens
   float rep = 1.f, inv = 1.f, freq = 0.f, pres = 0.f;
   bool tree = false;
@@ -193,47 +214,69 @@ logits_kernel(const LogitsArgs a, int n_slices, int run, int32_t* status) {
           if (id >= v0 && id < v1) atomicMax(&st.bias[id - v0], (uint32_t)i + 1u);
         }
       }
-      if (a.tokens && warp == 0) {
+      if (a.tokens && warp < 3) {
+        // three warps gather a part each of what the paths need
         const int nodes = min(min(q1, a.n) - q0, kTreeNodes);
-        if (min(q1, a.n) - q0 > kTreeNodes && lane == 0) set_status(status, TS_ERR_INVALID_ARG);
-        int id[2];
+        if (warp == 0) {
+          if (min(q1, a.n) - q0 > kTreeNodes && lane == 0) set_status(status, TS_ERR_INVALID_ARG);
+          TreeBits bits;
+          bits.build(a.parents + q0, nodes, lane, status);
+          st.path[lane] = bits.of(lane);
+          st.path[lane + 32] = bits.of(lane + 32);
+        } else {
+          int id[2];
+          bool here[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int at = lane + 32 * i;
-          id[i] = at > 0 && at < nodes ? a.tokens[q0 + at] : v0 - 1;   // the root is in the history
-          if (at > 0 && at < nodes && (id[i] < 0 || id[i] >= a.V)) set_status(status, TS_ERR_INVALID_ARG);
+          for (int i = 0; i < 2; ++i) {
+            const int at = lane + 32 * i;
+            const bool one = at > 0 && at < nodes;           // the root is in the history
+            id[i] = one ? a.tokens[q0 + at] : v0 - 1;
+            here[i] = id[i] >= v0 && id[i] < v1;
+            if (one && (id[i] < 0 || id[i] >= a.V)) set_status(status, TS_ERR_INVALID_ARG);
+          }
+          if (warp == 1) {
+            const unsigned lo = __ballot_sync(0xffffffffu, here[0]);
+            const unsigned hi = __ballot_sync(0xffffffffu, here[1]);
+            const unsigned long long all = (unsigned long long)hi << 32 | lo;
+            unsigned long long same[2] = {0, 0};
+            for (unsigned long long left = all; left; left &= left - 1) {
+              const int i = __ffsll(left) - 1;
+              const int x = __shfl_sync(0xffffffffu, i < 32 ? id[0] : id[1], i & 31);
+              if (id[0] == x) same[0] |= 1ull << i;
+              if (id[1] == x) same[1] |= 1ull << i;
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              st.token[lane + 32 * i] = id[i] - v0;
+              st.same[lane + 32 * i] = same[i];
+            }
+            if (lane == 0) st.here = all;
+          } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const bool known =
+                  here[i] && a.counts &&
+                  ((uint32_t)a.seen[(int64_t)s * words + (id[i] >> 5)] >> (id[i] & 31) & 1u);
+              st.before[lane + 32 * i] = known ? a.counts[(int64_t)s * a.V + id[i]] : 0;
+            }
+          }
         }
-        TreeBits bits;
-        bits.build(a.parents + q0, nodes, lane, status);
-        st.path[lane] = bits.of(lane);
-        st.path[lane + 32] = bits.of(lane + 32);
-        st.token[lane] = id[0] - v0;
-        st.token[lane + 32] = id[1] - v0;
-        const unsigned lo = __ballot_sync(0xffffffffu, id[0] >= v0 && id[0] < v1);
-        const unsigned hi = __ballot_sync(0xffffffffu, id[1] >= v0 && id[1] < v1);
-        if (lane == 0) st.here = (unsigned long long)hi << 32 | lo;
       }
       // this thread's tokens: their counts, all asked for at once
       met = own_bits(word) & valid;
+      const int32_t* counts = a.counts ? a.counts + (int64_t)s * a.V + v0 : nullptr;
       int c[kEach];
 #pragma unroll
       for (int e = 0; e < kEach; ++e) c[e] = 0;
-      counts = a.counts ? a.counts + (int64_t)s * a.V + v0 : nullptr;
       if (counts) {
 #pragma unroll
-        for (int e = 0; e < kEach; e += kVec ? kGroup : 1) {
-          if constexpr (kVec) {
-            if (met >> e & 15u) {
-              const int4 y = *reinterpret_cast<const int4*>(counts + slot(e));
-              c[e] = y.x;
-              c[e + 1] = y.y;
-              c[e + 2] = y.z;
-              c[e + 3] = y.w;
-            }
-          } else {
-            if (met >> e & 1u) c[e] = counts[slot(e)];
+        for (int e = 0; e < kEach; e += kG)
+          if (met >> e & kBits) {
+            const Floats y = *reinterpret_cast<const Floats*>(counts + slot(e));   // as bits
+            const int* w = reinterpret_cast<const int*>(&y);
+#pragma unroll
+            for (int i = 0; i < kG; ++i) c[e + i] = w[i];
           }
-        }
       }
 #pragma unroll
       for (int e = 0; e < kEach; ++e) st.less[slot(e)] = taken(freq, pres, c[e]);
@@ -254,19 +297,8 @@ logits_kernel(const LogitsArgs a, int n_slices, int run, int32_t* status) {
     }
     // ------------------------------------------------------ one row
     float x[kEach];
-    if constexpr (kVec) {
 #pragma unroll
-      for (int g = 0; g < kEach / kGroup; ++g) {
-        const float4 y = widen4<T>(raw[g]);
-        x[4 * g] = y.x;
-        x[4 * g + 1] = y.y;
-        x[4 * g + 2] = y.z;
-        x[4 * g + 3] = y.w;
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < kEach; ++e) x[e] = next[e];
-    }
+    for (int e = 0; e < kEach; e += kG) widen<T, kG>(raw[e / kG], x + e);
     const uint32_t may = own_bits(may_next);
     if (row + 1 < row1) {
       ask(row + 1);
@@ -278,63 +310,48 @@ logits_kernel(const LogitsArgs a, int n_slices, int run, int32_t* status) {
       for (int e = 0; e < kEach; ++e)
         if (biased >> e & 1u) x[e] += __uint_as_float(st.bias[slot(e)]);
     }
+    // Tokens drafted on this row's path: their owners count them in for the row.
     uint32_t do_now = met;
-    // nodes on this row's path with a token here: their owners take them by themselves
-    const unsigned long long drafted =
-        tree && row - q0 < kTreeNodes ? st.path[row - q0] & st.here : 0ull;
-    for (unsigned long long left = drafted; left; left &= left - 1) {
-      const int at = __ffsll(left) - 1, t = st.token[at];
-      if ((kVec ? t / kGroup : t) % kThreads != tid) continue;
-      const int mine = kVec ? t / (kGroup * kThreads) * kGroup + t % kGroup : t / kThreads;
-      int times = 0;
-      bool first = true;
-      for (unsigned long long all = drafted; all; all &= all - 1) {
-        const int i = __ffsll(all) - 1;
-        if (st.token[i] != t) continue;
-        ++times;
-        first &= i >= at;
+    unsigned long long changed = 0;
+    if (tree) {
+      const unsigned long long drafted = row - q0 < kTreeNodes ? st.path[row - q0] & st.here : 0ull;
+      for (unsigned long long left = drafted; left; left &= left - 1) {
+        const int at = __ffsll(left) - 1, t = st.token[at];
+        if (t / kG % kThreads != tid) continue;
+        const uint32_t bit = 1u << (t / (kG * kThreads) * kG + t % kG);
+        const unsigned long long same = drafted & st.same[at];
+        if (same & ((1ull << at) - 1)) continue;             // an earlier node took it
+        st.saved[at] = st.less[t];
+        st.less[t] = taken(freq, pres, st.before[at] + __popcll(same));
+        changed |= 1ull << at;
+        do_now |= bit;
       }
-      if (!first) continue;
-      if (counts && (met >> mine & 1u)) times += counts[t];
-#pragma unroll
-      for (int e = 0; e < kEach; ++e)
-        if (e == mine) x[e] = penalised(x[e], inv, rep, taken(freq, pres, times));
-      do_now &= ~(1u << mine);
     }
 #pragma unroll
-    for (int g = 0; g < kEach; g += kGroup) {
+    for (int g = 0; g < kEach; g += 4) {
       if (!__any_sync(0xffffffffu, do_now >> g & 15u)) continue;
-      float less[kGroup];
-      if constexpr (kVec) {
-        const float4 y = *reinterpret_cast<const float4*>(&st.less[slot(g)]);
-        less[0] = y.x;
-        less[1] = y.y;
-        less[2] = y.z;
-        less[3] = y.w;
-      } else {
+      float less[4];
 #pragma unroll
-        for (int e = g; e < g + kGroup; ++e) less[e - g] = st.less[slot(e)];
-      }
+      for (int i = 0; i < 4; i += kG)
+        *reinterpret_cast<Floats*>(less + i) = *reinterpret_cast<const Floats*>(&st.less[slot(g + i)]);
 #pragma unroll
-      for (int e = g; e < g + kGroup; ++e) {
+      for (int e = g; e < g + 4; ++e) {
         const float y = penalised(x[e], inv, rep, less[e - g]);
         x[e] = do_now >> e & 1u ? y : x[e];
       }
+    }
+    for (; changed; changed &= changed - 1) {
+      const int at = __ffsll(changed) - 1;
+      st.less[st.token[at]] = st.saved[at];
     }
     float* out = a.out + row * a.out_stride + v0;
 #pragma unroll
     for (int e = 0; e < kEach; ++e)
       if (!(may >> e & 1u)) x[e] = a.masked_value;
-    if constexpr (kVec) {
 #pragma unroll
-      for (int e = 0; e < kEach; e += kGroup)
-        if (valid >> e & 1u)
-          *reinterpret_cast<float4*>(out + slot(e)) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < kEach; ++e)
-        if (valid >> e & 1u) out[slot(e)] = x[e];
-    }
+    for (int e = 0; e < kEach; e += kG)
+      if (valid >> e & 1u)
+        *reinterpret_cast<Floats*>(out + slot(e)) = *reinterpret_cast<const Floats*>(x + e);
   }
 }
 
@@ -448,15 +465,19 @@ static int go_logits(const LogitsArgs& a, int32_t* status, cudaStream_t st) {
   // rows a block takes in a run: one as long as the SMs are not full
   const int64_t blocks = (int64_t)a.n * n_slices;
   const int run = (int)imax64(1, imin64(kMostRun, blocks / (kGb300Sms * kBlocksPerSm)));
-  pdl_config(&cfg, attr, dim3((unsigned)((a.n + run - 1) / run * n_slices)), dim3(kThreads),
-             sizeof(State), st);
-  // four values at once where every row starts on a boundary of four
-  auto fits = [](const void* p, int64_t stride, size_t size) {
-    return reinterpret_cast<uintptr_t>(p) % (kGroup * size) == 0 && stride % kGroup == 0;
+  // four or two values at once where every row starts on a boundary of as many (1024
+  // bf16 rows of 128256, 128254 and 128255 values: 143, 147 and 164 us)
+  auto fits = [&](int g) {
+    auto one = [&](const void* p, int64_t stride, size_t size) {
+      return reinterpret_cast<uintptr_t>(p) % (g * size) == 0 && stride % g == 0;
+    };
+    return a.V % g == 0 && one(a.logits, a.n > 1 ? a.row_stride : 0, sizeof(T)) &&
+           one(a.out, a.n > 1 ? a.out_stride : 0, 4) && one(a.counts, 0, 4);
   };
-  const bool vec = a.V % kGroup == 0 && fits(a.logits, a.n > 1 ? a.row_stride : 0, sizeof(T)) &&
-                   fits(a.out, a.n > 1 ? a.out_stride : 0, 4) && fits(a.counts, 0, 4);
-  auto kern = vec ? logits_kernel<T, true> : logits_kernel<T, false>;
+  const int g = fits(4) ? 4 : fits(2) ? 2 : 1;
+  pdl_config(&cfg, attr, dim3((unsigned)((a.n + run - 1) / run * n_slices)),
+             dim3(kThreads), sizeof(State), st);
+  auto kern = g == 4 ? logits_kernel<T, 4> : g == 2 ? logits_kernel<T, 2> : logits_kernel<T, 1>;
   cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(State));
   cudaLaunchKernelEx(&cfg, kern, a, n_slices, run, status);
   return launch_status("logits_kernel");
