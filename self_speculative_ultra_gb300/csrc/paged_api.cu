@@ -71,14 +71,23 @@ int64_t bound_kv(int max_pages, int page_size, int64_t max_kv) {
 // against 26.9; 6 streams of 94 tokens and at most 491 rows (24 blocks, 4 a SM)
 // 7.6 against 19.1, of 154 tokens and 1000 rows (39 blocks, 12 a SM) 29.1 against
 // 27.0; 32 rows of 8 KV heads over 100K rows (84 a SM) 127 against 83.
-// Draft trees of one tile need no plan (~11 us in all): there any number of blocks
-// but one at 5 trips a SM.  4 streams of 8 nodes over 1500 rows, 32/8 heads (5.1 a
-// SM) 14.1 against 16.2, 12 streams of 40 nodes over 300, 8/8 heads (5.7) 21.6
-// against 16.7, one of 40 nodes over 1500, 32/8 heads (6.3) 19.7 against 15.3.
+// Draft trees of one tile need no plan (10 to 12 us in all).  There more blocks than
+// one take the row kernel only where every one gets an SM of its own, at 6 trips a
+// SM.  4 streams of 13 nodes over 250 rows, 32/8 heads (128 blocks) 9.4 against 11.9,
+// 8 streams (256) 19.9 against 13.7; 14 of 8 nodes over 800, 16/4 heads (5.2 trips a
+// SM) 14.9 against 16.8, one of 40 nodes over 1500, 32/8 heads (6.3) 19.7 against 15.3.
+// Nor do up to four blocks over a long cache take it, whose join walks a block's
+// pieces one after the other: 2 nodes of 4/1 heads over 3000 rows 9.5 against 13.5,
+// over 12K 20.9 against 16.0, over 48K 42.8 against 17.4; 4 over 12K 18.4 against
+// 16.8, 8 16.0 against 18.8.
 bool few_rows(int n_seq, int max_q, int Hq, int Hkv, int64_t kv, bool tree) {
   const int64_t blocks = ((int64_t)max_q * (Hq / Hkv) + 15) / 16;
   const int64_t trips = (int64_t)n_seq * Hkv * blocks * ((kv + 127) / 128);
-  if (tree && max_q * (Hq / Hkv) <= kTcRows) return blocks <= 1 || trips <= 5 * kGb300Sms;
+  if (tree && max_q * (Hq / Hkv) <= kTcRows) {
+    const int64_t units = (int64_t)n_seq * Hkv * blocks;
+    if (units <= 4 && kv > 64 * 128) return false;
+    return blocks <= 1 || (units <= kGb300Sms && trips <= 6 * kGb300Sms);
+  }
   return blocks <= 1 || trips <= 8 * kGb300Sms || (blocks <= 4 && trips <= 13 * kGb300Sms);
 }
 
