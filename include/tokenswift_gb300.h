@@ -742,10 +742,11 @@ int ts_token_counts(const int32_t* tokens, int stride, const int32_t* lens, int 
  *
  * logits   n rows of V values, row_stride elements apart: fp32, or bf16, fp16
  *          with a flag.  out: n rows of V fp32 values, out_stride apart; may be
- *          logits itself where both are fp32 of one stride, else they must not
- *          overlap.
+ *          logits itself where both are fp32 of one stride, else what lies from
+ *          the first value to the last must not overlap.
  * cu_q     [n_seq + 1] int32: sequence s owns rows [cu_q[s], cu_q[s+1]), as in
- *          (6); rows behind the last are left as they were.
+ *          (6); rows of none are left as they were, and what the other arrays
+ *          hold for them is not looked at.
  * tree_tokens, parents  [n] int32, or both NULL: the rows are the nodes of draft
  *          trees (at most 64 a sequence, parents as in (7)), and the path of a
  *          node is its ancestors and itself without the root, whose token is

@@ -100,8 +100,8 @@ __device__ __forceinline__ float penalised(float x, float inv, float rep, float 
 // value goes through the penalties' arithmetic and is selected by its bit: the
 // tokens met lie anywhere, so branches around single ones only diverge.
 // Memory bound: a value is read and written once, and a mask's bit a row.  1024
-// rows of 128256 bf16 values under masks, biases and drafted paths: 143 us, 5.6
-// TB/s (0.83 of a copy); 64 fp32 rows of 151936: 17 us; four rows of 32000: 2.7.
+// rows of 128256 bf16 values under masks, biases and drafted paths: 135 us, 5.9
+// TB/s (0.88 of a copy); 64 fp32 rows of 151936: 17 us; four rows of 32000: 2.7.
 // What a row costs besides its values (addresses, masks, the path) is shared by a
 // thread's 16, what a sequence costs by up to 16 rows: with 8 values a thread 163
 // us, with 32 152, in blocks of 256 threads (three a SM) 153, with 8 rows 157.
@@ -163,8 +163,10 @@ logits_kernel(const LogitsArgs a, int n_slices, int run, int32_t* status) {
     for (int e = 0; e < kEach; e += kG)
       if (valid >> e & 1u) raw[e / kG] = __ldcs(reinterpret_cast<const Raw*>(in + slot(e)));
   };
+  // rows of no sequence are left as they are, and their masks are not looked at
+  const int first = a.cu_q[0], end = min(row1, a.cu_q[a.n_seq]);
   auto mask_row = [&](int row) -> int {
-    if ((!a.mask && !a.mask_rows) || row >= row1) return -1;
+    if ((!a.mask && !a.mask_rows) || row >= end) return -1;
     const int mr = a.mask_rows ? a.mask_rows[row] : row;
     if (mr >= -1 && mr < a.n_masks) return mr;
     if (v0 == 0 && tid == 0) set_status(status, TS_ERR_INVALID_ARG);
@@ -174,8 +176,8 @@ logits_kernel(const LogitsArgs a, int n_slices, int run, int32_t* status) {
     return mr < 0 ? 0xFFFFFFFFu : ask_bits(a.mask + (int64_t)mr * words);
   };
   ask(row0);
-  int mr = mask_row(row0 + 1);
-  uint32_t may_next = ask_mask(mask_row(row0));
+  int mr = row0 + 1 < first ? -1 : mask_row(row0 + 1);
+  uint32_t may_next = ask_mask(row0 < first ? -1 : mask_row(row0));
   if (blockIdx.x == 0)
     for (int s = tid; s < a.n_seq; s += kThreads) {
       const int a0 = a.cu_q[s], a1 = a.cu_q[s + 1];
@@ -185,11 +187,21 @@ logits_kernel(const LogitsArgs a, int n_slices, int run, int32_t* status) {
   uint32_t met = 0, biased = 0;            // its bits of this thread's tokens
   float rep = 1.f, inv = 1.f, freq = 0.f, pres = 0.f;
   bool tree = false;
-  for (int row = row0; row < row1; ++row) {
+  for (int row = row0; row < end; ++row) {
     if (row >= q1) {
       // ---------------------------------------------------- a sequence begins
       const int s = find_seq(a, row, lane);
-      if (s < 0) return;                   // rows behind the last are left as they are
+      if (s < 0) {
+        // in front of the first sequence (whose offset is read again: in a register
+        // over the loop it is one too many, 153 us for 146 at even vocabularies)
+        const int begin = a.cu_q[0];
+        if (begin <= row || begin >= end) return;
+        ask(begin);
+        may_next = ask_mask(mask_row(begin));
+        mr = mask_row(begin + 1);
+        row = begin - 1;
+        continue;
+      }
       q0 = max(a.cu_q[s], 0);
       q1 = a.cu_q[s + 1];
       rep = a.repetition ? a.repetition[s] : 1.f;
@@ -300,7 +312,7 @@ logits_kernel(const LogitsArgs a, int n_slices, int run, int32_t* status) {
 #pragma unroll
     for (int e = 0; e < kEach; e += kG) widen<T, kG>(raw[e / kG], x + e);
     const uint32_t may = own_bits(may_next);
-    if (row + 1 < row1) {
+    if (row + 1 < end) {
       ask(row + 1);
       may_next = ask_mask(mr);
       mr = mask_row(row + 2);
@@ -466,7 +478,7 @@ static int go_logits(const LogitsArgs& a, int32_t* status, cudaStream_t st) {
   const int64_t blocks = (int64_t)a.n * n_slices;
   const int run = (int)imax64(1, imin64(kMostRun, blocks / (kGb300Sms * kBlocksPerSm)));
   // four or two values at once where every row starts on a boundary of as many (1024
-  // bf16 rows of 128256, 128254 and 128255 values: 143, 147 and 164 us)
+  // bf16 rows of 128256, 128254 and 128255 values: 135, 147 and 163 us)
   auto fits = [&](int g) {
     auto one = [&](const void* p, int64_t stride, size_t size) {
       return reinterpret_cast<uintptr_t>(p) % (g * size) == 0 && stride % g == 0;

@@ -259,6 +259,32 @@ def test_bad_device_data_is_reported(ts, what):
             np.testing.assert_array_equal(out[i].cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("V", [3000, 8192])
+@pytest.mark.parametrize("n_seq,lead", [(3, 1), (3, 2), (400, 1), (400, 399)])
+def test_sequences_of_a_larger_batch(ts, V, n_seq, lead):
+    """The last of a batch's sequences alone: rows in front of the first and behind the
+    last are left as they were, whatever their masks, tokens and parents say."""
+    c = Case([5 if s == 1 else 3 for s in range(n_seq)], V, F32, seed=lead, extra=6, n_bias=3,
+             masks="shared")
+    args = c.args()
+    for name in ("seen", "counts", "repetition", "frequency", "presence", "bias_ids", "bias"):
+        args[name] = args[name][lead:].contiguous()
+    for name, what in (("mask_rows", 99), ("tree_tokens", -3), ("parents", 77)):
+        args[name] = args[name].clone()
+        args[name][:c.cu[lead]] = what
+        args[name][c.cu[-1]:] = what
+    out = torch.full((c.n, V), 55.0, device="cuda")
+    ts.ts_logits_process(c.logits, i32(c.cu[lead:]), out=out, status=c.status, **args)
+    torch.cuda.synchronize()
+    assert int(c.status.item()) == 0
+    assert (out[:c.cu[lead]] == 55.0).all() and (out[c.cu[-1]:] == 55.0).all()
+    got = out.cpu().numpy()
+    for s in sorted({lead, (lead + n_seq) // 2, n_seq - 1}):
+        for i in range(c.q_lens[s]):
+            want, _ = c.row(s, i, True)
+            np.testing.assert_array_equal(got[c.cu[s] + i], want)
+
+
 def test_logits_replay_and_streams(ts):
     c = Case([8, 8], 9000, BF, seed=9, n_bias=6, masks="each")
     args, cu = c.args(), i32(c.cu)
