@@ -685,10 +685,11 @@ int ts_paged_tree_attention(const void* q, const void* k_pages, const void* v_pa
  *          t <= path[s][t] < q_len (path[s][0] is not read), 1 <= n_path[s] <=
  *          min(q_len, path_stride).
  * key_min, key_max  DEVICE arrays of n_layers pointers to the pages' key bounds
- *          [n_pages, Hkv, d], or both NULL.  A page that starts at or behind row
- *          L and holds a committed row gets the bounds of its committed rows;
- *          the page in front is widened by its own.  (Rejected rows so leave
- *          no trace but in the page that holds row L - 1.)
+ *          [n_pages, Hkv, d] (16-byte aligned), or both NULL.  A page that
+ *          starts at or behind row L and holds a committed row gets the bounds
+ *          of its committed rows; the page in front is widened by its own.
+ *          (Rejected rows so leave no trace but in the page that holds row
+ *          L - 1.)
  * new_lens [n_seq] int32 out, or NULL: L + n_path[s], or seq_lens[s] where the
  *          sequence has no new token; not seq_lens itself.
  * A path, page or length out of its range is reported as TS_ERR_INVALID_ARG in

@@ -966,11 +966,16 @@ def _layers(x, name, dt, shape, dev):
     """The number of layers of per-layer tensors of one shape: a list of them, or
     one tensor with the layers in front."""
     if isinstance(x, torch.Tensor):
-        _need(x, dt, (x.shape[0], *shape), dev, name)
-        return x.shape[0]
-    for t in x:
-        _need(t, dt, shape, dev, name)
-    return len(x)
+        at = _need(x, dt, (x.shape[0], *shape), dev, name)
+        n = x.shape[0]
+    else:
+        at = 0
+        for t in x:
+            at |= _need(t, dt, shape, dev, name)
+        n = len(x)
+    if at & 15:                            # the kernel reads the addresses from a table
+        raise ValueError(f"{name}: a layer is not 16-byte aligned")
+    return n
 
 
 def ts_paged_kv_commit(k_pages, v_pages, cu_q, seq_lens, page_table, path, n_path, key_min=None,

@@ -511,6 +511,41 @@ def test_commit_reports_bad_tables(ts):
         assert status_of(b) == 1
 
 
+def test_commit_refuses_layers_that_start_off_a_boundary(ts):
+    """The kernel takes the addresses from a table, where the library cannot see them."""
+    b = pu.Batch([5], [20], 4, 2, 64, 16, BF)
+    k, v = layers_of(b, 1)
+    path, n_path = accepted(b.q_lens)
+    off = torch.zeros(k.numel() + 8, dtype=BF, device="cuda")[4:4 + k.numel()].view(k.shape)
+    mn, mx = k.amin(3), k.amax(3)
+    off_bounds = torch.zeros(mn.numel() + 8, dtype=BF, device="cuda")[1:1 + mn.numel()].view(mn.shape)
+    args = (b.cu_q, b.lens, b.table, path, n_path)
+    for kp, vp, lo, hi in ((off, v, mn, mx), (k, off, mn, mx), ([k[0]], [off[0]], None, None),
+                           (k, v, off_bounds, mx), (k, v, [mn[0]], [off_bounds[0]])):
+        with pytest.raises(ValueError, match="aligned"):
+            ts.ts_paged_kv_commit(kp, vp, *args, key_min=lo, key_max=hi)
+
+
+@pytest.mark.parametrize("Hq,top,kv", [(8, 3, 300), (8, 64, 900), (32, 40, 5000), (64, 64, 5000)])
+def test_sequences_of_a_larger_batch(ts, Hq, top, kv):
+    """The last of a batch's sequences alone: the first offset is not 0."""
+    b = pu.Batch([2, top, 1, top], [kv, kv, kv // 2, kv], Hq, 2, 128, 16, BF, seed=top, extra=3)
+    par = parents_of(b.q_lens, "mixed", extra=3)
+    want = oracle(b, par)
+    for lead in (1, 2):
+        o = torch.full((b.n, b.Hq, b.d), 55.0, dtype=b.dtype, device="cuda")
+        lse = torch.full((b.n, b.Hq), 55.0, dtype=torch.float32, device="cuda")
+        ts.ts_paged_tree_attention(b.q, b.k, b.v, b.cu_q[lead:].contiguous(),
+                                   b.lens[lead:].contiguous(), b.table[lead:].contiguous(), par,
+                                   top, o=o, lse=lse, status=b.status)
+        assert status_of(b) == 0
+        a, e = b.cu[lead], b.cu[-1]
+        for x in (o, lse):
+            assert (x[:a] == 55.0).all() and (x[e:] == 55.0).all()
+        pu.check_attention(o[a:e], lse[a:e], tuple(x[a:e] for x in want), b.dtype, b.d,
+                           p_round=P_ROUND[b.dtype])
+
+
 def test_commit_replays_with_new_paths(ts):
     b = pu.Batch([16, 16], [200, 100], 2, 2, 128, 32, BF, seed=7)
     k, v = layers_of(b, 4)
