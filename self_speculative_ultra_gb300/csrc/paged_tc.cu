@@ -734,9 +734,11 @@ struct LineWalk {
     kv = c0 = 0;
     if (left == 0) return;
     take(b, max_q, G, lane);
-    const uint32_t length = t.length(), in = l.w0 - l.at;
-    kv = in / length;                          // w0 lies in this sequence
-    c0 = in - kv * length;
+    // w0 lies in this sequence (bounded all the same, here and below: lengths that
+    // change under the call must neither leave the pool nor keep the warp)
+    const uint32_t length = max(t.length(), 1), in = l.w0 - l.at;
+    kv = min(in / length, (uint32_t)Hkv - 1u);
+    c0 = min(in - kv * length, length - 1u);
   }
   // n < 0: the stretch is at its end
   __device__ __forceinline__ Item next(const PagedBatch& b, int Hkv, int G, int max_q, int lane) {
@@ -744,7 +746,7 @@ struct LineWalk {
     w.n = -1;
     bool some = false;
     while (!some && left > 0) {
-      const int length = t.length(), c1 = min(c0 + left, length);
+      const int length = max(t.length(), 1), c1 = min(c0 + left, length);
       const int k0 = t.steps_at(c0), k1 = t.steps_at(c1);
       const bool starts = t.steps > 0 ? k0 == 0 : c0 == 0, ends = k1 == t.steps;
       some = k0 < k1 || (t.steps == 0 && starts);              // else between two tiles' steps
@@ -770,7 +772,7 @@ struct LineWalk {
         // (a sequence without tokens has no length; while the stretch goes on there
         // is one with)
         while (left > 0) {
-          ++s;
+          if (++s >= b.n_seq) left = 0;
           take(b, max_q, G, lane);
           if (t.nodes > 0) break;
         }
