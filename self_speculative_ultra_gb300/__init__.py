@@ -1006,8 +1006,10 @@ def ts_paged_kv_commit(k_pages, v_pages, cu_q, seq_lens, page_table, path, n_pat
     n_seq, max_pages, cu, lens, pt = _paged_batch(cu_q, seq_lens, page_table, dev)
     i32 = torch.int32
     T = path.shape[-1]
+    made = []
     if table is None:
         table = commit_pointer_table(k_pages, v_pages)
+        made.append(table)
     at = _need(table, torch.int64, (2, n_layers), dev, "table")
     mn = mx = st = None
     if key_min is not None or key_max is not None:
@@ -1019,6 +1021,7 @@ def ts_paged_kv_commit(k_pages, v_pages, cu_q, seq_lens, page_table, path, n_pat
             raise ValueError("key_min and key_max must have one entry per layer")
         if bounds_table is None:
             bounds_table = commit_pointer_table(key_min, key_max)
+            made.append(bounds_table)
         mn = _need(bounds_table, torch.int64, (2, n_layers), dev, "bounds_table")
         mx = mn + 8 * n_layers
     outputs = ()
@@ -1033,6 +1036,9 @@ def ts_paged_kv_commit(k_pages, v_pages, cu_q, seq_lens, page_table, path, n_pat
         n_layers, at, at + 8 * n_layers, Hkv, d, cu, lens, n_seq, pt, max_pages, ps, n_pages,
         _need(path, i32, (n_seq, T), dev, "path"), T, _need(n_path, i32, (n_seq,), dev, "n_path"),
         mn, mx, new, TS_PAGED_FP16 if dt is torch.float16 else 0, st))
+    if stream is not None:
+        for t in made:                     # from the current stream's memory, read on `stream`
+            t.record_stream(stream)
     return new_lens
 
 

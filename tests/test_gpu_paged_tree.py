@@ -546,6 +546,33 @@ def test_sequences_of_a_larger_batch(ts, Hq, top, kv):
                            p_round=P_ROUND[b.dtype])
 
 
+def test_a_table_made_by_the_call_outlives_it_on_another_stream(ts, monkeypatch):
+    b = pu.Batch([5], [20], 4, 2, 64, 16, BF)
+    k, v = layers_of(b, 3)
+    path, n_path = accepted(b.q_lens)
+    new = torch.zeros(1, dtype=torch.int32, device="cuda")
+    made, make = [], ts.commit_pointer_table
+
+    def note(*a):
+        t = make(*a)
+        made.append(t.data_ptr())
+        return t
+    monkeypatch.setattr(ts, "commit_pointer_table", note)
+    mn, mx = k.amin(3), k.amax(3)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(600_000_000)
+    ts.ts_paged_kv_commit(k, v, b.cu_q, b.lens, b.table, path, n_path, key_min=mn, key_max=mx,
+                          new_lens=new, status=b.status, stream=side)
+    held = [torch.empty(2, 3, dtype=torch.int64, device="cuda") for _ in range(64)]
+    waiting = not side.query()
+    torch.cuda.synchronize()
+    assert waiting and len(made) == 2
+    assert not set(made) & {t.data_ptr() for t in held}
+    assert status_of(b) == 0 and new.tolist() == [15 + int(n_path[0])]
+
+
 def test_commit_replays_with_new_paths(ts):
     b = pu.Batch([16, 16], [200, 100], 2, 2, 128, 32, BF, seed=7)
     k, v = layers_of(b, 4)
