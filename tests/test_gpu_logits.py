@@ -259,6 +259,45 @@ def test_bad_device_data_is_reported(ts, what):
             np.testing.assert_array_equal(out[i].cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("V", [5000, 5001])
+@pytest.mark.parametrize("bad,good", [([0, 6, 10 ** 6], 1), ([0, 6, 3], 1), ([0, 6, -1], 1),
+                                      ([0, 6, 14, 2], 2), ([2, 8, 14, 5, 5, 5], 2)])
+def test_sequences_in_front_of_bad_offsets(ts, V, bad, good):
+    """Sequences in front of an offset out of its range or order keep their rows,
+    masks and penalties."""
+    ns = len(bad) - 1
+    c = Case([3] * ns, V, BF, seed=8, n_bias=4, masks="shared", extra=20 - 3 * ns)
+    check_in_front(ts, c, bad, range(good))
+
+
+@pytest.mark.parametrize("tail", [[2], [9, 6, 6], [-7]])
+def test_blocks_of_rows_in_front_of_bad_offsets(ts, tail):
+    """Blocks of several rows, which begin in front of the last offset or behind it."""
+    c = Case([30] * 14 + [64] * 14 + [5] * len(tail), 4098, F32, seed=9, n_bias=4, masks="shared")
+    assert c.n * 3 // (152 * 6) > 1
+    check_in_front(ts, c, c.cu[:29] + tail, (0, 1, 13, 14, 15, 26, 27), same=True)
+
+
+def check_in_front(ts, c, bad, seqs, same=False):
+    """The rows of `seqs`; same: those are where the case has them, trees and all."""
+    c.cu = bad
+    if not same:
+        par = [0] * c.n
+        for s in seqs:
+            par[bad[s]:bad[s + 1]] = range(-1, bad[s + 1] - bad[s] - 1)
+        c.parents = i32(par)
+    out = torch.full((c.n, c.V), 55.0, device="cuda")
+    ts.ts_logits_process(c.logits, i32(bad), out=out, status=c.status, **c.args())
+    torch.cuda.synchronize()
+    assert int(c.status.item()) == 1
+    assert (out[:bad[0]] == 55.0).all()
+    got = out.cpu().numpy()
+    for s in seqs:
+        for i in range(bad[s + 1] - bad[s]):
+            want, _ = c.row(s, i, True)
+            np.testing.assert_array_equal(got[bad[s] + i], want)
+
+
 @pytest.mark.parametrize("V", [3000, 8192])
 @pytest.mark.parametrize("n_seq,lead", [(3, 1), (3, 2), (400, 1), (400, 399)])
 def test_sequences_of_a_larger_batch(ts, V, n_seq, lead):
