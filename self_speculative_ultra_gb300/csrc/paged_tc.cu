@@ -601,7 +601,7 @@ struct TreeTile {
     return c >= length() ? steps : c <= kLineFixed ? 0 : min((c - kLineFixed) * 8 / eighths, steps);
   }
   __device__ __forceinline__ void set(const PagedBatch& b, int s, int max_q, int G) {
-    nodes = 0;
+    q0 = nodes = see0 = kl = 0;       // behind the batch (all lanes' are shuffled)
     bad = false;
     if (s >= b.n_seq) return;
     const SeqSpan sp = seq_span(b, s);

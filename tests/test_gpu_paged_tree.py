@@ -133,6 +133,18 @@ def test_lines_of_tiles(ts, dtype, d, n, top, kv, Hq, Hkv):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("last", [0, 64])
+@pytest.mark.parametrize("n", [31, 32, 33, 63, 64, 65])
+def test_lines_that_end_at_the_lanes_of_a_warp(ts, d, last, n):
+    """A warp looks 32 streams ahead: batches that end in front of its last lane, with
+    it and behind it, with a stream that has nodes and with one that has none."""
+    q, k = _streams(n, n, 64, 700)
+    q[-1], k[-1] = last, 700
+    b = pu.Batch(q, k, 4, 2, d, 32, BF, seed=n, extra=2)
+    check(ts, b, parents_of(q, "mixed", seed=n, extra=2))
+
+
 @pytest.mark.parametrize("kv", [64 + x for x in (0, 1, 31, 32, 33, 63, 64, 65, 96, 127, 128, 129)])
 def test_every_place_in_a_tile(ts, kv):
     for dtype, Hq in ((BF, 4), (FP, 64)):
