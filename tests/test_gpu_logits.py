@@ -140,6 +140,27 @@ def test_row_strides(ts, dtype, pad, V):
     Case([3, 9], V, dtype, seed=pad, pad=pad, n_bias=9, masks="shared").run(ts)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF, FP], ids=["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("V", [2, 34, 4098, 20002])
+def test_even_vocabularies(ts, dtype, V):
+    """Rows on a boundary of two values but not of four."""
+    Case([7, 0, 1, 40, 64], V, dtype, seed=V, extra=2, n_bias=40, masks="each").run(ts)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF, FP], ids=["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("V,pad", [(8192, 2), (8194, 2), (8194, 4), (8194, 1)])
+def test_even_row_strides(ts, dtype, V, pad):
+    Case([3, 9], V, dtype, seed=pad, pad=pad, n_bias=9, masks="shared").run(ts)
+
+
+def test_even_rows_in_place(ts):
+    for V, pad in ((4098, 4), (8192, 2)):
+        c = Case([9, 30], V, F32, seed=4, n_bias=5, masks="each", pad=pad)
+        want = c.run(ts)
+        r = ts.ts_logits_process(c.logits, i32(c.cu), out=c.logits, **c.args())
+        assert r is c.logits and torch.equal(r, want)
+
+
 @pytest.mark.parametrize("tree", [False, True])
 @pytest.mark.parametrize("counts", [False, True])
 @pytest.mark.parametrize("n_bias", [0, 1, 700])
