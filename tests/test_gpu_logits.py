@@ -161,6 +161,32 @@ def test_even_rows_in_place(ts):
         assert r is c.logits and torch.equal(r, want)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF, FP], ids=["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("V", [20001, 20002, 20004])
+def test_runs_of_rows(ts, dtype, V):
+    """8 or 9 rows a block: runs that begin inside trees and go from one to the next,
+    whose paths hold a token many times, a mask a row; single rows and streams without
+    a node among them."""
+    q = [64, 40, 57, 1, 0, 64, 1, 1, 63, 48, 64, 51, 64, 3, 64, 60, 64, 64]
+    c = Case(q, V, dtype, seed=V, extra=7, n_bias=60, masks="each")
+    c.tokens[1::3] = c.rng.integers(0, 40, c.tokens[1::3].shape)
+    # 152 SMs hold 6 blocks of 2048 values each
+    assert c.n * ((V + 2047) // 2048) // (152 * 6) in (8, 9)
+    out = torch.full((c.n, V), 55.0, device="cuda")
+    ts.ts_logits_process(c.logits, i32(c.cu), out=out, status=c.status, **c.args())
+    torch.cuda.synchronize()
+    assert int(c.status.item()) == 0 and (out[c.cu[-1]:] == 55.0).all()
+    got = out.cpu().numpy()
+    for s in (0, 1, 3, 6, 7, 8, len(q) - 1):
+        for i in range(q[s]):
+            want, _ = c.row(s, i, True)
+            np.testing.assert_array_equal(got[c.cu[s] + i], want)
+            if i % 16 == 0:
+                Y, err = c.row(s, i, False)
+                fine = np.isfinite(Y)
+                assert (np.abs(got[c.cu[s] + i][fine] - Y[fine]) <= err[fine]).all()
+
+
 @pytest.mark.parametrize("tree", [False, True])
 @pytest.mark.parametrize("counts", [False, True])
 @pytest.mark.parametrize("n_bias", [0, 1, 700])
