@@ -187,6 +187,20 @@ def test_runs_of_rows(ts, dtype, V):
                 assert (np.abs(got[c.cu[s] + i][fine] - Y[fine]) <= err[fine]).all()
 
 
+@pytest.mark.parametrize("V", [500, 4097, 4098])
+@pytest.mark.parametrize("tree", [False, True])
+def test_counts_under_clear_bits_are_not_read(ts, V, tree):
+    """A state whose bits were cleared and whose counts were left: drafted tokens, and
+    neighbours of tokens that were met."""
+    c = Case([6, 20], V, BF, seed=V, tree=tree, n_bias=4, masks="shared")
+    c.counts = np.where(c.seen, c.counts, c.rng.integers(1, 50, c.counts.shape)).astype(np.int32)
+    if tree:
+        c.seen[:, c.tokens[1::2]] = False
+        c.seen[:, 5] = False
+    assert (c.counts[~c.seen] > 0).any()
+    c.run(ts)
+
+
 @pytest.mark.parametrize("tree", [False, True])
 @pytest.mark.parametrize("counts", [False, True])
 @pytest.mark.parametrize("n_bias", [0, 1, 700])
