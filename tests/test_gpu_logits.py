@@ -320,6 +320,21 @@ def test_bad_device_data_is_reported(ts, what):
             np.testing.assert_array_equal(out[i].cpu().numpy(), want)
 
 
+def test_the_sequence_beside_a_long_tree(ts):
+    for V in (5000, 8192):
+        c = Case([6, 70], V, BF, seed=8, n_bias=4, masks="shared")
+        par = [-1] + [0] * 5 + [-1] + [0] * 69
+        out = ts.ts_logits_process(c.logits, i32(c.cu), status=c.status,
+                                   **{**c.args(), "parents": i32(par)})
+        torch.cuda.synchronize()
+        assert int(c.status.item()) == 1
+        c.parents = i32(par)
+        got = out.cpu().numpy()
+        for i in range(6):
+            want, _ = c.row(0, i, True)
+            np.testing.assert_array_equal(got[i], want)
+
+
 @pytest.mark.parametrize("V", [5000, 5001])
 @pytest.mark.parametrize("bad,good", [([0, 6, 10 ** 6], 1), ([0, 6, 3], 1), ([0, 6, -1], 1),
                                       ([0, 6, 14, 2], 2), ([2, 8, 14, 5, 5, 5], 2)])

@@ -523,6 +523,38 @@ def test_commit_reports_bad_tables(ts):
         assert status_of(b) == 1
 
 
+@pytest.mark.parametrize("what,cu,lens,page,at", [
+    ("offset", [0, 8, 4], None, None, 1), ("offset", [0, 8, 2 ** 31 - 1], None, None, 1),
+    ("offset", [-1, 8, 16], None, None, 0), ("length", None, [40, 10 ** 9], None, 1),
+    ("length", None, [-1, 50], None, 0), ("short", None, [5, 50], None, 0),
+    ("page", None, None, -1, 0), ("page", None, None, 10 ** 9, 0), ("page", None, None, 2 ** 31 - 1, 0)])
+def test_commit_beside_bad_tables(ts, what, cu, lens, page, at):
+    """The faulty stream's rows, bounds and length stay, the other's are committed."""
+    b = pu.Batch([8, 8], [40, 50], 2, 2, 64, 16, BF, seed=6)
+    k, v = layers_of(b, 3)
+    mn, mx = (k.amin(3).float() - 1).to(BF), (k.amax(3).float() + 1).to(BF)
+    path = torch.tensor([[0, 3, 5, 6]] * 2, dtype=torch.int32, device="cuda")
+    n_path = torch.tensor([4, 4], dtype=torch.int32, device="cuda")
+    table, cu, lens = b.table.clone(), cu or b.cu, lens or b.kv_lens
+    if page is not None:
+        table[0, 2] = page
+    # the faulty stream as one without nodes
+    good_cu = [0, 0, 8] if at == 0 else [0, 8, 8]
+    refs = [po.kv_commit(*(pu.f64(x[i]) for x in (k, v, mn, mx)), good_cu, b.kv_lens,
+                         b.table_host.numpy(), path.cpu().numpy(), [4, 4])
+            for i in range(3)]
+    i32 = dict(dtype=torch.int32, device="cuda")
+    new = ts.ts_paged_kv_commit(k, v, torch.tensor(cu, **i32), torch.tensor(lens, **i32), table,
+                                path, n_path, key_min=mn, key_max=mx, status=b.status)
+    assert status_of(b) == 1
+    want = list(lens)
+    want[1 - at] = refs[0][4][1 - at]
+    assert new.tolist() == want
+    for i, ref in enumerate(refs):
+        for x, r in zip((k, v, mn, mx), ref):
+            np.testing.assert_array_equal(pu.f64(x[i]), r)
+
+
 def test_commit_refuses_layers_that_start_off_a_boundary(ts):
     """The kernel takes the addresses from a table, where the library cannot see them."""
     b = pu.Batch([5], [20], 4, 2, 64, 16, BF)
