@@ -115,6 +115,7 @@ struct State {
   int before[kTreeNodes];                  // how often they were generated before
   float saved[kTreeNodes];                 // `less` of a drafted token while a row counts it
 };
+static_assert(sizeof(State) <= 48 * 1024, "more shared memory has to be asked for");
 
 // kG: neighbouring values of a thread that its rows allow to go together (4, 2 or 1;
 // single values want 91 registers, and in the 80 of six blocks a SM take 434 us for
@@ -494,7 +495,6 @@ static int go_logits(const LogitsArgs& a, int32_t* status, cudaStream_t st) {
   pdl_config(&cfg, attr, dim3((unsigned)((a.n + run - 1) / run * n_slices)),
              dim3(kThreads), sizeof(State), st);
   auto kern = g == 4 ? logits_kernel<T, 4> : g == 2 ? logits_kernel<T, 2> : logits_kernel<T, 1>;
-  cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(State));
   cudaLaunchKernelEx(&cfg, kern, a, n_slices, run, status);
   return launch_status("logits_kernel");
 }
