@@ -61,10 +61,11 @@ int ts_version(void);
 
 /* Limit of one bounded device-side wait, in SM clock cycles, for kernels
  * launched after this call (from any thread): the verification kernel of (1)
- * and the chunk kernel of (6) and (7) give up a wait on another warp's or the copy engine's progress after
- * `cycles` clocks, write TS_ERR_TIMEOUT into `status`, wait for their own
- * copies and tensor-core work in flight (with the default limit), release
- * their tensor memory and return; that call's outputs are then undefined.
+ * and the chunk kernel of (6) and (7) give up a wait on another warp's or the
+ * copy engine's progress after `cycles` clocks, write TS_ERR_TIMEOUT into
+ * `status`, wait for their own copies and tensor-core work in flight (with the
+ * default limit), release their tensor memory and return; that call's outputs
+ * are then undefined.
  * `cycles` <= 0 restores the default, 2^31 cycles (about one second).  A
  * small limit exists to exercise the expiry path; the paper has no
  * counterpart.  Returns TS_OK. */
@@ -651,8 +652,11 @@ int ts_paged_attention_selected(const void* q, const void* k_pages, const void* 
  *   o[t,h,:] = softmax_j(s) . v_j,  lse[t,h] = ln sum_j exp(s_j).
  *
  * Batch, table, precision, NaN and errors as in ts_paged_attention (6): a
- * chain of nodes is a causal chunk.  A node none of whose rows is there
- * (seq_lens[s] < q_len) gets o = 0, lse = -inf.
+ * chain of nodes is a causal chunk.  (1) differs: it rounds the weights to fp16
+ * for bf16 caches too and returns o in fp32.  Over a bf16 cache a call of many
+ * rows has weights eight times coarser here, 2^-8 of each, but V keeps bf16's
+ * range.  A node none of whose rows is there (seq_lens[s] < q_len) gets o = 0,
+ * lse = -inf.
  * parents  [n] int32, device, packed as the tokens are: the node's parent
  *          within its own tree, 0 <= parents[i] < i, and -1 of each tree's
  *          first node.  Another value is reported as TS_ERR_INVALID_ARG in

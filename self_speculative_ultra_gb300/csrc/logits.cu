@@ -2,7 +2,7 @@
 // token counts that the penalties read.
 //
 //   x = logit + bias[v]
-//   x = (x > 0 ? x / repetition : x * repetition)
+//   x = (x > 0 ? x * (1 / repetition) : x * repetition)
 //       - (frequency c + presence (c > 0))     where v was met; c: how often
 //   x = masked_value                            where v is not allowed
 //
@@ -62,7 +62,7 @@ template <>
 struct FloatsOf<1> { using type = float; };
 
 // The sequence whose rows hold `row` (-1: none), searched by a whole warp in 32
-// steps at once: one round of loads up to 32 sequences, two up to a thousand.
+// steps at once: one round of loads up to 31 sequences, two up to 1023.
 __device__ __forceinline__ int find_seq(const LogitsArgs& a, int row, int lane) {
   // even batches: the sequence stands where its share of the rows does
   const int guess = (int)((int64_t)row * a.n_seq / a.n);
@@ -118,8 +118,9 @@ struct State {
 static_assert(sizeof(State) <= 48 * 1024, "more shared memory has to be asked for");
 
 // kG: neighbouring values of a thread that its rows allow to go together (4, 2 or 1;
-// single values want 91 registers, and in the 80 of six blocks a SM take 434 us for
-// 166).
+// single values want 96 registers, and in the 80 of six blocks a SM take 434 us for
+// 164 on 1024 rows of 128255, though 7.8 for 9.5 where 48 rows of 32003 are 768 blocks
+// for the 760 places of five a SM).
 template <typename T, int kG>
 __global__ void __launch_bounds__(kThreads, kG == 1 ? 5 : kBlocksPerSm)
 logits_kernel(const LogitsArgs a, int n_slices, int run, int32_t* status) {
@@ -483,7 +484,7 @@ static int go_logits(const LogitsArgs& a, int32_t* status, cudaStream_t st) {
   const int64_t blocks = (int64_t)a.n * n_slices;
   const int run = (int)imax64(1, imin64(kMostRun, blocks / (kGb300Sms * kBlocksPerSm)));
   // four or two values at once where every row starts on a boundary of as many (1024
-  // bf16 rows of 128256, 128254 and 128255 values: 135, 147 and 163 us)
+  // bf16 rows of 128256, 128254 and 128255 values: 135, 148 and 164 us)
   auto fits = [&](int g) {
     auto one = [&](const void* p, int64_t stride, size_t size) {
       return reinterpret_cast<uintptr_t>(p) % (g * size) == 0 && stride % g == 0;

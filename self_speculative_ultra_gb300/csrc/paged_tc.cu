@@ -21,10 +21,10 @@
 // node's ancestors are 64 bits a row, laid over the one or two key tiles that hold
 // the tree; all other tiles are as in a chunk.  A tile of at most 128 rows is one
 // group, which takes both S tiles in turn (0.9 us a step for 1.5).  Where every tree
-// is one tile there is no plan (see Line).  64 nodes over 100K rows, 32/8 heads: 81
-// us, 5.2 TB/s with start and join; 12 trees of 25 nodes over 24K rows, 40/8 heads:
-// 189 us (6.4 TB/s), of 51 nodes 229, of 64 (a tile of 256 rows and one of 64, which
-// read the keys twice) 365.
+// is one tile there is no plan (see Line).  64 nodes over 100K rows, 32/8 heads: 80
+// us, 5.2 TB/s with start and join (90 back to back for seconds, at the power cap); 12
+// trees of 25 nodes over 24K rows, 40/8 heads: 189 us (6.4 TB/s), of 51 nodes 229, of
+// 64 (a tile of 256 rows and one of 64, which read the keys twice) 364 to 371.
 //
 // Three launches.  The plan (one CTA) lists the work from the device-side
 // lengths in order of falling cost: the tiles of whole rounds over the SMs as
@@ -47,7 +47,9 @@
 //                below 2^-7, see kHead); sums in fp32.  P is rounded once, to
 //                the type of V, since the tensor core takes both operands of a
 //                product in one 16-bit type: off by half a step a weight, as the
-//                output's own rounding is, and averaged over the keys.
+//                output's own rounding is, and averaged over the keys.  (The call
+//                over a contiguous cache has P in fp16 and turns a bf16 V into fp16
+//                for it, which bounds |v|; here V keeps its type and range.)
 // At the end of an item the softmax warps write O / l (or the piece's O, m, l
 // in fp32); the next item's first scores are formed meanwhile.
 //
@@ -581,7 +583,7 @@ struct Work {
 // head) stand on a line, each as long as it costs, and CTA c takes the c-th of C
 // equal stretches of it, which it finds from the lengths by itself; a tile that
 // cuts fall into is joined as in the plan's list.  That saves the plan's launch (64
-// nodes over 100K rows 91 -> 81 us, nine short streams 33 -> 22).  The host sees to
+// nodes over 100K rows 91 -> 80 us, nine short streams 33 -> 22).  The host sees to
 // it that the line is shorter than 2^31.
 // The first copy waits for all of this, and for its instructions too, which a new
 // kernel fetches from afar: a warp does it alone, in few of them.
