@@ -765,10 +765,10 @@ int ts_token_counts(const int32_t* tokens, int stride, const int32_t* lens, int 
  *          of each row, -1 for none (with n_masks = 0 all are); NULL: row t has
  *          mask t.  A mask without a set bit leaves masked_value everywhere.
  * Ids, mask rows or a repetition penalty out of their range are reported as
- * TS_ERR_INVALID_ARG in `status` and count as absent.  So are offsets out of
- * their range or order: sequences in front of the first such offset keep the
- * rows that no other one claims, the other rows are unspecified (with more
- * than 31 sequences: all are).  No access leaves the buffers. */
+ * TS_ERR_INVALID_ARG in `status` and count as absent.  Offsets out of their
+ * range or order are reported too: sequences in front of the first such offset
+ * keep the rows that no other one claims, the other rows are unspecified (with
+ * more than 31 sequences: all are).  No access leaves the buffers. */
 #define TS_LOGITS_BF16 1
 #define TS_LOGITS_FP16 2
 int ts_logits_process(const void* logits, int64_t row_stride, int n, int V, const int32_t* cu_q,
